@@ -80,12 +80,14 @@ enum {
 };
 
 /* bits of *dev_err */
-#define PA_DEVERR_BAD_BLOCK 1 /* a needed block_table entry is < 0 or >= num_blocks */
+#define PA_DEVERR_BAD_BLOCK 1 /* a needed block_table entry is < 0 or >= num_blocks, or a slot
+                                 lies beyond the pool */
 #define PA_DEVERR_OVERFLOW 2  /* a position lies beyond max_blocks_per_seq * block_size,
                                  or a length is negative */
 #define PA_DEVERR_BAD_CU 4    /* cu_seq_lens not non-decreasing, or cu_seq_lens_k does not
                                  equal cache_seqlens + q lengths in pa_cache_update */
 #define PA_DEVERR_TIMEOUT 8   /* a bounded wait inside a kernel gave up */
+#define PA_DEVERR_NO_SPACE 16 /* pa_block_tables: too few free blocks, or slot_map too short */
 
 /*
  * Bytes of scratch workspace pa_decode needs for these sizes on the current
@@ -262,6 +264,134 @@ int pa_varlen_paged(const void *q, const void *k_cache, const void *v_cache,
                     void *out, int batch, int total_q, int num_heads, int num_kv_heads,
                     int head_dim, int num_blocks, int block_size, int max_blocks_per_seq,
                     pa_dtype dtype, float softmax_scale, int32_t *dev_err, void *stream);
+
+/*
+ * The 4-bit pool
+ * --------------
+ * kv_cache of the *_q4 calls is bytes [num_blocks, num_kv_heads, record],
+ * record = block_size * (head_dim + 8): the keys and the values of one kv
+ * head of one block, side by side, so that one bulk copy brings all a head
+ * needs of a block and no line holds another head's bytes.  pa_q4_block_bytes
+ * is num_kv_heads * record (0 for sizes that are not supported: head_dim 64
+ * or 128, block_size 16 or 32).
+ *
+ * A row x of head_dim values (one token, one kv head, K or V) is held as
+ * head_dim codes n of 4 bits, a step s and a low value b, both bf16; it
+ * stands for b + n s.  With fl = rounding to fp32 after each operation:
+ *   b   = min x, rounded down to bf16
+ *   r   = fl(fl(max x / 16 - b / 16) * fl(16 / 15))
+ *   s   = r rounded up to bf16; 0 when r < 2^-100
+ *   n_i = round-half-even(fl(fl(x_i / 16 - b / 16) * fl(16 / s))), at most 15
+ *         (0 when s = 0)
+ * so |x_i - (b + n_i s)| <= s / 2 up to the fp32 roundings.  A row that
+ * holds an infinity or a NaN (or fp32 values that round to an infinite b) is
+ * held as s = b = NaN, n = 0: the whole row reads back as NaN.
+ *
+ * Inside a record, for token t of the block and D = head_dim:
+ *   K codes  bytes [0, bs*D/2): row t at t*D/2, dim 2i in the low half of
+ *            byte i, dim 2i + 1 in its high half;
+ *   V codes  bytes [bs*D/2, bs*D): 16-bit units of 4 dims (dim 4x + k in bits
+ *            4k..4k+3).  Tokens 2p and 2p + 1 share 32-bit words: unit (t, x)
+ *            is unit number 2 (p D/4 + 8 u + x % 8) + t % 2 with p = t / 2 and
+ *            u = (x / 8) xor (p % 4) for D = 128, (x / 8) xor (p / 2 % 2) for
+ *            D = 64.  A word is then an operand of the tensor cores' value
+ *            product (dims on the rows, a token pair in a register) after one
+ *            mask, and the xor spreads the loads over the memory banks;
+ *   scales   bytes [bs*D, bs*(D+8)): 4 bf16 a token: K step, K low, V step,
+ *            V low.
+ */
+size_t pa_q4_block_bytes(int num_kv_heads, int head_dim, int block_size);
+
+/*
+ * Quantise and scatter: row i of k_chunk, v_chunk [total_q, num_kv_heads,
+ * head_dim] is written to slot slot_map[i] (physical block * block_size +
+ * offset, as pa_block_tables gives them).  Rows whose slot is negative are
+ * skipped (padding of a captured step); a slot >= num_blocks * block_size
+ * sets PA_DEVERR_BAD_BLOCK and is skipped.  A slot may appear once only: two
+ * rows in one slot leave a mixture of both.  dtype is that of the chunk.
+ * num_blocks * block_size < 2^31.
+ */
+int pa_cache_update_q4(const void *k_chunk, const void *v_chunk, const int32_t *slot_map,
+                       void *kv_cache, int total_q, int num_kv_heads, int head_dim,
+                       int num_blocks, int block_size, pa_dtype dtype, int32_t *dev_err,
+                       void *stream);
+
+/*
+ * Read back: rows [cu_seq_lens_k[r], cu_seq_lens_k[r+1]) of k_full, v_full
+ * [total_k, num_kv_heads, head_dim] receive logical positions 0, 1, .. of
+ * request r as values (b + n s in fp32, rounded to dtype), which pa_varlen
+ * takes as they are.  Rows behind cu_seq_lens_k[batch] are left as they
+ * were.  A needed block_table entry that is no block sets
+ * PA_DEVERR_BAD_BLOCK, a position beyond the table PA_DEVERR_OVERFLOW; those
+ * rows are zeroed.  cu_seq_lens_k that does not start at 0, decreases or
+ * passes total_k sets PA_DEVERR_BAD_CU; nothing behind total_k is written.
+ */
+int pa_cache_gather_q4(const void *kv_cache, const int32_t *block_table,
+                       const int32_t *cu_seq_lens_k, void *k_full, void *v_full, int batch,
+                       int total_k, int num_kv_heads, int head_dim, int num_blocks,
+                       int block_size, int max_blocks_per_seq, pa_dtype dtype, int32_t *dev_err,
+                       void *stream);
+
+/*
+ * pa_decode over the 4-bit pool: the new token is quantised into position
+ * L = cache_seqlens[b] and the query attends over positions 0..L as the pool
+ * holds them, the new token included (so a later step sees the same value).
+ *   out[b, h] = sum_j softmax_j(scale q.K_j) V_j,  K_j = bK_j + sK_j nK_j, V_j likewise
+ * q, k_new, v_new, out (and k_stored, v_stored) are of `dtype`; PA_BF16 and
+ * PA_F32 run the same tensor-core kernel, fp32 operands as sums of two halves.
+ * k_stored, v_stored [batch, num_kv_heads, head_dim], each or both NULL: the
+ * values the pool now stands for at L, for a caller that uses them again in
+ * this step (a later layer that shares these keys) or watches the error.
+ * Left as they were where the sequence's append was refused.
+ * block_table, cache_seqlens, workspace, device errors, placement and the
+ * limits num_heads / num_kv_heads <= 8, batch * num_kv_heads <= 262144 as
+ * pa_decode; every pointer is device memory.  A key or value row that is NaN
+ * makes the outputs it reaches NaN, as the formula does.
+ */
+size_t pa_decode_q4_workspace_size(int batch, int num_heads, int num_kv_heads, int head_dim,
+                                   int block_size, pa_dtype dtype);
+int pa_decode_q4(const void *q, void *kv_cache, const int32_t *block_table,
+                 const int32_t *cache_seqlens, const void *k_new, const void *v_new, void *out,
+                 void *k_stored, void *v_stored, int batch, int num_heads, int num_kv_heads,
+                 int head_dim, int num_blocks, int block_size, int max_blocks_per_seq,
+                 pa_dtype dtype, float softmax_scale, void *workspace, size_t workspace_bytes,
+                 int32_t *dev_err, void *stream);
+
+/*
+ * One serving step's block tables and slot map, built on the GPU from the
+ * requests' lengths: the device counterpart of pa_bm_append / pa_bm_free /
+ * pa_bm_tables (no reference counts: blocks shared by several requests stay
+ * with the host manager).  The step needs no host copy and can be captured.
+ *
+ * Request b holds L = cache_seqlens[b] tokens in the first ceil(L / bs)
+ * entries of its block_table row, and gets n = new_lens[b] new ones:
+ *   n >= 0  ceil((L+n)/bs) - ceil(L/bs) blocks are taken and entered in its
+ *           row;
+ *   n = -1  the request has ended: its blocks go back, its length becomes 0
+ *           (its row is left as it is; nothing reads it at length 0).
+ * free_blocks [num_blocks] is a stack of *num_free block ids (top at the
+ * end).  Ended requests push their blocks first, in order of (request,
+ * logical block); then the taken blocks are popped in the same order.
+ *   slot_map [total_slots]     the new tokens' slots, packed by
+ *                              cu_seq_lens_q; -1 behind the last token
+ *   cu_seq_lens_q [batch+1]    cumulative new tokens
+ *   cu_seq_lens_k [batch+1]    cumulative lengths after the step
+ *   seqlens_k [batch]          lengths after the step; may be cache_seqlens
+ *   num_free_out [1]           may be num_free
+ * All or nothing: with a negative length, n < -1 or a length beyond
+ * max_blocks_per_seq * block_size (PA_DEVERR_OVERFLOW), too few free blocks
+ * or more new tokens than total_slots (PA_DEVERR_NO_SPACE), a free stack that
+ * would not fit num_blocks (PA_DEVERR_BAD_BLOCK) or lengths that add up past
+ * 2^31 - 1 (PA_DEVERR_BAD_CU), the step changes no table, stack or length:
+ * slot_map is all -1, both cu arrays are 0.  A block id outside the pool met
+ * on the way sets PA_DEVERR_BAD_BLOCK, is passed on as -1, and tokens in it
+ * get slot -1.  batch <= 16384; num_blocks * block_size < 2^31.
+ */
+int pa_block_tables(const int32_t *cache_seqlens, const int32_t *new_lens, int32_t *block_table,
+                    int32_t *free_blocks, const int32_t *num_free, int32_t *slot_map,
+                    int32_t *cu_seq_lens_q, int32_t *cu_seq_lens_k, int32_t *seqlens_k,
+                    int32_t *num_free_out, int batch, int total_slots, int num_blocks,
+                    int block_size, int max_blocks_per_seq, int32_t *dev_err, void *stream);
 
 /* Static description of a status code (never NULL). */
 const char *pa_status_string(int status);

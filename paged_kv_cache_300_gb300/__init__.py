@@ -14,6 +14,11 @@ built, or no GPU is present, calls raise.
                      (optionally gather prefix + chunk into packed k/v)
     pa_varlen        packed variable-length attention (bf16: tcgen05)
     pa_varlen_paged  the same, reading keys through block_table from the pool
+    pa_block_tables  a step's block tables, slot map and cumulative lengths,
+                     built on the GPU from the requests' lengths
+    pa_cache_update_q4  quantise a chunk into the 4-bit pool, by slot map
+    pa_cache_gather_q4  read whole sequences of the 4-bit pool back
+    pa_decode_q4     the decode step over the 4-bit pool
 """
 from __future__ import annotations
 
@@ -28,7 +33,9 @@ __all__ = [
     "pa_decode_contiguous", "pa_decode_contiguous_workspace_size",
     "pa_cache_update", "pa_varlen", "pa_varlen_paged",
     "pa_decode_workspace_size", "pa_status_string", "pa_version", "DEVERR_BAD_BLOCK",
-    "DEVERR_OVERFLOW", "DEVERR_BAD_CU", "DEVERR_TIMEOUT",
+    "DEVERR_OVERFLOW", "DEVERR_BAD_CU", "DEVERR_TIMEOUT", "DEVERR_NO_SPACE", "pa_block_tables",
+    "pa_q4_block_bytes", "pa_q4_pool", "pa_cache_update_q4", "pa_cache_gather_q4", "pa_decode_q4",
+    "pa_decode_q4_workspace_size",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +43,7 @@ _LIB_PATH = os.path.join(_HERE, "_lib", "libpa300.so")
 
 PA_F32, PA_BF16 = 0, 1
 DEVERR_BAD_BLOCK, DEVERR_OVERFLOW, DEVERR_BAD_CU, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_NO_SPACE = 16
 
 _lock = threading.Lock()
 _lib = None
@@ -80,6 +88,18 @@ def load():
         lib.pa_varlen.restype = i
         lib.pa_varlen_paged.argtypes = [p] * 6 + [i] * 3 + [p] + [i] * 8 + [i, f, p, p]
         lib.pa_varlen_paged.restype = i
+        lib.pa_q4_block_bytes.argtypes = [i] * 3
+        lib.pa_q4_block_bytes.restype = sz
+        lib.pa_cache_update_q4.argtypes = [p] * 4 + [i] * 6 + [p, p]
+        lib.pa_cache_update_q4.restype = i
+        lib.pa_cache_gather_q4.argtypes = [p] * 5 + [i] * 8 + [p, p]
+        lib.pa_cache_gather_q4.restype = i
+        lib.pa_decode_q4_workspace_size.argtypes = [i] * 6
+        lib.pa_decode_q4_workspace_size.restype = sz
+        lib.pa_decode_q4.argtypes = [p] * 9 + [i] * 8 + [f, p, sz, p, p]
+        lib.pa_decode_q4.restype = i
+        lib.pa_block_tables.argtypes = [p] * 10 + [i] * 5 + [p, p]
+        lib.pa_block_tables.restype = i
         lib.pa_status_string.argtypes = [i]
         lib.pa_status_string.restype = ctypes.c_char_p
         lib.pa_version.argtypes = []
@@ -343,3 +363,238 @@ def pa_varlen_paged(q, k_cache, v_cache, block_table, cu_seq_lens_q, seqlens_k,
                                 _stream(stream))
     _call("pa_varlen_paged", rc)
     return out
+
+
+# ------------------------------------------------------------------ 4-bit pool
+def _int32_on(dev, **ts):
+    """Index tensors: int32, contiguous, on `dev`."""
+    for name, t in ts.items():
+        if t is None:
+            continue
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+        if t.device != dev:
+            raise ValueError("all tensors must be on the same device")
+        if not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous")
+
+
+def _like_on(dev, dtype, shape, **ts):
+    """Element tensors of one dtype and shape, contiguous, on `dev`."""
+    for name, t in ts.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have the shape {tuple(shape)}")
+        if t.device != dev:
+            raise ValueError("all tensors must be on the same device")
+        if not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous")
+
+
+def _q4_geometry(kv_cache, num_kv_heads, head_dim):
+    """Block size of a 4-bit pool [num_blocks, num_kv_heads, record]."""
+    if not kv_cache.is_cuda:
+        raise ValueError("all tensors must live on a CUDA device")
+    if kv_cache.dtype != torch.uint8 or kv_cache.dim() != 3 or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be a contiguous uint8 tensor "
+                         "[num_blocks, num_kv_heads, block_size * (head_dim + 8)]")
+    record = kv_cache.shape[2]
+    if kv_cache.shape[1] != num_kv_heads or record % (head_dim + 8) != 0:
+        raise ValueError("kv_cache does not fit the number of kv heads or the head_dim")
+    return record // (head_dim + 8)
+
+
+class _On:
+    """Makes a tensor's device the current one for a call and names the
+    stream: the given one, else that device's current stream."""
+
+    __slots__ = ("dev", "prev", "stream")
+
+    def __init__(self, dev, stream):
+        self.dev = dev.index
+        self.stream = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        self.prev = cur if cur != self.dev else None
+        if self.prev is not None:
+            torch.cuda.set_device(self.dev)
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+
+
+def pa_q4_block_bytes(num_kv_heads, head_dim, block_size) -> int:
+    """Bytes of one block of the 4-bit pool; 0 for sizes it does not have."""
+    return int(load().pa_q4_block_bytes(num_kv_heads, head_dim, block_size))
+
+
+def pa_q4_pool(num_blocks, num_kv_heads, head_dim, block_size, device="cuda"):
+    """A zeroed 4-bit pool: uint8 [num_blocks, num_kv_heads,
+    block_size * (head_dim + 8)] (layout in include/pa.h)."""
+    nbytes = pa_q4_block_bytes(num_kv_heads, head_dim, block_size)
+    if nbytes == 0:
+        raise ValueError("the 4-bit pool has head_dim 64 or 128 and block_size 16 or 32")
+    return torch.zeros(num_blocks, num_kv_heads, nbytes // num_kv_heads, dtype=torch.uint8,
+                       device=device)
+
+
+def pa_cache_update_q4(k_chunk, v_chunk, slot_map, kv_cache, dev_err=None, stream=None):
+    """Quantise the rows of k_chunk, v_chunk [T, Hkv, D] (bfloat16 or float32)
+    into the slots slot_map [T] int32 of the 4-bit pool; a negative slot skips
+    its row."""
+    t, hkv, d = k_chunk.shape
+    bs = _q4_geometry(kv_cache, hkv, d)
+    dev = kv_cache.device
+    dt = _dtype(k_chunk)
+    _like_on(dev, k_chunk.dtype, k_chunk.shape, k_chunk=k_chunk, v_chunk=v_chunk)
+    _int32_on(dev, slot_map=slot_map, dev_err=dev_err)
+    if slot_map.shape != (t,):
+        raise ValueError("slot_map must have one entry for each row")
+    with _On(dev, stream) as st:
+        rc = load().pa_cache_update_q4(k_chunk.data_ptr(), v_chunk.data_ptr(), slot_map.data_ptr(),
+                                       kv_cache.data_ptr(), t, hkv, d, kv_cache.shape[0], bs, dt,
+                                       None if dev_err is None else dev_err.data_ptr(), st)
+    _call("pa_cache_update_q4", rc)
+
+
+def pa_cache_gather_q4(kv_cache, block_table, cu_seq_lens_k, k_full, v_full, dev_err=None,
+                       stream=None):
+    """Read positions 0.. of every request back from the 4-bit pool into the
+    packed k_full, v_full [Tk, Hkv, D] (bfloat16 or float32), request r's rows
+    being [cu_seq_lens_k[r], cu_seq_lens_k[r+1]).  Returns (k_full, v_full)."""
+    tk, hkv, d = k_full.shape
+    bs = _q4_geometry(kv_cache, hkv, d)
+    dev = kv_cache.device
+    dt = _dtype(k_full)
+    _like_on(dev, k_full.dtype, k_full.shape, k_full=k_full, v_full=v_full)
+    _int32_on(dev, block_table=block_table, cu_seq_lens_k=cu_seq_lens_k, dev_err=dev_err)
+    b, mb = block_table.shape
+    if cu_seq_lens_k.shape != (b + 1,):
+        raise ValueError("cu_seq_lens_k must have one entry more than block_table has rows")
+    with _On(dev, stream) as st:
+        rc = load().pa_cache_gather_q4(kv_cache.data_ptr(), block_table.data_ptr(),
+                                       cu_seq_lens_k.data_ptr(), k_full.data_ptr(),
+                                       v_full.data_ptr(), b, tk, hkv, d, kv_cache.shape[0], bs, mb,
+                                       dt, None if dev_err is None else dev_err.data_ptr(), st)
+    _call("pa_cache_gather_q4", rc)
+    return k_full, v_full
+
+
+def pa_decode_q4_workspace_size(batch, num_heads, num_kv_heads, head_dim, block_size,
+                                dtype=torch.bfloat16) -> int:
+    dt = PA_BF16 if dtype == torch.bfloat16 else PA_F32
+    return int(load().pa_decode_q4_workspace_size(batch, num_heads, num_kv_heads, head_dim,
+                                                  block_size, dt))
+
+
+_TICKET_REGION = 1 << 20  # merge counters at the start of a decode workspace
+_q4_workspaces: dict = {}
+
+
+def _q4_workspace(dev, stream, handle, nbytes, counters):
+    """Workspace of a pa_decode_q4 call that was given none.  Eager calls
+    share one per (device, stream), zeroed when it is made.  A call that is
+    being captured gets its own from the graph's memory, with its counters
+    cleared inside the graph: two graphs may replay at the same time."""
+    if nbytes == 0:
+        return None
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws[:4 * counters].zero_()
+        return ws
+    key = (dev.index, handle)
+    ws = _q4_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        with torch.cuda.stream(stream):  # None: the current stream
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        _q4_workspaces[key] = ws
+    return ws
+
+
+def pa_decode_q4(q, kv_cache, block_table, cache_seqlens, k_new, v_new, out=None,
+                 softmax_scale: float = 0.0, k_stored=None, v_stored=None, workspace=None,
+                 dev_err=None, stream=None):
+    """Decode step over the 4-bit pool (see include/pa.h): k_new, v_new
+    [B, Hkv, D] are quantised in place at position cache_seqlens[b] and
+    q [B, Hq, D] attends over positions 0..cache_seqlens[b].  bfloat16 or
+    float32.  k_stored, v_stored, when given, receive the new token as the
+    pool now holds it.  Returns out [B, Hq, D]."""
+    b, hq, d = q.shape
+    hkv = k_new.shape[1]
+    bs = _q4_geometry(kv_cache, hkv, d)
+    dev = kv_cache.device
+    dt = _dtype(q)
+    _like_on(dev, q.dtype, q.shape, q=q, out=out)
+    _like_on(dev, q.dtype, (b, hkv, d), k_new=k_new, v_new=v_new, k_stored=k_stored,
+             v_stored=v_stored)
+    _int32_on(dev, block_table=block_table, cache_seqlens=cache_seqlens, dev_err=dev_err)
+    if block_table.shape[0] != b or cache_seqlens.shape != (b,):
+        raise ValueError("inconsistent shapes")
+    if out is None:
+        out = torch.empty_like(q)
+    lib = load()
+    with _On(dev, stream) as st:
+        if workspace is None:
+            nbytes = int(lib.pa_decode_q4_workspace_size(b, hq, hkv, d, bs, dt))
+            workspace = _q4_workspace(dev, stream, st, nbytes, b * hkv)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous and on the same device")
+        wptr, wbytes = (None, 0) if workspace is None else (
+            workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        rc = lib.pa_decode_q4(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
+                              cache_seqlens.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                              out.data_ptr(), None if k_stored is None else k_stored.data_ptr(),
+                              None if v_stored is None else v_stored.data_ptr(), b, hq, hkv, d,
+                              kv_cache.shape[0], bs, block_table.shape[1], dt,
+                              float(softmax_scale), wptr, wbytes,
+                              None if dev_err is None else dev_err.data_ptr(), st)
+    _call("pa_decode_q4", rc)
+    return out
+
+
+# ------------------------------------------------------------------ block tables
+def pa_block_tables(cache_seqlens, new_lens, block_table, free_blocks, num_free, slot_map,
+                    block_size, cu_seq_lens_q=None, cu_seq_lens_k=None, seqlens_k=None,
+                    num_free_out=None, dev_err=None, stream=None):
+    """One step's block tables from the requests' lengths (see include/pa.h).
+    cache_seqlens, new_lens [B]; block_table [B, MB] and free_blocks
+    [num_blocks] are updated in place; slot_map [any length] is filled, -1
+    behind the last token.  All int32.  num_free [1] is advanced in place
+    unless num_free_out is given.  Returns (cu_seq_lens_q, cu_seq_lens_k,
+    seqlens_k)."""
+    b, mb = block_table.shape
+    dev = block_table.device
+    if not block_table.is_cuda:
+        raise ValueError("all tensors must live on a CUDA device")
+    if cu_seq_lens_q is None:
+        cu_seq_lens_q = torch.empty(b + 1, dtype=torch.int32, device=dev)
+    if cu_seq_lens_k is None:
+        cu_seq_lens_k = torch.empty(b + 1, dtype=torch.int32, device=dev)
+    if seqlens_k is None:
+        seqlens_k = torch.empty(b, dtype=torch.int32, device=dev)
+    if num_free_out is None:
+        num_free_out = num_free
+    _int32_on(dev, cache_seqlens=cache_seqlens, new_lens=new_lens, block_table=block_table,
+              free_blocks=free_blocks, num_free=num_free, slot_map=slot_map,
+              cu_seq_lens_q=cu_seq_lens_q, cu_seq_lens_k=cu_seq_lens_k, seqlens_k=seqlens_k,
+              num_free_out=num_free_out, dev_err=dev_err)
+    if cache_seqlens.shape != (b,) or new_lens.shape != (b,) or seqlens_k.shape != (b,) or \
+            cu_seq_lens_q.shape != (b + 1,) or cu_seq_lens_k.shape != (b + 1,) or \
+            free_blocks.dim() != 1 or slot_map.dim() != 1 or num_free.numel() != 1 or \
+            num_free_out.numel() != 1:
+        raise ValueError("inconsistent shapes")
+    with _On(dev, stream) as st:
+        rc = load().pa_block_tables(
+            cache_seqlens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+            free_blocks.data_ptr(), num_free.data_ptr(), slot_map.data_ptr(),
+            cu_seq_lens_q.data_ptr(), cu_seq_lens_k.data_ptr(), seqlens_k.data_ptr(),
+            num_free_out.data_ptr(), b, slot_map.shape[0], free_blocks.shape[0], block_size, mb,
+            None if dev_err is None else dev_err.data_ptr(), st)
+    _call("pa_block_tables", rc)
+    return cu_seq_lens_q, cu_seq_lens_k, seqlens_k

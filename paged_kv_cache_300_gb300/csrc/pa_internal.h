@@ -119,6 +119,58 @@ int varlen_paged_bf16_launch(const VarlenArgs &a, const CUtensorMap &tm_q,
                              const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                              const CUtensorMap &tm_o, cudaStream_t s);
 
+// ------------------------------------------------------------------ 4-bit pool
+struct CacheQ4Args {
+    const void *k; // update: the chunk
+    const void *v;
+    const int32_t *slot_map;
+    void *kv_cache;
+    const int32_t *block_table; // gather
+    const int32_t *cu_k;
+    void *k_full;
+    void *v_full;
+    int32_t *dev_err;
+    int total; // rows of the chunk, or of k_full / v_full
+    int batch, num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq;
+};
+int cache_q4_launch(const CacheQ4Args &a, bool f32, bool gather, cudaStream_t s);
+
+struct DecodeQ4Args {
+    const void *q;
+    void *kv_cache;
+    const int32_t *block_table;
+    const int32_t *cache_seqlens;
+    const void *k_new;
+    const void *v_new;
+    void *out;
+    void *k_stored;
+    void *v_stored;
+    float *part;
+    int32_t *tickets;
+    int32_t *dev_err;
+    int batch, num_heads, num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq, group;
+    float scale, scale_log2;
+};
+size_t decode_q4_workspace(int batch, int num_heads, int num_kv_heads, int head_dim, int block_size);
+int decode_q4_launch(const DecodeQ4Args &a, bool f32, cudaStream_t s);
+
+struct TablesArgs {
+    const int32_t *cache_seqlens;
+    const int32_t *new_lens;
+    int32_t *block_table;
+    int32_t *free_blocks;
+    const int32_t *num_free;
+    int32_t *slot_map;
+    int32_t *cu_q;
+    int32_t *cu_k;
+    int32_t *seqlens_k;
+    int32_t *num_free_out;
+    int32_t *dev_err;
+    int batch, total_slots, num_blocks, block_size, max_blocks_per_seq;
+};
+constexpr int kTablesMaxBatch = 16384;
+int tables_launch(const TablesArgs &a, cudaStream_t s);
+
 // ------------------------------------------------------------------ helpers
 int num_sms();
 int encode_rows_map(CUtensorMap *map, const void *base, uint64_t rows, int heads, int head_dim,

@@ -1,0 +1,96 @@
+// Format of the 4-bit paged pool, shared by the kernels that write and read
+// it.  The format itself is stated in include/pa.h ("The 4-bit pool").
+#pragma once
+
+#include "pa_common.cuh"
+
+namespace pa {
+
+// Bytes of one record (one kv head of one block) and where its parts start.
+__host__ __device__ constexpr int q4_record_bytes(int d, int bs) { return bs * (d + 8); }
+__host__ __device__ constexpr int q4_v_offset(int d, int bs) { return bs * d / 2; }
+__host__ __device__ constexpr int q4_scale_offset(int d, int bs) { return bs * d; }
+
+// Number of the 16-bit unit that holds dims 4x..4x+3 of token t's value.
+template <int D>
+__device__ __forceinline__ int q4_v_unit(int t, int x)
+{
+    const int p = t >> 1;
+    const int u = (x >> 3) ^ ((D == 128 ? p : p >> 1) & (D / 32 - 1));
+    return 2 * (p * (D / 4) + u * 8 + (x & 7)) + (t & 1);
+}
+
+// Step, low and 16 / step of a row with the given extrema.  Each operation
+// is rounded on its own (no contraction), because the codes are defined by
+// these fp32 steps.
+struct Q4Scale {
+    float step, low;
+    float low16; // low / 16
+    float inv16; // 16 / step; 0 when every code is 0
+};
+// fp32 -> the next bf16 away from zero (bits), still in an fp32 register.
+__device__ __forceinline__ float bf16_away(float x)
+{
+    return __uint_as_float((__float_as_uint(x) + 0xffffu) & 0xffff0000u);
+}
+__device__ __forceinline__ Q4Scale q4_scale(float lo, float hi, bool finite)
+{
+    Q4Scale r;
+    r.low = lo < 0.f ? bf16_away(lo) : __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
+    r.low16 = __fmul_rn(r.low, 0.0625f);
+    const float range = __fmul_rn(__fsub_rn(__fmul_rn(hi, 0.0625f), r.low16), 16.0f / 15.0f);
+    r.step = range < 7.888609052210118e-31f /* 2^-100 */ ? 0.f : bf16_away(range);
+    if (!finite || fabsf(r.low) == INFINITY) {
+        r.step = r.low = __int_as_float(0x7fc00000);
+        r.inv16 = 0.f;
+        r.low16 = 0.f;
+    } else {
+        r.inv16 = r.step > 0.f ? __fdiv_rn(16.0f, r.step) : 0.f;
+    }
+    return r;
+}
+// Code of x; x is finite or the row is NaN (inv16 = 0, and the comparison
+// below turns a NaN product into code 0).
+__device__ __forceinline__ uint32_t q4_code(float x, const Q4Scale &s)
+{
+    const float n = rintf(__fmul_rn(__fsub_rn(__fmul_rn(x, 0.0625f), s.low16), s.inv16));
+    return n > 0.f ? (uint32_t)fminf(n, 15.f) : 0u;
+}
+__device__ __forceinline__ float q4_value(uint32_t n, float step, float low)
+{
+    return fmaf((float)n, step, low); // n * step is exact
+}
+// Two bf16 (step, low) as one 32-bit word; the values are bf16 already.
+__device__ __forceinline__ uint32_t q4_pack_scale(const Q4Scale &s)
+{
+    return (__float_as_uint(s.step) >> 16) | (__float_as_uint(s.low) & 0xffff0000u);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32<float>(float x)
+{
+    return x;
+}
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x)
+{
+    return __bfloat162float(x);
+}
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x)
+{
+    return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x)
+{
+    return __float2bfloat16_rn(x);
+}
+
+}  // namespace pa

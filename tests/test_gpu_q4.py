@@ -1,0 +1,450 @@
+"""The 4-bit pool on the GPU: update, read-back and decode against the plain
+reference."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_300_gb300 as pa
+from oracle import q4
+from tests.q4_util import NORM, check, decode_bound, make
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _needs_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pa.load()
+
+
+def _dev(c):
+    return {k: (v if isinstance(v, torch.Tensor) else torch.from_numpy(v)).to(DEV)
+            for k, v in c.items() if k != "bs"}
+
+
+def _f32(t):
+    return t.float().numpy()
+
+
+def _same_pool(got, want, bs, d):
+    """Codes and scales equal (a NaN scale is a NaN scale)."""
+    got = got.cpu().numpy()
+    assert np.array_equal(got[:, :, :bs * d], want[:, :, :bs * d])
+    g, w = (np.ascontiguousarray(x[:, :, bs * d:]).view("<u2").astype(np.int64) for x in (got, want))
+    nan = lambda x: (x & 0x7FFF) > 0x7F80  # noqa: E731
+    zero = lambda x: (x & 0x7FFF) == 0  # noqa: E731
+    assert ((g == w) | (nan(g) & nan(w)) | (zero(g) & zero(w))).all()
+
+
+# ------------------------------------------------------------------ update
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,bs,hkv", [(64, 16, 1), (64, 32, 3), (128, 16, 8), (128, 32, 5), (64, 32, 2)])
+@pytest.mark.parametrize("total", [1, 2, 37, 200])
+def test_update(dtype, d, bs, hkv, total):
+    rng = np.random.default_rng(total + d)
+    g = torch.Generator().manual_seed(total)
+    nb = -(-total // bs) + 3
+    start = int(rng.integers(0, 2 * bs))
+    slots = (start + np.arange(total)).astype(np.int32)  # a run that starts anywhere in a block
+    if total == 200:
+        slots = rng.permutation(nb * bs)[:total].astype(np.int32)  # and slots in any order
+    slots[rng.random(total) < 0.1] = -1
+    x = torch.randn(2, total, hkv, d, generator=g) * torch.exp(3 * torch.randn(2, total, hkv, 1, generator=g))
+    x[0, 0, 0] = 1.5                   # a row of one value
+    x[1, 0, hkv - 1] = 0.0
+    x[0, total // 2, 0, 3] = float("nan")
+    x[1, total // 2, 0, 9] = float("inf")
+    x = x.to(dtype)
+    pool = rng.integers(0, 256, (nb, hkv, q4.record_bytes(d, bs)), dtype=np.uint8)
+    got = torch.from_numpy(pool).to(DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.pa_cache_update_q4(x[0].to(DEV), x[1].to(DEV), torch.from_numpy(slots).to(DEV), got, dev_err=err)
+    torch.cuda.synchronize()
+    for i, s in enumerate(slots):
+        if s >= 0:
+            q4.write(pool, int(s), _f32(x[0, i]), _f32(x[1, i]), bs)
+    assert err.item() == 0
+    _same_pool(got, pool, bs, d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_update_of_extreme_rows(dtype):
+    """Rows from the smallest to the largest numbers, and rows whose range
+    passes the largest one."""
+    d, bs, hkv = 128, 16, 2
+    g = torch.Generator().manual_seed(3)
+    mag = 10.0 ** torch.linspace(-37, 38, 32)
+    x = torch.rand(2, 32, hkv, d, generator=g) * 2 - 1
+    x = (x * mag.view(1, -1, 1, 1)).clamp(-3.3e38, 3.3e38).to(dtype)
+    x[0, -1, 0, 0], x[0, -1, 0, 1] = 3.3e38, -3.3e38
+    pool = np.zeros((2, hkv, q4.record_bytes(d, bs)), dtype=np.uint8)
+    got = torch.from_numpy(pool).to(DEV)
+    pa.pa_cache_update_q4(x[0].to(DEV), x[1].to(DEV), torch.arange(32, dtype=torch.int32, device=DEV), got)
+    for i in range(32):
+        q4.write(pool, i, _f32(x[0, i]), _f32(x[1, i]), bs)
+    _same_pool(got, pool, bs, d)
+
+
+def test_update_skips_slots_beyond_the_pool():
+    d, bs, hkv = 64, 16, 2
+    x = torch.randn(3, hkv, d, device=DEV)
+    pool = torch.zeros(2, hkv, q4.record_bytes(d, bs), dtype=torch.uint8, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.pa_cache_update_q4(x, x, torch.tensor([32, 2**31 - 1, -5], dtype=torch.int32, device=DEV), pool, dev_err=err)
+    assert err.item() == pa.DEVERR_BAD_BLOCK and not pool.any()
+
+
+# ------------------------------------------------------------------ gather
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,bs,hkv", [(64, 16, 2), (64, 32, 5), (128, 16, 8), (128, 32, 1)])
+def test_gather(dtype, d, bs, hkv):
+    lens = [0, 1, bs - 1, bs, bs + 1, 77, 0, 3 * bs, 130]
+    c = make(5, lens, hkv, hkv, d, bs, dtype)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    extra = 9  # rows behind the last request stay as they were
+    kf = torch.full((cu[-1] + extra, hkv, d), 7.0, dtype=dtype, device=DEV)
+    vf = torch.full_like(kf, -7.0)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    g = _dev(c)
+    pa.pa_cache_gather_q4(g["pool"], g["table"], torch.from_numpy(cu).to(DEV), kf, vf, dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == 0
+    assert (kf[cu[-1]:] == 7).all() and (vf[cu[-1]:] == -7).all()
+    for b, n in enumerate(lens):
+        k, v, _, _ = q4.read(c["pool"], c["table"][b], n, d, bs)
+        for got, want in ((kf, k), (vf, v)):
+            # b + n s is at most 15 bits of fp32 wide where the two are of one
+            # size; its fp32 rounding, then the one to dtype
+            w = torch.from_numpy(want).float().to(dtype)
+            assert torch.equal(got[cu[b]:cu[b + 1]].cpu(), w), (b, n)
+
+
+def test_gather_zeroes_what_it_cannot_read():
+    d, bs, hkv = 128, 16, 2
+    c = make(6, [40, 40, 40], hkv, hkv, d, bs, BF16)
+    c["table"] = np.ascontiguousarray(c["table"][:, :3])
+    c["table"][0, 1] = -1
+    c["table"][1, 2] = 10 ** 6
+    cu = torch.tensor([0, 40, 80, 130], dtype=torch.int32, device=DEV)  # the third runs over its row of 48
+    kf = torch.full((130, hkv, d), 3.0, dtype=BF16, device=DEV)
+    vf = torch.full_like(kf, 3.0)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    g = _dev(c)
+    pa.pa_cache_gather_q4(g["pool"], g["table"], cu, kf, vf, dev_err=err)
+    assert err.item() == pa.DEVERR_BAD_BLOCK | pa.DEVERR_OVERFLOW
+    for t in (kf, vf):
+        assert not t[16:32].any() and not t[72:80].any() and not t[128:].any()
+    k, _, _, _ = q4.read(c["pool"], c["table"][0], 16, d, bs)
+    assert torch.equal(kf[:16].cpu(), torch.from_numpy(k).float().to(BF16))
+
+
+def test_gather_with_bad_cumulative_lengths_stays_inside():
+    d, bs, hkv = 64, 16, 2
+    c = make(6, [40, 40], hkv, hkv, d, bs, F32)
+    g = _dev(c)
+    for cu in ([0, 50, 40], [3, 20, 40], [0, 20, 90], [0, -5, 40]):
+        kf = torch.full((60, hkv, d), 3.0, device=DEV)
+        vf = torch.full_like(kf, 3.0)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        pa.pa_cache_gather_q4(g["pool"], g["table"], torch.tensor(cu, dtype=torch.int32, device=DEV), kf[:40], vf[:40],
+                              dev_err=err)
+        assert err.item() & pa.DEVERR_BAD_CU, cu
+        assert (kf[40:] == 3).all() and (vf[40:] == 3).all()
+
+
+# ------------------------------------------------------------------ decode
+def _decode(c, **kw):
+    g = _dev(c)
+    dtype = c["q"].dtype
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ks, vs = torch.empty_like(g["k_new"]), torch.empty_like(g["v_new"])
+    out = pa.pa_decode_q4(g["q"], g["pool"], g["table"], g["lens"], g["k_new"], g["v_new"], k_stored=ks, v_stored=vs,
+                          dev_err=err, **kw)
+    torch.cuda.synchronize()
+    assert out.dtype == dtype
+    return out, g["pool"], ks, vs, err.item()
+
+
+def _against_reference(c, scale=None, norm=True, **kw):
+    dtype, bs, d = c["q"].dtype, c["bs"], c["q"].shape[2]
+    out, pool, ks, vs, err = _decode(c, **kw)
+    assert err == 0
+    want_pool = c["pool"].copy()
+    ref, seen = q4.decode(_f32(c["q"]), want_pool, c["table"], c["lens"], _f32(c["k_new"]), _f32(c["v_new"]), bs, scale)
+    _same_pool(pool, want_pool, bs, d)
+    for b, (k, v, _, _) in enumerate(seen):
+        assert torch.equal(ks[b].cpu(), torch.from_numpy(k[-1]).float().to(dtype))
+        assert torch.equal(vs[b].cpu(), torch.from_numpy(v[-1]).float().to(dtype))
+    bound = decode_bound(c["q"], seen, ref, dtype, d ** -0.5 if scale is None else scale)
+    check(out, ref, bound, norm=NORM[dtype] if norm else None)
+    return out
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,bs", [(64, 16), (64, 32), (128, 16), (128, 32)])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (4, 2), (8, 8), (32, 8), (8, 1), (21, 3), (12, 6), (40, 5), (16, 16)])
+def test_decode(dtype, d, bs, hq, hkv):
+    lens = [0, 1, bs - 2, bs - 1, bs, bs + 1, 2 * bs - 1, 63, 64, 200, 517]
+    _against_reference(make(hq * 100 + hkv, lens, hq, hkv, d, bs, dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lens", [[0], [5000], [3, 20000, 900], [1500] * 40, list(range(0, 300))])
+def test_decode_lengths(dtype, lens):
+    _against_reference(make(11, lens, 8, 2, 128, 16, dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_decode_one_long_sequence(dtype):
+    _against_reference(make(12, [70001], 8, 1, 64, 32, dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,bs", [(64, 32), (128, 16)])
+def test_decode_peaked_and_scaled(dtype, d, bs):
+    """Scores that span hundreds (one key takes nearly all), and another scale."""
+    c = make(13, [40, 333, 1000], 8, 2, d, bs, dtype)
+    c["q"] = (c["q"].float() * 30).to(dtype)
+    _against_reference(c, norm=False)
+    c["q"] = (c["q"].float() / 60).to(dtype)
+    _against_reference(c, scale=0.7, softmax_scale=0.7, norm=False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("k_gain,v_gain,q_gain", [(1e-6, 1.0, 1e6), (1e6, 1e-6, 1e-6), (1.0, 1e-20, 1.0),
+                                                  (1.0, 1e20, 1.0), (1e-15, 3e4, 1e15)])
+def test_decode_magnitudes(dtype, k_gain, v_gain, q_gain):
+    """Keys, values and queries far from 1: the 16-bit operands of the
+    products must not leave their range."""
+    c = make(14, [100, 17, 400], 8, 2, 128, 16, dtype, k_gain=k_gain, v_gain=v_gain)
+    c["q"] = (c["q"].float() * q_gain).to(dtype)
+    _against_reference(c)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_decode_values_of_very_different_sizes(dtype):
+    """Tokens whose values differ by 2^40 in size, the large ones hardly seen."""
+    c = make(15, [300, 300], 8, 2, 64, 16, dtype)
+    d, bs = 64, 16
+    sc = np.ascontiguousarray(c["pool"][:, :, bs * d:]).view("<u2")
+    f = (sc.astype(np.uint32) << 16).view(np.float32).reshape(*sc.shape[:2], bs, 4)
+    f[:, :, ::3, 2:] *= 2.0 ** -40
+    c["pool"][:, :, bs * d:] = (f.reshape(sc.shape).view(np.uint32) >> 16).astype("<u2").view(np.uint8)
+    _against_reference(c)
+
+
+def test_decode_of_constant_rows():
+    """Every value row holds one number (step 0)."""
+    c = make(16, [50, 3], 4, 2, 64, 16, F32)
+    sc = np.ascontiguousarray(c["pool"][:, :, 16 * 64:]).view("<u2").reshape(*c["pool"].shape[:2], 16, 4).copy()
+    sc[..., 2] = 0
+    c["pool"][:, :, 16 * 64:] = sc.reshape(*c["pool"].shape[:2], -1).view(np.uint8)
+    c["v_new"][:] = 0.25
+    _against_reference(c)
+
+
+def test_decode_zero_query_is_the_mean():
+    c = make(17, [100], 2, 1, 64, 16, F32)
+    c["q"].zero_()
+    _against_reference(c)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_decode_nan_rows_reach_their_heads_only(dtype):
+    d, bs = 128, 16
+    c = make(18, [200, 200, 200], 8, 2, d, bs, dtype)
+    at = lambda b, t: (c["table"][b, t // bs], bs * d + 8 * (t % bs))  # noqa: E731
+    blk, o = at(0, 77)
+    c["pool"][blk, 1, o:o + 4] = 255       # a key of kv head 1, sequence 0
+    blk, o = at(2, 5)
+    c["pool"][blk, 0, o + 4:o + 8] = 255   # a value of kv head 0, sequence 2
+    out, _, _, _, err = _decode(c)
+    assert err == 0
+    nan = torch.isnan(out).cpu()
+    want = torch.zeros_like(nan)
+    want[0, 4:] = True
+    want[2, :4] = True
+    assert torch.equal(nan, want)
+    c["q"][1, 3, 9] = float("nan")
+    out, _, _, _, _ = _decode(c)
+    want[1, 3] = True
+    assert torch.equal(torch.isnan(out).cpu(), want)
+
+
+def test_decode_nan_new_token():
+    c = make(19, [33, 20], 4, 2, 64, 16, BF16)
+    c["k_new"][0, 1, 3] = float("inf")
+    c["v_new"][1, 0, 0] = float("nan")
+    out, pool, ks, vs, err = _decode(c)
+    want_pool = c["pool"].copy()
+    q4.decode(_f32(c["q"]), want_pool, c["table"], c["lens"], _f32(c["k_new"]), _f32(c["v_new"]), 16)
+    _same_pool(pool, want_pool, 16, 64)
+    assert torch.isnan(ks[0, 1]).all() and torch.isfinite(ks[0, 0]).all() and torch.isnan(vs[1, 0]).all()
+    assert torch.isnan(out[0, 2:]).all() and torch.isfinite(out[0, :2]).all()
+    assert torch.isnan(out[1, :2]).all() and torch.isfinite(out[1, 2:]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 32)])
+def test_decode_bad_blocks_and_lengths(dtype, d, bs):
+    lens = [100, 100, 5, 100, 900]
+    c = make(20, lens, 8, 2, d, bs, dtype)
+    good, pool_good, _, _, _ = _decode(c)
+    c["table"][0, 1] = -1
+    c["table"][1, 100 // bs] = len(c["pool"])   # the append's own block
+    c["table"][4, 900 // bs - 3] = 2 ** 31 - 1
+    c["lens"][2] = -1
+    before = c["pool"].copy()
+    out, pool, _, _, err = _decode(c)
+    assert err == pa.DEVERR_BAD_BLOCK | pa.DEVERR_OVERFLOW
+    for b in (0, 1, 2, 4):
+        assert not out[b].any()
+    assert torch.equal(out[3], good[3])
+    # no append was written where the block or the length is bad
+    for b in (1, 2):
+        own = c["table"][b][(c["table"][b] >= 0) & (c["table"][b] < len(before))]
+        assert np.array_equal(pool.cpu().numpy()[own], before[own])
+    c["lens"][2] = c["table"].shape[1] * bs
+    out, _, _, _, err = _decode(c)
+    assert err & pa.DEVERR_OVERFLOW and not out[2].any() and torch.equal(out[3], good[3])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_decode_does_not_depend_on_placement(dtype):
+    c = make(21, [1000, 37, 512], 16, 4, 128, 16, dtype)
+    a = _decode(c)[0]
+    rng = np.random.default_rng(0)
+    perm = rng.permutation(len(c["pool"]))
+    moved = np.empty_like(c["pool"])
+    moved[perm] = c["pool"]
+    c["table"] = np.where(c["table"] >= 0, perm[c["table"]], -1).astype(np.int32)
+    c["pool"] = moved
+    assert torch.equal(a, _decode(c)[0])
+
+
+def test_decode_with_shared_prefix_blocks():
+    _against_reference(make(22, [300, 290, 161, 300], 8, 2, 128, 16, BF16, shared_blocks=10))
+
+
+def test_decode_again_gives_the_same_bits():
+    c = make(23, [4000, 100, 2500], 32, 8, 128, 16, BF16)
+    a = _decode(c)[0]
+    assert all(torch.equal(a, _decode(c)[0]) for _ in range(3))
+
+
+def test_decode_on_a_stream_of_its_own():
+    c = make(24, [700, 30], 8, 2, 128, 16, BF16)
+    want = _decode(c)[0]
+    g = _dev(c)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(g["q"])
+    pa.pa_decode_q4(g["q"], g["pool"], g["table"], g["lens"], g["k_new"], g["v_new"], out, stream=s)
+    s.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_two_captured_graphs_replay_at_once():
+    """Graphs captured without a workspace of their own have one each."""
+    cases = [make(25 + i, [3000, 2000, 2600], 8, 2, 128, 16, BF16) for i in range(2)]
+    want = [_decode(c)[0] for c in cases]
+    graphs, outs, keep = [], [], []
+    for c in cases:
+        g = _dev(c)
+        out = torch.zeros_like(g["q"])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pa.pa_decode_q4(g["q"], g["pool"], g["table"], g["lens"], g["k_new"], g["v_new"], out)
+        graphs.append(graph), outs.append(out), keep.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for out, w in zip(outs, want):
+        assert torch.equal(out, w)
+
+
+def test_one_workspace_for_calls_of_different_sizes():
+    cases = [make(30, [900, 20], 8, 2, 128, 16, BF16), make(31, list(range(0, 900, 9)), 16, 16, 64, 32, F32),
+             make(32, [6000], 8, 1, 128, 32, BF16)]
+    size = max(pa.pa_decode_q4_workspace_size(c["q"].shape[0], c["q"].shape[1], c["k_new"].shape[1], c["q"].shape[2],
+                                              c["bs"], c["q"].dtype) for c in cases)
+    ws = torch.zeros(max(size, 16), dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        for c in cases:
+            _against_reference(c, workspace=ws)
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("d,bs,hq,hkv", [(128, 16, 8, 2), (128, 32, 16, 8)])
+def test_serving_steps(d, bs, hq, hkv):
+    """Prompts and tokens of four requests through all four operators: tables
+    and slots on the GPU, the chunk into the pool, whole sequences read back
+    for the varlen attention, then decode steps; one request ends and its
+    blocks serve the others."""
+    g = torch.Generator().manual_seed(77)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(BF16)  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    b, mb, nb = 4, 12, 30
+    pool = pa.pa_q4_pool(nb, hkv, d, bs)
+    table = torch.full((b, mb), -1, dtype=torch.int32, device=DEV)
+    free = torch.randperm(nb, generator=g).int().to(DEV)
+    count, err = i32([nb]), i32([0])
+    lens = i32([0] * b)
+    hpool, hist = np.zeros((nb, hkv, q4.record_bytes(d, bs)), dtype=np.uint8), [0] * b
+    for new in ([37, 1, 0, 64], [3, 20, 50, 9]):  # two prefill chunks
+        total = sum(new)
+        slots = torch.empty(total + 5, dtype=torch.int32, device=DEV)
+        cu_q, cu_k, after = pa.pa_block_tables(lens, i32(new), table, free, count, slots, bs, dev_err=err)
+        k, v, q = rnd(total + 5, hkv, d), rnd(total + 5, hkv, d), rnd(total, hq, d)
+        pa.pa_cache_update_q4(k.to(DEV), v.to(DEV), slots, pool, dev_err=err)
+        tk = sum(hist) + total
+        kf = torch.empty(tk, hkv, d, dtype=BF16, device=DEV)
+        vf = torch.empty_like(kf)
+        pa.pa_cache_gather_q4(pool, table, cu_k, kf, vf, dev_err=err)
+        hist = [h + n for h, n in zip(hist, new)]
+        out = pa.pa_varlen(q.to(DEV), kf, vf, cu_q, cu_k, max(new), max(hist), True, dev_err=err)
+        assert err.item() == 0
+        for i, s in enumerate(slots.cpu().tolist()):
+            if s >= 0:
+                q4.write(hpool, s, _f32(k[i]), _f32(v[i]), bs)
+        at = 0
+        for r in range(b):
+            kk, vv, _, _ = q4.read(hpool, table[r].cpu().numpy(), hist[r], d, bs)
+            kk, vv = (torch.from_numpy(x).float().to(BF16).double() for x in (kk, vv))
+            for i in range(new[r]):
+                n = hist[r] - new[r] + i + 1
+                w = torch.einsum("hgd,thd->hgt", q[at].double().view(hkv, -1, d), kk[:n]) * d ** -0.5
+                ref = torch.einsum("hgt,thd->hgd", torch.softmax(w, -1), vv[:n]).reshape(hq, d)
+                assert (out[at].cpu().double() - ref).abs().max() <= 1e-2 + 1e-2 * ref.abs().max()
+                at += 1
+        lens = after
+    ending = 3
+    for step in range(bs + 2):
+        new = [1] * b
+        if step == 2:  # a step between, in which one request only leaves
+            new = [0] * b
+            new[ending] = -1
+        slots = torch.empty(b, dtype=torch.int32, device=DEV)
+        before = lens
+        _, _, lens = pa.pa_block_tables(before, i32(new), table, free, count, slots, bs, dev_err=err)
+        if step == 2:
+            hist[ending] = 0
+            continue
+        q, kn, vn = rnd(b, hq, d), rnd(b, hkv, d), rnd(b, hkv, d)
+        out = pa.pa_decode_q4(q.to(DEV), pool, table, before, kn.to(DEV), vn.to(DEV), dev_err=err)
+        assert err.item() == 0
+        tab = table.cpu().numpy()
+        ref, seen = q4.decode(_f32(q), hpool, tab, np.array(hist), _f32(kn), _f32(vn), bs)
+        check(out, ref, decode_bound(q, seen, ref, BF16, d ** -0.5), f"step {step}", norm=NORM[BF16])
+        hist = [h + 1 for h in hist]
+        assert lens.cpu().tolist() == hist
+    used = sum(-(-h // bs) for h in hist)
+    assert count.item() == nb - used
+    assert np.unique(np.concatenate([table[r].cpu().numpy()[:-(-hist[r] // bs)] for r in range(b)])).size == used

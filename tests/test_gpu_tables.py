@@ -1,0 +1,173 @@
+"""pa_block_tables against the plain reference (whole numbers: equal)."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_300_gb300 as pa
+from oracle import q4
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _needs_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pa.load()
+
+
+def make(seed, lens, new, bs, spare, wide=None, slack=0):
+    rng = np.random.default_rng(seed)
+    held = [-(-n // bs) for n in lens]
+    nb = sum(held) + spare + slack
+    perm = rng.permutation(nb).astype(np.int32)
+    wide = wide or max(-(-(n + max(m, 0)) // bs) for n, m in zip(lens, new)) + 1
+    table = np.full((len(lens), wide), -1, dtype=np.int32)
+    at = 0
+    for b, h in enumerate(held):
+        table[b, :h] = perm[at:at + h]
+        at += h
+    free = np.full(nb, -1, dtype=np.int32)
+    free[:spare] = perm[at:at + spare]
+    return np.array(lens, dtype=np.int32), np.array(new, dtype=np.int32), table, free
+
+
+def run(lens, new, table, free, num_free, total, bs, **kw):
+    t = lambda x: torch.from_numpy(np.array(x)).to(DEV)  # noqa: E731
+    d = dict(lens=t(lens), table=t(table), free=t(free), nf=t(np.array([num_free], dtype=np.int32)),
+             slots=torch.full((total,), 12345, dtype=torch.int32, device=DEV),
+             err=torch.zeros(1, dtype=torch.int32, device=DEV))
+    out = pa.pa_block_tables(d["lens"], t(new), d["table"], d["free"], d["nf"], d["slots"], bs, dev_err=d["err"], **kw)
+    torch.cuda.synchronize()
+    return d, [x.cpu().numpy() for x in out]
+
+
+def same(d, out, want):
+    table, free, num_free, slots, cu_q, cu_k, after = want
+    assert np.array_equal(out[0], cu_q) and np.array_equal(out[1], cu_k) and np.array_equal(out[2], after)
+    assert np.array_equal(d["slots"].cpu().numpy(), slots)
+    assert np.array_equal(d["table"].cpu().numpy(), table)
+    assert int(d["nf"].item()) == num_free
+    # the stack is what counts; what lies behind its top is nobody's
+    assert np.array_equal(d["free"].cpu().numpy()[:num_free], free[:num_free])
+
+
+CASES = {
+    "one": ([1000], [1], 32),
+    "first token": ([0], [1], 16),
+    "nothing new": ([5, 0, 16], [0, 0, 0], 16),
+    "all end": ([5, 0, 16, 17], [-1, -1, -1, -1], 16),
+    "block borders": ([15, 16, 17, 31, 32, 0], [1, 1, 15, 2, 32, 33], 16),
+    "odd block size": ([3, 10, 0], [8, 1, 25], 5),
+    "one long prompt": ([7] + [100] * 9, [20000] + [1] * 9, 16),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+@pytest.mark.parametrize("tail", [0, 37])
+def test_small(name, tail):
+    lens, new, bs = CASES[name]
+    tokens = sum(max(m, 0) for m in new)
+    need = sum(-(-(n + m) // bs) - -(-n // bs) for n, m in zip(lens, new) if m > 0)
+    lens, new, table, free = make(1, lens, new, bs, need + 1)
+    want = q4.block_tables(lens, new, table, free, need + 1, tokens + tail, bs)
+    d, out = run(lens, new, table, free, need + 1, tokens + tail, bs)
+    assert int(d["err"].item()) == 0
+    same(d, out, want)
+
+
+@pytest.mark.parametrize("batch,new_hi,bs", [(255, 1, 16), (1025, 40, 16), (4097, 9, 32), (16384, 3, 16), (33, 3000, 32)])
+def test_random_steps_with_ended_requests(batch, new_hi, bs):
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, 700, batch)
+    new = np.where(rng.random(batch) < 0.2, -1, rng.integers(0, new_hi + 1, batch))
+    tokens = int(np.maximum(new, 0).sum())
+    take = int(sum(-(-(n + m) // bs) - -(-n // bs) for n, m in zip(lens.tolist(), new.tolist()) if m > 0))
+    back = int(sum(-(-n // bs) for n, m in zip(lens.tolist(), new.tolist()) if m < 0))
+    spare = max(0, take - back // 2)  # some of the taken blocks have just been given back
+    lens, new, table, free = make(batch, lens.tolist(), new.tolist(), bs, spare, slack=5)
+    want = q4.block_tables(lens, new, table, free, spare, tokens + 3, bs)
+    assert want is not None
+    d, out = run(lens, new, table, free, spare, tokens + 3, bs)
+    assert int(d["err"].item()) == 0
+    same(d, out, want)
+
+
+def test_empty_batch():
+    z = torch.zeros(0, dtype=torch.int32, device=DEV)
+    nf = torch.tensor([3], dtype=torch.int32, device=DEV)
+    slots = torch.full((7,), 5, dtype=torch.int32, device=DEV)
+    cu_q, cu_k, lens = pa.pa_block_tables(z, z, z.view(0, 4), torch.zeros(9, dtype=torch.int32, device=DEV), nf, slots, 16)
+    assert cu_q.tolist() == [0] and cu_k.tolist() == [0] and lens.numel() == 0
+    assert slots.tolist() == [-1] * 7 and nf.item() == 3
+
+
+REFUSED = {
+    "no space": ([16, 16], [40, 16], dict(spare=3, total=56), pa.DEVERR_NO_SPACE),
+    "slot map short": ([16, 16], [4, 4], dict(spare=3, total=7), pa.DEVERR_NO_SPACE),
+    "beyond the row": ([16, 16], [17, 1], dict(spare=9, total=99, wide=2), pa.DEVERR_OVERFLOW),
+    "negative length": ([16, -1], [1, 1], dict(spare=9, total=99, wide=4), pa.DEVERR_OVERFLOW),
+    "new below -1": ([16, 16], [1, -2], dict(spare=9, total=99, wide=4), pa.DEVERR_OVERFLOW),
+    "stack overfull": ([16, 16], [1, -1], dict(spare=3, total=99, count=5), pa.DEVERR_BAD_BLOCK),  # 5 + 1 of 5 blocks
+    "count negative": ([16, 16], [0, 0], dict(spare=3, total=9, count=-1), pa.DEVERR_BAD_BLOCK),
+    "count too large": ([16, 16], [0, 0], dict(spare=3, total=9, count=6), pa.DEVERR_BAD_BLOCK),
+}
+
+
+@pytest.mark.parametrize("name", REFUSED)
+def test_a_refused_step_changes_nothing(name):
+    lens, new, o, flag = REFUSED[name]
+    safe = [max(n, 0) for n in lens]
+    _, _, table, free = make(2, safe, [0, 0], 16, o["spare"], wide=o.get("wide", 8))
+    count = o.get("count", o["spare"])
+    lens, new = np.array(lens, dtype=np.int32), np.array(new, dtype=np.int32)
+    d, out = run(lens, new, table, free, count, o["total"], 16)
+    assert int(d["err"].item()) & flag
+    assert np.array_equal(d["table"].cpu().numpy(), table) and np.array_equal(d["free"].cpu().numpy(), free)
+    assert int(d["nf"].item()) == count
+    assert (d["slots"] == -1).all()
+    assert not out[0].any() and not out[1].any() and np.array_equal(out[2], lens)
+
+
+def test_ids_outside_the_pool_become_minus_one():
+    lens, new, table, free = make(3, [20, 40, 16], [3, -1, 1], 16, 2, slack=4)
+    table[0, 1] = 99   # needed: token 20's block
+    table[1, 2] = -7   # given back
+    d, out = run(lens, new, table, free, 2, 6, 16)
+    want = q4.block_tables(lens, new, table, free, 2, 6, 16)
+    assert int(d["err"].item()) == pa.DEVERR_BAD_BLOCK
+    same(d, out, want)
+    assert d["slots"].cpu().tolist()[:4] == [-1] * 4  # the last block given back was taken next
+
+
+def test_captured_step_advances_lengths_and_stack_in_place():
+    """A step that writes its lengths and its stack back, captured once and
+    replayed: every replay is the next step."""
+    bs, b, steps = 16, 12, 40
+    rng = np.random.default_rng(8)
+    lens0 = rng.integers(0, 60, b).tolist()
+    lens, new, table, free = make(9, lens0, [1] * b, bs, b * 4, wide=10)
+    t = lambda x: torch.from_numpy(np.array(x)).to(DEV)  # noqa: E731
+    g_len, g_new, g_tab, g_free = t(lens), t(new), t(table), t(free)
+    nf = t(np.array([b * 4], dtype=np.int32))
+    slots = torch.empty(b, dtype=torch.int32, device=DEV)
+    outs = [torch.empty(b + 1, dtype=torch.int32, device=DEV) for _ in range(2)]
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def step():
+        pa.pa_block_tables(g_len, g_new, g_tab, g_free, nf, slots, bs, cu_seq_lens_q=outs[0], cu_seq_lens_k=outs[1],
+                           seqlens_k=g_len, dev_err=err)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    count = b * 4
+    for _ in range(steps):
+        graph.replay()
+        table, free, count, want, cu_q, cu_k, lens = q4.block_tables(lens, new, table, free, count, b, bs)
+        torch.cuda.synchronize()
+        assert np.array_equal(slots.cpu().numpy(), want) and np.array_equal(g_tab.cpu().numpy(), table)
+        assert np.array_equal(g_len.cpu().numpy(), lens) and nf.item() == count
+        assert np.array_equal(outs[1].cpu().numpy(), cu_k)
+    assert err.item() == 0
