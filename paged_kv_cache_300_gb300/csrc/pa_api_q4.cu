@@ -99,7 +99,7 @@ size_t pa_decode_q4_workspace_size(int batch, int num_heads, int num_kv_heads, i
     if ((dtype != PA_F32 && dtype != PA_BF16) || batch <= 0 || num_heads <= 0) return 0;
     if (check_pool(num_kv_heads, head_dim, 1, block_size) != PA_OK || num_heads % num_kv_heads != 0)
         return 0;
-    return decode_q4_workspace(batch, num_heads, num_kv_heads, head_dim, block_size);
+    return decode_q4_workspace(batch, num_heads, num_kv_heads, head_dim, block_size, dtype == PA_F32);
 }
 
 int pa_decode_q4(const void *q, void *kv_cache, const int32_t *block_table,
@@ -122,8 +122,7 @@ int pa_decode_q4(const void *q, void *kv_cache, const int32_t *block_table,
         !aligned(out, 16) || !aligned(k_stored, 16) || !aligned(v_stored, 16) || !aligned(block_table, 4) ||
         !aligned(cache_seqlens, 4))
         return PA_ERR_SHAPE;
-    const size_t need = decode_q4_workspace(batch, num_heads, num_kv_heads, head_dim, block_size);
-    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return PA_ERR_WORKSPACE;
+    if (!workspace || !aligned(workspace, 16)) return PA_ERR_WORKSPACE;
     DecodeQ4Args a{};
     a.q = q;
     a.kv_cache = kv_cache;
@@ -147,7 +146,7 @@ int pa_decode_q4(const void *q, void *kv_cache, const int32_t *block_table,
     a.group = num_heads / num_kv_heads;
     a.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)head_dim);
     a.scale_log2 = a.scale * 1.4426950408889634f;
-    return decode_q4_launch(a, dtype == PA_F32, static_cast<cudaStream_t>(stream));
+    return decode_q4_launch(a, dtype == PA_F32, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int pa_block_tables(const int32_t *cache_seqlens, const int32_t *new_lens, int32_t *block_table,

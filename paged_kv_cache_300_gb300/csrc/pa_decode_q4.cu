@@ -1,13 +1,246 @@
 // Decode attention over the 4-bit paged pool (include/pa.h, pa_decode_q4).
+//
+// Mathematics.  With codes n, steps s and lows b (K and V each) a query's
+// score of token j is  x_j = scale (s_j (q . n_j) + b_j sum(q))  and its output
+// (sum_j (p_j s_j) n_j + sum_j p_j b_j) / sum_j p_j,  p_j = 2^(x_j log2 e - m).
+// So both products run on the raw codes, and step and low enter once per
+// (token, head) instead of once per element.
+//
+// Codes as matrix operands.  A nibble n at bits 0-3 of a half is the f16
+// subnormal n 2^-24, at bits 4-7 it is n 2^-20, both exact, and mma.sync
+// multiplies subnormals exactly.  So  w & 0x000f000f  and  w & 0x00f000f0  of a
+// word (and of w >> 8) are four operand registers: 5 instructions turn 8 codes
+// into operands, with no conversion, subtraction or scaling.  The powers of two
+// leave through q (its elements that meet the 2^-20 codes carry 2^-4) and
+// through the output rows.
+//  * S^T[token, head] = K q^T: A = 16 tokens x 16 dims, the lane's words of
+//    rows lane/4 and lane/4 + 8; which dims share a k-step is free as long as
+//    q's fragments follow, so rows are read 16 bytes at a time.
+//  * O^T[dim, head] += V^T (p s)^T: A's registers hold token pairs, which is
+//    how the pool stores V (a 32-bit word = 4 dims of tokens 2p, 2p + 1).
+//  * Codes are not negative, and the tensor cores cut their sums instead of
+//    rounding them: a plain sum of (p s) n drifts by 2^-25 a tile, which for
+//    10,000 tokens is more than a bf16 step of an output that cancels against
+//    sum p b.  So odd tokens run as -(p s) (15 - n) + (p s) 15: complementing
+//    a code costs nothing (the mask above takes an xor in the same
+//    instruction), the products come in both signs and the cuts cancel.
+//  * q is scaled by a power of two per head into f16's range (a bf16 number
+//    keeps all its bits); fp32 operands run as a sum of two f16 numbers.
+//  * p s is rounded to f16 (half a step 2^-11; the sum of p is not rounded).
+//    Its reference m is a running maximum of x + log2(s), so that p s, not p,
+//    is at most 2^14; it moves only when p s would pass that, which leaves
+//    28 bits below the largest term before f16 loses bits of a weight.
+//
+// Work.  HBM-bound on (D + 8) / 2D bytes an element.  One stage is 32 or 64
+// tokens of one kv head: up to four records, each one bulk copy.  A CTA has up
+// to 8 warps, TW of them sharing the tokens of each of HS kv heads; each
+// resolves its part of the block table and fills its own ring.
+// The flat list of (head group, sequence, block) is cut into equal ranges, one
+// per CTA (every CTA derives them from cache_seqlens); a sequence cut by a
+// range's border leaves partials (acc, m, l) that its last CTA joins in
+// logical order.  The warps of a head join in shared memory first.
 #include "pa_internal.h"
 #include "pa_q4.cuh"
 
+#include <cuda_fp16.h>
 #include <math.h>
 
 namespace pa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxWarps = 8;
+// Largest log2 of a weight p s before the reference moves, and where it is
+// put then.
+constexpr float kWeightMax = 14.f, kWeightNew = 9.f;
+// Steps below 2^-80 count as 2^-80 in the reference: p stays below 2^94, its
+// sums inside fp32.
+constexpr float kStepFloor = 8.271806125530277e-25f;
+
+enum { kLast = 1, kAppend = 2, kBad = 4, kWhole = 8 };
+
+// What the loader notes about one stage; the second half is written for a
+// segment's last stage only.
+struct alignas(16) Meta {
+    int b, hg, len, cnt;       // sequence, head group, cache_seqlens[b], tokens | flags << 8
+    int blocks, nblk, sb, pad; // blocks of the segment and of the sequence, blocks before the sequence
+};
+
+// A warp's loader, in shared memory, where it costs the sums no registers.
+// The walk covers the warp's share of every segment: of a sequence's blocks
+// [j0, je) in the CTA's range, the stages ct, ct + tw, ...  Table entries come
+// in windows of 32 of the warp's blocks, the next one (of this segment or of
+// the next) fetched while the present one is used.
+struct alignas(16) LoadState {
+    uint64_t base; // the pool's record of the warp's head in block 0
+    int e, elim;   // window cursor; stages before elim are SB whole blocks inside the segment
+    int j0, je, ok, nblk;
+    int b, hg, len, rem; // rem: units of the CTA's range from j0 on
+    int sb, li0, lend, wsel; // blocks before b; stage at the window's start; last stage; window in use
+    int len1, len2, pad[2];  // lengths of the next sequence and of the one after it
+    int window[64];
+};
+
+struct DecodeQ4Geom {
+    int hs, tw;          // kv heads of a CTA, warps that share one head
+    int head_groups, nst;
+    int slot_floats;     // floats of one partial
+    int min_tokens;      // of a CTA's range
+};
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// D += A(16x16, row) * B(16x8, col), f16 inputs, fp32 accumulators.  Not
+// volatile: independent products may be issued in any order.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// (w & m) ^ x in one instruction.
+__device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t m, uint32_t x)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(w), "r"(m), "r"(x));
+    return d;
+}
+
+__device__ __forceinline__ float log2_approx(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Wait for a barrier's phase without giving the thread up: an unsuccessful
+// try_wait suspends it for microseconds on this GPU, many times the waits met
+// here (a copy's rest, a neighbour's shuffles).  The limit is about a second.
+__device__ __forceinline__ bool spin_wait(uint64_t *bar, uint32_t parity)
+{
+    for (uint32_t i = 0; i < (1u << 25); ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+
+// Barrier of the warps that share a head: one arrival a warp, and a wait with
+// a limit like every other one here.  False when it gave up.
+__device__ __forceinline__ bool group_sync(uint64_t *bar, int warps, uint32_t &phase)
+{
+    __syncwarp();
+    if (warps == 1) return true;
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    const bool ok = spin_wait(bar, phase);
+    phase ^= 1;
+    return __all_sync(kFull, ok);
+}
+
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&w)[N], const uint8_t *p)
+{
+    if constexpr (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+    }
+}
+
+// N consecutive elements of q, N a multiple of 8, loaded 16 bytes at a time.
+template <typename T, int N>
+struct QWords;
+template <int N>
+struct QWords<__nv_bfloat16, N> {
+    uint4 w[N / 8];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool ok)
+    {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i)
+            w[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint4 &v = w[i >> 3];
+        const uint32_t x = (i >> 1 & 3) == 0 ? v.x : (i >> 1 & 3) == 1 ? v.y : (i >> 1 & 3) == 2 ? v.z : v.w;
+        return i & 1 ? bf16_hi(x) : bf16_lo(x);
+    }
+};
+template <int N>
+struct QWords<float, N> {
+    float4 w[N / 4];
+    __device__ __forceinline__ void load(const float *p, bool ok)
+    {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            w[i] = ok ? __ldg(reinterpret_cast<const float4 *>(p) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        const float4 &v = w[i >> 2];
+        return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+    }
+};
+
+// CTA whose range holds cost position pos.
+__device__ __forceinline__ int cta_of(long long pos, int P, long long Ctot)
+{
+    return (int)(((pos + 1) * P - 1) / Ctot);
+}
+
+// Blocks of a sequence with L cached tokens and its new one (1 where the
+// length is refused).
+__device__ __forceinline__ int seq_blocks(int L, long long cap, int bs, bool *ok)
+{
+    *ok = L >= 0 && (long long)L + 1 <= cap;
+    return *ok ? L / bs + 1 : 1;
+}
+
+// A CTA's range holds at least this many tokens of its heads: below that,
+// more CTAs cost more in partials than they save.
+constexpr int kMinTokens = 256;
+// Parts of a sequence that its last CTA joins, at most (see make_plan).
+constexpr int kMaxParts = 16;
+
+template <typename T>
+__device__ __forceinline__ void store4(T *p, float a, float b, float c, float d);
+template <>
+__device__ __forceinline__ void store4<float>(float *p, float a, float b, float c, float d)
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
+template <>
+__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, float a, float b, float c, float d)
+{
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+}
 
 // Quantises one row held as EPL values a lane (dims lane*EPL ..) by a whole
 // warp; returns the lane's codes, 4 bits each.
@@ -34,133 +267,1028 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&x)[EPL], Q4Scale 
     return c;
 }
 
-// One warp per (sequence, query head), fp32 arithmetic throughout.
-template <int D, typename T>
-__global__ void __launch_bounds__(128) decode_q4_kernel(const DecodeQ4Args a)
+// Quantise the new token's rows of kv head kvh, write them into the pool and
+// into the staged record (token t of the record at `rec`).
+template <int D, int BS, typename T>
+__device__ __noinline__ void append(const DecodeQ4Args &a, int b, int kvh, int L, int t, uint8_t *rec)
 {
     constexpr int EPL = D / 32;
     const int lane = threadIdx.x & 31;
-    const long long gw = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (gw >= (long long)a.batch * a.num_heads) return;
-    const int b = (int)(gw / a.num_heads), h = (int)(gw % a.num_heads);
-    const int G = a.group, kvh = h / G, Hkv = a.num_kv_heads, bs = a.block_size;
-    const int mbps = a.max_blocks_per_seq, L = a.cache_seqlens[b];
-    T *out = static_cast<T *>(a.out) + ((size_t)b * a.num_heads + h) * D + lane * EPL;
-    bool bad = L < 0 || (long long)L + 1 > (long long)mbps * bs;
-    if (bad && lane == 0) flag_error(a.dev_err, PA_DEVERR_OVERFLOW);
-    const int nblk = bad ? 0 : L / bs + 1;
-    const int32_t *tab = a.block_table + (size_t)b * mbps;
-    for (int j = 0; j < nblk && !bad; ++j)
-        if (tab[j] < 0 || tab[j] >= a.num_blocks) {
-            bad = true;
-            if (lane == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
-        }
-    if (bad) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) out[i] = from_f32<T>(0.f);
-        return;
-    }
-    // the new token's row, quantised as it is stored
-    float kn[EPL], vn[EPL], qv[EPL], acc[EPL];
-    const size_t src = ((size_t)b * Hkv + kvh) * D + lane * EPL;
+    const size_t src = ((size_t)b * a.num_kv_heads + kvh) * D + lane * EPL;
+    float k[EPL], v[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        kn[i] = to_f32<T>(static_cast<const T *>(a.k_new)[src + i]);
-        vn[i] = to_f32<T>(static_cast<const T *>(a.v_new)[src + i]);
-        qv[i] = to_f32<T>(static_cast<const T *>(a.q)[((size_t)b * a.num_heads + h) * D + lane * EPL + i]);
-        acc[i] = 0.f;
+        k[i] = to_f32<T>(static_cast<const T *>(a.k_new)[src + i]);
+        v[i] = to_f32<T>(static_cast<const T *>(a.v_new)[src + i]);
     }
     Q4Scale ks, vs;
-    uint32_t kc = quantise_row<EPL>(kn, ks), vc = quantise_row<EPL>(vn, vs);
+    const uint32_t kc = quantise_row<EPL>(k, ks), vc = quantise_row<EPL>(v, vs);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        kn[i] = q4_value((kc >> (4 * i)) & 15u, ks.step, ks.low);
-        vn[i] = q4_value((vc >> (4 * i)) & 15u, vs.step, vs.low);
+        if (a.k_stored)
+            static_cast<T *>(a.k_stored)[src + i] = from_f32<T>(q4_value((kc >> (4 * i)) & 15u, ks.step, ks.low));
+        if (a.v_stored)
+            static_cast<T *>(a.v_stored)[src + i] = from_f32<T>(q4_value((vc >> (4 * i)) & 15u, vs.step, vs.low));
     }
-    const size_t rb = q4_record_bytes(D, bs);
-    uint8_t *pool = static_cast<uint8_t *>(a.kv_cache);
-    if (h % G == 0) { // one warp per kv head appends
-        uint8_t *rec = pool + ((size_t)tab[nblk - 1] * Hkv + kvh) * rb;
-        const int t = L % bs;
-        uint32_t kw = kc, vw = vc;
-        if (EPL == 2) {
-            kw |= __shfl_down_sync(kFull, kc, 1) << 8;
-            vw |= __shfl_down_sync(kFull, vc, 1) << 8;
-        }
+    uint32_t kw = kc, vw = vc;
+    if (EPL == 2) { // 4 dims in the even lanes
+        kw |= __shfl_down_sync(kFull, kc, 1) << 8;
+        vw |= __shfl_down_sync(kFull, vc, 1) << 8;
+    }
+    const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks_per_seq + L / BS);
+    uint8_t *dst = static_cast<uint8_t *>(a.kv_cache) +
+                   ((size_t)blk * a.num_kv_heads + kvh) * q4_record_bytes(D, BS);
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+        uint8_t *p = side ? dst : rec;
         if (EPL == 4 || (lane & 1) == 0) {
             const int unit = EPL == 4 ? lane : lane >> 1;
-            reinterpret_cast<uint16_t *>(rec)[t * (D / 4) + unit] = (uint16_t)kw;
-            reinterpret_cast<uint16_t *>(rec + q4_v_offset(D, bs))[q4_v_unit<D>(t, unit)] = (uint16_t)vw;
+            reinterpret_cast<uint16_t *>(p)[t * (D / 4) + unit] = (uint16_t)kw;
+            reinterpret_cast<uint16_t *>(p + q4_v_offset(D, BS))[q4_v_unit<D>(t, unit)] = (uint16_t)vw;
         }
         if (lane == 0)
-            *reinterpret_cast<uint2 *>(rec + q4_scale_offset(D, bs) + t * 8) =
+            *reinterpret_cast<uint2 *>(p + q4_scale_offset(D, BS) + t * 8) =
                 make_uint2(q4_pack_scale(ks), q4_pack_scale(vs));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// Join the parts of a sequence in logical order and store its output rows.
+// A part is `group` rows of D sums and, behind them, (m, l) of each row; a
+// refused part has l = -inf.  A thread takes NE pieces of four dims at a time,
+// with the loads of KU parts in flight.  Not inlined: it runs once a sequence
+// and its registers would weigh on the loop.
+template <int D, typename T, int NE>
+__device__ __noinline__ void fold(const float *first, size_t step, int nseg, int group, int thread, int threads, T *out)
+{
+    constexpr int KU = NE >= 8 ? 1 : NE >= 4 ? 2 : 4;
+#pragma unroll 1
+    for (int e0 = thread; e0 < group * (D / 4); e0 += threads * NE) {
+        float M[NE], l[NE];
+        float4 o[NE];
+        bool refused = false;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            if (a.k_stored) static_cast<T *>(a.k_stored)[src + i] = from_f32<T>(kn[i]);
-            if (a.v_stored) static_cast<T *>(a.v_stored)[src + i] = from_f32<T>(vn[i]);
+        for (int n = 0; n < NE; ++n) {
+            M[n] = -INFINITY;
+            l[n] = 0.f;
+            o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
+        for (int k0 = 0; k0 < nseg; k0 += KU) {
+            float2 z[KU][NE];
+            float4 x[KU][NE];
+#pragma unroll
+            for (int k = 0; k < KU; ++k)
+#pragma unroll
+                for (int n = 0; n < NE; ++n) {
+                    const int e = e0 + threads * n, g = min(e / (D / 4), group - 1);
+                    const float *part = first + min(k0 + k, nseg - 1) * step;
+                    z[k][n] = __ldcg(reinterpret_cast<const float2 *>(part + group * D + 2 * g));
+                    x[k][n] = __ldcg(reinterpret_cast<const float4 *>(part + g * D + e % (D / 4) * 4));
+                }
+#pragma unroll
+            for (int k = 0; k < KU; ++k) {
+                if (k0 + k >= nseg) break;
+#pragma unroll
+                for (int n = 0; n < NE; ++n) {
+                    const float top = fmaxf(M[n], z[k][n].x);
+                    const float fo = top == -INFINITY ? 1.f : exp2_approx(M[n] - top);
+                    const float f = top == -INFINITY ? 1.f : exp2_approx(z[k][n].x - top);
+                    refused |= z[k][n].y == -INFINITY;
+                    M[n] = top;
+                    l[n] = fmaf(z[k][n].y, f, l[n] * fo);
+                    o[n].x = fmaf(x[k][n].x, f, o[n].x * fo);
+                    o[n].y = fmaf(x[k][n].y, f, o[n].y * fo);
+                    o[n].z = fmaf(x[k][n].z, f, o[n].z * fo);
+                    o[n].w = fmaf(x[k][n].w, f, o[n].w * fo);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NE; ++n) {
+            const int e = e0 + threads * n;
+            if (e >= group * (D / 4)) break;
+            const float inv = 1.f / l[n];
+            if (refused)
+                store4<T>(out + e * 4, 0.f, 0.f, 0.f, 0.f);
+            else
+                store4<T>(out + e * 4, o[n].x * inv, o[n].y * inv, o[n].z * inv, o[n].w * inv);
         }
     }
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j <= L; ++j) {
-        float kr[EPL], vr[EPL];
-        if (j == L) {
+}
+
+__device__ __forceinline__ void copy4_async(void *dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+}
+
+// The loader's slower steps: everything but a stage of whole blocks inside a
+// segment.  Not inlined, so that its registers do not weigh on the sums.
+template <int D, int BS, int SB, typename T>
+struct Loader {
+    static constexpr int REC = q4_record_bytes(D, BS);
+
+    // fetch the entries of the warp's blocks o0.. of a segment into window w
+    static __device__ __forceinline__ void fetch(const DecodeQ4Args &a, LoadState &ld, int w, int b, bool ok, int j0,
+                                                 int je, int o0, int tw, int ct)
+    {
+        const int lane = threadIdx.x & 31, o = o0 + lane;
+        const int blk = j0 + ((o / SB) * tw + ct) * SB + o % SB;
+        if (ok && blk < je)
+            copy4_async(&ld.window[w * 32 + lane], a.block_table + (size_t)b * a.max_blocks_per_seq + blk);
+        else
+            ld.window[w * 32 + lane] = -1;
+    }
+    // q and the new rows of a sequence: in L2 by the time they are read
+    static __device__ __forceinline__ void warm(const DecodeQ4Args &a, int b, int kvh, bool ends)
+    {
+        const int lane = threadIdx.x & 31;
+        const size_t row = (size_t)b * a.num_kv_heads + kvh;
+        for (int o = lane * 128; o < a.group * D * (int)sizeof(T); o += 32 * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(a.q) +
+                                                          row * a.group * D * sizeof(T) + o));
+        if (ends && lane < 2)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                static_cast<const char *>(lane ? a.v_new : a.k_new) + row * D * sizeof(T)));
+    }
+    // start of the segment (b, hg) from block j0 on, with `rem` units left;
+    // len2 has been fetched
+    static __device__ __forceinline__ void enter(const DecodeQ4Args &a, LoadState &ld, int b, int hg, int len, int j0,
+                                                 int rem, int sb, int tw, int ct, int kvh)
+    {
+        const int lane = threadIdx.x & 31, B = a.batch;
+        bool ok;
+        const int nblk = seq_blocks(len, (long long)a.max_blocks_per_seq * BS, BS, &ok);
+        const int je = min(nblk, j0 + rem), stages = (je - j0 + SB - 1) / SB;
+        const int len1 = ld.len2;
+        __syncwarp();
+        if (lane == 0) {
+            ld.j0 = j0;
+            ld.je = je;
+            ld.ok = ok;
+            ld.nblk = nblk;
+            ld.b = b;
+            ld.hg = hg;
+            ld.len = len;
+            ld.rem = rem;
+            ld.sb = sb;
+            ld.li0 = 0;
+            ld.lend = max(0, (stages - ct + tw - 1) / tw - 1);
+            ld.len1 = len1;
+            ld.base = reinterpret_cast<uint64_t>(a.kv_cache) + (size_t)kvh * REC;
+            const int b2 = b + 2;
+            copy4_async(&ld.len2, a.cache_seqlens + (b2 < B ? b2 : B > 1 ? b2 - B : 0));
+        }
+        __syncwarp();
+    }
+    // the window after the one in use, which starts at stage li0
+    static __device__ __forceinline__ void fetch_next(const DecodeQ4Args &a, LoadState &ld, int tw, int ct, int hs,
+                                                      int ch)
+    {
+        const int o0 = ld.li0 * SB + 32, j0 = ld.j0, je = ld.je, b = ld.b, rem = ld.rem - (je - j0);
+        if (((o0 / SB) * tw + ct) * SB < je - j0) {
+            fetch(a, ld, ld.wsel ^ 1, b, ld.ok, j0, je, o0, tw, ct);
+        } else if (rem > 0) {
+            const bool wrap = b + 1 == a.batch;
+            bool ok;
+            const int n = seq_blocks(ld.len1, (long long)a.max_blocks_per_seq * BS, BS, &ok);
+            const int e = min(n, rem);
+            fetch(a, ld, ld.wsel ^ 1, wrap ? 0 : b + 1, ok, 0, e, 0, tw, ct);
+            warm(a, wrap ? 0 : b + 1, (wrap ? ld.hg + 1 : ld.hg) * hs + ch, e == n);
+        }
+    }
+    // any stage into the slot (stage buffer dst, barrier, note)
+    static __device__ __noinline__ void issue(const DecodeQ4Args &a, LoadState &ld, uint32_t dst, uint64_t *bar,
+                                              Meta *meta, int tw, int ct, int hs, int ch)
+    {
+        const int lane = threadIdx.x & 31;
+        copy_async_wait(); // windows and lengths
+        const int rem0 = ld.rem;
+        if (rem0 <= 0) return;
+        const int j0 = ld.j0, je = ld.je, nblk = ld.nblk, len = ld.len, b = ld.b, hg = ld.hg, sb = ld.sb;
+        const bool ok = ld.ok != 0;
+        const int e = ld.e, li = ld.li0 + (e - ld.wsel * 32) / SB, lend = ld.lend;
+        const int blk0 = j0 + (li * tw + ct) * SB;
+        const int blocks = max(0, min(SB, je - blk0));
+        const int p = ld.window[e + (lane & (SB - 1))];
+        const bool here = lane < blocks;
+        const bool valid = here && ok && p >= 0 && p < a.num_blocks;
+        if (here && ok && !valid) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
+        const int loads = __popc(__ballot_sync(kFull, valid));
+        const bool last = li == lend;
+        if (lane == 0) {
+            const int pos0 = blk0 * BS;
+            const int cnt = blocks > 0 && ok ? min(blocks * BS, len - pos0 + 1) : 0;
+            int flags = last ? kLast : 0;
+            if (loads < blocks || !ok) flags |= kBad;
+            if (ok && loads == blocks && blocks > 0 && len < pos0 + blocks * BS) flags |= kAppend;
+            if (j0 == 0 && je == nblk) flags |= kWhole;
+            int4 *mt = reinterpret_cast<int4 *>(meta);
+            mt[0] = make_int4(b, hg, len, cnt | flags << 8);
+            mt[1] = make_int4(je - j0, nblk, sb, 0);
+            if (loads > 0)
+                mbar_arrive_expect_tx(bar, loads * REC);
+            else
+                mbar_arrive(bar);
+        }
+        __syncwarp();
+        if (valid)
+            bulk_load(dst + lane * REC,
+                      static_cast<const uint8_t *>(a.kv_cache) + ((size_t)p * a.num_kv_heads + hg * hs + ch) * REC, REC,
+                      bar);
+        bool switched = false;
+        if (last) {
+            const int rem = rem0 - (je - j0);
+            if (rem <= 0) {
+                if (lane == 0) ld.rem = ld.e = ld.elim = 0;
+                __syncwarp();
+                return;
+            }
+            const bool wrap = b + 1 == a.batch;
+            const int hg1 = wrap ? hg + 1 : hg;
+            enter(a, ld, wrap ? 0 : b + 1, hg1, ld.len1, 0, rem, wrap ? 0 : sb + nblk, tw, ct, hg1 * hs + ch);
+            switched = true;
+        } else if (((li + 1) * SB & 31) == 0) {
+            if (lane == 0) ld.li0 = li + 1;
+            switched = true;
+        }
+        const int w = ld.wsel ^ (switched ? 1 : 0);
+        __syncwarp();
+        const int first = w * 32, at = switched ? first : e + SB; // the cursor
+        const int li1 = switched ? ld.li0 : li + 1, li0 = ld.li0;
+        if (lane == 0) ld.wsel = w;
+        __syncwarp();
+        // whole blocks inside the segment, in this window; the first stage of
+        // a segment and the last one of a segment or a window come here
+        const int upto = min(ld.lend, li0 + 32 / SB - 1); // stages before this one
+        const int v = ld.window[first + lane];
+        const bool in = lane < (upto - li0) * SB;
+        const bool fine = __all_sync(kFull, !in || (v >= 0 && v < a.num_blocks));
+        if (lane == 0) {
+            ld.e = at;
+            ld.elim = fine && li1 > 0 ? first + (upto - li0) * SB : 0;
+        }
+        __syncwarp();
+        if (switched) fetch_next(a, ld, tw, ct, hs, ch);
+    }
+};
+
+// Columns of the products.  A product has 8 columns; a group of at most 8 / R
+// query heads stands in them R times, and copy `rep` of a score belongs to
+// tile `rep` of R: every lane then turns the scores of its own tile into
+// weights (1 / R of the work), the weights of a tile are left in its own copy
+// (the others are masked to zero), and the copies' sums are added at the end.
+// R = 1 has two tiles a stage as well, and every lane works on both.
+template <int D, int BS, int R, typename T>
+__global__ void __launch_bounds__(kMaxWarps * 32, 2)
+    decode_q4_kernel(const DecodeQ4Args a, const DecodeQ4Geom gm)
+{
+    constexpr bool F32 = sizeof(T) == 4;
+    constexpr int REC = q4_record_bytes(D, BS);
+    constexpr int NTILE = R < 2 ? 2 : R;            // 16-token tiles of a stage
+    constexpr int ST = 16 * NTILE;                  // tokens of a stage
+    constexpr int SB = ST / BS;                     // blocks of a stage
+    constexpr int STAGE = ST * (D + 8);             // bytes
+    constexpr int KW = D / 32;                      // words of a lane's row part
+    constexpr int MT = D / 16;                      // 16-dim tiles of the output
+    constexpr int DL = D / 8;                       // output dims of a lane
+    constexpr int CW = 8 / R;                       // columns of one copy
+    constexpr int XT = NTILE / R;                   // tiles whose scores a lane works on
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_warp[kMaxWarps];
+    __shared__ int s_total, s_len;
+    __shared__ long long s_start[2];
+    __shared__ long long s_u[2];
+    __shared__ float s_m[kMaxWarps][8], s_l[kMaxWarps][8], s_b[kMaxWarps][8];
+    __shared__ int s_last[kMaxWarps];
+    __shared__ uint64_t s_group[kMaxWarps];
+    __shared__ LoadState s_load[kMaxWarps];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hs = gm.hs, tw = gm.tw, ncw = hs * tw, nst = gm.nst;
+    const int NT = ncw * 32;
+    const int B = a.batch, mbps = a.max_blocks_per_seq;
+    const long long cap = (long long)mbps * BS;
+    // rings of the consumers, barriers, metadata, join buffers
+    uint8_t *ring = smem;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + (size_t)ncw * nst * STAGE);
+    Meta *meta = reinterpret_cast<Meta *>(full + ((ncw * nst + 1) & ~1));
+    float *join = reinterpret_cast<float *>(meta + ncw * nst);
+
+    if (tid < ncw * nst) {
+        mbar_init(&full[tid], 1);
+        if (tid < hs) mbar_init(&s_group[tid], tw);
+        fence_mbar_init();
+    }
+    grid_dep_trigger();
+    for (int b = tid * 32; b < B; b += NT * 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.cache_seqlens + b));
+    // nothing above read or wrote memory that a predecessor may write
+    grid_dep_wait();
+
+    // ---- block-wide scan of the sequences' block counts
+    const int per = (B + NT - 1) / NT;
+    const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
+    int local = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        bool ok;
+        local += seq_blocks(__ldg(a.cache_seqlens + b), cap, BS, &ok);
+        if (!ok && blockIdx.x == 0) flag_error(a.dev_err, PA_DEVERR_OVERFLOW);
+    }
+    int incl = local;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                kr[i] = kn[i];
-                vr[i] = vn[i];
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        const int v = lane < ncw ? s_warp[lane] : 0;
+        int inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += t;
+        }
+        if (lane < ncw) s_warp[lane] = inc - v;
+        if (lane == ncw - 1) s_total = inc;
+    }
+    __syncthreads();
+    const long long ublk = s_total;
+    const long long U = ublk * gm.head_groups;
+    const int P = (int)max(1ll, min((long long)gridDim.x, U / (gm.min_tokens / BS)));
+    if ((int)blockIdx.x >= P) return;
+    {
+        const long long sbt = (long long)s_warp[warp] + incl - local; // units before b_lo
+        for (int e = 0; e < 2; ++e) {
+            const long long cc = (long long)(blockIdx.x + e) * U / P;
+            if (cc >= U) {
+                if (tid == 0) s_u[e] = U;
+                continue;
+            }
+            const long long r = cc % ublk;
+            if (r < sbt || r >= sbt + local) continue;
+            s_u[e] = cc;
+            if (e == 0) {
+                long long sb = sbt;
+                for (int b = b_lo; b < b_hi; ++b) {
+                    bool ok;
+                    const int n = seq_blocks(__ldg(a.cache_seqlens + b), cap, BS, &ok);
+                    if (r < sb + n) {
+                        s_start[0] = b;
+                        s_start[1] = sb;
+                        s_len = __ldg(a.cache_seqlens + b);
+                        break;
+                    }
+                    sb += n;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const long long u0 = s_u[0], u1 = s_u[1];
+    const int G = a.group, Hkv = a.num_kv_heads, Hq = a.num_heads;
+
+    const int ct = warp / hs, ch = warp % hs; // token share, head within the group
+    const uint32_t block_bytes = (uint32_t)Hkv * REC;
+
+    // ================= loader =================
+    // Every warp fills its own ring: it issues a stage's copies as soon as it
+    // has used the slot up, so no other warp and no second barrier is waited
+    // for.
+    using L = Loader<D, BS, SB, T>;
+    LoadState &ld = s_load[warp];
+    auto issue = [&](int at) {
+        const uint32_t dst = smem_u32(ring + at * STAGE);
+        const int e = ld.e;
+        if (e < ld.elim) { // SB whole blocks inside a segment
+            const uint8_t *base = reinterpret_cast<const uint8_t *>(ld.base);
+            const int p = ld.window[e + (lane & (SB - 1))];
+            __syncwarp();
+            if (lane == 0) {
+                meta[at].cnt = ST;
+                mbar_arrive_expect_tx(&full[at], SB * REC);
+                ld.e = e + SB;
+            }
+            __syncwarp();
+            if (lane < SB) bulk_load(dst + lane * REC, base + (size_t)p * block_bytes, REC, &full[at]);
+        } else {
+            L::issue(a, ld, dst, &full[at], &meta[at], tw, ct, hs, ch);
+        }
+    };
+    {
+        const int b = (int)s_start[0], hg = (int)(u0 / ublk), j0 = (int)(u0 % ublk - s_start[1]);
+        if (lane == 0) {
+            copy4_async(&ld.len2, a.cache_seqlens + (b + 1 < B ? b + 1 : 0));
+            ld.e = ld.elim = ld.wsel = 0;
+        }
+        copy_async_wait();
+        L::enter(a, ld, b, hg, s_len, j0, (int)(u1 - u0), (int)s_start[1], tw, ct, hg * hs + ch);
+        L::fetch(a, ld, 0, b, ld.ok, j0, ld.je, 0, tw, ct);
+        L::warm(a, b, hg * hs + ch, ld.je == ld.nblk);
+        L::fetch_next(a, ld, tw, ct, hs, ch);
+#pragma unroll 1
+        for (int i = 0; i < nst; ++i) issue(warp * nst + i);
+    }
+
+    // ================= sums =================
+    const int r = lane >> 2, c = lane & 3; // C fragment: rows r, r + 8; columns 2c, 2c + 1
+    const int rep = R == 1 ? 0 : c / (4 / R);  // copy of the lane's C columns: its tile
+    const int col = 2 * c % CW;                // head of the lane's first column
+    const int brep = r / CW;                   // copy of the lane's B column r
+    const int gthreads = tw * 32, gtid = ct * 32 + lane; // threads that share the head
+    const uint32_t k_off = r * (D / 2) + c * (D / 8);
+    const uint32_t v_off = q4_v_offset(D, BS) +
+                           (D == 128 ? c * 128 + (((r >> 1) ^ c) << 5) + ((r & 1) << 4)
+                                     : c * 64 + (((r >> 2) ^ (c >> 1)) << 5) + ((r & 3) << 3));
+    // place of tile t's parts: whole records for 16-token blocks, halves of a
+    // record for 32-token ones
+    auto tile_at = [](int t, int row_bytes) { return BS == 16 ? t * REC : (t >> 1) * REC + (t & 1) * 16 * row_bytes; };
+    const uint32_t s_off = q4_scale_offset(D, BS) + r * 8;
+    T *outp = static_cast<T *>(a.out);
+    const float odd15 = (r & 1) ? 15.f : 0.f; // rows r and r + 8 are tokens of r's parity
+    const uint32_t odd_sign = (r & 1) ? 0x80008000u : 0u;
+
+    uint32_t qh[KW][2][2], ql[F32 ? KW : 1][2][2];
+    float acc[MT][4];
+    float c0 = 0.f, c1 = 0.f, qs0 = 0.f, qs1 = 0.f, h0 = 0.f, h1 = 0.f; // score factors of the two columns
+    float m0, m1, l0, l1, lo0, lo1;
+    int stage = 0;
+    uint32_t phase = 0, gphase = 0;
+    auto sync = [&] {
+        const bool ok = group_sync(&s_group[ch], tw, gphase);
+        if (!ok && lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
+        return ok;
+    };
+    int left = (int)(u1 - u0); // units whose segments have not ended here
+
+    while (left > 0) { // segments
+        bool bad = false;
+        int at = warp * nst + stage;
+        { // q's loads run beside the first stage's copies
+            m0 = m1 = -INFINITY;
+            l0 = l1 = lo0 = lo1 = 0.f;
+            // q of column r's head, the dims of this lane's words
+            const int g = r % CW;
+            QWords<T, KW * 8> qw;
+            qw.load(static_cast<const T *>(a.q) +
+                        ((size_t)meta[at].b * Hq + (size_t)(meta[at].hg * hs + ch) * G + g) * D + c * (KW * 8),
+                    g < G);
+            float amax = 0.f, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < KW * 8; ++i) {
+                const float x = qw.get(i);
+                amax = fmaxf(amax, fabsf(x));
+                sum += x;
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+                sum += __shfl_xor_sync(kFull, sum, o);
+            }
+            // 2^e brings the largest element to [2^14, 2^15)
+            int e = amax > 0.f ? 14 - ((int)(__float_as_uint(amax) >> 23) - 127) : 0;
+            e = max(-100, min(100, e));
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            const float down = __uint_as_float((uint32_t)(127 + 24 - e) << 23) * a.scale_log2;
+#pragma unroll
+            for (int i = 0; i < KW; ++i)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const float x0 = qw.get(8 * i + 2 * s) * up, x1 = qw.get(8 * i + 2 * s + 4) * up;
+                    const float y0 = qw.get(8 * i + 2 * s + 1) * up * 0.0625f, y1 = qw.get(8 * i + 2 * s + 5) * up * 0.0625f;
+                    qh[i][s][0] = pack_f16(x0, x1);
+                    qh[i][s][1] = pack_f16(y0, y1);
+                    if constexpr (F32) {
+                        const __half2 hx = *reinterpret_cast<__half2 *>(&qh[i][s][0]);
+                        const __half2 hy = *reinterpret_cast<__half2 *>(&qh[i][s][1]);
+                        ql[i][s][0] = pack_f16(x0 - __low2float(hx), x1 - __high2float(hx));
+                        ql[i][s][1] = pack_f16(y0 - __low2float(hy), y1 - __high2float(hy));
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+            // 7.5 sum q in the products' units (fp32 only)
+            const float half = sum * up * (7.5f / 16777216.f);
+            if constexpr (F32) {
+                h0 = __shfl_sync(kFull, half, 4 * col);
+                h1 = __shfl_sync(kFull, half, 4 * col + 4);
+            }
+            sum *= a.scale_log2;
+            c0 = __shfl_sync(kFull, down, 4 * col);
+            c1 = __shfl_sync(kFull, down, 4 * col + 4);
+            qs0 = __shfl_sync(kFull, sum, 4 * col);
+            qs1 = __shfl_sync(kFull, sum, 4 * col + 4);
+        }
+        Meta mt;
+        int flags;
+#pragma unroll 1
+        do { // stages
+        const int cf = meta[at].cnt; // written by this warp when it issued the stage
+        flags = cf >> 8;
+        if (!spin_wait(&full[at], phase)) {
+            if (lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
+            return;
+        }
+        uint8_t *st = ring + at * STAGE;
+        int cnt = ST;
+        if (cf != ST) { // not SB whole blocks inside a segment
+            bad |= (flags & kBad) != 0;
+            cnt = (flags & kBad) ? 0 : cf & 255;
+            if (flags & kAppend)
+                append<D, BS, T>(a, meta[at].b, meta[at].hg * hs + ch, meta[at].len, (cnt - 1) % BS,
+                                 st + (cnt - 1) / BS * REC);
+        }
+        if (cnt > 0) {
+            // ---- products of the tiles, one chain each
+            float dot[NTILE][4] = {};
+#pragma unroll
+            for (int tile = 0; tile < NTILE; ++tile) {
+                uint32_t ka[KW], kb[KW];
+                const uint8_t *tk = st + tile_at(tile, D / 2) + k_off;
+                lds<KW>(ka, tk);
+                lds<KW>(kb, tk + 4 * D);
+#pragma unroll
+                for (int i = 0; i < KW; ++i)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const uint32_t wa = s ? ka[i] >> 8 : ka[i], wb = s ? kb[i] >> 8 : kb[i];
+                        const uint32_t a0 = wa & 0x000f000fu, a1 = wb & 0x000f000fu;
+                        const uint32_t a2 = wa & 0x00f000f0u, a3 = wb & 0x00f000f0u;
+                        if constexpr (F32) {
+                            // small part first, one sum of 16 at a time: the
+                            // tensor cores cut each sum at the size of its
+                            // largest term
+                            float part[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma_f16(part, a0, a1, a2, a3, ql[i][s][0], ql[i][s][1]);
+                            mma_f16(part, a0, a1, a2, a3, qh[i][s][0], qh[i][s][1]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) dot[tile][k] += part[k];
+                        } else {
+                            mma_f16(dot[tile], a0, a1, a2, a3, qh[i][s][0], qh[i][s][1]);
+                        }
+                    }
+            }
+            if constexpr (R == 2) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dot[0][k] = rep ? dot[1][k] : dot[0][k];
+            } else if constexpr (R == 4) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float u = (rep & 1) ? dot[1][k] : dot[0][k], v = (rep & 1) ? dot[3][k] : dot[2][k];
+                    dot[0][k] = (rep & 2) ? v : u;
+                }
+            }
+            // ---- scores of the lane's tokens r, r + 8 of its tiles
+            float x[XT][4], vst[XT][2], vlo[XT][2];
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < XT; ++t) {
+                const int tile = R == 1 ? t : rep;
+                const uint8_t *ts = st + (BS == 16 ? tile * REC : (tile >> 1) * REC + (tile & 1) * 128) + s_off;
+                uint32_t sc[2][2];
+                lds<2>(sc[0], ts);
+                lds<2>(sc[1], ts + 64);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float ks = bf16_lo(sc[k][0]), kl = bf16_hi(sc[k][0]);
+                    vst[t][k] = bf16_lo(sc[k][1]);
+                    vlo[t][k] = fmaf(vst[t][k], odd15, bf16_hi(sc[k][1]));
+                    if constexpr (F32) {
+                        // around the middle code, where the two terms do not cancel
+                        const float mid = fmaf(ks, 7.5f, kl);
+                        x[t][2 * k] = fmaf(ks * c0, dot[t][2 * k] - h0, mid * qs0);
+                        x[t][2 * k + 1] = fmaf(ks * c1, dot[t][2 * k + 1] - h1, mid * qs1);
+                    } else {
+                        x[t][2 * k] = fmaf(ks * c0, dot[t][2 * k], kl * qs0);
+                        x[t][2 * k + 1] = fmaf(ks * c1, dot[t][2 * k + 1], kl * qs1);
+                    }
+                }
+            }
+            if (cnt < ST) { // tokens behind the sequence's: whatever the pool holds there
+#pragma unroll
+                for (int t = 0; t < XT; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if ((R == 1 ? t : rep) * 16 + k * 8 + r >= cnt) {
+                            x[t][2 * k] = x[t][2 * k + 1] = -INFINITY;
+                            vst[t][k] = vlo[t][k] = 0.f;
+                        }
+            }
+#pragma unroll
+            for (int t = 0; t < XT; ++t)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float lv = log2_approx(fmaxf(vst[t][k], kStepFloor));
+                    t0 = fmaxf(t0, x[t][2 * k] + lv);
+                    t1 = fmaxf(t1, x[t][2 * k + 1] + lv);
+                }
+            // ---- move the reference where a weight would leave its range
+            if (__any_sync(kFull, t0 > m0 + kWeightMax || t1 > m1 + kWeightMax)) {
+#pragma unroll
+                for (int o = R == 4 ? 1 : R == 2 ? 2 : 4; o < 32; o <<= 1) {
+                    t0 = fmaxf(t0, __shfl_xor_sync(kFull, t0, o));
+                    t1 = fmaxf(t1, __shfl_xor_sync(kFull, t1, o));
+                }
+                const float n0 = fmaxf(m0, t0 - kWeightNew), n1 = fmaxf(m1, t1 - kWeightNew);
+                const float f0 = n0 == -INFINITY ? 1.f : exp2_approx(m0 - n0);
+                const float f1 = n1 == -INFINITY ? 1.f : exp2_approx(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= f0;
+                l1 *= f1;
+                lo0 *= f0;
+                lo1 *= f1;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    acc[i][0] *= f0;
+                    acc[i][1] *= f1;
+                    acc[i][2] *= f0;
+                    acc[i][3] *= f1;
+                }
+            }
+            // ---- weights, as the values' B operand
+            uint32_t wh[XT][2], wl[F32 ? XT : 1][2];
+#pragma unroll
+            for (int t = 0; t < XT; ++t)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float p0 = exp2_approx(x[t][2 * k] - m0), p1 = exp2_approx(x[t][2 * k + 1] - m1);
+                    l0 += p0;
+                    l1 += p1;
+                    lo0 = fmaf(p0, vlo[t][k], lo0);
+                    lo1 = fmaf(p1, vlo[t][k], lo1);
+                    const float w0 = p0 * vst[t][k], w1 = p1 * vst[t][k];
+                    const uint32_t w = pack_f16(w0, w1);
+                    wh[t][k] = movmatrix_trans(w ^ odd_sign);
+                    if constexpr (F32) {
+                        const __half2 h = *reinterpret_cast<const __half2 *>(&w);
+                        wl[t][k] = movmatrix_trans(pack_f16(w0 - __low2float(h), w1 - __high2float(h)) ^ odd_sign);
+                    }
+                }
+            // ---- O^T += V^T (p s)^T
+#pragma unroll
+            for (int pair = 0; pair < NTILE / 2; ++pair) {
+                uint32_t va[2][2][KW], bh[2][2], bl[2][2];
+#pragma unroll
+                for (int tt = 0; tt < 2; ++tt) {
+                    const int tile = 2 * pair + tt;
+                    const uint8_t *tv = st + tile_at(tile, D / 2) + v_off;
+                    lds<KW>(va[tt][0], tv);
+                    lds<KW>(va[tt][1], tv + 4 * D);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const bool own = R == 1 || brep == tile;
+                        bh[tt][k] = own ? wh[R == 1 ? tt : 0][k] : 0u;
+                        if constexpr (F32) bl[tt][k] = own ? wl[R == 1 ? tt : 0][k] : 0u;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < KW; ++i)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        float(&o)[4] = acc[2 * i + s];
+                        uint32_t va4[2][4];
+#pragma unroll
+                        for (int tt = 0; tt < 2; ++tt) {
+                            // the high halves are the odd tokens: 15 - n
+                            const uint32_t wa = s ? va[tt][0][i] >> 8 : va[tt][0][i];
+                            const uint32_t wb = s ? va[tt][1][i] >> 8 : va[tt][1][i];
+                            va4[tt][0] = and_xor(wa, 0x000f000fu, 0x000f0000u);
+                            va4[tt][1] = and_xor(wa, 0x00f000f0u, 0x00f00000u);
+                            va4[tt][2] = and_xor(wb, 0x000f000fu, 0x000f0000u);
+                            va4[tt][3] = and_xor(wb, 0x00f000f0u, 0x00f00000u);
+                        }
+                        if constexpr (F32) { // small part first, each sum added with rounding
+                            float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int tt = 0; tt < 2; ++tt)
+                                mma_f16(part, va4[tt][0], va4[tt][1], va4[tt][2], va4[tt][3], bl[tt][0], bl[tt][1]);
+#pragma unroll
+                            for (int tt = 0; tt < 2; ++tt)
+                                mma_f16(part, va4[tt][0], va4[tt][1], va4[tt][2], va4[tt][3], bh[tt][0], bh[tt][1]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) o[k] += part[k];
+                        } else {
+#pragma unroll
+                            for (int tt = 0; tt < 2; ++tt)
+                                mma_f16(o, va4[tt][0], va4[tt][1], va4[tt][2], va4[tt][3], bh[tt][0], bh[tt][1]);
+                        }
+                    }
+            }
+        }
+        if (flags & kLast) mt = meta[at];
+        __syncwarp(); // the slot is used up
+        issue(at);
+        ++at;
+        if (++stage == nst) {
+            stage = 0;
+            at = warp * nst;
+            phase ^= 1;
+        }
+        } while (!(flags & kLast));
+
+        // ================= end of this CTA's share of the sequence =================
+        const int kvh = mt.hg * hs + ch;
+        const long long seg = (long long)mt.hg * ublk + mt.sb; // position of the sequence's first unit
+        left -= mt.blocks;
+#pragma unroll
+        for (int o = R == 4 ? 1 : R == 2 ? 2 : 4; o < 32; o <<= 1) {
+            l0 += __shfl_xor_sync(kFull, l0, o);
+            l1 += __shfl_xor_sync(kFull, l1, o);
+            lo0 += __shfl_xor_sync(kFull, lo0, o);
+            lo1 += __shfl_xor_sync(kFull, lo1, o);
+        }
+        // Codes of odd dims were 2^-20, of even ones 2^-24.  With copies, a
+        // lane keeps one of its two columns (R = 4: and half of its dims) and
+        // hands the rest to the lane that keeps those.
+        constexpr int NV = 2 * DL / R;      // values of a lane
+        constexpr int NH = R == 1 ? 2 : 1;  // heads of a lane
+        float val[NV];
+        const bool second = R > 1 && (R == 2 ? rep : rep & 1);
+        const int head0 = R == 1 ? col : R == 2 ? col + rep : (rep & 1);
+        const int dim0 = r * DL + (R == 4 ? (rep >> 1) * (DL / 2) : 0);
+#pragma unroll
+        for (int k = 0; k < DL; ++k) {
+            const float sc = (k & 1) ? 1048576.f : 16777216.f;
+            const float v0 = acc[k >> 1][2 * (k & 1)] * sc, v1 = acc[k >> 1][2 * (k & 1) + 1] * sc;
+            if constexpr (R == 1) {
+                val[k] = v0;
+                val[DL + k] = v1;
+            } else {
+                const float give = second ? v0 : v1, keep = second ? v1 : v0;
+                const float sum = keep + __shfl_xor_sync(kFull, give, R == 2 ? 2 : 1);
+                if constexpr (R == 2) {
+                    val[k] = sum;
+                } else {
+                    acc[k >> 1][2 * (k & 1)] = sum;
+                }
+            }
+        }
+        if constexpr (R == 4) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const float lo_half = acc[k >> 1][2 * (k & 1)], hi_half = acc[(k + NV) >> 1][2 * (k & 1)];
+                const float give = (rep & 2) ? lo_half : hi_half, keep = (rep & 2) ? hi_half : lo_half;
+                val[k] = keep + __shfl_xor_sync(kFull, give, 2);
+            }
+        }
+        float mh[NH], lh[NH], bh[NH];
+        mh[0] = second ? m1 : m0;
+        lh[0] = second ? l1 : l0;
+        bh[0] = second ? lo1 : lo0;
+        if constexpr (NH == 2) {
+            mh[1] = m1;
+            lh[1] = l1;
+            bh[1] = lo1;
+        }
+        const size_t orow = ((size_t)mt.b * Hq + (size_t)kvh * G) * D;
+        const long long segrow = (long long)mt.hg * B + mt.b;
+        float *slot = a.part + ((size_t)(blockIdx.x + segrow) * hs + ch) * gm.slot_floats;
+        const bool whole = (flags & kWhole) != 0;
+        if (tw == 1) {
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+                const int g = head0 + n;
+                if (g >= G) continue;
+                const float inv = 1.f / lh[n];
+#pragma unroll
+                for (int k = 0; k < NV / NH; k += 4) {
+                    const float *v = val + n * (NV / NH) + k;
+                    const float y0 = v[0] + bh[n], y1 = v[1] + bh[n], y2 = v[2] + bh[n], y3 = v[3] + bh[n];
+                    if (whole) {
+                        T *o = outp + orow + (size_t)g * D + dim0 + k;
+                        if (bad)
+                            store4<T>(o, 0.f, 0.f, 0.f, 0.f);
+                        else
+                            store4<T>(o, y0 * inv, y1 * inv, y2 * inv, y3 * inv);
+                    } else {
+                        *reinterpret_cast<float4 *>(slot + g * D + dim0 + k) = make_float4(y0, y1, y2, y3);
+                    }
+                }
+                if (!whole && r == 0 && (R < 4 || rep < 2))
+                    *reinterpret_cast<float2 *>(slot + G * D + 2 * g) = make_float2(mh[n], bad ? -INFINITY : lh[n]);
             }
         } else {
-            const uint8_t *rec = pool + ((size_t)tab[j / bs] * Hkv + kvh) * rb;
-            const int t = j % bs, unit = lane * EPL / 4;
-            uint32_t kw = reinterpret_cast<const uint16_t *>(rec)[t * (D / 4) + unit];
-            uint32_t vw = reinterpret_cast<const uint16_t *>(rec + q4_v_offset(D, bs))[q4_v_unit<D>(t, unit)];
-            if (EPL == 2) {
-                kw >>= 8 * (lane & 1);
-                vw >>= 8 * (lane & 1);
-            }
-            const uint2 sc = *reinterpret_cast<const uint2 *>(rec + q4_scale_offset(D, bs) + t * 8);
+            // join the warps that share the head in shared memory
+            if (r == 0 && (R < 4 || rep < 2)) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                kr[i] = q4_value((kw >> (4 * i)) & 15u, bf16_lo(sc.x), bf16_hi(sc.x));
-                vr[i] = q4_value((vw >> (4 * i)) & 15u, bf16_lo(sc.y), bf16_hi(sc.y));
+                for (int n = 0; n < NH; ++n) {
+                    s_m[warp][head0 + n] = mh[n];
+                    s_l[warp][head0 + n] = bad ? -INFINITY : lh[n];
+                    s_b[warp][head0 + n] = bh[n];
+                }
+            }
+            if (!sync()) return;
+            float *mine = join + (size_t)warp * G * D;
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+                const int g = head0 + n;
+                if (g >= G) continue;
+                float M = mh[n];
+                for (int t = 0; t < tw; ++t) M = fmaxf(M, s_m[t * hs + ch][g]);
+                const float f = M == -INFINITY ? 1.f : exp2_approx(mh[n] - M);
+#pragma unroll
+                for (int k = 0; k < NV / NH; k += 4) {
+                    const float *v = val + n * (NV / NH) + k;
+                    *reinterpret_cast<float4 *>(mine + g * D + dim0 + k) =
+                        make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+                }
+            }
+            if (!sync()) return;
+            for (int e = gtid; e < G * (D / 4); e += gthreads) {
+                const int g = e / (D / 4), d = e % (D / 4) * 4;
+                float M = -INFINITY;
+                for (int t = 0; t < tw; ++t) M = fmaxf(M, s_m[t * hs + ch][g]);
+                float l = 0.f, low = 0.f;
+                bool refused = false; // a block or the length was
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int t = 0; t < tw; ++t) {
+                    const int w = t * hs + ch;
+                    const float f = M == -INFINITY ? 1.f : exp2_approx(s_m[w][g] - M);
+                    refused |= s_l[w][g] == -INFINITY;
+                    l = fmaf(s_l[w][g], f, l);
+                    low = fmaf(s_b[w][g], f, low);
+                    const float4 x = *reinterpret_cast<const float4 *>(join + (size_t)w * G * D + g * D + d);
+                    o.x += x.x;
+                    o.y += x.y;
+                    o.z += x.z;
+                    o.w += x.w;
+                }
+                o.x += low;
+                o.y += low;
+                o.z += low;
+                o.w += low;
+                if (whole) {
+                    const float inv = 1.f / l;
+                    if (refused)
+                        store4<T>(outp + orow + (size_t)g * D + d, 0.f, 0.f, 0.f, 0.f);
+                    else
+                        store4<T>(outp + orow + (size_t)g * D + d, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                } else {
+                    *reinterpret_cast<float4 *>(slot + g * D + d) = o;
+                    if (d == 0)
+                        *reinterpret_cast<float2 *>(slot + G * D + 2 * g) = make_float2(M, refused ? -INFINITY : l);
+                }
             }
         }
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) dot = fmaf(qv[i], kr[i], dot);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-        const float s = dot * a.scale;
-        const float mn = fmaxf(m, s);
-        const float mu = mn == -INFINITY ? 0.f : mn;
-        const float alpha = expf(m - mu), p = expf(s - mu);
-        l = l * alpha + p;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) acc[i] = acc[i] * alpha + p * vr[i];
-        m = mn;
+        if (!whole) {
+            // The partial is ordered before the ticket by the barrier, and
+            // the ticket is an acquire-release at GPU scope.
+            const int cfirst = cta_of(seg, P, U), nseg = cta_of(seg + mt.nblk - 1, P, U) - cfirst + 1;
+            if (!sync()) return;
+            int32_t *ticket = a.tickets + (size_t)mt.b * Hkv + kvh;
+            int last = 0;
+            if (gtid == 0) {
+                int old;
+                asm volatile("atom.add.acq_rel.gpu.s32 %0, [%1], 1;" : "=r"(old) : "l"(ticket) : "memory");
+                last = old == nseg - 1;
+                if (last) *ticket = 0;
+                s_last[ch] = last;
+            }
+            if (!sync()) return;
+            last = tw == 1 ? __shfl_sync(kFull, last, 0) : s_last[ch];
+            if (last) {
+                const float *first = a.part + ((size_t)(cfirst + segrow) * hs + ch) * gm.slot_floats;
+                const size_t step = (size_t)hs * gm.slot_floats;
+                if (tw == 1)
+                    fold<D, T, CW * D / 128>(first, step, nseg, G, gtid, 32, outp + orow);
+                else
+                    fold<D, T, 1>(first, step, nseg, G, gtid, gthreads, outp + orow);
+            }
+        }
+        if (!sync()) return; // the join buffers are free again
     }
-    const float inv = 1.f / l;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) out[i] = from_f32<T>(acc[i] * inv);
+}
+
+constexpr int kMaxDev = 64;
+constexpr size_t kSmemPerCta = 108 * 1024; // two CTAs an SM, beside their static arrays
+
+template <int D, int R>
+size_t smem_bytes(int ncw, int tw, int nst, int group)
+{
+    const int stage_tokens = 16 * (R < 2 ? 2 : R);
+    return (size_t)ncw * nst * (stage_tokens * (D + 8) + 8 + sizeof(Meta)) + 8 +
+           (tw > 1 ? (size_t)ncw * group * D * 4 : 0);
+}
+
+struct Plan {
+    DecodeQ4Geom gm;
+    int ctas;
+    size_t smem;
+};
+
+template <int D, int BS, int R, typename T>
+int make_plan(int batch, int num_kv_heads, int group, Plan *p)
+{
+    const int sms = num_sms();
+    if (sms <= 0) return PA_ERR_DEVICE;
+    p->ctas = 2 * sms;
+    // Heads of a CTA: the most that leave a sequence cut into at most
+    // kMaxParts parts by the CTAs' ranges.  With fewer rows than that, the
+    // warps of a CTA share a head's tokens and join in shared memory.
+    int hs = 1;
+    for (int h = 2; h <= kMaxWarps && h <= num_kv_heads; ++h)
+        if (num_kv_heads % h == 0 && (long long)kMaxParts * batch * num_kv_heads >= (long long)p->ctas * h) hs = h;
+    const int tw = kMaxWarps / hs, ncw = hs * tw;
+    int nst = 6;
+    while (nst > 2 && smem_bytes<D, R>(ncw, tw, nst, group) > kSmemPerCta) --nst;
+    p->smem = smem_bytes<D, R>(ncw, tw, nst, group);
+    static int raised[kMaxDev];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return PA_ERR_DEVICE;
+    if (!__atomic_load_n(&raised[dev], __ATOMIC_ACQUIRE)) {
+        if (cudaFuncSetAttribute(decode_q4_kernel<D, BS, R, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmemPerCta) != cudaSuccess)
+            return PA_ERR_LAUNCH;
+        __atomic_store_n(&raised[dev], 1, __ATOMIC_RELEASE);
+    }
+    p->gm.hs = hs;
+    p->gm.tw = tw;
+    p->gm.head_groups = num_kv_heads / hs;
+    p->gm.nst = nst;
+    p->gm.slot_floats = group * D + 16;
+    p->gm.min_tokens = kMinTokens;
+    return PA_OK;
+}
+
+size_t plan_workspace(const Plan &p, int batch)
+{
+    return kTicketRegionBytes + ((size_t)p.ctas + (size_t)p.gm.head_groups * batch) * p.gm.hs * p.gm.slot_floats * 4;
+}
+
+template <int D, int BS, int R, typename T>
+int plan_and_launch(const DecodeQ4Args *a, int batch, int num_kv_heads, int group, size_t have, size_t *need,
+                    cudaStream_t s)
+{
+    Plan p;
+    const int rc = make_plan<D, BS, R, T>(batch, num_kv_heads, group, &p);
+    if (rc != PA_OK) return rc;
+    *need = plan_workspace(p, batch);
+    if (a == nullptr) return PA_OK;
+    if (have < *need) return PA_ERR_WORKSPACE;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.ctas);
+    cfg.blockDim = dim3(p.gm.hs * p.gm.tw * 32);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, decode_q4_kernel<D, BS, R, T>, *a, p.gm) == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
+}
+
+// Copies of the head group in the products' columns: as many as fit, up to
+// the tiles of a stage.  Four (64-token stages) for head_dim 64 only: at 128
+// two such stages a warp would not leave room for a second CTA on the SM.
+template <int D, int BS, typename T>
+int by_copies(const DecodeQ4Args *a, int batch, int num_kv_heads, int group, size_t have, size_t *need, cudaStream_t s)
+{
+    if constexpr (D == 64) {
+        if (group <= 2) return plan_and_launch<D, BS, 4, T>(a, batch, num_kv_heads, group, have, need, s);
+    }
+    if (group <= 4) return plan_and_launch<D, BS, 2, T>(a, batch, num_kv_heads, group, have, need, s);
+    return plan_and_launch<D, BS, 1, T>(a, batch, num_kv_heads, group, have, need, s);
+}
+
+int dispatch(const DecodeQ4Args *a, int batch, int num_kv_heads, int group, int d, int bs, bool f32, size_t have,
+             size_t *need, cudaStream_t s)
+{
+#define PA_Q4(D_, BS_)                                                                                        \
+    if (d == D_ && bs == BS_)                                                                                 \
+        return f32 ? by_copies<D_, BS_, float>(a, batch, num_kv_heads, group, have, need, s)                  \
+                   : by_copies<D_, BS_, __nv_bfloat16>(a, batch, num_kv_heads, group, have, need, s);
+    PA_Q4(64, 16)
+    PA_Q4(64, 32)
+    PA_Q4(128, 16)
+    PA_Q4(128, 32)
+#undef PA_Q4
+    return PA_ERR_UNSUPPORTED;
 }
 
 }  // namespace
 
-size_t decode_q4_workspace(int, int, int, int, int) { return 0; }
-
-int decode_q4_launch(const DecodeQ4Args &a, bool f32, cudaStream_t s)
+size_t decode_q4_workspace(int batch, int num_heads, int num_kv_heads, int head_dim, int block_size, bool f32)
 {
-    const long long warps = (long long)a.batch * a.num_heads;
-    const unsigned grid = (unsigned)((warps + 3) / 4);
-    if (a.head_dim == 64) {
-        if (f32) decode_q4_kernel<64, float><<<grid, 128, 0, s>>>(a);
-        else decode_q4_kernel<64, __nv_bfloat16><<<grid, 128, 0, s>>>(a);
-    } else {
-        if (f32) decode_q4_kernel<128, float><<<grid, 128, 0, s>>>(a);
-        else decode_q4_kernel<128, __nv_bfloat16><<<grid, 128, 0, s>>>(a);
-    }
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
+    size_t need = 0;
+    const int rc = dispatch(nullptr, batch, num_kv_heads, num_heads / num_kv_heads, head_dim, block_size, f32, 0,
+                            &need, nullptr);
+    return rc == PA_OK ? need : 0;
+}
+
+int decode_q4_launch(const DecodeQ4Args &a, bool f32, size_t workspace_bytes, cudaStream_t s)
+{
+    size_t need = 0;
+    return dispatch(&a, a.batch, a.num_kv_heads, a.group, a.head_dim, a.block_size, f32, workspace_bytes, &need, s);
 }
 
 }  // namespace pa

@@ -151,8 +151,9 @@ struct DecodeQ4Args {
     int batch, num_heads, num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq, group;
     float scale, scale_log2;
 };
-size_t decode_q4_workspace(int batch, int num_heads, int num_kv_heads, int head_dim, int block_size);
-int decode_q4_launch(const DecodeQ4Args &a, bool f32, cudaStream_t s);
+size_t decode_q4_workspace(int batch, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                           bool f32);
+int decode_q4_launch(const DecodeQ4Args &a, bool f32, size_t workspace_bytes, cudaStream_t s);
 
 struct TablesArgs {
     const int32_t *cache_seqlens;

@@ -203,6 +203,43 @@ def test_decode_one_long_sequence(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,bs,hq,hkv", [(128, 16, 8, 8), (64, 32, 16, 2), (64, 16, 16, 16)])
+def test_decode_long_walks(dtype, d, bs, hq, hkv):
+    """Enough tokens that every warp walks hundreds of blocks; the pool is
+    made on the GPU and four sequences are checked."""
+    b, lo, hi = 72, 6000, 12000
+    rng = np.random.default_rng(d + hkv)
+    lens = rng.integers(lo, hi, b).astype(np.int32)
+    held = lens // bs + 1
+    nb = int(held.sum())
+    perm = rng.permutation(nb).astype(np.int32)
+    table = np.full((b, held.max()), -1, dtype=np.int32)
+    for i, at in enumerate(np.cumsum(held) - held):
+        table[i, :held[i]] = perm[at:at + held[i]]
+    g = torch.Generator(device=DEV).manual_seed(5)
+    pool = torch.randint(0, 256, (nb, hkv, q4.record_bytes(d, bs)), dtype=torch.uint8, device=DEV, generator=g)
+    scales = torch.randn(nb, hkv, bs, 4, device=DEV, generator=g) * torch.tensor([0.02, 0.2, 0.02, 0.4], device=DEV)
+    scales += torch.tensor([0.3, -2.2, 0.3, -2.2], device=DEV)
+    pool[:, :, bs * d:] = scales.to(BF16).view(torch.uint8).view(nb, hkv, bs * 8)
+    rand = lambda *s: torch.randn(*s, device=DEV, generator=g).to(dtype)  # noqa: E731
+    q, kn, vn = rand(b, hq, d), rand(b, hkv, d), rand(b, hkv, d)
+    pick = [0, 17, 40, b - 1]
+    rows = [table[i, :held[i]].astype(np.int64) for i in pick]
+    blocks = pool[torch.from_numpy(np.concatenate(rows)).to(DEV)].cpu().numpy()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = pa.pa_decode_q4(q, pool, torch.from_numpy(table).to(DEV), torch.from_numpy(lens).to(DEV), kn, vn, dev_err=err)
+    assert err.item() == 0
+    small = np.full((4, held.max()), -1, dtype=np.int32)
+    at = 0
+    for j, r in enumerate(rows):
+        small[j, :len(r)] = np.arange(at, at + len(r))
+        at += len(r)
+    sel = lambda x: x[torch.tensor(pick, device=DEV)].cpu()  # noqa: E731
+    ref, seen = q4.decode(_f32(sel(q)), blocks, small, lens[pick], _f32(sel(kn)), _f32(sel(vn)), bs)
+    check(sel(out), ref, decode_bound(sel(q), seen, ref, dtype, d ** -0.5), norm=NORM[dtype])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("d,bs", [(64, 32), (128, 16)])
 def test_decode_peaked_and_scaled(dtype, d, bs):
     """Scores that span hundreds (one key takes nearly all), and another scale."""
