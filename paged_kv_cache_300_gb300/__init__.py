@@ -366,67 +366,61 @@ def pa_varlen_paged(q, k_cache, v_cache, block_table, cu_seq_lens_q, seqlens_k,
 
 
 # ------------------------------------------------------------------ 4-bit pool
-def _int32_on(dev, **ts):
-    """Index tensors: int32, contiguous, on `dev`."""
+# A step of a small model is a few microseconds on the GPU, so the checks below
+# touch each tensor as few times as they can.  They pass or fail as a whole;
+# _refuse then says which tensor it was.
+def _fits(index, dtype, *ts):
+    """Every tensor given is of `dtype`, contiguous and on device `index`."""
+    for t in ts:
+        if t is not None and (t.dtype is not dtype or t.get_device() != index
+                              or not t.is_contiguous()):
+            return False
+    return True
+
+
+def _refuse(index, dtype, **ts):
     for name, t in ts.items():
         if t is None:
             continue
-        if t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32")
-        if t.device != dev:
-            raise ValueError("all tensors must be on the same device")
-        if not t.is_contiguous():
-            raise ValueError("all tensors must be contiguous")
-
-
-def _like_on(dev, dtype, shape, **ts):
-    """Element tensors of one dtype and shape, contiguous, on `dev`."""
-    for name, t in ts.items():
-        if t is None:
-            continue
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have the shape {tuple(shape)}")
-        if t.device != dev:
-            raise ValueError("all tensors must be on the same device")
+        if t.get_device() != index:
+            raise ValueError("all tensors must be on the same CUDA device")
         if not t.is_contiguous():
-            raise ValueError("all tensors must be contiguous")
+            raise ValueError(f"{name} must be contiguous")
+    raise ValueError("inconsistent shapes")
 
 
 def _q4_geometry(kv_cache, num_kv_heads, head_dim):
-    """Block size of a 4-bit pool [num_blocks, num_kv_heads, record]."""
+    """(device index, number of blocks, block size) of a 4-bit pool
+    [num_blocks, num_kv_heads, block_size * (head_dim + 8)]."""
     if not kv_cache.is_cuda:
         raise ValueError("all tensors must live on a CUDA device")
-    if kv_cache.dtype != torch.uint8 or kv_cache.dim() != 3 or not kv_cache.is_contiguous():
+    if kv_cache.dtype is not torch.uint8 or kv_cache.dim() != 3 or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be a contiguous uint8 tensor "
                          "[num_blocks, num_kv_heads, block_size * (head_dim + 8)]")
-    record = kv_cache.shape[2]
-    if kv_cache.shape[1] != num_kv_heads or record % (head_dim + 8) != 0:
+    nb, h, record = kv_cache.shape
+    if h != num_kv_heads or record % (head_dim + 8) != 0:
         raise ValueError("kv_cache does not fit the number of kv heads or the head_dim")
-    return record // (head_dim + 8)
+    return kv_cache.get_device(), nb, record // (head_dim + 8)
 
 
-class _On:
-    """Makes a tensor's device the current one for a call and names the
-    stream: the given one, else that device's current stream."""
+def _launch(name, index, stream, *args):
+    """Call the library with the tensors' device current, on `stream` (default:
+    that device's current stream)."""
+    fn = getattr(_lib or load(), name)
+    cur = torch.cuda.current_device()
+    if cur == index:
+        rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    if rc != 0:
+        raise PAError(name, rc)
 
-    __slots__ = ("dev", "prev", "stream")
 
-    def __init__(self, dev, stream):
-        self.dev = dev.index
-        self.stream = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        self.prev = cur if cur != self.dev else None
-        if self.prev is not None:
-            torch.cuda.set_device(self.dev)
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def pa_q4_block_bytes(num_kv_heads, head_dim, block_size) -> int:
@@ -448,19 +442,16 @@ def pa_cache_update_q4(k_chunk, v_chunk, slot_map, kv_cache, dev_err=None, strea
     """Quantise the rows of k_chunk, v_chunk [T, Hkv, D] (bfloat16 or float32)
     into the slots slot_map [T] int32 of the 4-bit pool; a negative slot skips
     its row."""
-    t, hkv, d = k_chunk.shape
-    bs = _q4_geometry(kv_cache, hkv, d)
-    dev = kv_cache.device
+    shape = k_chunk.shape
+    t, hkv, d = shape
     dt = _dtype(k_chunk)
-    _like_on(dev, k_chunk.dtype, k_chunk.shape, k_chunk=k_chunk, v_chunk=v_chunk)
-    _int32_on(dev, slot_map=slot_map, dev_err=dev_err)
-    if slot_map.shape != (t,):
-        raise ValueError("slot_map must have one entry for each row")
-    with _On(dev, stream) as st:
-        rc = load().pa_cache_update_q4(k_chunk.data_ptr(), v_chunk.data_ptr(), slot_map.data_ptr(),
-                                       kv_cache.data_ptr(), t, hkv, d, kv_cache.shape[0], bs, dt,
-                                       None if dev_err is None else dev_err.data_ptr(), st)
-    _call("pa_cache_update_q4", rc)
+    index, nb, bs = _q4_geometry(kv_cache, hkv, d)
+    if v_chunk.shape != shape or not _fits(index, k_chunk.dtype, k_chunk, v_chunk):
+        _refuse(index, k_chunk.dtype, k_chunk=k_chunk, v_chunk=v_chunk)
+    if slot_map.shape != (t,) or not _fits(index, torch.int32, slot_map, dev_err):
+        _refuse(index, torch.int32, slot_map=slot_map, dev_err=dev_err)
+    _launch("pa_cache_update_q4", index, stream, k_chunk.data_ptr(), v_chunk.data_ptr(),
+            slot_map.data_ptr(), kv_cache.data_ptr(), t, hkv, d, nb, bs, dt, _addr(dev_err))
 
 
 def pa_cache_gather_q4(kv_cache, block_table, cu_seq_lens_k, k_full, v_full, dev_err=None,
@@ -468,52 +459,59 @@ def pa_cache_gather_q4(kv_cache, block_table, cu_seq_lens_k, k_full, v_full, dev
     """Read positions 0.. of every request back from the 4-bit pool into the
     packed k_full, v_full [Tk, Hkv, D] (bfloat16 or float32), request r's rows
     being [cu_seq_lens_k[r], cu_seq_lens_k[r+1]).  Returns (k_full, v_full)."""
-    tk, hkv, d = k_full.shape
-    bs = _q4_geometry(kv_cache, hkv, d)
-    dev = kv_cache.device
+    shape = k_full.shape
+    tk, hkv, d = shape
     dt = _dtype(k_full)
-    _like_on(dev, k_full.dtype, k_full.shape, k_full=k_full, v_full=v_full)
-    _int32_on(dev, block_table=block_table, cu_seq_lens_k=cu_seq_lens_k, dev_err=dev_err)
+    index, nb, bs = _q4_geometry(kv_cache, hkv, d)
     b, mb = block_table.shape
-    if cu_seq_lens_k.shape != (b + 1,):
-        raise ValueError("cu_seq_lens_k must have one entry more than block_table has rows")
-    with _On(dev, stream) as st:
-        rc = load().pa_cache_gather_q4(kv_cache.data_ptr(), block_table.data_ptr(),
-                                       cu_seq_lens_k.data_ptr(), k_full.data_ptr(),
-                                       v_full.data_ptr(), b, tk, hkv, d, kv_cache.shape[0], bs, mb,
-                                       dt, None if dev_err is None else dev_err.data_ptr(), st)
-    _call("pa_cache_gather_q4", rc)
+    if v_full.shape != shape or not _fits(index, k_full.dtype, k_full, v_full):
+        _refuse(index, k_full.dtype, k_full=k_full, v_full=v_full)
+    if cu_seq_lens_k.shape != (b + 1,) or \
+            not _fits(index, torch.int32, block_table, cu_seq_lens_k, dev_err):
+        _refuse(index, torch.int32, block_table=block_table, cu_seq_lens_k=cu_seq_lens_k,
+                dev_err=dev_err)
+    _launch("pa_cache_gather_q4", index, stream, kv_cache.data_ptr(), block_table.data_ptr(),
+            cu_seq_lens_k.data_ptr(), k_full.data_ptr(), v_full.data_ptr(), b, tk, hkv, d, nb, bs,
+            mb, dt, _addr(dev_err))
     return k_full, v_full
 
 
 def pa_decode_q4_workspace_size(batch, num_heads, num_kv_heads, head_dim, block_size,
                                 dtype=torch.bfloat16) -> int:
+    """Bytes of workspace pa_decode_q4 needs on the current device."""
     dt = PA_BF16 if dtype == torch.bfloat16 else PA_F32
     return int(load().pa_decode_q4_workspace_size(batch, num_heads, num_kv_heads, head_dim,
                                                   block_size, dt))
 
 
-_TICKET_REGION = 1 << 20  # merge counters at the start of a decode workspace
 _q4_workspaces: dict = {}
+_q4_sizes: dict = {}
 
 
-def _q4_workspace(dev, stream, handle, nbytes, counters):
+def _q4_workspace(index, stream, sizes):
     """Workspace of a pa_decode_q4 call that was given none.  Eager calls
     share one per (device, stream), zeroed when it is made.  A call that is
     being captured gets its own from the graph's memory, with its counters
-    cleared inside the graph: two graphs may replay at the same time."""
+    (one int32 per sequence and kv head, at its start) cleared inside the
+    graph: two graphs may replay at the same time."""
+    key = (index,) + sizes
+    nbytes = _q4_sizes.get(key)
+    if nbytes is None:
+        with torch.cuda.device(index):
+            nbytes = int(load().pa_decode_q4_workspace_size(*sizes))
+        _q4_sizes[key] = nbytes
     if nbytes == 0:
-        return None
+        return None  # sizes the call refuses, or an empty batch
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        ws[:4 * counters].zero_()
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
+        ws[:4 * sizes[0] * sizes[2]].zero_()
         return ws
-    key = (dev.index, handle)
-    ws = _q4_workspaces.get(key)
+    handle = (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
+    ws = _q4_workspaces.get((index, handle))
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(stream):  # None: the current stream
-            ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-        _q4_workspaces[key] = ws
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
+        _q4_workspaces[(index, handle)] = ws
     return ws
 
 
@@ -525,36 +523,35 @@ def pa_decode_q4(q, kv_cache, block_table, cache_seqlens, k_new, v_new, out=None
     q [B, Hq, D] attends over positions 0..cache_seqlens[b].  bfloat16 or
     float32.  k_stored, v_stored, when given, receive the new token as the
     pool now holds it.  Returns out [B, Hq, D]."""
-    b, hq, d = q.shape
-    hkv = k_new.shape[1]
-    bs = _q4_geometry(kv_cache, hkv, d)
-    dev = kv_cache.device
+    shape, rows = q.shape, k_new.shape
+    b, hq, d = shape
+    hkv = rows[1]
+    dtype = q.dtype
     dt = _dtype(q)
-    _like_on(dev, q.dtype, q.shape, q=q, out=out)
-    _like_on(dev, q.dtype, (b, hkv, d), k_new=k_new, v_new=v_new, k_stored=k_stored,
-             v_stored=v_stored)
-    _int32_on(dev, block_table=block_table, cache_seqlens=cache_seqlens, dev_err=dev_err)
-    if block_table.shape[0] != b or cache_seqlens.shape != (b,):
-        raise ValueError("inconsistent shapes")
+    index, nb, bs = _q4_geometry(kv_cache, hkv, d)
     if out is None:
         out = torch.empty_like(q)
-    lib = load()
-    with _On(dev, stream) as st:
-        if workspace is None:
-            nbytes = int(lib.pa_decode_q4_workspace_size(b, hq, hkv, d, bs, dt))
-            workspace = _q4_workspace(dev, stream, st, nbytes, b * hkv)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous and on the same device")
-        wptr, wbytes = (None, 0) if workspace is None else (
-            workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        rc = lib.pa_decode_q4(q.data_ptr(), kv_cache.data_ptr(), block_table.data_ptr(),
-                              cache_seqlens.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-                              out.data_ptr(), None if k_stored is None else k_stored.data_ptr(),
-                              None if v_stored is None else v_stored.data_ptr(), b, hq, hkv, d,
-                              kv_cache.shape[0], bs, block_table.shape[1], dt,
-                              float(softmax_scale), wptr, wbytes,
-                              None if dev_err is None else dev_err.data_ptr(), st)
-    _call("pa_decode_q4", rc)
+    if out.shape != shape or rows != (b, hkv, d) or v_new.shape != rows or \
+            (k_stored is not None and k_stored.shape != rows) or \
+            (v_stored is not None and v_stored.shape != rows):
+        raise ValueError("inconsistent shapes")
+    if not _fits(index, dtype, q, out, k_new, v_new, k_stored, v_stored):
+        _refuse(index, dtype, q=q, out=out, k_new=k_new, v_new=v_new, k_stored=k_stored,
+                v_stored=v_stored)
+    tb, mb = block_table.shape
+    if tb != b or cache_seqlens.shape != (b,) or \
+            not _fits(index, torch.int32, block_table, cache_seqlens, dev_err):
+        _refuse(index, torch.int32, block_table=block_table, cache_seqlens=cache_seqlens,
+                dev_err=dev_err)
+    if workspace is None:
+        workspace = _q4_workspace(index, stream, (b, hq, hkv, d, bs, dt))
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the same device")
+    wptr, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    _launch("pa_decode_q4", index, stream, q.data_ptr(), kv_cache.data_ptr(),
+            block_table.data_ptr(), cache_seqlens.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+            out.data_ptr(), _addr(k_stored), _addr(v_stored), b, hq, hkv, d, nb, bs, mb, dt,
+            softmax_scale, wptr, wbytes, _addr(dev_err))
     return out
 
 
@@ -568,33 +565,32 @@ def pa_block_tables(cache_seqlens, new_lens, block_table, free_blocks, num_free,
     behind the last token.  All int32.  num_free [1] is advanced in place
     unless num_free_out is given.  Returns (cu_seq_lens_q, cu_seq_lens_k,
     seqlens_k)."""
-    b, mb = block_table.shape
-    dev = block_table.device
     if not block_table.is_cuda:
         raise ValueError("all tensors must live on a CUDA device")
+    b, mb = block_table.shape
+    index = block_table.get_device()
     if cu_seq_lens_q is None:
-        cu_seq_lens_q = torch.empty(b + 1, dtype=torch.int32, device=dev)
+        cu_seq_lens_q = torch.empty(b + 1, dtype=torch.int32, device=block_table.device)
     if cu_seq_lens_k is None:
-        cu_seq_lens_k = torch.empty(b + 1, dtype=torch.int32, device=dev)
+        cu_seq_lens_k = torch.empty(b + 1, dtype=torch.int32, device=block_table.device)
     if seqlens_k is None:
-        seqlens_k = torch.empty(b, dtype=torch.int32, device=dev)
+        seqlens_k = torch.empty(b, dtype=torch.int32, device=block_table.device)
     if num_free_out is None:
         num_free_out = num_free
-    _int32_on(dev, cache_seqlens=cache_seqlens, new_lens=new_lens, block_table=block_table,
-              free_blocks=free_blocks, num_free=num_free, slot_map=slot_map,
-              cu_seq_lens_q=cu_seq_lens_q, cu_seq_lens_k=cu_seq_lens_k, seqlens_k=seqlens_k,
-              num_free_out=num_free_out, dev_err=dev_err)
+    if not _fits(index, torch.int32, cache_seqlens, new_lens, block_table, free_blocks, num_free,
+                 slot_map, cu_seq_lens_q, cu_seq_lens_k, seqlens_k, num_free_out, dev_err):
+        _refuse(index, torch.int32, cache_seqlens=cache_seqlens, new_lens=new_lens,
+                block_table=block_table, free_blocks=free_blocks, num_free=num_free,
+                slot_map=slot_map, cu_seq_lens_q=cu_seq_lens_q, cu_seq_lens_k=cu_seq_lens_k,
+                seqlens_k=seqlens_k, num_free_out=num_free_out, dev_err=dev_err)
     if cache_seqlens.shape != (b,) or new_lens.shape != (b,) or seqlens_k.shape != (b,) or \
             cu_seq_lens_q.shape != (b + 1,) or cu_seq_lens_k.shape != (b + 1,) or \
             free_blocks.dim() != 1 or slot_map.dim() != 1 or num_free.numel() != 1 or \
             num_free_out.numel() != 1:
         raise ValueError("inconsistent shapes")
-    with _On(dev, stream) as st:
-        rc = load().pa_block_tables(
-            cache_seqlens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
-            free_blocks.data_ptr(), num_free.data_ptr(), slot_map.data_ptr(),
-            cu_seq_lens_q.data_ptr(), cu_seq_lens_k.data_ptr(), seqlens_k.data_ptr(),
-            num_free_out.data_ptr(), b, slot_map.shape[0], free_blocks.shape[0], block_size, mb,
-            None if dev_err is None else dev_err.data_ptr(), st)
-    _call("pa_block_tables", rc)
+    _launch("pa_block_tables", index, stream, cache_seqlens.data_ptr(), new_lens.data_ptr(),
+            block_table.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(),
+            slot_map.data_ptr(), cu_seq_lens_q.data_ptr(), cu_seq_lens_k.data_ptr(),
+            seqlens_k.data_ptr(), num_free_out.data_ptr(), b, slot_map.numel(),
+            free_blocks.numel(), block_size, mb, _addr(dev_err))
     return cu_seq_lens_q, cu_seq_lens_k, seqlens_k

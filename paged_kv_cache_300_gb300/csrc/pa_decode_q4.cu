@@ -209,6 +209,14 @@ struct QWords<float, N> {
     }
 };
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // CTA whose range holds cost position pos.
 __device__ __forceinline__ int cta_of(long long pos, int P, long long Ctot)
 {
@@ -669,16 +677,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
         const uint32_t dst = smem_u32(ring + at * STAGE);
         const int e = ld.e;
         if (e < ld.elim) { // SB whole blocks inside a segment
-            const uint8_t *base = reinterpret_cast<const uint8_t *>(ld.base);
-            const int p = ld.window[e + (lane & (SB - 1))];
-            __syncwarp();
-            if (lane == 0) {
+            if (elect_one()) {
+                const uint8_t *base = reinterpret_cast<const uint8_t *>(ld.base);
                 meta[at].cnt = ST;
                 mbar_arrive_expect_tx(&full[at], SB * REC);
+#pragma unroll
+                for (int k = 0; k < SB; ++k)
+                    bulk_load(dst + k * REC, base + (size_t)ld.window[e + k] * block_bytes, REC, &full[at]);
                 ld.e = e + SB;
             }
             __syncwarp();
-            if (lane < SB) bulk_load(dst + lane * REC, base + (size_t)p * block_bytes, REC, &full[at]);
         } else {
             L::issue(a, ld, dst, &full[at], &meta[at], tw, ct, hs, ch);
         }
