@@ -345,7 +345,8 @@ int pa_cache_gather_q4(const void *kv_cache, const int32_t *block_table,
  * Left as they were where the sequence's append was refused.
  * block_table, cache_seqlens, workspace, device errors, placement and the
  * limits num_heads / num_kv_heads <= 8, batch * num_kv_heads <= 262144 as
- * pa_decode; every pointer is device memory.  A key or value row that is NaN
+ * pa_decode, and batch * max_blocks_per_seq * num_kv_heads < 2^31; every
+ * pointer is device memory.  Elements of q above 2^115 may overflow.  A key or value row that is NaN
  * makes the outputs it reaches NaN, as the formula does.
  */
 size_t pa_decode_q4_workspace_size(int batch, int num_heads, int num_kv_heads, int head_dim,

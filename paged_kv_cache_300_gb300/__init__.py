@@ -405,16 +405,22 @@ def _q4_geometry(kv_cache, num_kv_heads, head_dim):
     return kv_cache.get_device(), nb, record // (head_dim + 8)
 
 
+# The current stream's handle; torch.cuda.current_stream() makes an object for
+# it first, which takes longer (3 us) than the launch.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(name, index, stream, *args):
     """Call the library with the tensors' device current, on `stream` (default:
     that device's current stream)."""
     fn = getattr(_lib or load(), name)
-    cur = torch.cuda.current_device()
-    if cur == index:
-        rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    handle = _current_raw_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, handle)
     else:
         with torch.cuda.device(index):
-            rc = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+            rc = fn(*args, handle)
     if rc != 0:
         raise PAError(name, rc)
 
@@ -506,7 +512,7 @@ def _q4_workspace(index, stream, sizes):
         ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
         ws[:4 * sizes[0] * sizes[2]].zero_()
         return ws
-    handle = (torch.cuda.current_stream(index) if stream is None else stream).cuda_stream
+    handle = _current_raw_stream(index) if stream is None else stream.cuda_stream
     ws = _q4_workspaces.get((index, handle))
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.stream(stream):  # None: the current stream

@@ -116,6 +116,8 @@ int pa_decode_q4(const void *q, void *kv_cache, const int32_t *block_table,
     if (num_heads % num_kv_heads != 0) return PA_ERR_SHAPE;
     if (num_heads / num_kv_heads > 8 || (long long)batch * num_kv_heads * 4 > (long long)kTicketRegionBytes)
         return PA_ERR_UNSUPPORTED;
+    // positions of the work's split are 32-bit numbers
+    if ((long long)batch * max_blocks_per_seq >= (1ll << 31) / num_kv_heads) return PA_ERR_UNSUPPORTED;
     if (batch == 0) return PA_OK;
     if (!q || !kv_cache || !block_table || !cache_seqlens || !k_new || !v_new || !out) return PA_ERR_NULL;
     if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) ||

@@ -27,9 +27,9 @@
 //  * q is scaled by a power of two per head into f16's range (a bf16 number
 //    keeps all its bits); fp32 operands run as a sum of two f16 numbers.
 //  * p s is rounded to f16 (half a step 2^-11; the sum of p is not rounded).
-//    Its reference m is a running maximum of x + log2(s), so that p s, not p,
-//    is at most 2^14; it moves only when p s would pass that, which leaves
-//    28 bits below the largest term before f16 loses bits of a weight.
+//    Its reference m follows the maximum of x + log2(s), so that p s, not p, is
+//    at most 2^14; it moves only when p s would pass that, which leaves 23 bits
+//    or more below the largest term before f16 loses bits of a weight.
 //
 // Work.  HBM-bound on (D + 8) / 2D bytes an element.  One stage is 32 or 64
 // tokens of one kv head: up to four records, each one bulk copy.  A CTA has up
@@ -50,12 +50,12 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxWarps = 8;
-// Largest log2 of a weight p s before the reference moves, and where it is
-// put then.
-constexpr float kWeightMax = 14.f, kWeightNew = 9.f;
-// Steps below 2^-80 count as 2^-80 in the reference: p stays below 2^94, its
-// sums inside fp32.
-constexpr float kStepFloor = 8.271806125530277e-25f;
+// Largest weight p s before the reference moves (2^14), and the log2 of the
+// largest one after it has moved.
+constexpr float kWeightMax = 16384.f, kWeightNew = 9.f;
+// Steps below 2^-80 count as 2^-80 in the reference, and p stays below 2^94:
+// its sums stay inside fp32.
+constexpr float kStepFloor = 8.271806125530277e-25f, kProbMax = 1.9807040628566084e28f;
 
 enum { kLast = 1, kAppend = 2, kBad = 4, kWhole = 8 };
 
@@ -86,6 +86,7 @@ struct DecodeQ4Geom {
     int head_groups, nst;
     int slot_floats;     // floats of one partial
     int min_tokens;      // of a CTA's range
+    int seq_tokens;      // cost of a sequence
 };
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
@@ -217,11 +218,27 @@ __device__ __forceinline__ bool elect_one()
     return ok != 0;
 }
 
-// CTA whose range holds cost position pos.
-__device__ __forceinline__ int cta_of(long long pos, int P, long long Ctot)
-{
-    return (int)(((pos + 1) * P - 1) / Ctot);
-}
+// The work's split.  Blocks stand in the order (head group, sequence, logical
+// block), every sequence with cs positions of its own before them: what its
+// start and end cost a CTA, in blocks (see kSeqTokens).  The positions are cut
+// into P equal ranges.
+struct Split {
+    uint32_t q, r; // positions of a range, and the rest spread over the first ones
+    int P;
+    float inv;     // ranges a position
+    __device__ __forceinline__ Split(uint32_t total, int P_)
+        : q(total / (uint32_t)P_), r(total % (uint32_t)P_), P(P_), inv((float)P_ / (float)total)
+    {
+    }
+    __device__ __forceinline__ uint32_t start(int c) const { return c * q + c * r / (uint32_t)P; }
+    __device__ __forceinline__ int range_of(uint32_t pos) const
+    {
+        int c = min(P - 1, (int)((float)pos * inv));
+        while (start(c) > pos) --c;
+        while (c + 1 < P && start(c + 1) <= pos) ++c;
+        return c;
+    }
+};
 
 // Blocks of a sequence with L cached tokens and its new one (1 where the
 // length is refused).
@@ -233,90 +250,48 @@ __device__ __forceinline__ int seq_blocks(int L, long long cap, int bs, bool *ok
 
 // A CTA's range holds at least this many tokens of its heads: below that,
 // more CTAs cost more in partials than they save.
-constexpr int kMinTokens = 256;
+constexpr int kMinTokens = 128;
+// What the start and end of a sequence cost a warp, in tokens of its head.
+constexpr int kSeqTokens = 128;
 // Parts of a sequence that its last CTA joins, at most (see make_plan).
 constexpr int kMaxParts = 16;
 
-template <typename T>
-__device__ __forceinline__ void store4(T *p, float a, float b, float c, float d);
-template <>
-__device__ __forceinline__ void store4<float>(float *p, float a, float b, float c, float d)
-{
-    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
-}
-template <>
-__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, float a, float b, float c, float d)
-{
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
-}
-
-// Quantises one row held as EPL values a lane (dims lane*EPL ..) by a whole
-// warp; returns the lane's codes, 4 bits each.
-template <int EPL>
-__device__ __forceinline__ uint32_t quantise_row(const float (&x)[EPL], Q4Scale &s)
-{
-    float lo = INFINITY, hi = -INFINITY;
-    bool finite = true;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        finite = finite && fabsf(x[i]) < INFINITY;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
-    }
-    s = q4_scale(lo, hi, __all_sync(kFull, finite));
-    uint32_t c = 0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) c |= q4_code(x[i], s) << (4 * i);
-    return c;
-}
-
-// Quantise the new token's rows of kv head kvh, write them into the pool and
-// into the staged record (token t of the record at `rec`).
+// Quantise the new token's rows of kv head kvh, K in the lower half-warp and V
+// in the upper one, and write them into the pool and into the staged record
+// (token t of the record at `rec`).
 template <int D, int BS, typename T>
 __device__ __noinline__ void append(const DecodeQ4Args &a, int b, int kvh, int L, int t, uint8_t *rec)
 {
-    constexpr int EPL = D / 32;
-    const int lane = threadIdx.x & 31;
-    const size_t src = ((size_t)b * a.num_kv_heads + kvh) * D + lane * EPL;
-    float k[EPL], v[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        k[i] = to_f32<T>(static_cast<const T *>(a.k_new)[src + i]);
-        v[i] = to_f32<T>(static_cast<const T *>(a.v_new)[src + i]);
-    }
-    Q4Scale ks, vs;
-    const uint32_t kc = quantise_row<EPL>(k, ks), vc = quantise_row<EPL>(v, vs);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        if (a.k_stored)
-            static_cast<T *>(a.k_stored)[src + i] = from_f32<T>(q4_value((kc >> (4 * i)) & 15u, ks.step, ks.low));
-        if (a.v_stored)
-            static_cast<T *>(a.v_stored)[src + i] = from_f32<T>(q4_value((vc >> (4 * i)) & 15u, vs.step, vs.low));
-    }
-    uint32_t kw = kc, vw = vc;
-    if (EPL == 2) { // 4 dims in the even lanes
-        kw |= __shfl_down_sync(kFull, kc, 1) << 8;
-        vw |= __shfl_down_sync(kFull, vc, 1) << 8;
-    }
+    constexpr int EPL = D / 16;
+    const int lane = threadIdx.x & 31, l = lane & 15;
+    const bool value = lane >= 16;
+    const size_t src = ((size_t)b * a.num_kv_heads + kvh) * D + l * EPL;
+    float x[EPL];
+    load_row<EPL>(x, static_cast<const T *>(value ? a.v_new : a.k_new) + src);
     const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks_per_seq + L / BS);
+    Q4Scale s;
+    const uint32_t c = q4_half_warp<EPL>(x, s);
+    if (T *kept = static_cast<T *>(value ? a.v_stored : a.k_stored)) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4)
+            store4(kept + src + i, q4_value((c >> (4 * i)) & 15u, s.step, s.low),
+                   q4_value((c >> (4 * i + 4)) & 15u, s.step, s.low), q4_value((c >> (4 * i + 8)) & 15u, s.step, s.low),
+                   q4_value((c >> (4 * i + 12)) & 15u, s.step, s.low));
+    }
     uint8_t *dst = static_cast<uint8_t *>(a.kv_cache) +
                    ((size_t)blk * a.num_kv_heads + kvh) * q4_record_bytes(D, BS);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
         uint8_t *p = side ? dst : rec;
-        if (EPL == 4 || (lane & 1) == 0) {
-            const int unit = EPL == 4 ? lane : lane >> 1;
-            reinterpret_cast<uint16_t *>(p)[t * (D / 4) + unit] = (uint16_t)kw;
-            reinterpret_cast<uint16_t *>(p + q4_v_offset(D, BS))[q4_v_unit<D>(t, unit)] = (uint16_t)vw;
+#pragma unroll
+        for (int h = 0; h < EPL / 4; ++h) { // 16-bit units of four dims
+            const int unit = l * (EPL / 4) + h;
+            uint16_t *at = value ? reinterpret_cast<uint16_t *>(p + q4_v_offset(D, BS)) + q4_v_unit<D>(t, unit)
+                                 : reinterpret_cast<uint16_t *>(p) + t * (D / 4) + unit;
+            *at = (uint16_t)(c >> (16 * h));
         }
-        if (lane == 0)
-            *reinterpret_cast<uint2 *>(p + q4_scale_offset(D, BS) + t * 8) =
-                make_uint2(q4_pack_scale(ks), q4_pack_scale(vs));
+        if (l == 0)
+            *reinterpret_cast<uint32_t *>(p + q4_scale_offset(D, BS) + t * 8 + (value ? 4 : 0)) = q4_pack_scale(s);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -330,7 +305,7 @@ __device__ __noinline__ void append(const DecodeQ4Args &a, int b, int kvh, int L
 template <int D, typename T, int NE>
 __device__ __noinline__ void fold(const float *first, size_t step, int nseg, int group, int thread, int threads, T *out)
 {
-    constexpr int KU = NE >= 8 ? 1 : NE >= 4 ? 2 : 4;
+    constexpr int KU = NE >= 8 ? 2 : 4;
 #pragma unroll 1
     for (int e0 = thread; e0 < group * (D / 4); e0 += threads * NE) {
         float M[NE], l[NE];
@@ -379,9 +354,9 @@ __device__ __noinline__ void fold(const float *first, size_t step, int nseg, int
             if (e >= group * (D / 4)) break;
             const float inv = 1.f / l[n];
             if (refused)
-                store4<T>(out + e * 4, 0.f, 0.f, 0.f, 0.f);
+                store4(out + e * 4, 0.f, 0.f, 0.f, 0.f);
             else
-                store4<T>(out + e * 4, o[n].x * inv, o[n].y * inv, o[n].z * inv, o[n].w * inv);
+                store4(out + e * 4, o[n].x * inv, o[n].y * inv, o[n].z * inv, o[n].w * inv);
         }
     }
 }
@@ -570,9 +545,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     constexpr int XT = NTILE / R;                   // tiles whose scores a lane works on
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_warp[kMaxWarps];
-    __shared__ int s_total, s_len;
-    __shared__ long long s_start[2];
-    __shared__ long long s_u[2];
+    __shared__ int s_total;
+    __shared__ int s_first[4];  // first sequence, blocks before it, its length, the next one's
+    __shared__ uint32_t s_u[2]; // first and one-past-last block of the range
     __shared__ float s_m[kMaxWarps][8], s_l[kMaxWarps][8], s_b[kMaxWarps][8];
     __shared__ int s_last[kMaxWarps];
     __shared__ uint64_t s_group[kMaxWarps];
@@ -629,39 +604,52 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
         if (lane == ncw - 1) s_total = inc;
     }
     __syncthreads();
-    const long long ublk = s_total;
-    const long long U = ublk * gm.head_groups;
-    const int P = (int)max(1ll, min((long long)gridDim.x, U / (gm.min_tokens / BS)));
+    const uint32_t ublk = s_total, U = ublk * gm.head_groups;
+    // ranges: one a CTA, as many as the work fills (a sequence of a head group
+    // at least), and the same number for every head group
+    int P = min((int)gridDim.x, max((int)(U / (uint32_t)(gm.min_tokens / BS)), B * gm.head_groups));
+    if (P > gm.head_groups) P = P / gm.head_groups * gm.head_groups;
     if ((int)blockIdx.x >= P) return;
+    const uint32_t cs = min((uint32_t)(gm.seq_tokens * tw / BS), U / (uint32_t)P / 4);
+    const uint32_t cblk = ublk + cs * B; // positions of a head group
+    const Split split(cblk * gm.head_groups, P);
     {
-        const long long sbt = (long long)s_warp[warp] + incl - local; // units before b_lo
+        // first block at or after the range's first position, and after its last
+        const uint32_t sbt = s_warp[warp] + incl - local; // blocks before b_lo
+        const uint32_t sct = sbt + cs * b_lo, span = local + cs * (b_hi - b_lo);
+#pragma unroll 1
         for (int e = 0; e < 2; ++e) {
-            const long long cc = (long long)(blockIdx.x + e) * U / P;
-            if (cc >= U) {
+            const uint32_t cc = split.start(blockIdx.x + e);
+            if ((int)blockIdx.x + e == P) {
                 if (tid == 0) s_u[e] = U;
                 continue;
             }
-            const long long r = cc % ublk;
-            if (r < sbt || r >= sbt + local) continue;
-            s_u[e] = cc;
-            if (e == 0) {
-                long long sb = sbt;
-                for (int b = b_lo; b < b_hi; ++b) {
-                    bool ok;
-                    const int n = seq_blocks(__ldg(a.cache_seqlens + b), cap, BS, &ok);
-                    if (r < sb + n) {
-                        s_start[0] = b;
-                        s_start[1] = sb;
-                        s_len = __ldg(a.cache_seqlens + b);
-                        break;
+            const uint32_t h = cc / cblk, r = cc % cblk;
+            if (r < sct || r >= sct + span) continue;
+            uint32_t sb = sbt, sc = sct;
+            for (int b = b_lo; b < b_hi; ++b) {
+                bool ok;
+                const int len = __ldg(a.cache_seqlens + b);
+                const int n = seq_blocks(len, cap, BS, &ok);
+                if (r < sc + cs + n) {
+                    const uint32_t j = r < sc + cs ? 0 : r - sc - cs;
+                    s_u[e] = h * ublk + sb + j;
+                    if (e == 0) {
+                        s_first[0] = b;
+                        s_first[1] = sb;
+                        s_first[2] = len;
+                        s_first[3] = __ldg(a.cache_seqlens + (b + 1 < B ? b + 1 : 0));
                     }
-                    sb += n;
+                    break;
                 }
+                sb += n;
+                sc += cs + n;
             }
         }
     }
     __syncthreads();
-    const long long u0 = s_u[0], u1 = s_u[1];
+    const uint32_t u0 = s_u[0], u1 = s_u[1];
+    if (u0 >= u1) return;
     const int G = a.group, Hkv = a.num_kv_heads, Hq = a.num_heads;
 
     const int ct = warp / hs, ch = warp % hs; // token share, head within the group
@@ -692,13 +680,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
         }
     };
     {
-        const int b = (int)s_start[0], hg = (int)(u0 / ublk), j0 = (int)(u0 % ublk - s_start[1]);
+        const int b = s_first[0], hg = (int)(u0 / ublk), j0 = (int)(u0 % ublk) - s_first[1];
         if (lane == 0) {
-            copy4_async(&ld.len2, a.cache_seqlens + (b + 1 < B ? b + 1 : 0));
+            ld.len2 = s_first[3];
             ld.e = ld.elim = ld.wsel = 0;
         }
-        copy_async_wait();
-        L::enter(a, ld, b, hg, s_len, j0, (int)(u1 - u0), (int)s_start[1], tw, ct, hg * hs + ch);
+        __syncwarp();
+        L::enter(a, ld, b, hg, s_first[2], j0, (int)(u1 - u0), s_first[1], tw, ct, hg * hs + ch);
         L::fetch(a, ld, 0, b, ld.ok, j0, ld.je, 0, tw, ct);
         L::warm(a, b, hg * hs + ch, ld.je == ld.nblk);
         L::fetch_next(a, ld, tw, ct, hs, ch);
@@ -738,10 +726,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     int left = (int)(u1 - u0); // units whose segments have not ended here
 
     while (left > 0) { // segments
-        bool bad = false;
+        bool bad = false, fresh; // fresh: no reference yet
         int at = warp * nst + stage;
         { // q's loads run beside the first stage's copies
-            m0 = m1 = -INFINITY;
+            m0 = m1 = 0.f;
+            fresh = true;
             l0 = l1 = lo0 = lo1 = 0.f;
             // q of column r's head, the dims of this lane's words
             const int g = r % CW;
@@ -856,7 +845,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
             }
             // ---- scores of the lane's tokens r, r + 8 of its tiles
             float x[XT][4], vst[XT][2], vlo[XT][2];
-            float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
             for (int t = 0; t < XT; ++t) {
                 const int tile = R == 1 ? t : rep;
@@ -872,11 +860,11 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                     if constexpr (F32) {
                         // around the middle code, where the two terms do not cancel
                         const float mid = fmaf(ks, 7.5f, kl);
-                        x[t][2 * k] = fmaf(ks * c0, dot[t][2 * k] - h0, mid * qs0);
-                        x[t][2 * k + 1] = fmaf(ks * c1, dot[t][2 * k + 1] - h1, mid * qs1);
+                        x[t][2 * k] = fmaf(ks * c0, dot[t][2 * k] - h0, fmaf(mid, qs0, -m0));
+                        x[t][2 * k + 1] = fmaf(ks * c1, dot[t][2 * k + 1] - h1, fmaf(mid, qs1, -m1));
                     } else {
-                        x[t][2 * k] = fmaf(ks * c0, dot[t][2 * k], kl * qs0);
-                        x[t][2 * k + 1] = fmaf(ks * c1, dot[t][2 * k + 1], kl * qs1);
+                        x[t][2 * k] = fmaf(ks * c0, dot[t][2 * k], fmaf(kl, qs0, -m0));
+                        x[t][2 * k + 1] = fmaf(ks * c1, dot[t][2 * k + 1], fmaf(kl, qs1, -m1));
                     }
                 }
             }
@@ -890,26 +878,44 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                             vst[t][k] = vlo[t][k] = 0.f;
                         }
             }
+            // ---- weights p and p s; the reference moves where one of them
+            // would leave its range
+            float p[XT][4], w[XT][4];
+            float top_w = 0.f, top_p = 0.f;
+            auto weigh = [&] {
 #pragma unroll
-            for (int t = 0; t < XT; ++t)
+                for (int t = 0; t < XT; ++t)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float lv = log2_approx(fmaxf(vst[t][k], kStepFloor));
-                    t0 = fmaxf(t0, x[t][2 * k] + lv);
-                    t1 = fmaxf(t1, x[t][2 * k + 1] + lv);
-                }
-            // ---- move the reference where a weight would leave its range
-            if (__any_sync(kFull, t0 > m0 + kWeightMax || t1 > m1 + kWeightMax)) {
+                    for (int k = 0; k < 4; ++k) {
+                        p[t][k] = exp2_approx(x[t][k]);
+                        w[t][k] = p[t][k] * vst[t][k >> 1];
+                        top_p = fmaxf(top_p, p[t][k]);
+                        top_w = fmaxf(top_w, w[t][k]);
+                    }
+            };
+            weigh();
+            if (__any_sync(kFull, top_w > kWeightMax || top_p > kProbMax) || fresh) {
+                float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < XT; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float lv = log2_approx(fmaxf(vst[t][k], kStepFloor));
+                        t0 = fmaxf(t0, x[t][2 * k] + lv);
+                        t1 = fmaxf(t1, x[t][2 * k + 1] + lv);
+                    }
 #pragma unroll
                 for (int o = R == 4 ? 1 : R == 2 ? 2 : 4; o < 32; o <<= 1) {
                     t0 = fmaxf(t0, __shfl_xor_sync(kFull, t0, o));
                     t1 = fmaxf(t1, __shfl_xor_sync(kFull, t1, o));
                 }
-                const float n0 = fmaxf(m0, t0 - kWeightNew), n1 = fmaxf(m1, t1 - kWeightNew);
-                const float f0 = n0 == -INFINITY ? 1.f : exp2_approx(m0 - n0);
-                const float f1 = n1 == -INFINITY ? 1.f : exp2_approx(m1 - n1);
-                m0 = n0;
-                m1 = n1;
+                // by how much; a column without a number keeps its reference
+                const float s0 = t0 == -INFINITY ? 0.f : fresh ? t0 - kWeightNew : fmaxf(0.f, t0 - kWeightNew);
+                const float s1 = t1 == -INFINITY ? 0.f : fresh ? t1 - kWeightNew : fmaxf(0.f, t1 - kWeightNew);
+                const float f0 = fresh ? 0.f : exp2_approx(-s0), f1 = fresh ? 0.f : exp2_approx(-s1);
+                fresh = false;
+                m0 += s0;
+                m1 += s1;
                 l0 *= f0;
                 l1 *= f1;
                 lo0 *= f0;
@@ -921,23 +927,30 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                     acc[i][2] *= f0;
                     acc[i][3] *= f1;
                 }
+#pragma unroll
+                for (int t = 0; t < XT; ++t)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        x[t][2 * k] -= s0;
+                        x[t][2 * k + 1] -= s1;
+                    }
+                weigh();
             }
-            // ---- weights, as the values' B operand
+            // ---- their sums, and the values' B operand
             uint32_t wh[XT][2], wl[F32 ? XT : 1][2];
 #pragma unroll
             for (int t = 0; t < XT; ++t)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float p0 = exp2_approx(x[t][2 * k] - m0), p1 = exp2_approx(x[t][2 * k + 1] - m1);
-                    l0 += p0;
-                    l1 += p1;
-                    lo0 = fmaf(p0, vlo[t][k], lo0);
-                    lo1 = fmaf(p1, vlo[t][k], lo1);
-                    const float w0 = p0 * vst[t][k], w1 = p1 * vst[t][k];
-                    const uint32_t w = pack_f16(w0, w1);
-                    wh[t][k] = movmatrix_trans(w ^ odd_sign);
+                    l0 += p[t][2 * k];
+                    l1 += p[t][2 * k + 1];
+                    lo0 = fmaf(p[t][2 * k], vlo[t][k], lo0);
+                    lo1 = fmaf(p[t][2 * k + 1], vlo[t][k], lo1);
+                    const float w0 = w[t][2 * k], w1 = w[t][2 * k + 1];
+                    const uint32_t pk = pack_f16(w0, w1);
+                    wh[t][k] = movmatrix_trans(pk ^ odd_sign);
                     if constexpr (F32) {
-                        const __half2 h = *reinterpret_cast<const __half2 *>(&w);
+                        const __half2 h = *reinterpret_cast<const __half2 *>(&pk);
                         wl[t][k] = movmatrix_trans(pack_f16(w0 - __low2float(h), w1 - __high2float(h)) ^ odd_sign);
                     }
                 }
@@ -1005,7 +1018,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
 
         // ================= end of this CTA's share of the sequence =================
         const int kvh = mt.hg * hs + ch;
-        const long long seg = (long long)mt.hg * ublk + mt.sb; // position of the sequence's first unit
         left -= mt.blocks;
 #pragma unroll
         for (int o = R == 4 ? 1 : R == 2 ? 2 : 4; o < 32; o <<= 1) {
@@ -1014,6 +1026,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
             lo0 += __shfl_xor_sync(kFull, lo0, o);
             lo1 += __shfl_xor_sync(kFull, lo1, o);
         }
+        if (fresh) m0 = m1 = -INFINITY; // no token of the share was summed
         // Codes of odd dims were 2^-20, of even ones 2^-24.  With copies, a
         // lane keeps one of its two columns (R = 4: and half of its dims) and
         // hands the rest to the lane that keeps those.
@@ -1074,9 +1087,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                     if (whole) {
                         T *o = outp + orow + (size_t)g * D + dim0 + k;
                         if (bad)
-                            store4<T>(o, 0.f, 0.f, 0.f, 0.f);
+                            store4(o, 0.f, 0.f, 0.f, 0.f);
                         else
-                            store4<T>(o, y0 * inv, y1 * inv, y2 * inv, y3 * inv);
+                            store4(o, y0 * inv, y1 * inv, y2 * inv, y3 * inv);
                     } else {
                         *reinterpret_cast<float4 *>(slot + g * D + dim0 + k) = make_float4(y0, y1, y2, y3);
                     }
@@ -1137,9 +1150,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                 if (whole) {
                     const float inv = 1.f / l;
                     if (refused)
-                        store4<T>(outp + orow + (size_t)g * D + d, 0.f, 0.f, 0.f, 0.f);
+                        store4(outp + orow + (size_t)g * D + d, 0.f, 0.f, 0.f, 0.f);
                     else
-                        store4<T>(outp + orow + (size_t)g * D + d, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                        store4(outp + orow + (size_t)g * D + d, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
                 } else {
                     *reinterpret_cast<float4 *>(slot + g * D + d) = o;
                     if (d == 0)
@@ -1150,7 +1163,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
         if (!whole) {
             // The partial is ordered before the ticket by the barrier, and
             // the ticket is an acquire-release at GPU scope.
-            const int cfirst = cta_of(seg, P, U), nseg = cta_of(seg + mt.nblk - 1, P, U) - cfirst + 1;
+            const uint32_t pos = mt.hg * cblk + mt.sb + cs * (mt.b + 1); // of the sequence's first block
+            const int cfirst = split.range_of(pos), nseg = split.range_of(pos + mt.nblk - 1) - cfirst + 1;
             if (!sync()) return;
             int32_t *ticket = a.tickets + (size_t)mt.b * Hkv + kvh;
             int last = 0;
@@ -1224,6 +1238,7 @@ int make_plan(int batch, int num_kv_heads, int group, Plan *p)
     p->gm.nst = nst;
     p->gm.slot_floats = group * D + 16;
     p->gm.min_tokens = kMinTokens;
+    p->gm.seq_tokens = kSeqTokens;
     return PA_OK;
 }
 

@@ -68,6 +68,32 @@ __device__ __forceinline__ uint32_t q4_pack_scale(const Q4Scale &s)
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Quantises a row held by 16 neighbouring lanes, EPL = D / 16 values each (two
+// rows a warp): s is the row's scale, the result the lane's codes, 4 bits each.
+template <int EPL>
+__device__ __forceinline__ uint32_t q4_half_warp(const float (&x)[EPL], Q4Scale &s)
+{
+    float lo = x[0], hi = x[0];
+    bool finite = fabsf(x[0]) < INFINITY;
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) {
+        lo = fminf(lo, x[i]);
+        hi = fmaxf(hi, x[i]);
+        finite = finite && fabsf(x[i]) < INFINITY;
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    const unsigned row = 0xffffu << (threadIdx.x & 16);
+    s = q4_scale(lo, hi, (__ballot_sync(0xffffffffu, finite) & row) == row);
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) c |= q4_code(x[i], s) << (4 * i);
+    return c;
+}
+
 template <typename T>
 __device__ __forceinline__ float to_f32(T x);
 template <>
@@ -91,6 +117,53 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x)
 {
     return __float2bfloat16_rn(x);
+}
+
+// N consecutive elements (N a multiple of 4), loaded 16 or 8 bytes at a time.
+template <int N>
+__device__ __forceinline__ void load_row(float (&x)[N], const float *p)
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p + i));
+        x[i] = v.x;
+        x[i + 1] = v.y;
+        x[i + 2] = v.z;
+        x[i + 3] = v.w;
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_row(float (&x)[N], const __nv_bfloat16 *p)
+{
+    uint32_t w[N / 2];
+    if constexpr (N % 8 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+        }
+    } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+        w[0] = v.x;
+        w[1] = v.y;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+// Four consecutive elements, rounded once.
+__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d)
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float a, float b, float c, float d)
+{
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
 }
 
 }  // namespace pa
