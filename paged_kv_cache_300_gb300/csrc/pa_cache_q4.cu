@@ -8,74 +8,91 @@ namespace pa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kThreads = 256;
+constexpr int kMinWarps = 4096; // of an update that has work for them
 
-// One warp per (chunk row, kv head): lane l holds dims l*EPL .. l*EPL+EPL-1
-// of K and of V.
+// ------------------------------------------------------------------ update
+// A warp takes one chunk row, or two where they are neighbours in one token
+// pair of a block, and `heads` of its kv heads: K in the lower half-warp, V in
+// the upper one.  Two tokens of a pair share the words of V, so a pair's V is
+// written as whole words; a lone token writes its halves of them.
 template <int D, typename T>
-__global__ void __launch_bounds__(256) update_q4_kernel(const CacheQ4Args a)
+__global__ void __launch_bounds__(kThreads) update_q4_kernel(const CacheQ4Args a, const int heads, const int bs_shift)
 {
-    constexpr int EPL = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int hkv = a.num_kv_heads, bs = a.block_size;
-    if (w >= (long long)a.total * hkv) return;
-    const long long row = w / hkv;
-    const int h = (int)(w % hkv);
-    const int slot = a.slot_map[row];
+    constexpr int EPL = D / 16;
+    const int lane = threadIdx.x & 31, l = lane & 15;
+    const bool value = lane >= 16;
+    const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    grid_dep_trigger();
+    grid_dep_wait();
+    if (row >= a.total) return;
+    const int slots = a.num_blocks << bs_shift;
+    const int slot = __ldg(a.slot_map + row);
     if (slot < 0) return;
-    if (slot >= (long long)a.num_blocks * bs) {
-        if (lane == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
+    if (slot >= slots) {
+        if (lane == 0 && blockIdx.y == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
         return;
     }
-    uint8_t *rec = static_cast<uint8_t *>(a.kv_cache) +
-                   ((size_t)(slot / bs) * hkv + h) * q4_record_bytes(D, bs);
-    const int t = slot % bs;
-    const T *src[2] = {static_cast<const T *>(a.k), static_cast<const T *>(a.v)};
-    for (int kv = 0; kv < 2; ++kv) {
-        float x[EPL];
-        float lo = INFINITY, hi = -INFINITY;
-        bool finite = true;
+    // the odd token of a pair whose even one stands before it in the chunk
+    if ((slot & 1) && row > 0 && __ldg(a.slot_map + row - 1) == slot - 1) return;
+    const bool two = !(slot & 1) && row + 1 < a.total && __ldg(a.slot_map + row + 1) == slot + 1;
+    const int hkv = a.num_kv_heads, bs = 1 << bs_shift, t = slot & (bs - 1);
+    const int h0 = blockIdx.y * heads, h1 = min(hkv, h0 + heads);
+    const int rec_bytes = q4_record_bytes(D, bs);
+    uint8_t *rec = static_cast<uint8_t *>(a.kv_cache) + ((size_t)(slot >> bs_shift) * hkv + h0) * rec_bytes;
+    const T *src = static_cast<const T *>(value ? a.v : a.k) + ((size_t)row * hkv + h0) * D + l * EPL;
+    const size_t next = (size_t)hkv * D;
+    const int vu = q4_v_offset(D, bs) / 2 + q4_v_unit<D>(t, l * (EPL / 4)); // the lane's first unit of V
+    const int ku = t * (D / 4) + l * (EPL / 4);
+    for (int h = h0; h < h1; ++h, rec += rec_bytes, src += D) {
+        float x[EPL], y[EPL];
+        load_row<EPL>(x, src);
+        if (two) load_row<EPL>(y, src + next);
+        Q4Scale s0, s1;
+        const uint32_t c0 = q4_half_warp<EPL>(x, s0);
+        uint16_t *unit = reinterpret_cast<uint16_t *>(rec) + (value ? vu : ku);
+        uint32_t *scale = reinterpret_cast<uint32_t *>(rec + q4_scale_offset(D, bs) + t * 8 + (value ? 4 : 0));
+        if (l == 0) scale[0] = q4_pack_scale(s0);
+        if (two) {
+            const uint32_t c1 = q4_half_warp<EPL>(y, s1);
+            if (l == 0) scale[2] = q4_pack_scale(s1);
+            if (value) { // even token in the low halves
+                if constexpr (EPL == 8)
+                    *reinterpret_cast<uint2 *>(unit) = make_uint2(__byte_perm(c0, c1, 0x5410), __byte_perm(c0, c1, 0x7632));
+                else
+                    *reinterpret_cast<uint32_t *>(unit) = __byte_perm(c0, c1, 0x5410);
+            } else if constexpr (EPL == 8) {
+                *reinterpret_cast<uint32_t *>(unit) = c0;
+                *reinterpret_cast<uint32_t *>(unit + D / 4) = c1;
+            } else {
+                unit[0] = (uint16_t)c0;
+                unit[D / 4] = (uint16_t)c1;
+            }
+        } else if (value) {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            x[i] = to_f32<T>(src[kv][(row * hkv + h) * D + lane * EPL + i]);
-            lo = fminf(lo, x[i]);
-            hi = fmaxf(hi, x[i]);
-            finite = finite && fabsf(x[i]) < INFINITY;
+            for (int k = 0; k < EPL / 4; ++k) unit[2 * k] = (uint16_t)(c0 >> (16 * k));
+        } else if constexpr (EPL == 8) {
+            *reinterpret_cast<uint32_t *>(unit) = c0;
+        } else {
+            unit[0] = (uint16_t)c0;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
-        }
-        finite = __all_sync(kFull, finite);
-        const Q4Scale s = q4_scale(lo, hi, finite);
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) c |= q4_code(x[i], s) << (4 * i);
-        if (EPL == 2) c |= __shfl_down_sync(kFull, c, 1) << 8; // 4 dims in even lanes
-        if (EPL == 4 || (lane & 1) == 0) {
-            const int unit = EPL == 4 ? lane : lane >> 1;
-            uint16_t *dst = kv == 0 ? reinterpret_cast<uint16_t *>(rec) + t * (D / 4) + unit
-                                    : reinterpret_cast<uint16_t *>(rec + q4_v_offset(D, bs)) +
-                                          q4_v_unit<D>(t, unit);
-            *dst = (uint16_t)c;
-        }
-        if (lane == 0)
-            *reinterpret_cast<uint32_t *>(rec + q4_scale_offset(D, bs) + t * 8 + kv * 4) =
-                q4_pack_scale(s);
     }
 }
 
-// Largest r in [0, n) with cu[r] <= x.
-__device__ __forceinline__ int owner(const int32_t *cu, int n, long long x)
+// ------------------------------------------------------------------ gather
+// Largest r in [0, n) with off(r) <= x, off(r) = cu[r] / bs + r (never
+// decreasing), by the whole warp: 32 probes a step.
+__device__ __forceinline__ int tile_owner(const int32_t *cu, int n, int x, int bs_shift)
 {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(cu + mid) <= x)
-            lo = mid;
-        else
-            hi = mid;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = n; // the answer is in [lo, lo + len)
+    while (len > 1) {
+        const int step = (len + 31) / 32, r = lo + lane * step;
+        const bool below = lane * step < len && (__ldg(cu + r) >> bs_shift) + r <= x;
+        const int last = 31 - __clz((int)(__ballot_sync(kFull, below) | 1u));
+        const int end = lo + len;
+        lo += last * step;
+        len = min(step, end - lo);
     }
     return lo;
 }
@@ -90,65 +107,115 @@ __device__ __forceinline__ void check_cu(const CacheQ4Args &a)
     if (bad) flag_error(a.dev_err, PA_DEVERR_BAD_CU);
 }
 
-// One warp per (packed row, kv head).
-template <int D, typename T>
-__global__ void __launch_bounds__(256) gather_q4_kernel(const CacheQ4Args a)
+// Eight codes of 4 bits as fp32 values, rounded once.
+__device__ __forceinline__ void unpack8(float (&v)[8], uint32_t c, float step, float low)
 {
-    constexpr int EPL = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int hkv = a.num_kv_heads, bs = a.block_size;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) // 2^23 + n, made of bits, less 2^23
+        v[i] = fmaf(__uint_as_float(((c >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.f, step, low);
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8])
+{
+    __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
+{
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                    pack_bf16(v[6], v[7])));
+}
+
+// A CTA takes one block of one request: tile i belongs to the last request r
+// with cu[r] / bs + r <= i (every request has at least as many tiles as
+// blocks).  A thread turns 8 dims of a token pair of one head, K and V, into
+// four stores of 8 values; neighbours in dims, then heads, are neighbours in
+// the packed rows.
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads) gather_q4_kernel(const CacheQ4Args a, const int bs_shift)
+{
+    constexpr int I = D / 8;
+    grid_dep_trigger();
+    grid_dep_wait();
     if (blockIdx.x == 0) check_cu(a);
-    if (w >= (long long)a.total * hkv) return;
-    const int row = (int)(w / hkv), h = (int)(w % hkv);
-    const int b = owner(a.cu_k, a.batch, row);
-    const int k0 = __ldg(a.cu_k + b), k1 = __ldg(a.cu_k + b + 1);
-    if (k0 < 0 || row < k0 || row >= k1) return; // behind the last row, or flagged by check_cu
-    const int pos = row - k0, lb = pos / bs, t = pos % bs;
+    const int bs = 1 << bs_shift, hkv = a.num_kv_heads;
+    const int b = tile_owner(a.cu_k, a.batch, blockIdx.x, bs_shift);
+    const int k0 = __ldg(a.cu_k + b), k1 = min(__ldg(a.cu_k + b + 1), a.total);
+    const int lb = (int)blockIdx.x - (k0 >> bs_shift) - b;
+    if (k0 < 0 || lb < 0 || (long long)lb << bs_shift >= k1 - k0) return; // no tile, or flagged by check_cu
+    const int pos0 = lb << bs_shift, rows = min(bs, k1 - k0 - pos0);
     int blk = -1;
     if (lb >= a.max_blocks_per_seq) {
-        if (lane == 0) flag_error(a.dev_err, PA_DEVERR_OVERFLOW);
+        if (threadIdx.x == 0) flag_error(a.dev_err, PA_DEVERR_OVERFLOW);
     } else {
         blk = __ldg(a.block_table + (size_t)b * a.max_blocks_per_seq + lb);
         if (blk < 0 || blk >= a.num_blocks) {
-            if (lane == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
+            if (threadIdx.x == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
             blk = -1;
         }
     }
-    const uint8_t *rec = static_cast<const uint8_t *>(a.kv_cache) +
-                         ((size_t)(blk < 0 ? 0 : blk) * hkv + h) * q4_record_bytes(D, bs);
-    T *dst[2] = {static_cast<T *>(a.k_full), static_cast<T *>(a.v_full)};
-    for (int kv = 0; kv < 2; ++kv) {
-        T *o = dst[kv] + ((size_t)row * hkv + h) * D + lane * EPL;
-        uint32_t c = 0;
-        float step = 0.f, low = 0.f;
+    const int rec_bytes = q4_record_bytes(D, bs);
+    const uint8_t *base = static_cast<const uint8_t *>(a.kv_cache) + (size_t)(blk < 0 ? 0 : blk) * hkv * rec_bytes;
+    const size_t row_elts = (size_t)hkv * D;
+    const size_t out0 = (size_t)(k0 + pos0) * row_elts;
+    T *ko = static_cast<T *>(a.k_full) + out0, *vo = static_cast<T *>(a.v_full) + out0;
+    const int items = ((rows + 1) >> 1) * hkv * I;
+#pragma unroll 2
+    for (int e = threadIdx.x; e < items; e += kThreads) {
+        const int i = e % I, hp = e / I, h = hp % hkv, p = hp / hkv;
+        uint32_t kc[2] = {0u, 0u};
+        uint2 vw = make_uint2(0u, 0u);
+        uint4 sc = make_uint4(0u, 0u, 0u, 0u);
         if (blk >= 0) {
-            const int unit = lane * EPL / 4;
-            const uint16_t *p = kv == 0 ? reinterpret_cast<const uint16_t *>(rec) + t * (D / 4) + unit
-                                        : reinterpret_cast<const uint16_t *>(rec + q4_v_offset(D, bs)) +
-                                              q4_v_unit<D>(t, unit);
-            c = *p;
-            if (EPL == 2) c >>= 8 * (lane & 1);
-            const uint32_t s = *reinterpret_cast<const uint32_t *>(rec + q4_scale_offset(D, bs) +
-                                                                   t * 8 + kv * 4);
-            step = bf16_lo(s);
-            low = bf16_hi(s);
+            const uint8_t *rec = base + (size_t)h * rec_bytes;
+            const uint32_t *kr = reinterpret_cast<const uint32_t *>(rec) + 2 * p * I + i;
+            kc[0] = __ldg(kr);
+            kc[1] = __ldg(kr + I);
+            vw = __ldg(reinterpret_cast<const uint2 *>(rec + q4_v_offset(D, bs) + 2 * q4_v_unit<D>(2 * p, 2 * i)));
+            sc = __ldg(reinterpret_cast<const uint4 *>(rec + q4_scale_offset(D, bs) + p * 16));
         }
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) o[i] = from_f32<T>(q4_value((c >> (4 * i)) & 15u, step, low));
+        const size_t o = (size_t)(2 * p) * row_elts + h * D + i * 8;
+        float v[8];
+        unpack8(v, kc[0], bf16_lo(sc.x), bf16_hi(sc.x));
+        store8(ko + o, v);
+        unpack8(v, __byte_perm(vw.x, vw.y, 0x5410), bf16_lo(sc.y), bf16_hi(sc.y));
+        store8(vo + o, v);
+        if (2 * p + 1 < rows) {
+            unpack8(v, kc[1], bf16_lo(sc.z), bf16_hi(sc.z));
+            store8(ko + o + row_elts, v);
+            unpack8(v, __byte_perm(vw.x, vw.y, 0x7632), bf16_lo(sc.w), bf16_hi(sc.w));
+            store8(vo + o + row_elts, v);
+        }
     }
+}
+
+// Launches that may start while the kernel before them ends; they wait for it
+// before they read anything.
+template <typename... A>
+int launch_after(void (*kernel)(A...), dim3 grid, cudaStream_t s, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
 }
 
 template <int D, typename T>
 int launch(const CacheQ4Args &a, bool gather, cudaStream_t s)
 {
-    const long long warps = (long long)a.total * a.num_kv_heads;
-    const unsigned grid = (unsigned)((warps + 7) / 8);
-    if (gather)
-        gather_q4_kernel<D, T><<<grid, 256, 0, s>>>(a);
-    else
-        update_q4_kernel<D, T><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
+    const int shift = a.block_size == 32 ? 5 : 4;
+    if (gather) return launch_after(gather_q4_kernel<D, T>, dim3((a.total >> shift) + a.batch), s, a, shift);
+    // heads of a warp: few rows are spread over more warps
+    const int hkv = a.num_kv_heads;
+    int heads = (int)min((long long)hkv, max(1ll, (long long)a.total * hkv / kMinWarps));
+    if (hkv / heads > 65535) heads = (hkv + 65534) / 65535;
+    const unsigned gx = ((unsigned)a.total + kThreads / 32 - 1) / (kThreads / 32);
+    return launch_after(update_q4_kernel<D, T>, dim3(gx, (hkv + heads - 1) / heads), s, a, heads, shift);
 }
 
 }  // namespace

@@ -49,13 +49,6 @@ __device__ __forceinline__ Q4Scale q4_scale(float lo, float hi, bool finite)
     }
     return r;
 }
-// Code of x; x is finite or the row is NaN (inv16 = 0, and the comparison
-// below turns a NaN product into code 0).
-__device__ __forceinline__ uint32_t q4_code(float x, const Q4Scale &s)
-{
-    const float n = rintf(__fmul_rn(__fsub_rn(__fmul_rn(x, 0.0625f), s.low16), s.inv16));
-    return n > 0.f ? (uint32_t)fminf(n, 15.f) : 0u;
-}
 __device__ __forceinline__ float q4_value(uint32_t n, float step, float low)
 {
     return fmaf((float)n, step, low); // n * step is exact
@@ -88,10 +81,17 @@ __device__ __forceinline__ uint32_t q4_half_warp(const float (&x)[EPL], Q4Scale 
     }
     const unsigned row = 0xffffu << (threadIdx.x & 16);
     s = q4_scale(lo, hi, (__ballot_sync(0xffffffffu, finite) & row) == row);
+    // n = round-half-even((x / 16 - b / 16) * (16 / s)), which lies in 0..15: the
+    // sum with 2^23 rounds it into the low bits.  x / 16 is exact, so the first
+    // step is one rounding as a fused operation too; the product is not fused.
+    // The sums of the bits leave out 0x4b000000 (the bits of 2^23) at every
+    // step; only the first two places keep something of it.
     uint32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) c |= q4_code(x[i], s) << (4 * i);
-    return c;
+    for (int i = EPL - 1; i >= 0; --i)
+        c = c * 16u + __float_as_uint(__fadd_rn(__fmul_rn(fmaf(x[i], 0.0625f, -s.low16), s.inv16), 8388608.f));
+    c -= 0xfb000000u;
+    return s.inv16 > 0.f ? (EPL == 8 ? c : c & 0xffffu) : 0u;
 }
 
 template <typename T>

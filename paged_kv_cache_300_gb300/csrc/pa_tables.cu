@@ -2,7 +2,14 @@
 // lengths from the requests' lengths (include/pa.h states the rules).
 //
 // Everything follows from four prefix sums over the requests: new tokens,
-// blocks taken, blocks given back, lengths after the step.
+// blocks taken, blocks given back, lengths after the step.  The bytes are few
+// (4 a slot, 20 a request); what a call costs is latency.  So one launch does
+// it all: a cluster of CTAs in which each makes all the sums for itself (no
+// traffic between CTAs), then takes its share of the requests and of the
+// slots.  Two cluster barriers order the rest: given-back blocks are on the
+// stack before a block is taken from it, and lengths and the stack's size,
+// which may be written in place, are read by everybody before.  A small step
+// is one CTA (kClusterSlots).
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
@@ -11,135 +18,177 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 1024;
+constexpr int kCluster = 8;
+// From this many slots on the step is a cluster's work.
+constexpr int kClusterSlots = 4096;
+constexpr int kRun = 8; // neighbouring slots of a thread
 
-// What one request adds to the four sums.
+// What requests add to the four sums.
 struct Need {
     long long tok, take, back, after;
+    __device__ __forceinline__ void add(const Need &o)
+    {
+        tok += o.tok;
+        take += o.take;
+        back += o.back;
+        after += o.after;
+    }
 };
 
-__device__ __forceinline__ Need need_of(const TablesArgs &a, int b, int &err)
+__device__ __forceinline__ int ceil_div(int x, int d) { return x / d + (x % d != 0); }
+
+__device__ __forceinline__ Need need_of(const TablesArgs &a, int L, int n, int &err)
 {
-    const int L = a.cache_seqlens[b], n = a.new_lens[b], bs = a.block_size;
+    const int bs = a.block_size;
     Need r{0, 0, 0, 0};
-    if (L < 0 || n < -1 || (long long)L + (n > 0 ? n : 0) > (long long)a.max_blocks_per_seq * bs) {
+    if (L < 0 || n < -1 || (long long)L + max(n, 0) > (long long)a.max_blocks_per_seq * bs) {
         err |= PA_DEVERR_OVERFLOW;
         return r;
     }
-    const long long held = ((long long)L + bs - 1) / bs;
+    const int held = ceil_div(L, bs);
     if (n < 0) {
         r.back = held;
     } else {
         r.tok = n;
-        r.after = (long long)L + n;
-        r.take = (r.after + bs - 1) / bs - held;
+        r.after = L + n; // at most max_blocks_per_seq * block_size < 2^31
+        r.take = ceil_div(L + n, bs) - held;
     }
     return r;
 }
 
-// Inclusive sum of x over the block; *total is the block's sum.
-__device__ __forceinline__ long long block_scan(long long x, long long *s_warp, long long *total)
+__device__ __forceinline__ void cluster_sync(bool cluster)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(kFull, x, o);
-        if (lane >= o) x += t;
+    if (cluster) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
     }
-    __syncthreads();
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        long long w = s_warp[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(kFull, w, o);
-            if (lane >= o) w += t;
-        }
-        s_warp[lane] = w;
-    }
-    __syncthreads();
-    *total = s_warp[kThreads / 32 - 1];
-    return x + (warp > 0 ? s_warp[warp - 1] : 0);
 }
 
 __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a)
 {
-    extern __shared__ int s_off[]; // [B + 1] new tokens before a request, [B] blocks taken before it
-    __shared__ long long s_warp[kThreads / 32];
+    extern __shared__ int s_dyn[];
+    __shared__ Need s_warp[kThreads / 32];
     __shared__ int s_err;
-    const int tid = threadIdx.x, B = a.batch, bs = a.block_size;
-    int *s_cu = s_off, *s_take = s_off + B + 1;
-    if (tid == 0) s_err = 0;
-    __syncthreads();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.batch, bs = a.block_size;
+    const int ncta = gridDim.x, cta = blockIdx.x;
+    const bool cluster = ncta > 1;
+    int *s_cu = s_dyn;             // [B + 1] new tokens before a request
+    int *s_take = s_dyn + B + 1;   // [B] blocks taken before it
+    int *s_len = s_dyn + 2 * B + 1; // [B] its length
+    if (tid == 0) {
+        s_err = 0;
+        s_cu[0] = 0;
+    }
+    grid_dep_trigger();
+    grid_dep_wait();
     const int F = *a.num_free;
     int err = F < 0 || F > a.num_blocks ? PA_DEVERR_BAD_BLOCK : 0;
-    long long tok = 0, take = 0, back = 0, after = 0;
-    // ---- sums, and the offsets that need nothing else
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
-        const int b = b0 + tid;
-        const Need r = b < B ? need_of(a, b, err) : Need{0, 0, 0, 0};
-        long long t0, t1, t2, t3;
-        const long long x0 = tok + block_scan(r.tok, s_warp, &t0);
-        const long long x1 = take + block_scan(r.take, s_warp, &t1);
-        block_scan(r.back, s_warp, &t2);
-        block_scan(r.after, s_warp, &t3);
-        if (b < B) {
-            s_cu[b + 1] = (int)x0;
-            s_take[b] = (int)(x1 - r.take);
-        }
-        tok += t0;
-        take += t1;
-        back += t2;
-        after += t3;
+
+    // ---- the sums: a thread's run of requests, then over the threads
+    const int per = (B + kThreads - 1) / kThreads;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    Need mine{0, 0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+        const int L = a.cache_seqlens[b];
+        s_len[b] = L;
+        mine.add(need_of(a, L, a.new_lens[b], err));
     }
-    if (tid == 0) s_cu[0] = 0;
-    if (after > 0x7fffffffll || tok > 0x7fffffffll) err |= PA_DEVERR_BAD_CU;
-    if (tok > a.total_slots || take > F + back) err |= PA_DEVERR_NO_SPACE;
-    if (F + back > a.num_blocks) err |= PA_DEVERR_BAD_BLOCK;
+    Need incl = mine;
+    auto warp_scan = [&](Need &x) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Need t{__shfl_up_sync(kFull, x.tok, o), __shfl_up_sync(kFull, x.take, o),
+                         __shfl_up_sync(kFull, x.back, o), __shfl_up_sync(kFull, x.after, o)};
+            if (lane >= o) x.add(t);
+        }
+    };
+    warp_scan(incl);
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        Need w = s_warp[lane];
+        warp_scan(w);
+        s_warp[lane] = w;
+    }
     if (err) atomicOr(&s_err, err);
     __syncthreads();
-    const bool refused = s_err != 0;
-    if (refused) {
-        if (tid == 0) {
-            flag_error(a.dev_err, s_err);
-            a.cu_q[0] = a.cu_k[0] = 0;
-            *a.num_free_out = F;
+    const Need all = s_warp[kThreads / 32 - 1];
+    if (warp > 0) incl.add(s_warp[warp - 1]);
+    err = s_err;
+    if (all.after > 0x7fffffffll || all.tok > 0x7fffffffll) err |= PA_DEVERR_BAD_CU;
+    if (all.tok > a.total_slots || all.take > F + all.back) err |= PA_DEVERR_NO_SPACE;
+    if (F + all.back > a.num_blocks) err |= PA_DEVERR_BAD_BLOCK;
+    if (err) { // the same in every CTA: nothing changes
+        cluster_sync(cluster);
+        if (cta == 0) {
+            if (tid == 0) {
+                flag_error(a.dev_err, err);
+                a.cu_q[0] = a.cu_k[0] = 0;
+                *a.num_free_out = F;
+            }
+            for (int b = tid; b < B; b += kThreads) {
+                a.cu_q[b + 1] = a.cu_k[b + 1] = 0;
+                a.seqlens_k[b] = s_len[b];
+            }
         }
-        for (int b = tid; b < B; b += kThreads) {
-            a.cu_q[b + 1] = a.cu_k[b + 1] = 0;
-            a.seqlens_k[b] = a.cache_seqlens[b];
-        }
-        for (int i = tid; i < a.total_slots; i += kThreads) a.slot_map[i] = -1;
+        for (int i = cta * kThreads + tid; i < a.total_slots; i += ncta * kThreads) a.slot_map[i] = -1;
         return;
     }
-    // ---- ended requests push their blocks
-    const int warp = tid >> 5, lane = tid & 31;
+
+    // ---- offsets; ended requests push their blocks
     int flags = 0;
-    if (back > 0) {
-        long long base = F;
-        for (int b0 = 0; b0 < B; b0 += kThreads) {
-            const int b = b0 + tid;
-            int e = 0;
-            const Need r = b < B ? need_of(a, b, e) : Need{0, 0, 0, 0};
-            long long t;
-            const long long x = base + block_scan(r.back, s_warp, &t) - r.back;
-            for (int j = 0; j < r.back; ++j) {
-                int p = a.block_table[(size_t)b * a.max_blocks_per_seq + j];
-                if (p < 0 || p >= a.num_blocks) {
-                    p = -1;
-                    flags |= PA_DEVERR_BAD_BLOCK;
+    {
+        Need at = incl; // sums before the thread's run
+        at.tok -= mine.tok;
+        at.take -= mine.take;
+        at.back -= mine.back;
+        at.after -= mine.after;
+        for (int k = 0; k < per; ++k) { // the same count in every lane
+            const int b = b0 + k;
+            const bool in = b < b1;
+            const Need r = in ? need_of(a, s_len[b], a.new_lens[b], err) : Need{0, 0, 0, 0};
+            // the warp's ended requests, one after the other, 32 blocks at a time
+            unsigned ended = __ballot_sync(kFull, r.back > 0 && b % ncta == cta);
+            while (ended) {
+                const int who = __ffs(ended) - 1;
+                ended &= ended - 1;
+                const int n = __shfl_sync(kFull, (int)r.back, who), q = __shfl_sync(kFull, b, who);
+                const int to = F + __shfl_sync(kFull, (int)at.back, who);
+                const int32_t *row = a.block_table + (size_t)q * a.max_blocks_per_seq;
+#pragma unroll 4
+                for (int j = lane; j < n; j += 32) {
+                    int p = __ldg(row + j);
+                    if (p < 0 || p >= a.num_blocks) {
+                        p = -1;
+                        flags |= PA_DEVERR_BAD_BLOCK;
+                    }
+                    a.free_blocks[to + j] = p;
                 }
-                a.free_blocks[x + j] = p;
             }
-            base += t;
+            if (in) {
+                s_take[b] = (int)at.take;
+                at.add(r);
+                s_cu[b + 1] = (int)at.tok;
+                if (b % ncta == cta) {
+                    a.cu_q[b + 1] = (int)at.tok;
+                    a.cu_k[b + 1] = (int)at.after;
+                }
+            }
         }
     }
-    __syncthreads();
-    // ---- slots and new table entries, token by token
-    const long long top = F + back;
-    for (int i = tid; i < a.total_slots; i += kThreads) {
-        int slot = -1;
-        if (i < tok) {
+    cluster_sync(cluster);
+
+    // ---- slots and new table entries, runs of kRun slots a thread
+    const int top = (int)(F + all.back), tok = (int)all.tok;
+    for (long long i0 = ((long long)cta * kThreads + tid) * kRun; i0 < a.total_slots;
+         i0 += (long long)ncta * kThreads * kRun) {
+        int slot[kRun];
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) slot[k] = -1;
+        if (i0 < tok) {
+            const int i = (int)i0;
             int lo = 0, hi = B; // the request with s_cu[lo] <= i < s_cu[lo + 1]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
@@ -148,41 +197,61 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a)
                 else
                     hi = mid;
             }
-            const int b = lo, L = a.cache_seqlens[b];
-            const int pos = L + (i - s_cu[b]), lb = pos / bs;
-            const int held = (int)(((long long)L + bs - 1) / bs);
-            int32_t *entry = a.block_table + (size_t)b * a.max_blocks_per_seq + lb;
-            int p = lb < held ? *entry : a.free_blocks[top - 1 - (s_take[b] + lb - held)];
-            if (p < 0 || p >= a.num_blocks) {
-                p = -1;
-                flags |= PA_DEVERR_BAD_BLOCK;
+            int b = lo - 1, end = i, lb = 0, off = 0, held = 0, take = 0, p = -1;
+            int32_t *row = nullptr;
+            bool entry = false;
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) {
+                if (i + k >= tok) break;
+                if (i + k == end) { // the next request with new tokens
+                    do ++b;
+                    while (s_cu[b + 1] <= i + k);
+                    end = s_cu[b + 1];
+                    const int L = s_len[b], pos = L + (i + k - s_cu[b]);
+                    lb = pos / bs;
+                    off = pos - lb * bs;
+                    held = ceil_div(L, bs);
+                    take = s_take[b];
+                    row = a.block_table + (size_t)b * a.max_blocks_per_seq;
+                    entry = true;
+                } else if (++off == bs) {
+                    off = 0;
+                    ++lb;
+                    entry = true;
+                }
+                if (entry) {
+                    entry = false;
+                    p = lb < held ? row[lb] : a.free_blocks[top - 1 - (take + lb - held)];
+                    if (p < 0 || p >= a.num_blocks) {
+                        p = -1;
+                        flags |= PA_DEVERR_BAD_BLOCK;
+                    }
+                }
+                if (off == 0 && lb >= held) row[lb] = p;
+                if (p >= 0) slot[k] = p * bs + off;
             }
-            if (lb >= held && pos % bs == 0) *entry = p;
-            if (p >= 0) slot = p * bs + pos % bs;
         }
-        a.slot_map[i] = slot;
+        int32_t *dst = a.slot_map + i0;
+        if (i0 + kRun <= a.total_slots && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+            reinterpret_cast<int4 *>(dst)[0] = make_int4(slot[0], slot[1], slot[2], slot[3]);
+            reinterpret_cast<int4 *>(dst)[1] = make_int4(slot[4], slot[5], slot[6], slot[7]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kRun; ++k)
+                if (i0 + k < a.total_slots) dst[k] = slot[k];
+        }
     }
     if (flags) flag_error(a.dev_err, flags);
-    __syncthreads(); // lengths may be rewritten in place from here on
-    long long sum = 0;
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
-        const int b = b0 + tid;
-        int e = 0;
-        const Need r = b < B ? need_of(a, b, e) : Need{0, 0, 0, 0};
-        long long t;
-        const long long x = sum + block_scan(r.after, s_warp, &t);
-        if (b < B) {
-            a.cu_q[b + 1] = s_cu[b + 1];
-            a.cu_k[b + 1] = (int)x;
-            a.seqlens_k[b] = (int)r.after;
-        }
-        sum += t;
+    // ---- what may be written in place: everybody has read it before the
+    // last barrier (lengths and new_lens above it, the stack's size first)
+    for (int b = cta * kThreads + tid; b < B; b += ncta * kThreads) {
+        const int n = s_cu[b + 1] - s_cu[b];
+        // an ended request's length is 0: its slice of cu_k is empty
+        a.seqlens_k[b] = a.new_lens[b] < 0 ? 0 : s_len[b] + n;
     }
-    (void)warp;
-    (void)lane;
-    if (tid == 0) {
+    if (cta == 0 && tid == 0) {
         a.cu_q[0] = a.cu_k[0] = 0;
-        *a.num_free_out = (int)(top - take);
+        *a.num_free_out = (int)(top - all.take);
     }
 }
 
@@ -190,12 +259,32 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a)
 
 int tables_launch(const TablesArgs &a, cudaStream_t s)
 {
-    const int smem = (2 * a.batch + 1) * 4;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return PA_ERR_LAUNCH;
-    tables_kernel<<<1, kThreads, smem, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
+    const size_t smem = (size_t)(3 * a.batch + 1) * 4;
+    static int raised[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_DEVICE;
+    if (smem > 48 * 1024 && !__atomic_load_n(&raised[dev], __ATOMIC_ACQUIRE)) {
+        if (cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (3 * kTablesMaxBatch + 1) * 4) != cudaSuccess)
+            return PA_ERR_LAUNCH;
+        __atomic_store_n(&raised[dev], 1, __ATOMIC_RELEASE);
+    }
+    cudaLaunchConfig_t cfg = {};
+    const int ctas = a.total_slots >= kClusterSlots ? kCluster : 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, tables_kernel, a) == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
 }
 
 }  // namespace pa
