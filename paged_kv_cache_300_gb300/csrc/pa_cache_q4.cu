@@ -45,16 +45,16 @@ __global__ void __launch_bounds__(kThreads) update_q4_kernel(const CacheQ4Args a
     const int vu = q4_v_offset(D, bs) / 2 + q4_v_unit<D>(t, l * (EPL / 4)); // the lane's first unit of V
     const int ku = t * (D / 4) + l * (EPL / 4);
     for (int h = h0; h < h1; ++h, rec += rec_bytes, src += D) {
-        float x[EPL], y[EPL];
-        load_row<EPL>(x, src);
-        if (two) load_row<EPL>(y, src + next);
+        Q4Row<T, EPL> x, y;
+        x.load(src);
+        if (two) y.load(src + next);
         Q4Scale s0, s1;
-        const uint32_t c0 = q4_half_warp<EPL>(x, s0);
+        const uint32_t c0 = q4_half_warp(x, s0);
         uint16_t *unit = reinterpret_cast<uint16_t *>(rec) + (value ? vu : ku);
         uint32_t *scale = reinterpret_cast<uint32_t *>(rec + q4_scale_offset(D, bs) + t * 8 + (value ? 4 : 0));
         if (l == 0) scale[0] = q4_pack_scale(s0);
         if (two) {
-            const uint32_t c1 = q4_half_warp<EPL>(y, s1);
+            const uint32_t c1 = q4_half_warp(y, s1);
             if (l == 0) scale[2] = q4_pack_scale(s1);
             if (value) { // even token in the low halves
                 if constexpr (EPL == 8)

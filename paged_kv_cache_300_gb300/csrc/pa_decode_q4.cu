@@ -266,11 +266,11 @@ __device__ __noinline__ void append(const DecodeQ4Args &a, int b, int kvh, int L
     const int lane = threadIdx.x & 31, l = lane & 15;
     const bool value = lane >= 16;
     const size_t src = ((size_t)b * a.num_kv_heads + kvh) * D + l * EPL;
-    float x[EPL];
-    load_row<EPL>(x, static_cast<const T *>(value ? a.v_new : a.k_new) + src);
+    Q4Row<T, EPL> x;
+    x.load(static_cast<const T *>(value ? a.v_new : a.k_new) + src);
     const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks_per_seq + L / BS);
     Q4Scale s;
-    const uint32_t c = q4_half_warp<EPL>(x, s);
+    const uint32_t c = q4_half_warp(x, s);
     if (T *kept = static_cast<T *>(value ? a.v_stored : a.k_stored)) {
 #pragma unroll
         for (int i = 0; i < EPL; i += 4)

@@ -61,26 +61,93 @@ __device__ __forceinline__ uint32_t q4_pack_scale(const Q4Scale &s)
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// N values of a row in the type they came in: bf16 stays packed in pairs until
+// a value is needed.
+template <typename T, int N>
+struct Q4Row;
+template <int N>
+struct Q4Row<float, N> {
+    float v[N];
+    __device__ __forceinline__ void load(const float *p)
+    {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(p + i));
+            v[i] = x.x;
+            v[i + 1] = x.y;
+            v[i + 2] = x.z;
+            v[i + 3] = x.w;
+        }
+    }
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+    // extrema over 16 neighbouring lanes; NaN anywhere leaves finite false
+    __device__ __forceinline__ void extrema(float &lo, float &hi, bool &finite) const
+    {
+        lo = hi = v[0];
+        bool ok = fabsf(v[0]) < INFINITY;
+#pragma unroll
+        for (int i = 1; i < N; ++i) {
+            lo = fminf(lo, v[i]);
+            hi = fmaxf(hi, v[i]);
+            ok = ok && fabsf(v[i]) < INFINITY;
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        const unsigned row = 0xffffu << (threadIdx.x & 16);
+        finite = (__ballot_sync(0xffffffffu, ok) & row) == row;
+    }
+};
+template <int N>
+struct Q4Row<__nv_bfloat16, N> {
+    uint32_t w[N / 2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p)
+    {
+        if constexpr (N == 8) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+            w[0] = x.x;
+            w[1] = x.y;
+            w[2] = x.z;
+            w[3] = x.w;
+        } else {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+            w[0] = x.x;
+            w[1] = x.y;
+        }
+    }
+    __device__ __forceinline__ float get(int i) const { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
+    // pairs at a time; then (max x, max -x) travel as one pair.  max with
+    // NaN is NaN here.
+    __device__ __forceinline__ void extrema(float &lo, float &hi, bool &finite) const
+    {
+        auto bf = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
+        auto un = [](__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t *>(&h); };
+        uint32_t a = w[0], b = w[0] ^ 0x80008000u;
+#pragma unroll
+        for (int i = 1; i < N / 2; ++i) {
+            a = un(__hmax2_nan(bf(a), bf(w[i])));
+            b = un(__hmax2_nan(bf(b), bf(w[i] ^ 0x80008000u)));
+        }
+        uint32_t m = un(__hmax2_nan(bf(__byte_perm(a, b, 0x5410)), bf(__byte_perm(a, b, 0x7632))));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = un(__hmax2_nan(bf(m), bf(__shfl_xor_sync(0xffffffffu, m, o))));
+        hi = bf16_lo(m);
+        lo = -bf16_hi(m);
+        finite = fabsf(hi) < INFINITY && fabsf(lo) < INFINITY; // false for NaN
+    }
+};
+
 // Quantises a row held by 16 neighbouring lanes, EPL = D / 16 values each (two
 // rows a warp): s is the row's scale, the result the lane's codes, 4 bits each.
-template <int EPL>
-__device__ __forceinline__ uint32_t q4_half_warp(const float (&x)[EPL], Q4Scale &s)
+template <typename T, int EPL>
+__device__ __forceinline__ uint32_t q4_half_warp(const Q4Row<T, EPL> &x, Q4Scale &s)
 {
-    float lo = x[0], hi = x[0];
-    bool finite = fabsf(x[0]) < INFINITY;
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        finite = finite && fabsf(x[i]) < INFINITY;
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    const unsigned row = 0xffffu << (threadIdx.x & 16);
-    s = q4_scale(lo, hi, (__ballot_sync(0xffffffffu, finite) & row) == row);
+    float lo, hi;
+    bool finite;
+    x.extrema(lo, hi, finite);
+    s = q4_scale(lo, hi, finite);
     // n = round-half-even((x / 16 - b / 16) * (16 / s)), which lies in 0..15: the
     // sum with 2^23 rounds it into the low bits.  x / 16 is exact, so the first
     // step is one rounding as a fused operation too; the product is not fused.
@@ -89,7 +156,7 @@ __device__ __forceinline__ uint32_t q4_half_warp(const float (&x)[EPL], Q4Scale 
     uint32_t c = 0;
 #pragma unroll
     for (int i = EPL - 1; i >= 0; --i)
-        c = c * 16u + __float_as_uint(__fadd_rn(__fmul_rn(fmaf(x[i], 0.0625f, -s.low16), s.inv16), 8388608.f));
+        c = c * 16u + __float_as_uint(__fadd_rn(__fmul_rn(fmaf(x.get(i), 0.0625f, -s.low16), s.inv16), 8388608.f));
     c -= 0xfb000000u;
     return s.inv16 > 0.f ? (EPL == 8 ? c : c & 0xffffu) : 0u;
 }
@@ -119,43 +186,6 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x)
     return __float2bfloat16_rn(x);
 }
 
-// N consecutive elements (N a multiple of 4), loaded 16 or 8 bytes at a time.
-template <int N>
-__device__ __forceinline__ void load_row(float (&x)[N], const float *p)
-{
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p + i));
-        x[i] = v.x;
-        x[i + 1] = v.y;
-        x[i + 2] = v.z;
-        x[i + 3] = v.w;
-    }
-}
-template <int N>
-__device__ __forceinline__ void load_row(float (&x)[N], const __nv_bfloat16 *p)
-{
-    uint32_t w[N / 2];
-    if constexpr (N % 8 == 0) {
-#pragma unroll
-        for (int i = 0; i < N / 8; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-            w[4 * i] = v.x;
-            w[4 * i + 1] = v.y;
-            w[4 * i + 2] = v.z;
-            w[4 * i + 3] = v.w;
-        }
-    } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-        w[0] = v.x;
-        w[1] = v.y;
-    }
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
 // Four consecutive elements, rounded once.
 __device__ __forceinline__ void store4(float *p, float a, float b, float c, float d)
 {

@@ -18,9 +18,9 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 1024;
-constexpr int kCluster = 8;
-// From this many slots on the step is a cluster's work.
-constexpr int kClusterSlots = 4096;
+// From this many slots on the step is a cluster's work, 8 CTAs (the portable
+// size) or 16.
+constexpr int kClusterSlots = 4096, kLargeSlots = 65536;
 constexpr int kRun = 8; // neighbouring slots of a thread
 
 // What requests add to the four sums.
@@ -35,7 +35,16 @@ struct Need {
     }
 };
 
-__device__ __forceinline__ int ceil_div(int x, int d) { return x / d + (x % d != 0); }
+// x / block_size for x >= 0: a shift for the usual sizes.
+__device__ __forceinline__ int div_bs(const TablesArgs &a, int x)
+{
+    return a.shift >= 0 ? x >> a.shift : x / a.block_size;
+}
+__device__ __forceinline__ int ceil_bs(const TablesArgs &a, int x)
+{
+    const int q = div_bs(a, x);
+    return q + (q * a.block_size != x);
+}
 
 __device__ __forceinline__ Need need_of(const TablesArgs &a, int L, int n, int &err)
 {
@@ -45,13 +54,13 @@ __device__ __forceinline__ Need need_of(const TablesArgs &a, int L, int n, int &
         err |= PA_DEVERR_OVERFLOW;
         return r;
     }
-    const int held = ceil_div(L, bs);
+    const int held = ceil_bs(a, L);
     if (n < 0) {
         r.back = held;
     } else {
         r.tok = n;
         r.after = L + n; // at most max_blocks_per_seq * block_size < 2^31
-        r.take = ceil_div(L + n, bs) - held;
+        r.take = ceil_bs(a, L + n) - held;
     }
     return r;
 }
@@ -180,59 +189,50 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a)
     }
     cluster_sync(cluster);
 
-    // ---- slots and new table entries, runs of kRun slots a thread
+    // ---- slots and new table entries
     const int top = (int)(F + all.back), tok = (int)all.tok;
-    for (long long i0 = ((long long)cta * kThreads + tid) * kRun; i0 < a.total_slots;
-         i0 += (long long)ncta * kThreads * kRun) {
+    const bool tall = (long long)tok >= 16ll * B; // many tokens a request: runs, else single slots
+    const int run = tall ? kRun : 1;
+    for (long long i0 = ((long long)cta * kThreads + tid) * run; i0 < a.total_slots;
+         i0 += (long long)ncta * kThreads * run) {
         int slot[kRun];
 #pragma unroll
         for (int k = 0; k < kRun; ++k) slot[k] = -1;
         if (i0 < tok) {
-            const int i = (int)i0;
-            int lo = 0, hi = B; // the request with s_cu[lo] <= i < s_cu[lo + 1]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
+            const int i = (int)i0, n = min(run, tok - i);
+            int b = 0, hi = B; // the request with s_cu[b] <= i < s_cu[b + 1]
+            while (hi - b > 1) {
+                const int mid = (b + hi) >> 1;
                 if (s_cu[mid] <= i)
-                    lo = mid;
+                    b = mid;
                 else
                     hi = mid;
             }
-            int b = lo - 1, end = i, lb = 0, off = 0, held = 0, take = 0, p = -1;
-            int32_t *row = nullptr;
-            bool entry = false;
+            // one piece after the other that lies in one block of one request
+            for (int k = 0; k < n;) {
+                const int L = s_len[b], pos = L + (i + k - s_cu[b]);
+                const int lb = div_bs(a, pos), off = pos - lb * bs, held = ceil_bs(a, L);
+                int32_t *entry = a.block_table + (size_t)b * a.max_blocks_per_seq + lb;
+                int p = __ldcg(lb < held ? entry : a.free_blocks + (top - 1 - (s_take[b] + lb - held)));
+                if (p < 0 || p >= a.num_blocks) {
+                    p = -1;
+                    flags |= PA_DEVERR_BAD_BLOCK;
+                }
+                if (off == 0 && lb >= held) *entry = p;
+                const int m = min(min(n - k, bs - off), s_cu[b + 1] - (i + k));
+                const int base = p * bs + off - k;
 #pragma unroll
-            for (int k = 0; k < kRun; ++k) {
-                if (i + k >= tok) break;
-                if (i + k == end) { // the next request with new tokens
-                    do ++b;
-                    while (s_cu[b + 1] <= i + k);
-                    end = s_cu[b + 1];
-                    const int L = s_len[b], pos = L + (i + k - s_cu[b]);
-                    lb = pos / bs;
-                    off = pos - lb * bs;
-                    held = ceil_div(L, bs);
-                    take = s_take[b];
-                    row = a.block_table + (size_t)b * a.max_blocks_per_seq;
-                    entry = true;
-                } else if (++off == bs) {
-                    off = 0;
-                    ++lb;
-                    entry = true;
-                }
-                if (entry) {
-                    entry = false;
-                    p = lb < held ? row[lb] : a.free_blocks[top - 1 - (take + lb - held)];
-                    if (p < 0 || p >= a.num_blocks) {
-                        p = -1;
-                        flags |= PA_DEVERR_BAD_BLOCK;
-                    }
-                }
-                if (off == 0 && lb >= held) row[lb] = p;
-                if (p >= 0) slot[k] = p * bs + off;
+                for (int q = 0; q < kRun; ++q)
+                    if (q >= k && q < k + m && p >= 0) slot[q] = base + q;
+                k += m;
+                if (k < n)
+                    while (s_cu[b + 1] <= i + k) ++b; // past requests without new tokens
             }
         }
         int32_t *dst = a.slot_map + i0;
-        if (i0 + kRun <= a.total_slots && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
+        if (!tall) {
+            *dst = slot[0];
+        } else if (i0 + kRun <= a.total_slots && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
             reinterpret_cast<int4 *>(dst)[0] = make_int4(slot[0], slot[1], slot[2], slot[3]);
             reinterpret_cast<int4 *>(dst)[1] = make_int4(slot[4], slot[5], slot[6], slot[7]);
         } else {
@@ -257,20 +257,25 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a)
 
 }  // namespace
 
-int tables_launch(const TablesArgs &a, cudaStream_t s)
+int tables_launch(const TablesArgs &args, cudaStream_t s)
 {
-    const size_t smem = (size_t)(3 * a.batch + 1) * 4;
+    const size_t smem = (size_t)(3 * args.batch + 1) * 4;
+    TablesArgs a = args;
+    a.shift = -1;
+    for (int k = 0; k < 31; ++k)
+        if (a.block_size == 1 << k) a.shift = k;
     static int raised[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_DEVICE;
-    if (smem > 48 * 1024 && !__atomic_load_n(&raised[dev], __ATOMIC_ACQUIRE)) {
+    if (!__atomic_load_n(&raised[dev], __ATOMIC_ACQUIRE)) {
         if (cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (3 * kTablesMaxBatch + 1) * 4) != cudaSuccess)
+                                 (3 * kTablesMaxBatch + 1) * 4) != cudaSuccess ||
+            cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return PA_ERR_LAUNCH;
         __atomic_store_n(&raised[dev], 1, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg = {};
-    const int ctas = a.total_slots >= kClusterSlots ? kCluster : 1;
+    const int ctas = a.total_slots >= kLargeSlots ? 16 : a.total_slots >= kClusterSlots ? 8 : 1;
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
