@@ -12,69 +12,89 @@ constexpr int kThreads = 256;
 constexpr int kMinWarps = 4096; // of an update that has work for them
 
 // ------------------------------------------------------------------ update
-// A warp takes one chunk row, or two where they are neighbours in one token
-// pair of a block, and `heads` of its kv heads: K in the lower half-warp, V in
-// the upper one.  Two tokens of a pair share the words of V, so a pair's V is
-// written as whole words; a lone token writes its halves of them.
+// A CTA looks at kRows chunk rows.  A warp takes one of them, or two where they
+// are neighbours in one token pair of a block, and `heads` of its kv heads: K
+// in the lower half-warp, V in the upper one.  Two tokens of a pair share the
+// words of V, so a pair's V is written as whole words; a lone token writes its
+// halves of them.  The next head's rows are on their way while one is worked on.
+constexpr int kRows = 16;
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) update_q4_kernel(const CacheQ4Args a, const int heads, const int bs_shift)
 {
     constexpr int EPL = D / 16;
     const int lane = threadIdx.x & 31, l = lane & 15;
     const bool value = lane >= 16;
-    const int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     grid_dep_trigger();
     grid_dep_wait();
-    if (row >= a.total) return;
-    const int slots = a.num_blocks << bs_shift;
-    const int slot = __ldg(a.slot_map + row);
-    if (slot < 0) return;
-    if (slot >= slots) {
-        if (lane == 0 && blockIdx.y == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
-        return;
-    }
-    // the odd token of a pair whose even one stands before it in the chunk
-    if ((slot & 1) && row > 0 && __ldg(a.slot_map + row - 1) == slot - 1) return;
-    const bool two = !(slot & 1) && row + 1 < a.total && __ldg(a.slot_map + row + 1) == slot + 1;
-    const int hkv = a.num_kv_heads, bs = 1 << bs_shift, t = slot & (bs - 1);
-    const int h0 = blockIdx.y * heads, h1 = min(hkv, h0 + heads);
+    // Rows that lead: all but the odd token of a pair whose even one stands
+    // before it in the chunk, and padding.
+    const int row0 = blockIdx.x * kRows, mine = row0 + l;
+    const int slot_l = mine < a.total ? __ldg(a.slot_map + mine) : -1;
+    const int before = mine > 0 && mine < a.total ? __ldg(a.slot_map + mine - 1) : -1;
+    const int after = mine + 1 < a.total ? __ldg(a.slot_map + mine + 1) : -1;
+    const bool inside = slot_l < a.num_blocks << bs_shift;
+    if (!inside && lane < 16 && threadIdx.x < 32 && blockIdx.y == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
+    const bool leads = slot_l >= 0 && inside && !((slot_l & 1) && before == slot_l - 1);
+    const bool paired = !(slot_l & 1) && after == slot_l + 1;
+    unsigned todo = __ballot_sync(kFull, leads) & 0xffffu;
+    const unsigned pairs = __ballot_sync(kFull, paired);
+    const int hkv = a.num_kv_heads, bs = 1 << bs_shift;
+    const int h0 = blockIdx.y * heads, n = min(hkv, h0 + heads) - h0;
     const int rec_bytes = q4_record_bytes(D, bs);
-    uint8_t *rec = static_cast<uint8_t *>(a.kv_cache) + ((size_t)(slot >> bs_shift) * hkv + h0) * rec_bytes;
-    const T *src = static_cast<const T *>(value ? a.v : a.k) + ((size_t)row * hkv + h0) * D + l * EPL;
     const size_t next = (size_t)hkv * D;
-    const int vu = q4_v_offset(D, bs) / 2 + q4_v_unit<D>(t, l * (EPL / 4)); // the lane's first unit of V
-    const int ku = t * (D / 4) + l * (EPL / 4);
-    for (int h = h0; h < h1; ++h, rec += rec_bytes, src += D) {
+    for (int k = threadIdx.x >> 5;; k += kThreads / 32) {
+        // the warp's k-th leading row
+        const int i = (int)__fns(todo, 0, k + 1);
+        if (i < 0 || i >= kRows) break;
+        const int slot = __shfl_sync(kFull, slot_l, i), t = slot & (bs - 1);
+        const bool two = pairs >> i & 1;
+        uint8_t *rec = static_cast<uint8_t *>(a.kv_cache) + ((size_t)(slot >> bs_shift) * hkv + h0) * rec_bytes;
+        const T *src = static_cast<const T *>(value ? a.v : a.k) + ((size_t)(row0 + i) * hkv + h0) * D + l * EPL;
+        uint16_t *unit = reinterpret_cast<uint16_t *>(rec) +
+                         (value ? q4_v_offset(D, bs) / 2 + q4_v_unit<D>(t, l * (EPL / 4)) // the lane's first unit
+                                : t * (D / 4) + l * (EPL / 4));
+        uint32_t *scale = reinterpret_cast<uint32_t *>(rec + q4_scale_offset(D, bs) + t * 8 + (value ? 4 : 0));
         Q4Row<T, EPL> x, y;
         x.load(src);
         if (two) y.load(src + next);
-        Q4Scale s0, s1;
-        const uint32_t c0 = q4_half_warp(x, s0);
-        uint16_t *unit = reinterpret_cast<uint16_t *>(rec) + (value ? vu : ku);
-        uint32_t *scale = reinterpret_cast<uint32_t *>(rec + q4_scale_offset(D, bs) + t * 8 + (value ? 4 : 0));
-        if (l == 0) scale[0] = q4_pack_scale(s0);
-        if (two) {
-            const uint32_t c1 = q4_half_warp(y, s1);
-            if (l == 0) scale[2] = q4_pack_scale(s1);
-            if (value) { // even token in the low halves
-                if constexpr (EPL == 8)
-                    *reinterpret_cast<uint2 *>(unit) = make_uint2(__byte_perm(c0, c1, 0x5410), __byte_perm(c0, c1, 0x7632));
-                else
-                    *reinterpret_cast<uint32_t *>(unit) = __byte_perm(c0, c1, 0x5410);
+        for (int h = 0; h < n; ++h) {
+            Q4Row<T, EPL> x1, y1;
+            src += D;
+            if (h + 1 < n) {
+                x1.load(src);
+                if (two) y1.load(src + next);
+            }
+            Q4Scale s0, s1;
+            const uint32_t c0 = q4_half_warp(x, s0);
+            if (l == 0) scale[0] = q4_pack_scale(s0);
+            if (two) {
+                const uint32_t c1 = q4_half_warp(y, s1);
+                if (l == 0) scale[2] = q4_pack_scale(s1);
+                if (value) { // even token in the low halves
+                    if constexpr (EPL == 8)
+                        *reinterpret_cast<uint2 *>(unit) =
+                            make_uint2(__byte_perm(c0, c1, 0x5410), __byte_perm(c0, c1, 0x7632));
+                    else
+                        *reinterpret_cast<uint32_t *>(unit) = __byte_perm(c0, c1, 0x5410);
+                } else if constexpr (EPL == 8) {
+                    *reinterpret_cast<uint32_t *>(unit) = c0;
+                    *reinterpret_cast<uint32_t *>(unit + D / 4) = c1;
+                } else {
+                    unit[0] = (uint16_t)c0;
+                    unit[D / 4] = (uint16_t)c1;
+                }
+            } else if (value) {
+#pragma unroll
+                for (int u = 0; u < EPL / 4; ++u) unit[2 * u] = (uint16_t)(c0 >> (16 * u));
             } else if constexpr (EPL == 8) {
                 *reinterpret_cast<uint32_t *>(unit) = c0;
-                *reinterpret_cast<uint32_t *>(unit + D / 4) = c1;
             } else {
                 unit[0] = (uint16_t)c0;
-                unit[D / 4] = (uint16_t)c1;
             }
-        } else if (value) {
-#pragma unroll
-            for (int k = 0; k < EPL / 4; ++k) unit[2 * k] = (uint16_t)(c0 >> (16 * k));
-        } else if constexpr (EPL == 8) {
-            *reinterpret_cast<uint32_t *>(unit) = c0;
-        } else {
-            unit[0] = (uint16_t)c0;
+            x = x1;
+            y = y1;
+            unit += rec_bytes / 2;
+            scale += rec_bytes / 4;
         }
     }
 }
@@ -214,7 +234,7 @@ int launch(const CacheQ4Args &a, bool gather, cudaStream_t s)
     const int hkv = a.num_kv_heads;
     int heads = (int)min((long long)hkv, max(1ll, (long long)a.total * hkv / kMinWarps));
     if (hkv / heads > 65535) heads = (hkv + 65534) / 65535;
-    const unsigned gx = ((unsigned)a.total + kThreads / 32 - 1) / (kThreads / 32);
+    const unsigned gx = ((unsigned)a.total + kRows - 1) / kRows;
     return launch_after(update_q4_kernel<D, T>, dim3(gx, (hkv + heads - 1) / heads), s, a, heads, shift);
 }
 

@@ -33,6 +33,17 @@ __device__ __forceinline__ float bf16_away(float x)
 {
     return __uint_as_float((__float_as_uint(x) + 0xffffu) & 0xffff0000u);
 }
+// 1 / s for a positive bf16 s between 2^-100 and 2^125, correctly rounded: one
+// Newton step with fused operations (Markstein).  The residual e = 1 - s r of
+// an approximation within 2^-22 is exact (s has 8 bits, r has 24), r + r e is
+// off by e^2 <= 2^-44 of it, and 1 / s of an 8-bit s is at least 2^-33 of it
+// away from any rounding border.
+__device__ __forceinline__ float q4_reciprocal(float s)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return fmaf(r, fmaf(-s, r, 1.f), r);
+}
 __device__ __forceinline__ Q4Scale q4_scale(float lo, float hi, bool finite)
 {
     Q4Scale r;
@@ -45,7 +56,7 @@ __device__ __forceinline__ Q4Scale q4_scale(float lo, float hi, bool finite)
         r.inv16 = 0.f;
         r.low16 = 0.f;
     } else {
-        r.inv16 = r.step > 0.f ? __fdiv_rn(16.0f, r.step) : 0.f;
+        r.inv16 = r.step > 0.f ? 16.0f * q4_reciprocal(r.step) : 0.f;
     }
     return r;
 }
