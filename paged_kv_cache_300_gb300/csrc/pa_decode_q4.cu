@@ -53,9 +53,9 @@ constexpr int kMaxWarps = 8;
 // Largest weight p s before the reference moves (2^14), and the log2 of the
 // largest one after it has moved.
 constexpr float kWeightMax = 16384.f, kWeightNew = 9.f;
-// Steps below 2^-80 count as 2^-80 in the reference, and p stays below 2^94:
-// its sums stay inside fp32.
-constexpr float kStepFloor = 8.271806125530277e-25f, kProbMax = 1.9807040628566084e28f;
+// Steps below 2^-80 count as 2^-80 there: p stays below 2^94 and its sums inside
+// fp32.
+constexpr float kStepFloor = 8.271806125530277e-25f;
 
 enum { kLast = 1, kAppend = 2, kBad = 4, kWhole = 8 };
 
@@ -69,8 +69,9 @@ struct alignas(16) Meta {
 // A warp's loader, in shared memory, where it costs the sums no registers.
 // The walk covers the warp's share of every segment: of a sequence's blocks
 // [j0, je) in the CTA's range, the stages ct, ct + tw, ...  Table entries come
-// in windows of 32 of the warp's blocks, the next one (of this segment or of
+// in windows of kWindow of the warp's blocks, the next one (of this segment or of
 // the next) fetched while the present one is used.
+constexpr int kWindow = 64;
 struct alignas(16) LoadState {
     uint64_t base; // the pool's record of the warp's head in block 0
     int e, elim;   // window cursor; stages before elim are SB whole blocks inside the segment
@@ -78,7 +79,7 @@ struct alignas(16) LoadState {
     int b, hg, len, rem; // rem: units of the CTA's range from j0 on
     int sb, li0, lend, wsel; // blocks before b; stage at the window's start; last stage; window in use
     int len1, len2, pad[2];  // lengths of the next sequence and of the one after it
-    int window[64];
+    int window[2 * kWindow];
 };
 
 struct DecodeQ4Geom {
@@ -252,7 +253,7 @@ __device__ __forceinline__ int seq_blocks(int L, long long cap, int bs, bool *ok
 // more CTAs cost more in partials than they save.
 constexpr int kMinTokens = 128;
 // What the start and end of a sequence cost a warp, in tokens of its head.
-constexpr int kSeqTokens = 128;
+constexpr int kSeqTokens = 200;
 // Parts of a sequence that its last CTA joins, at most (see make_plan).
 constexpr int kMaxParts = 16;
 
@@ -381,12 +382,16 @@ struct Loader {
     static __device__ __forceinline__ void fetch(const DecodeQ4Args &a, LoadState &ld, int w, int b, bool ok, int j0,
                                                  int je, int o0, int tw, int ct)
     {
-        const int lane = threadIdx.x & 31, o = o0 + lane;
-        const int blk = j0 + ((o / SB) * tw + ct) * SB + o % SB;
-        if (ok && blk < je)
-            copy4_async(&ld.window[w * 32 + lane], a.block_table + (size_t)b * a.max_blocks_per_seq + blk);
-        else
-            ld.window[w * 32 + lane] = -1;
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int k = lane; k < kWindow; k += 32) {
+            const int o = o0 + k;
+            const int blk = j0 + ((o / SB) * tw + ct) * SB + o % SB;
+            if (ok && blk < je)
+                copy4_async(&ld.window[w * kWindow + k], a.block_table + (size_t)b * a.max_blocks_per_seq + blk);
+            else
+                ld.window[w * kWindow + k] = -1;
+        }
     }
     // q and the new rows of a sequence: in L2 by the time they are read
     static __device__ __forceinline__ void warm(const DecodeQ4Args &a, int b, int kvh, bool ends)
@@ -434,7 +439,7 @@ struct Loader {
     static __device__ __forceinline__ void fetch_next(const DecodeQ4Args &a, LoadState &ld, int tw, int ct, int hs,
                                                       int ch)
     {
-        const int o0 = ld.li0 * SB + 32, j0 = ld.j0, je = ld.je, b = ld.b, rem = ld.rem - (je - j0);
+        const int o0 = ld.li0 * SB + kWindow, j0 = ld.j0, je = ld.je, b = ld.b, rem = ld.rem - (je - j0);
         if (((o0 / SB) * tw + ct) * SB < je - j0) {
             fetch(a, ld, ld.wsel ^ 1, b, ld.ok, j0, je, o0, tw, ct);
         } else if (rem > 0) {
@@ -456,7 +461,7 @@ struct Loader {
         if (rem0 <= 0) return;
         const int j0 = ld.j0, je = ld.je, nblk = ld.nblk, len = ld.len, b = ld.b, hg = ld.hg, sb = ld.sb;
         const bool ok = ld.ok != 0;
-        const int e = ld.e, li = ld.li0 + (e - ld.wsel * 32) / SB, lend = ld.lend;
+        const int e = ld.e, li = ld.li0 + (e - ld.wsel * kWindow) / SB, lend = ld.lend;
         const int blk0 = j0 + (li * tw + ct) * SB;
         const int blocks = max(0, min(SB, je - blk0));
         const int p = ld.window[e + (lane & (SB - 1))];
@@ -497,22 +502,26 @@ struct Loader {
             const int hg1 = wrap ? hg + 1 : hg;
             enter(a, ld, wrap ? 0 : b + 1, hg1, ld.len1, 0, rem, wrap ? 0 : sb + nblk, tw, ct, hg1 * hs + ch);
             switched = true;
-        } else if (((li + 1) * SB & 31) == 0) {
+        } else if (((li + 1) * SB & (kWindow - 1)) == 0) {
             if (lane == 0) ld.li0 = li + 1;
             switched = true;
         }
         const int w = ld.wsel ^ (switched ? 1 : 0);
         __syncwarp();
-        const int first = w * 32, at = switched ? first : e + SB; // the cursor
+        const int first = w * kWindow, at = switched ? first : e + SB; // the cursor
         const int li1 = switched ? ld.li0 : li + 1, li0 = ld.li0;
         if (lane == 0) ld.wsel = w;
         __syncwarp();
         // whole blocks inside the segment, in this window; the first stage of
         // a segment and the last one of a segment or a window come here
-        const int upto = min(ld.lend, li0 + 32 / SB - 1); // stages before this one
-        const int v = ld.window[first + lane];
-        const bool in = lane < (upto - li0) * SB;
-        const bool fine = __all_sync(kFull, !in || (v >= 0 && v < a.num_blocks));
+        const int upto = min(ld.lend, li0 + kWindow / SB - 1); // stages before this one
+        bool fine = true;
+#pragma unroll
+        for (int k = lane; k < kWindow; k += 32) {
+            const int v = ld.window[first + k];
+            fine = fine && (k >= (upto - li0) * SB || (v >= 0 && v < a.num_blocks));
+        }
+        fine = __all_sync(kFull, fine);
         if (lane == 0) {
             ld.e = at;
             ld.elim = fine && li1 > 0 ? first + (upto - li0) * SB : 0;
@@ -878,23 +887,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                             vst[t][k] = vlo[t][k] = 0.f;
                         }
             }
-            // ---- weights p and p s; the reference moves where one of them
-            // would leave its range
-            float p[XT][4], w[XT][4];
-            float top_w = 0.f, top_p = 0.f;
-            auto weigh = [&] {
+            // ---- the reference moves where a weight p s would leave its range
+            // (or p, where the step is very small)
+            float top = 0.f;
 #pragma unroll
-                for (int t = 0; t < XT; ++t)
+            for (int t = 0; t < XT; ++t)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        p[t][k] = exp2_approx(x[t][k]);
-                        w[t][k] = p[t][k] * vst[t][k >> 1];
-                        top_p = fmaxf(top_p, p[t][k]);
-                        top_w = fmaxf(top_w, w[t][k]);
-                    }
-            };
-            weigh();
-            if (__any_sync(kFull, top_w > kWeightMax || top_p > kProbMax) || fresh) {
+                for (int k = 0; k < 2; ++k)
+                    top = fmaxf(top, exp2_approx(fmaxf(x[t][2 * k], x[t][2 * k + 1])) * fmaxf(vst[t][k], kStepFloor));
+            if (__any_sync(kFull, top > kWeightMax) || fresh) {
                 float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
                 for (int t = 0; t < XT; ++t)
@@ -934,19 +935,19 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                         x[t][2 * k] -= s0;
                         x[t][2 * k + 1] -= s1;
                     }
-                weigh();
             }
-            // ---- their sums, and the values' B operand
+            // ---- weights, their sums, and the values' B operand
             uint32_t wh[XT][2], wl[F32 ? XT : 1][2];
 #pragma unroll
             for (int t = 0; t < XT; ++t)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    l0 += p[t][2 * k];
-                    l1 += p[t][2 * k + 1];
-                    lo0 = fmaf(p[t][2 * k], vlo[t][k], lo0);
-                    lo1 = fmaf(p[t][2 * k + 1], vlo[t][k], lo1);
-                    const float w0 = w[t][2 * k], w1 = w[t][2 * k + 1];
+                    const float p0 = exp2_approx(x[t][2 * k]), p1 = exp2_approx(x[t][2 * k + 1]);
+                    l0 += p0;
+                    l1 += p1;
+                    lo0 = fmaf(p0, vlo[t][k], lo0);
+                    lo1 = fmaf(p1, vlo[t][k], lo1);
+                    const float w0 = p0 * vst[t][k], w1 = p1 * vst[t][k];
                     const uint32_t pk = pack_f16(w0, w1);
                     wh[t][k] = movmatrix_trans(pk ^ odd_sign);
                     if constexpr (F32) {
@@ -1220,7 +1221,7 @@ int make_plan(int batch, int num_kv_heads, int group, Plan *p)
     for (int h = 2; h <= kMaxWarps && h <= num_kv_heads; ++h)
         if (num_kv_heads % h == 0 && (long long)kMaxParts * batch * num_kv_heads >= (long long)p->ctas * h) hs = h;
     const int tw = kMaxWarps / hs, ncw = hs * tw;
-    int nst = 6;
+    int nst = 2;
     while (nst > 2 && smem_bytes<D, R>(ncw, tw, nst, group) > kSmemPerCta) --nst;
     p->smem = smem_bytes<D, R>(ncw, tw, nst, group);
     static int raised[kMaxDev];
