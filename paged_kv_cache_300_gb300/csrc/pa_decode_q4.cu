@@ -300,64 +300,94 @@ __device__ __noinline__ void append(const DecodeQ4Args &a, int b, int kvh, int L
 
 // Join the parts of a sequence in logical order and store its output rows.
 // A part is `group` rows of D sums and, behind them, (m, l) of each row; a
-// refused part has l = -inf.  A thread takes NE pieces of four dims at a time,
-// with the loads of KU parts in flight.  Not inlined: it runs once a sequence
+// refused part has l = -inf.  D / 4 lanes stand for a row's columns, four dims
+// each, and for as many parts' (m, l): they find the weights 2^(m - max m) by
+// shuffles while the first KU parts' columns are on their way.  A warp takes NE
+// such rows (or pairs of rows) at a time.  Not inlined: it runs once a sequence
 // and its registers would weigh on the loop.
 template <int D, typename T, int NE>
-__device__ __noinline__ void fold(const float *first, size_t step, int nseg, int group, int thread, int threads, T *out)
+__device__ __noinline__ void fold(const float *first, size_t step, int nseg, int group, int warp, int warps, T *out)
 {
-    constexpr int KU = NE >= 8 ? 2 : 4;
+    constexpr int HL = D / 4, RW = 32 / HL; // lanes of a row, rows of a warp
+    constexpr int KU = NE == 1 ? 8 : 5;
+    const int lane = threadIdx.x & 31, sub = lane % HL;
 #pragma unroll 1
-    for (int e0 = thread; e0 < group * (D / 4); e0 += threads * NE) {
+    for (int r0 = warp * NE * RW; r0 < group; r0 += warps * NE * RW) {
+        int g[NE];
         float M[NE], l[NE];
         float4 o[NE];
-        bool refused = false;
+        bool refused[NE];
 #pragma unroll
         for (int n = 0; n < NE; ++n) {
+            g[n] = min(r0 + n * RW + lane / HL, group - 1);
             M[n] = -INFINITY;
             l[n] = 0.f;
             o[n] = make_float4(0.f, 0.f, 0.f, 0.f);
+            refused[n] = false;
         }
 #pragma unroll 1
-        for (int k0 = 0; k0 < nseg; k0 += KU) {
-            float2 z[KU][NE];
-            float4 x[KU][NE];
+        for (int k0 = 0; k0 < nseg; k0 += HL) {
+            const int parts = min(HL, nseg - k0);
+            const float *base = first + (size_t)k0 * step;
+            float2 z[NE];
+            float f[NE];
 #pragma unroll
-            for (int k = 0; k < KU; ++k)
+            for (int n = 0; n < NE; ++n)
+                z[n] = sub < parts ? __ldcg(reinterpret_cast<const float2 *>(base + sub * step + group * D + 2 * g[n]))
+                                   : make_float2(-INFINITY, 0.f);
+#pragma unroll 1
+            for (int k = 0; k < parts; k += KU) {
+                float4 x[NE][KU];
 #pragma unroll
-                for (int n = 0; n < NE; ++n) {
-                    const int e = e0 + threads * n, g = min(e / (D / 4), group - 1);
-                    const float *part = first + min(k0 + k, nseg - 1) * step;
-                    z[k][n] = __ldcg(reinterpret_cast<const float2 *>(part + group * D + 2 * g));
-                    x[k][n] = __ldcg(reinterpret_cast<const float4 *>(part + g * D + e % (D / 4) * 4));
+                for (int n = 0; n < NE; ++n)
+#pragma unroll
+                    for (int u = 0; u < KU; ++u)
+                        x[n][u] = k + u < parts ? __ldcg(reinterpret_cast<const float4 *>(
+                                                      base + (size_t)(k + u) * step + g[n] * D + 4 * sub))
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k == 0) { // the chunk's weights
+#pragma unroll
+                    for (int n = 0; n < NE; ++n) {
+                        float top = fmaxf(M[n], z[n].x);
+#pragma unroll
+                        for (int q = HL / 2; q > 0; q >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, q));
+                        const float fo = top == -INFINITY ? 1.f : exp2_approx(M[n] - top);
+                        f[n] = top == -INFINITY ? 1.f : exp2_approx(z[n].x - top);
+                        const unsigned bad = __ballot_sync(kFull, z[n].y == -INFINITY);
+                        refused[n] = refused[n] || (HL == 32 ? bad : bad >> (lane & 16) & 0xffffu);
+                        float s = z[n].y * f[n];
+#pragma unroll
+                        for (int q = HL / 2; q > 0; q >>= 1) s += __shfl_xor_sync(kFull, s, q);
+                        M[n] = top;
+                        l[n] = fmaf(l[n], fo, s);
+                        o[n].x *= fo;
+                        o[n].y *= fo;
+                        o[n].z *= fo;
+                        o[n].w *= fo;
+                    }
                 }
 #pragma unroll
-            for (int k = 0; k < KU; ++k) {
-                if (k0 + k >= nseg) break;
+                for (int n = 0; n < NE; ++n)
 #pragma unroll
-                for (int n = 0; n < NE; ++n) {
-                    const float top = fmaxf(M[n], z[k][n].x);
-                    const float fo = top == -INFINITY ? 1.f : exp2_approx(M[n] - top);
-                    const float f = top == -INFINITY ? 1.f : exp2_approx(z[k][n].x - top);
-                    refused |= z[k][n].y == -INFINITY;
-                    M[n] = top;
-                    l[n] = fmaf(z[k][n].y, f, l[n] * fo);
-                    o[n].x = fmaf(x[k][n].x, f, o[n].x * fo);
-                    o[n].y = fmaf(x[k][n].y, f, o[n].y * fo);
-                    o[n].z = fmaf(x[k][n].z, f, o[n].z * fo);
-                    o[n].w = fmaf(x[k][n].w, f, o[n].w * fo);
-                }
+                    for (int u = 0; u < KU; ++u) {
+                        if (k + u >= parts) break;
+                        const float w = __shfl_sync(kFull, f[n], k + u, HL);
+                        o[n].x = fmaf(x[n][u].x, w, o[n].x);
+                        o[n].y = fmaf(x[n][u].y, w, o[n].y);
+                        o[n].z = fmaf(x[n][u].z, w, o[n].z);
+                        o[n].w = fmaf(x[n][u].w, w, o[n].w);
+                    }
             }
         }
 #pragma unroll
         for (int n = 0; n < NE; ++n) {
-            const int e = e0 + threads * n;
-            if (e >= group * (D / 4)) break;
+            if (r0 + n * RW + lane / HL >= group) break;
             const float inv = 1.f / l[n];
-            if (refused)
-                store4(out + e * 4, 0.f, 0.f, 0.f, 0.f);
+            T *y = out + (size_t)g[n] * D + 4 * sub;
+            if (refused[n])
+                store4(y, 0.f, 0.f, 0.f, 0.f);
             else
-                store4(out + e * 4, o[n].x * inv, o[n].y * inv, o[n].z * inv, o[n].w * inv);
+                store4(y, o[n].x * inv, o[n].y * inv, o[n].z * inv, o[n].w * inv);
         }
     }
 }
@@ -1108,30 +1138,26 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                     s_b[warp][head0 + n] = bh[n];
                 }
             }
-            if (!sync()) return;
             float *mine = join + (size_t)warp * G * D;
 #pragma unroll
             for (int n = 0; n < NH; ++n) {
-                const int g = head0 + n;
-                if (g >= G) continue;
-                float M = mh[n];
-                for (int t = 0; t < tw; ++t) M = fmaxf(M, s_m[t * hs + ch][g]);
-                const float f = M == -INFINITY ? 1.f : exp2_approx(mh[n] - M);
+                if (head0 + n >= G) continue;
 #pragma unroll
                 for (int k = 0; k < NV / NH; k += 4) {
                     const float *v = val + n * (NV / NH) + k;
-                    *reinterpret_cast<float4 *>(mine + g * D + dim0 + k) =
-                        make_float4(v[0] * f, v[1] * f, v[2] * f, v[3] * f);
+                    *reinterpret_cast<float4 *>(mine + (head0 + n) * D + dim0 + k) = make_float4(v[0], v[1], v[2], v[3]);
                 }
             }
             if (!sync()) return;
             for (int e = gtid; e < G * (D / 4); e += gthreads) {
                 const int g = e / (D / 4), d = e % (D / 4) * 4;
                 float M = -INFINITY;
+#pragma unroll 4
                 for (int t = 0; t < tw; ++t) M = fmaxf(M, s_m[t * hs + ch][g]);
                 float l = 0.f, low = 0.f;
                 bool refused = false; // a block or the length was
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                 for (int t = 0; t < tw; ++t) {
                     const int w = t * hs + ch;
                     const float f = M == -INFINITY ? 1.f : exp2_approx(s_m[w][g] - M);
@@ -1139,10 +1165,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                     l = fmaf(s_l[w][g], f, l);
                     low = fmaf(s_b[w][g], f, low);
                     const float4 x = *reinterpret_cast<const float4 *>(join + (size_t)w * G * D + g * D + d);
-                    o.x += x.x;
-                    o.y += x.y;
-                    o.z += x.z;
-                    o.w += x.w;
+                    o.x = fmaf(x.x, f, o.x);
+                    o.y = fmaf(x.y, f, o.y);
+                    o.z = fmaf(x.z, f, o.z);
+                    o.w = fmaf(x.w, f, o.w);
                 }
                 o.x += low;
                 o.y += low;
@@ -1182,9 +1208,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                 const float *first = a.part + ((size_t)(cfirst + segrow) * hs + ch) * gm.slot_floats;
                 const size_t step = (size_t)hs * gm.slot_floats;
                 if (tw == 1)
-                    fold<D, T, CW * D / 128>(first, step, nseg, G, gtid, 32, outp + orow);
+                    fold<D, T, (CW * D / 128 > 1 ? 2 : 1)>(first, step, nseg, G, 0, 1, outp + orow);
                 else
-                    fold<D, T, 1>(first, step, nseg, G, gtid, gthreads, outp + orow);
+                    fold<D, T, 1>(first, step, nseg, G, ct, tw, outp + orow);
             }
         }
         if (!sync()) return; // the join buffers are free again
