@@ -57,6 +57,9 @@ constexpr float kWeightMax = 16384.f, kWeightNew = 9.f;
 // fp32.
 constexpr float kStepFloor = 8.271806125530277e-25f;
 
+// A batch of at most this many sequences has its lengths in shared memory.
+constexpr int kMaxLens = 512;
+
 enum { kLast = 1, kAppend = 2, kBad = 4, kWhole = 8 };
 
 // What the loader notes about one stage; the second half is written for a
@@ -86,8 +89,6 @@ struct DecodeQ4Geom {
     int hs, tw;          // kv heads of a CTA, warps that share one head
     int head_groups, nst;
     int slot_floats;     // floats of one partial
-    int min_tokens;      // of a CTA's range
-    int seq_tokens;      // cost of a sequence
 };
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
@@ -224,14 +225,22 @@ __device__ __forceinline__ bool elect_one()
 // start and end cost a CTA, in blocks (see kSeqTokens).  The positions are cut
 // into P equal ranges.
 struct Split {
-    uint32_t q, r; // positions of a range, and the rest spread over the first ones
+    uint32_t q, r; // positions of a range, and the rest, spread over the ranges
     int P;
-    float inv;     // ranges a position
-    __device__ __forceinline__ Split(uint32_t total, int P_)
-        : q(total / (uint32_t)P_), r(total % (uint32_t)P_), P(P_), inv((float)P_ / (float)total)
+    float inv_p, inv; // 1 / P, ranges a position
+    __device__ __forceinline__ Split(uint32_t total, int P_) : P(P_)
     {
+        q = total / (uint32_t)P_;
+        r = total - q * (uint32_t)P_;
+        inv_p = __fdividef(1.f, (float)P_);
+        inv = __fdividef((float)P_, (float)total);
     }
-    __device__ __forceinline__ uint32_t start(int c) const { return c * q + c * r / (uint32_t)P; }
+    // c r < P^2 < 2^20 here: half above a whole number, the quotient is never
+    // nearer to the next one than the float's error
+    __device__ __forceinline__ uint32_t start(int c) const
+    {
+        return c * q + (uint32_t)(((float)(c * r) + 0.5f) * inv_p);
+    }
     __device__ __forceinline__ int range_of(uint32_t pos) const
     {
         int c = min(P - 1, (int)((float)pos * inv));
@@ -255,7 +264,7 @@ constexpr int kMinTokens = 128;
 // What the start and end of a sequence cost a warp, in tokens of its head.
 constexpr int kSeqTokens = 200;
 // Parts of a sequence that its last CTA joins, at most (see make_plan).
-constexpr int kMaxParts = 16;
+constexpr int kMaxParts = 8;
 
 // Quantise the new token's rows of kv head kvh, K in the lower half-warp and V
 // in the upper one, and write them into the pool and into the staged record
@@ -587,6 +596,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     __shared__ int s_total;
     __shared__ int s_first[4];  // first sequence, blocks before it, its length, the next one's
     __shared__ uint32_t s_u[2]; // first and one-past-last block of the range
+    __shared__ int s_lens[kMaxLens];
     __shared__ float s_m[kMaxWarps][8], s_l[kMaxWarps][8], s_b[kMaxWarps][8];
     __shared__ int s_last[kMaxWarps];
     __shared__ uint64_t s_group[kMaxWarps];
@@ -618,9 +628,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     const int per = (B + NT - 1) / NT;
     const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
     int local = 0;
+    const bool cached = B <= kMaxLens;
+    auto len_of = [&](int b) { return cached ? s_lens[b] : __ldg(a.cache_seqlens + b); };
     for (int b = b_lo; b < b_hi; ++b) {
         bool ok;
-        local += seq_blocks(__ldg(a.cache_seqlens + b), cap, BS, &ok);
+        const int len = __ldg(a.cache_seqlens + b);
+        if (cached) s_lens[b] = len;
+        local += seq_blocks(len, cap, BS, &ok);
         if (!ok && blockIdx.x == 0) flag_error(a.dev_err, PA_DEVERR_OVERFLOW);
     }
     int incl = local;
@@ -646,10 +660,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     const uint32_t ublk = s_total, U = ublk * gm.head_groups;
     // ranges: one a CTA, as many as the work fills (a sequence of a head group
     // at least), and the same number for every head group
-    int P = min((int)gridDim.x, max((int)(U / (uint32_t)(gm.min_tokens / BS)), B * gm.head_groups));
-    if (P > gm.head_groups) P = P / gm.head_groups * gm.head_groups;
+    int P = min((int)gridDim.x, max((int)(U / (uint32_t)(kMinTokens / BS)), B * gm.head_groups));
+    if (gm.head_groups > 1 && P > gm.head_groups) P = P / gm.head_groups * gm.head_groups;
     if ((int)blockIdx.x >= P) return;
-    const uint32_t cs = min((uint32_t)(gm.seq_tokens * tw / BS), U / (uint32_t)P / 4);
+    const uint32_t cs = min((uint32_t)(kSeqTokens * tw / BS), U / (uint32_t)P / 4);
     const uint32_t cblk = ublk + cs * B; // positions of a head group
     const Split split(cblk * gm.head_groups, P);
     {
@@ -663,12 +677,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                 if (tid == 0) s_u[e] = U;
                 continue;
             }
-            const uint32_t h = cc / cblk, r = cc % cblk;
+            const uint32_t h = gm.head_groups == 1 ? 0 : cc / cblk, r = cc - h * cblk;
             if (r < sct || r >= sct + span) continue;
             uint32_t sb = sbt, sc = sct;
             for (int b = b_lo; b < b_hi; ++b) {
                 bool ok;
-                const int len = __ldg(a.cache_seqlens + b);
+                const int len = len_of(b);
                 const int n = seq_blocks(len, cap, BS, &ok);
                 if (r < sc + cs + n) {
                     const uint32_t j = r < sc + cs ? 0 : r - sc - cs;
@@ -677,7 +691,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
                         s_first[0] = b;
                         s_first[1] = sb;
                         s_first[2] = len;
-                        s_first[3] = __ldg(a.cache_seqlens + (b + 1 < B ? b + 1 : 0));
+                        s_first[3] = len_of(b + 1 < B ? b + 1 : 0);
                     }
                     break;
                 }
@@ -719,7 +733,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
         }
     };
     {
-        const int b = s_first[0], hg = (int)(u0 / ublk), j0 = (int)(u0 % ublk) - s_first[1];
+        const int b = s_first[0], hg = gm.head_groups == 1 ? 0 : (int)(u0 / ublk);
+        const int j0 = (int)(u0 - hg * ublk) - s_first[1];
         if (lane == 0) {
             ld.len2 = s_first[3];
             ld.e = ld.elim = ld.wsel = 0;
@@ -767,11 +782,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     while (left > 0) { // segments
         bool bad = false, fresh; // fresh: no reference yet
         int at = warp * nst + stage;
-        { // q's loads run beside the first stage's copies
+        { // q of column r's head, the dims of this lane's words; its loads run beside the first stage's copies
             m0 = m1 = 0.f;
             fresh = true;
             l0 = l1 = lo0 = lo1 = 0.f;
-            // q of column r's head, the dims of this lane's words
             const int g = r % CW;
             QWords<T, KW * 8> qw;
             qw.load(static_cast<const T *>(a.q) +
@@ -1207,8 +1221,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
             if (last) {
                 const float *first = a.part + ((size_t)(cfirst + segrow) * hs + ch) * gm.slot_floats;
                 const size_t step = (size_t)hs * gm.slot_floats;
-                if (tw == 1)
-                    fold<D, T, (CW * D / 128 > 1 ? 2 : 1)>(first, step, nseg, G, 0, 1, outp + orow);
+                if (CW * D / 128 > 1 && G * D > tw * 128) // more rows than warps
+                    fold<D, T, 2>(first, step, nseg, G, ct, tw, outp + orow);
                 else
                     fold<D, T, 1>(first, step, nseg, G, ct, tw, outp + orow);
             }
@@ -1264,8 +1278,6 @@ int make_plan(int batch, int num_kv_heads, int group, Plan *p)
     p->gm.head_groups = num_kv_heads / hs;
     p->gm.nst = nst;
     p->gm.slot_floats = group * D + 16;
-    p->gm.min_tokens = kMinTokens;
-    p->gm.seq_tokens = kSeqTokens;
     return PA_OK;
 }
 
