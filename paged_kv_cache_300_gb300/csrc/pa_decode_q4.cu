@@ -49,7 +49,8 @@ namespace pa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 16;
+constexpr int kSlots = 2; // of a warp's ring
 // Largest weight p s before the reference moves (2^14), and the log2 of the
 // largest one after it has moved.
 constexpr float kWeightMax = 16384.f, kWeightNew = 9.f;
@@ -87,7 +88,7 @@ struct alignas(16) LoadState {
 
 struct DecodeQ4Geom {
     int hs, tw;          // kv heads of a CTA, warps that share one head
-    int head_groups, nst;
+    int head_groups;
     int slot_floats;     // floats of one partial
 };
 
@@ -577,7 +578,7 @@ struct Loader {
 // (the others are masked to zero), and the copies' sums are added at the end.
 // R = 1 has two tiles a stage as well, and every lane works on both.
 template <int D, int BS, int R, typename T>
-__global__ void __launch_bounds__(kMaxWarps * 32, 2)
+__global__ void __launch_bounds__(kMaxWarps * 32, 1)
     decode_q4_kernel(const DecodeQ4Args a, const DecodeQ4Geom gm)
 {
     constexpr bool F32 = sizeof(T) == 4;
@@ -603,7 +604,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
     __shared__ LoadState s_load[kMaxWarps];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hs = gm.hs, tw = gm.tw, ncw = hs * tw, nst = gm.nst;
+    constexpr int nst = kSlots;
+    const int hs = gm.hs, tw = gm.tw, ncw = hs * tw;
     const int NT = ncw * 32;
     const int B = a.batch, mbps = a.max_blocks_per_seq;
     const long long cap = (long long)mbps * BS;
@@ -1232,13 +1234,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2)
 }
 
 constexpr int kMaxDev = 64;
-constexpr size_t kSmemPerCta = 108 * 1024; // two CTAs an SM, beside their static arrays
+constexpr size_t kSmemPerCta = 210 * 1024; // one CTA an SM, beside its static arrays
 
 template <int D, int R>
-size_t smem_bytes(int ncw, int tw, int nst, int group)
+size_t smem_bytes(int ncw, int tw, int group)
 {
     const int stage_tokens = 16 * (R < 2 ? 2 : R);
-    return (size_t)ncw * nst * (stage_tokens * (D + 8) + 8 + sizeof(Meta)) + 8 +
+    return (size_t)ncw * kSlots * (stage_tokens * (D + 8) + 8 + sizeof(Meta)) + 8 +
            (tw > 1 ? (size_t)ncw * group * D * 4 : 0);
 }
 
@@ -1253,7 +1255,7 @@ int make_plan(int batch, int num_kv_heads, int group, Plan *p)
 {
     const int sms = num_sms();
     if (sms <= 0) return PA_ERR_DEVICE;
-    p->ctas = 2 * sms;
+    p->ctas = sms;
     // Heads of a CTA: the most that leave a sequence cut into at most
     // kMaxParts parts by the CTAs' ranges.  With fewer rows than that, the
     // warps of a CTA share a head's tokens and join in shared memory.
@@ -1261,9 +1263,8 @@ int make_plan(int batch, int num_kv_heads, int group, Plan *p)
     for (int h = 2; h <= kMaxWarps && h <= num_kv_heads; ++h)
         if (num_kv_heads % h == 0 && (long long)kMaxParts * batch * num_kv_heads >= (long long)p->ctas * h) hs = h;
     const int tw = kMaxWarps / hs, ncw = hs * tw;
-    int nst = 2;
-    while (nst > 2 && smem_bytes<D, R>(ncw, tw, nst, group) > kSmemPerCta) --nst;
-    p->smem = smem_bytes<D, R>(ncw, tw, nst, group);
+    p->smem = smem_bytes<D, R>(ncw, tw, group);
+    if (p->smem > kSmemPerCta) return PA_ERR_UNSUPPORTED; // not reached: 205 KB at most
     static int raised[kMaxDev];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return PA_ERR_DEVICE;
@@ -1276,7 +1277,6 @@ int make_plan(int batch, int num_kv_heads, int group, Plan *p)
     p->gm.hs = hs;
     p->gm.tw = tw;
     p->gm.head_groups = num_kv_heads / hs;
-    p->gm.nst = nst;
     p->gm.slot_floats = group * D + 16;
     return PA_OK;
 }
