@@ -309,7 +309,7 @@ size_t pa_q4_block_bytes(int num_kv_heads, int head_dim, int block_size);
  * skipped (padding of a captured step); a slot >= num_blocks * block_size
  * sets PA_DEVERR_BAD_BLOCK and is skipped.  A slot may appear once only: two
  * rows in one slot leave a mixture of both.  dtype is that of the chunk.
- * num_blocks * block_size < 2^31.
+ * num_blocks * block_size and total_q * num_kv_heads stay below 2^31 - 64.
  */
 int pa_cache_update_q4(const void *k_chunk, const void *v_chunk, const int32_t *slot_map,
                        void *kv_cache, int total_q, int num_kv_heads, int head_dim,
@@ -320,8 +320,8 @@ int pa_cache_update_q4(const void *k_chunk, const void *v_chunk, const int32_t *
  * Read back: rows [cu_seq_lens_k[r], cu_seq_lens_k[r+1]) of k_full, v_full
  * [total_k, num_kv_heads, head_dim] receive logical positions 0, 1, .. of
  * request r as values (b + n s in fp32, rounded to dtype), which pa_varlen
- * takes as they are.  Rows behind cu_seq_lens_k[batch] are left as they
- * were.  A needed block_table entry that is no block sets
+ * takes as they are (total_k * num_kv_heads < 2^31 - 64).  Rows behind
+ * cu_seq_lens_k[batch] are left as they were.  A needed block_table entry that is no block sets
  * PA_DEVERR_BAD_BLOCK, a position beyond the table PA_DEVERR_OVERFLOW; those
  * rows are zeroed.  cu_seq_lens_k that does not start at 0, decreases or
  * passes total_k sets PA_DEVERR_BAD_CU; nothing behind total_k is written.
@@ -347,7 +347,9 @@ int pa_cache_gather_q4(const void *kv_cache, const int32_t *block_table,
  * limits num_heads / num_kv_heads <= 8, batch * num_kv_heads <= 262144 as
  * pa_decode, and batch * max_blocks_per_seq * num_kv_heads < 2^31; every
  * pointer is device memory.  Elements of q above 2^115 may overflow.  A key or value row that is NaN
- * makes the outputs it reaches NaN, as the formula does.
+ * makes the outputs it reaches NaN, as the formula does.  Value steps below
+ * 2^-80 are weighed as the others but may lose their codes (the low value
+ * stays).
  */
 size_t pa_decode_q4_workspace_size(int batch, int num_heads, int num_kv_heads, int head_dim,
                                    int block_size, pa_dtype dtype);
@@ -368,8 +370,10 @@ int pa_decode_q4(const void *q, void *kv_cache, const int32_t *block_table,
  * entries of its block_table row, and gets n = new_lens[b] new ones:
  *   n >= 0  ceil((L+n)/bs) - ceil(L/bs) blocks are taken and entered in its
  *           row;
- *   n = -1  the request has ended: its blocks go back, its length becomes 0
- *           (its row is left as it is; nothing reads it at length 0).
+ *   n = -1  the request has ended: its blocks go back and its length becomes 0.
+ *           Its row is left as it is and names blocks that others may own by
+ *           now: give the row a new request before it is decoded again, or a
+ *           negative length, which pa_decode_q4 refuses for that row alone.
  * free_blocks [num_blocks] is a stack of *num_free block ids (top at the
  * end).  Ended requests push their blocks first, in order of (request,
  * logical block); then the taken blocks are popped in the same order.

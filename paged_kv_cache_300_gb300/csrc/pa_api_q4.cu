@@ -40,8 +40,8 @@ int pa_cache_update_q4(const void *k_chunk, const void *v_chunk, const int32_t *
     const int rc = check_pool(num_kv_heads, head_dim, num_blocks, block_size);
     if (rc != PA_OK) return rc;
     if (total_q < 0) return PA_ERR_SHAPE;
-    // the launch covers (row, head) pairs with one 32-bit grid dimension
-    if ((long long)total_q * num_kv_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    // rows are counted in 32 bits, sixteen at a time
+    if ((long long)total_q * num_kv_heads >= (1ll << 31) - 64) return PA_ERR_UNSUPPORTED;
     if (total_q == 0) return PA_OK;
     if (!k_chunk || !v_chunk || !slot_map || !kv_cache) return PA_ERR_NULL;
     if (!aligned(k_chunk, 16) || !aligned(v_chunk, 16) || !aligned(kv_cache, 16) || !aligned(slot_map, 4))
@@ -70,7 +70,7 @@ int pa_cache_gather_q4(const void *kv_cache, const int32_t *block_table,
     const int rc = check_pool(num_kv_heads, head_dim, num_blocks, block_size);
     if (rc != PA_OK) return rc;
     if (batch < 0 || total_k < 0 || max_blocks_per_seq <= 0) return PA_ERR_SHAPE;
-    if ((long long)total_k * num_kv_heads >= (1ll << 31)) return PA_ERR_UNSUPPORTED;
+    if ((long long)total_k * num_kv_heads >= (1ll << 31) - 64) return PA_ERR_UNSUPPORTED;
     if (batch == 0 || total_k == 0) return PA_OK;
     if (!kv_cache || !block_table || !cu_seq_lens_k || !k_full || !v_full) return PA_ERR_NULL;
     if (!aligned(kv_cache, 16) || !aligned(k_full, 16) || !aligned(v_full, 16) || !aligned(block_table, 4) ||

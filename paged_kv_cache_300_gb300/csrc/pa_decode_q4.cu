@@ -117,6 +117,20 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t m, uint32_t x)
     return d;
 }
 
+// Codes as they come out of a mask are f16 subnormals.  The tensor cores align
+// a subnormal's product by the smallest exponent, so it keeps some 17 bits of
+// the 24: plenty beside bf16 operands, too few for fp32 ones, whose codes are
+// made normal numbers first (times 2^14, exact).
+template <bool F32>
+__device__ __forceinline__ uint32_t operand(uint32_t codes)
+{
+    if constexpr (F32) {
+        const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&codes), __float2half2_rn(16384.f));
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return codes;
+}
+
 __device__ __forceinline__ float log2_approx(float x)
 {
     float y;
@@ -255,7 +269,8 @@ struct Split {
 // length is refused).
 __device__ __forceinline__ int seq_blocks(int L, long long cap, int bs, bool *ok)
 {
-    *ok = L >= 0 && (long long)L + 1 <= cap;
+    // positions of a stage's end stay below 2^31 too
+    *ok = L >= 0 && L < 0x7fffff80 && (long long)L + 1 <= cap;
     return *ok ? L / bs + 1 : 1;
 }
 
@@ -592,6 +607,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     constexpr int DL = D / 8;                       // output dims of a lane
     constexpr int CW = 8 / R;                       // columns of one copy
     constexpr int XT = NTILE / R;                   // tiles whose scores a lane works on
+    constexpr int kCodeShift = F32 ? 10 : 24;       // operands are codes times 2^-shift
+    constexpr float kCodeScale = F32 ? 1024.f : 16777216.f;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_warp[kMaxWarps];
     __shared__ int s_total;
@@ -809,7 +826,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             int e = amax > 0.f ? 14 - ((int)(__float_as_uint(amax) >> 23) - 127) : 0;
             e = max(-100, min(100, e));
             const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-            const float down = __uint_as_float((uint32_t)(127 + 24 - e) << 23) * a.scale_log2;
+            const float down = __uint_as_float((uint32_t)(127 + kCodeShift - e) << 23) * a.scale_log2;
 #pragma unroll
             for (int i = 0; i < KW; ++i)
 #pragma unroll
@@ -828,7 +845,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 #pragma unroll
             for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
             // 7.5 sum q in the products' units (fp32 only)
-            const float half = sum * up * (7.5f / 16777216.f);
+            const float half = sum * up * (7.5f / kCodeScale);
             if constexpr (F32) {
                 h0 = __shfl_sync(kFull, half, 4 * col);
                 h1 = __shfl_sync(kFull, half, 4 * col + 4);
@@ -872,8 +889,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         const uint32_t wa = s ? ka[i] >> 8 : ka[i], wb = s ? kb[i] >> 8 : kb[i];
-                        const uint32_t a0 = wa & 0x000f000fu, a1 = wb & 0x000f000fu;
-                        const uint32_t a2 = wa & 0x00f000f0u, a3 = wb & 0x00f000f0u;
+                        const uint32_t a0 = operand<F32>(wa & 0x000f000fu), a1 = operand<F32>(wb & 0x000f000fu);
+                        const uint32_t a2 = operand<F32>(wa & 0x00f000f0u), a3 = operand<F32>(wb & 0x00f000f0u);
                         if constexpr (F32) {
                             // small part first, one sum of 16 at a time: the
                             // tensor cores cut each sum at the size of its
@@ -1029,10 +1046,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                             // the high halves are the odd tokens: 15 - n
                             const uint32_t wa = s ? va[tt][0][i] >> 8 : va[tt][0][i];
                             const uint32_t wb = s ? va[tt][1][i] >> 8 : va[tt][1][i];
-                            va4[tt][0] = and_xor(wa, 0x000f000fu, 0x000f0000u);
-                            va4[tt][1] = and_xor(wa, 0x00f000f0u, 0x00f00000u);
-                            va4[tt][2] = and_xor(wb, 0x000f000fu, 0x000f0000u);
-                            va4[tt][3] = and_xor(wb, 0x00f000f0u, 0x00f00000u);
+                            va4[tt][0] = operand<F32>(and_xor(wa, 0x000f000fu, 0x000f0000u));
+                            va4[tt][1] = operand<F32>(and_xor(wa, 0x00f000f0u, 0x00f00000u));
+                            va4[tt][2] = operand<F32>(and_xor(wb, 0x000f000fu, 0x000f0000u));
+                            va4[tt][3] = operand<F32>(and_xor(wb, 0x00f000f0u, 0x00f00000u));
                         }
                         if constexpr (F32) { // small part first, each sum added with rounding
                             float part[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1074,7 +1091,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             lo1 += __shfl_xor_sync(kFull, lo1, o);
         }
         if (fresh) m0 = m1 = -INFINITY; // no token of the share was summed
-        // Codes of odd dims were 2^-20, of even ones 2^-24.  With copies, a
+        // Codes of odd dims were 16 times those of even ones.  With copies, a
         // lane keeps one of its two columns (R = 4: and half of its dims) and
         // hands the rest to the lane that keeps those.
         constexpr int NV = 2 * DL / R;      // values of a lane
@@ -1085,7 +1102,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         const int dim0 = r * DL + (R == 4 ? (rep >> 1) * (DL / 2) : 0);
 #pragma unroll
         for (int k = 0; k < DL; ++k) {
-            const float sc = (k & 1) ? 1048576.f : 16777216.f;
+            const float sc = (k & 1) ? kCodeScale / 16.f : kCodeScale;
             const float v0 = acc[k >> 1][2 * (k & 1)] * sc, v1 = acc[k >> 1][2 * (k & 1) + 1] * sc;
             if constexpr (R == 1) {
                 val[k] = v0;
@@ -1263,8 +1280,9 @@ int make_plan(int batch, int num_kv_heads, int group, Plan *p)
     for (int h = 2; h <= kMaxWarps && h <= num_kv_heads; ++h)
         if (num_kv_heads % h == 0 && (long long)kMaxParts * batch * num_kv_heads >= (long long)p->ctas * h) hs = h;
     const int tw = kMaxWarps / hs, ncw = hs * tw;
+    static_assert(kMaxWarps * (kSlots * (16 * (R < 2 ? 2 : R) * (D + 8) + 8 + sizeof(Meta)) + 8 / R * D * 4) + 8 <=
+                  kSmemPerCta, "a full CTA's rings and join buffers fit");
     p->smem = smem_bytes<D, R>(ncw, tw, group);
-    if (p->smem > kSmemPerCta) return PA_ERR_UNSUPPORTED; // not reached: 205 KB at most
     static int raised[kMaxDev];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return PA_ERR_DEVICE;

@@ -122,6 +122,24 @@ def test_gather(dtype, d, bs, hkv):
             assert torch.equal(got[cu[b]:cu[b + 1]].cpu(), w), (b, n)
 
 
+@pytest.mark.parametrize("batch", [31, 33, 1100])
+def test_gather_many_requests(batch):
+    """Lengths 0 to 40 in a large batch: finding a tile's request."""
+    d, bs, hkv = 64, 16, 1
+    lens = [(7 * i * i) % 41 if i % 3 else 0 for i in range(batch)]
+    c = make(8, lens, hkv, hkv, d, bs, BF16)
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    kf = torch.zeros(int(cu[-1]), hkv, d, dtype=BF16, device=DEV)
+    vf = torch.zeros_like(kf)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    g = _dev(c)
+    pa.pa_cache_gather_q4(g["pool"], g["table"], torch.from_numpy(cu).to(DEV), kf, vf, dev_err=err)
+    assert err.item() == 0
+    want = [q4.read(c["pool"], c["table"][b], n, d, bs)[:2] for b, n in enumerate(lens)]
+    for got, i in ((kf, 0), (vf, 1)):
+        assert torch.equal(got.cpu(), torch.from_numpy(np.concatenate([w[i] for w in want])).float().to(BF16))
+
+
 def test_gather_zeroes_what_it_cannot_read():
     d, bs, hkv = 128, 16, 2
     c = make(6, [40, 40, 40], hkv, hkv, d, bs, BF16)
@@ -195,6 +213,18 @@ def test_decode(dtype, d, bs, hq, hkv):
 @pytest.mark.parametrize("lens", [[0], [5000], [3, 20000, 900], [1500] * 40, list(range(0, 300))])
 def test_decode_lengths(dtype, lens):
     _against_reference(make(11, lens, 8, 2, 128, 16, dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 7, 7), (64, 26, 13), (64, 32, 32), (128, 48, 12), (128, 64, 8), (64, 88, 11)])
+def test_decode_many_rows(dtype, d, hq, hkv):
+    """Batches in which a warp has a head of its own, or two share one."""
+    _against_reference(make(hkv, [(37 * i) % 211 for i in range(60)], hq, hkv, d, 16, dtype))
+
+
+@pytest.mark.parametrize("batch", [511, 512, 513, 1500])
+def test_decode_batches_around_the_cached_lengths(batch):
+    _against_reference(make(batch, [(5 * i) % 40 for i in range(batch)], 2, 2, 64, 16, BF16))
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -344,9 +374,10 @@ def test_decode_bad_blocks_and_lengths(dtype, d, bs):
     for b in (1, 2):
         own = c["table"][b][(c["table"][b] >= 0) & (c["table"][b] < len(before))]
         assert np.array_equal(pool.cpu().numpy()[own], before[own])
-    c["lens"][2] = c["table"].shape[1] * bs
-    out, _, _, _, err = _decode(c)
-    assert err & pa.DEVERR_OVERFLOW and not out[2].any() and torch.equal(out[3], good[3])
+    for n in (c["table"].shape[1] * bs, 2 ** 31 - 1):
+        c["lens"][2] = n
+        out, _, _, _, err = _decode(c)
+        assert err & pa.DEVERR_OVERFLOW and not out[2].any() and torch.equal(out[3], good[3])
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])

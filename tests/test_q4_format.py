@@ -119,7 +119,7 @@ COMMON = [(dict(dt=7), -2), (dict(hkv=0), -3), (dict(nb=0), -3), (dict(d=96), -4
 
 @pytest.mark.parametrize("over,status", COMMON + [
     (dict(t=-1), -3), (dict(k=None), -1), (dict(slots=None), -1), (dict(v=4096 + 4), -3), (dict(slots=4098), -3),
-    (dict(t=0, k=None), 0), (dict(t=1 << 30, hkv=2), -4)])
+    (dict(t=0, k=None), 0), (dict(t=(1 << 30) - 32, hkv=2), -4)])
 def test_update_refuses_before_any_launch(lib, over, status):
     assert _update(lib, **over) == status
 
