@@ -127,19 +127,20 @@ __device__ __forceinline__ void check_cu(const CacheQ4Args &a)
     if (bad) flag_error(a.dev_err, PA_DEVERR_BAD_CU);
 }
 
-// Eight codes of 4 bits as fp32 values, rounded once.
-__device__ __forceinline__ void unpack8(float (&v)[8], uint32_t c, float step, float low)
+// N codes of 4 bits as values, rounded once; 2^23 + n is made of bits.
+template <int N>
+__device__ __forceinline__ void unpack(float (&v)[N], uint32_t c, float step, float low)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) // 2^23 + n, made of bits, less 2^23
+    for (int i = 0; i < N; ++i)
         v[i] = fmaf(__uint_as_float(((c >> (4 * i)) & 15u) | 0x4b000000u) - 8388608.f, step, low);
 }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8])
+// 16 bytes of values; they are read again, if at all, by another kernel.
+__device__ __forceinline__ void store16(float *p, const float (&v)[4])
 {
     __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
+__device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&v)[8])
 {
     __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                                                     pack_bf16(v[6], v[7])));
@@ -147,13 +148,13 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8])
 
 // A CTA takes one block of one request: tile i belongs to the last request r
 // with cu[r] / bs + r <= i (every request has at least as many tiles as
-// blocks).  A thread turns 8 dims of a token pair of one head, K and V, into
-// four stores of 8 values; neighbours in dims, then heads, are neighbours in
-// the packed rows.
+// blocks).  A thread turns N dims of a token pair of one head, K and V, into
+// four stores of 16 bytes; neighbours in dims, then heads, are neighbours in the
+// packed rows, so a warp stores whole sectors.
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) gather_q4_kernel(const CacheQ4Args a, const int bs_shift)
 {
-    constexpr int I = D / 8;
+    constexpr int N = 16 / sizeof(T), I = D / N;
     grid_dep_trigger();
     grid_dep_wait();
     if (blockIdx.x == 0) check_cu(a);
@@ -182,28 +183,38 @@ __global__ void __launch_bounds__(kThreads) gather_q4_kernel(const CacheQ4Args a
 #pragma unroll 2
     for (int e = threadIdx.x; e < items; e += kThreads) {
         const int i = e % I, hp = e / I, h = hp % hkv, p = hp / hkv;
-        uint32_t kc[2] = {0u, 0u};
-        uint2 vw = make_uint2(0u, 0u);
+        uint32_t kc[2] = {0u, 0u}, vc[2] = {0u, 0u};
         uint4 sc = make_uint4(0u, 0u, 0u, 0u);
         if (blk >= 0) {
             const uint8_t *rec = base + (size_t)h * rec_bytes;
-            const uint32_t *kr = reinterpret_cast<const uint32_t *>(rec) + 2 * p * I + i;
-            kc[0] = __ldg(kr);
-            kc[1] = __ldg(kr + I);
-            vw = __ldg(reinterpret_cast<const uint2 *>(rec + q4_v_offset(D, bs) + 2 * q4_v_unit<D>(2 * p, 2 * i)));
+            const uint8_t *kr = rec + p * D + i * (N / 2);
+            const uint8_t *vr = rec + q4_v_offset(D, bs) + 2 * q4_v_unit<D>(2 * p, i * (N / 4));
+            if constexpr (N == 8) {
+                kc[0] = __ldg(reinterpret_cast<const uint32_t *>(kr));
+                kc[1] = __ldg(reinterpret_cast<const uint32_t *>(kr + D / 2));
+                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(vr));
+                vc[0] = __byte_perm(w.x, w.y, 0x5410);
+                vc[1] = __byte_perm(w.x, w.y, 0x7632);
+            } else {
+                kc[0] = __ldg(reinterpret_cast<const uint16_t *>(kr));
+                kc[1] = __ldg(reinterpret_cast<const uint16_t *>(kr + D / 2));
+                const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(vr));
+                vc[0] = w & 0xffffu;
+                vc[1] = w >> 16;
+            }
             sc = __ldg(reinterpret_cast<const uint4 *>(rec + q4_scale_offset(D, bs) + p * 16));
         }
-        const size_t o = (size_t)(2 * p) * row_elts + h * D + i * 8;
-        float v[8];
-        unpack8(v, kc[0], bf16_lo(sc.x), bf16_hi(sc.x));
-        store8(ko + o, v);
-        unpack8(v, __byte_perm(vw.x, vw.y, 0x5410), bf16_lo(sc.y), bf16_hi(sc.y));
-        store8(vo + o, v);
+        const size_t o = (size_t)(2 * p) * row_elts + h * D + i * N;
+        float v[N];
+        unpack<N>(v, kc[0], bf16_lo(sc.x), bf16_hi(sc.x));
+        store16(ko + o, v);
+        unpack<N>(v, vc[0], bf16_lo(sc.y), bf16_hi(sc.y));
+        store16(vo + o, v);
         if (2 * p + 1 < rows) {
-            unpack8(v, kc[1], bf16_lo(sc.z), bf16_hi(sc.z));
-            store8(ko + o + row_elts, v);
-            unpack8(v, __byte_perm(vw.x, vw.y, 0x7632), bf16_lo(sc.w), bf16_hi(sc.w));
-            store8(vo + o + row_elts, v);
+            unpack<N>(v, kc[1], bf16_lo(sc.z), bf16_hi(sc.z));
+            store16(ko + o + row_elts, v);
+            unpack<N>(v, vc[1], bf16_lo(sc.w), bf16_hi(sc.w));
+            store16(vo + o + row_elts, v);
         }
     }
 }
