@@ -9,97 +9,126 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr int kMinWarps = 4096; // of an update that has work for them
 
 // ------------------------------------------------------------------ update
 // A CTA looks at kRows chunk rows.  A warp takes one of them, or two where they
-// are neighbours in one token pair of a block, and `heads` of its kv heads: K
-// in the lower half-warp, V in the upper one.  Two tokens of a pair share the
-// words of V, so a pair's V is written as whole words; a lone token writes its
-// halves of them.  The next head's rows are on their way while one is worked on.
+// are neighbours in one token pair of a block, and `heads` of its kv heads:
+// eight lanes a row, K and V of the first token, then of the second.  Two
+// tokens of a pair share the words of V, so a pair's V is written as whole
+// words, each token's lanes writing half of them; a lone token writes its halves
+// of the words.
+//
+// What bounds it: reading the chunk (5/4 of its bytes move in all) on one side,
+// instructions on the other.  33K rows of 8 bf16 heads x 128 dims (174 MB): 34
+// us, 5.1 TB/s.  With 16 lanes a row, a pair's rows one after the other, it was
+// 44 us and 289 instructions for four rows of 128; now 176, because a row's scale
+// is computed once for 16 elements a lane and arithmetic goes in pairs.
 constexpr int kRows = 16;
+// Heads whose rows are held or on their way.  The same chunk with the read-back
+// behind it: 82 us with 1 (no loads beside the sums), 76 with 2, 75 with 3.
+constexpr int kAhead = 2;
+// Warps that an update is spread over, at least, before a warp takes several
+// heads: about half of what the SMs hold.  A decode step's few rows then run a
+// head a warp, and a large chunk reads its slots once for all heads.
+constexpr int kMinWarps = 4096;
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads) update_q4_kernel(const CacheQ4Args a, const int heads, const int bs_shift)
+__global__ void __launch_bounds__(kThreads, 5) update_q4_kernel(const CacheQ4Args a, const int heads, const int bs_shift)
 {
-    constexpr int EPL = D / 16;
-    const int lane = threadIdx.x & 31, l = lane & 15;
-    const bool value = lane >= 16;
+    constexpr int NC = D / 64;
+    const int lane = threadIdx.x & 31, l = lane & 7;
+    const bool value = lane & 16, second = lane & 8;
     grid_dep_trigger();
     grid_dep_wait();
     // Rows that lead: all but the odd token of a pair whose even one stands
     // before it in the chunk, and padding.
-    const int row0 = blockIdx.x * kRows, mine = row0 + l;
+    const int row0 = blockIdx.x * kRows, mine = row0 + (lane & (kRows - 1));
     const int slot_l = mine < a.total ? __ldg(a.slot_map + mine) : -1;
     const int before = mine > 0 && mine < a.total ? __ldg(a.slot_map + mine - 1) : -1;
     const int after = mine + 1 < a.total ? __ldg(a.slot_map + mine + 1) : -1;
     const bool inside = slot_l < a.num_blocks << bs_shift;
-    if (!inside && lane < 16 && threadIdx.x < 32 && blockIdx.y == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
-    const bool leads = slot_l >= 0 && inside && !((slot_l & 1) && before == slot_l - 1);
+    if (!inside && lane < kRows && threadIdx.x < 32 && blockIdx.y == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
+    const bool leads = lane < kRows && slot_l >= 0 && inside && !((slot_l & 1) && before == slot_l - 1);
     const bool paired = !(slot_l & 1) && after == slot_l + 1;
-    unsigned todo = __ballot_sync(kFull, leads) & 0xffffu;
-    const unsigned pairs = __ballot_sync(kFull, paired);
+    const unsigned todo = __ballot_sync(kFull, leads), pairs = __ballot_sync(kFull, paired);
+    const int rank = __popc(todo & ((1u << lane) - 1u));
     const int hkv = a.num_kv_heads, bs = 1 << bs_shift;
     const int h0 = blockIdx.y * heads, n = min(hkv, h0 + heads) - h0;
     const int rec_bytes = q4_record_bytes(D, bs);
-    const size_t next = (size_t)hkv * D;
-    for (int k = threadIdx.x >> 5;; k += kThreads / 32) {
+    for (int k = threadIdx.x >> 5; k < __popc(todo); k += kThreads / 32) {
         // the warp's k-th leading row
-        const int i = (int)__fns(todo, 0, k + 1);
-        if (i < 0 || i >= kRows) break;
+        const int i = __ffs(__ballot_sync(kFull, leads && rank == k)) - 1;
         const int slot = __shfl_sync(kFull, slot_l, i), t = slot & (bs - 1);
-        const bool two = pairs >> i & 1;
+        const bool two = pairs >> i & 1, mute = second && !two;
         uint8_t *rec = static_cast<uint8_t *>(a.kv_cache) + ((size_t)(slot >> bs_shift) * hkv + h0) * rec_bytes;
-        const T *src = static_cast<const T *>(value ? a.v : a.k) + ((size_t)(row0 + i) * hkv + h0) * D + l * EPL;
-        uint16_t *unit = reinterpret_cast<uint16_t *>(rec) +
-                         (value ? q4_v_offset(D, bs) / 2 + q4_v_unit<D>(t, l * (EPL / 4)) // the lane's first unit
-                                : t * (D / 4) + l * (EPL / 4));
-        uint32_t *scale = reinterpret_cast<uint32_t *>(rec + q4_scale_offset(D, bs) + t * 8 + (value ? 4 : 0));
-        Q4Row<T, EPL> x, y;
-        x.load(src);
-        if (two) y.load(src + next);
-        for (int h = 0; h < n; ++h) {
-            Q4Row<T, EPL> x1, y1;
-            src += D;
-            if (h + 1 < n) {
-                x1.load(src);
-                if (two) y1.load(src + next);
-            }
-            Q4Scale s0, s1;
-            const uint32_t c0 = q4_half_warp(x, s0);
-            if (l == 0) scale[0] = q4_pack_scale(s0);
-            if (two) {
-                const uint32_t c1 = q4_half_warp(y, s1);
-                if (l == 0) scale[2] = q4_pack_scale(s1);
-                if (value) { // even token in the low halves
-                    if constexpr (EPL == 8)
-                        *reinterpret_cast<uint2 *>(unit) =
-                            make_uint2(__byte_perm(c0, c1, 0x5410), __byte_perm(c0, c1, 0x7632));
-                    else
-                        *reinterpret_cast<uint32_t *>(unit) = __byte_perm(c0, c1, 0x5410);
-                } else if constexpr (EPL == 8) {
-                    *reinterpret_cast<uint32_t *>(unit) = c0;
-                    *reinterpret_cast<uint32_t *>(unit + D / 4) = c1;
-                } else {
-                    unit[0] = (uint16_t)c0;
-                    unit[D / 4] = (uint16_t)c1;
-                }
-            } else if (value) {
+        const T *src = static_cast<const T *>(value ? a.v : a.k) +
+                       ((size_t)(row0 + i + (second && two)) * hkv + h0) * D + l * 8;
+        // of a pair's V, the first token's lanes write the words of chunk 0 (D = 64:
+        // of their first unit), the second token's those of chunk 1
+        uint8_t *dst = rec;
+        if (!value)
+            dst += (t + (second && two)) * (D / 2) + l * 4;
+        else if (two)
+            dst += q4_v_offset(D, bs) + 2 * q4_v_unit<D>(t, 2 * l + (second ? (NC == 2 ? 16 : 1) : 0));
+        else
+            dst += q4_v_offset(D, bs) + 2 * q4_v_unit<D>(t, 2 * l);
+        // of a lone token's V: from the units of chunk 0 to those of chunk 1
+        const int chunk = q4_v_unit<D>(t, NC == 2 ? 16 + 2 * l : 2 * l) - q4_v_unit<D>(t, 2 * l);
+        uint32_t *scale = reinterpret_cast<uint32_t *>(rec + q4_scale_offset(D, bs) + (t + second) * 8 + (value ? 4 : 0));
+        Q4Row<T, NC> rows[kAhead];
 #pragma unroll
-                for (int u = 0; u < EPL / 4; ++u) unit[2 * u] = (uint16_t)(c0 >> (16 * u));
-            } else if constexpr (EPL == 8) {
-                *reinterpret_cast<uint32_t *>(unit) = c0;
-            } else {
-                unit[0] = (uint16_t)c0;
+        for (int p = 0; p < kAhead; ++p, src += D)
+            if (p < n) rows[p].load(src);
+        int left = n;
+        for (;;) {
+#pragma unroll
+            for (int p = 0; p < kAhead; ++p) {
+                if (left-- <= 0) break;
+                Q4Scale s;
+                uint32_t c[NC];
+                q4_quantise(rows[p], s, c);
+                if (left >= kAhead) rows[p].load(src);
+                src += D;
+                if (two) {
+                    const uint32_t got = __shfl_xor_sync(kFull, NC == 2 && !second ? c[NC - 1] : c[0], 8);
+                    if (!value) {
+#pragma unroll
+                        for (int u = 0; u < NC; ++u) *reinterpret_cast<uint32_t *>(dst + 32 * u) = c[u];
+                    } else { // the first token in the low halves
+                        const uint32_t even = second ? got : c[0], odd = second ? c[NC - 1] : got;
+                        const uint32_t w0 = __byte_perm(even, odd, 0x5410), w1 = __byte_perm(even, odd, 0x7632);
+                        if constexpr (NC == 2)
+                            *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
+                        else
+                            *reinterpret_cast<uint32_t *>(dst) = second ? w1 : w0;
+                    }
+                } else if (!mute) {
+                    if (!value) {
+#pragma unroll
+                        for (int u = 0; u < NC; ++u) *reinterpret_cast<uint32_t *>(dst + 32 * u) = c[u];
+                    } else {
+                        uint16_t *unit = reinterpret_cast<uint16_t *>(dst);
+#pragma unroll
+                        for (int u = 0; u < NC; ++u) {
+                            unit[u * chunk] = (uint16_t)c[u];
+                            unit[u * chunk + 2] = (uint16_t)(c[u] >> 16);
+                        }
+                    }
+                }
+                if (l == 0 && !mute) *scale = q4_pack_scale(s);
+                dst += rec_bytes;
+                scale += rec_bytes / 4;
             }
-            x = x1;
-            y = y1;
-            unit += rec_bytes / 2;
-            scale += rec_bytes / 4;
+            if (left <= 0) break;
         }
     }
 }
 
 // ------------------------------------------------------------------ gather
+// What bounds it: writing the rows.  145K rows of 8 bf16 heads x 128 dims (750
+// MB): 116 us, 6.5 TB/s, 95% of a copy's rate.  fp32, 24K rows of 6 heads x 64
+// dims (84 MB): 18 us, 4.6 TB/s; with 8 values a thread, whose two stores leave
+// every other 16 bytes to the next instruction, it was 24.5 us.
+//
 // Largest r in [0, n) with off(r) <= x, off(r) = cu[r] / bs + r (never
 // decreasing), by the whole warp: 32 probes a step.
 __device__ __forceinline__ int tile_owner(const int32_t *cu, int n, int x, int bs_shift)

@@ -176,6 +176,17 @@ __device__ __forceinline__ bool group_sync(uint64_t *bar, int warps, uint32_t &p
     return __all_sync(kFull, ok);
 }
 
+// Before a warp that gave up leaves: the copies into its ring have ended, or
+// the wait for them has.
+template <int NST>
+__device__ __noinline__ void drain(uint64_t *bars, int stage, uint32_t phase)
+{
+    for (int i = 0; i < NST; ++i) {
+        const int at = (stage + i) % NST;
+        spin_wait(&bars[at], phase ^ (stage + i >= NST));
+    }
+}
+
 template <int N>
 __device__ __forceinline__ void lds(uint32_t (&w)[N], const uint8_t *p)
 {
@@ -282,42 +293,51 @@ constexpr int kSeqTokens = 200;
 // Parts of a sequence that its last CTA joins, at most (see make_plan).
 constexpr int kMaxParts = 8;
 
-// Quantise the new token's rows of kv head kvh, K in the lower half-warp and V
-// in the upper one, and write them into the pool and into the staged record
-// (token t of the record at `rec`).
+// Quantise the new token's rows of kv head kvh, K in lanes 0-7 and V in 8-15,
+// and write them into the pool and into the staged record (token t of the
+// record at `rec`).
 template <int D, int BS, typename T>
 __device__ __noinline__ void append(const DecodeQ4Args &a, int b, int kvh, int L, int t, uint8_t *rec)
 {
-    constexpr int EPL = D / 16;
-    const int lane = threadIdx.x & 31, l = lane & 15;
-    const bool value = lane >= 16;
-    const size_t src = ((size_t)b * a.num_kv_heads + kvh) * D + l * EPL;
-    Q4Row<T, EPL> x;
+    constexpr int NC = D / 64;
+    const int lane = threadIdx.x & 31, l = lane & 7;
+    const bool value = lane & 8;
+    const size_t src = ((size_t)b * a.num_kv_heads + kvh) * D + l * 8;
+    Q4Row<T, NC> x;
     x.load(static_cast<const T *>(value ? a.v_new : a.k_new) + src);
     const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks_per_seq + L / BS);
     Q4Scale s;
-    const uint32_t c = q4_half_warp(x, s);
-    if (T *kept = static_cast<T *>(value ? a.v_stored : a.k_stored)) {
+    uint32_t c[NC];
+    q4_quantise(x, s, c);
+    if (lane < 16) {
+        if (T *kept = static_cast<T *>(value ? a.v_stored : a.k_stored)) {
 #pragma unroll
-        for (int i = 0; i < EPL; i += 4)
-            store4(kept + src + i, q4_value((c >> (4 * i)) & 15u, s.step, s.low),
-                   q4_value((c >> (4 * i + 4)) & 15u, s.step, s.low), q4_value((c >> (4 * i + 8)) & 15u, s.step, s.low),
-                   q4_value((c >> (4 * i + 12)) & 15u, s.step, s.low));
-    }
-    uint8_t *dst = static_cast<uint8_t *>(a.kv_cache) +
-                   ((size_t)blk * a.num_kv_heads + kvh) * q4_record_bytes(D, BS);
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        uint8_t *p = side ? dst : rec;
-#pragma unroll
-        for (int h = 0; h < EPL / 4; ++h) { // 16-bit units of four dims
-            const int unit = l * (EPL / 4) + h;
-            uint16_t *at = value ? reinterpret_cast<uint16_t *>(p + q4_v_offset(D, BS)) + q4_v_unit<D>(t, unit)
-                                 : reinterpret_cast<uint16_t *>(p) + t * (D / 4) + unit;
-            *at = (uint16_t)(c >> (16 * h));
+            for (int i = 0; i < 2 * NC; ++i) {
+                const uint32_t n = c[i >> 1] >> (i & 1) * 16;
+                store4(kept + src + (i >> 1) * 64 + (i & 1) * 4, q4_value(n & 15u, s.step, s.low),
+                       q4_value(n >> 4 & 15u, s.step, s.low), q4_value(n >> 8 & 15u, s.step, s.low),
+                       q4_value(n >> 12 & 15u, s.step, s.low));
+            }
         }
-        if (l == 0)
-            *reinterpret_cast<uint32_t *>(p + q4_scale_offset(D, BS) + t * 8 + (value ? 4 : 0)) = q4_pack_scale(s);
+        uint8_t *dst = static_cast<uint8_t *>(a.kv_cache) +
+                       ((size_t)blk * a.num_kv_heads + kvh) * q4_record_bytes(D, BS);
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            uint8_t *p = side ? dst : rec;
+#pragma unroll
+            for (int u = 0; u < NC; ++u) {
+                if (value) {
+                    uint16_t *unit = reinterpret_cast<uint16_t *>(p + q4_v_offset(D, BS)) +
+                                     q4_v_unit<D>(t, u * 16 + 2 * l);
+                    unit[0] = (uint16_t)c[u];
+                    unit[2] = (uint16_t)(c[u] >> 16);
+                } else {
+                    *reinterpret_cast<uint32_t *>(p + t * (D / 2) + u * 32 + l * 4) = c[u];
+                }
+            }
+            if (l == 0)
+                *reinterpret_cast<uint32_t *>(p + q4_scale_offset(D, BS) + t * 8 + (value ? 4 : 0)) = q4_pack_scale(s);
+        }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -793,7 +813,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     uint32_t phase = 0, gphase = 0;
     auto sync = [&] {
         const bool ok = group_sync(&s_group[ch], tw, gphase);
-        if (!ok && lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
+        if (!ok) {
+            if (lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
+            drain<nst>(full + warp * nst, stage, phase);
+        }
         return ok;
     };
     int left = (int)(u1 - u0); // units whose segments have not ended here
@@ -864,6 +887,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         flags = cf >> 8;
         if (!spin_wait(&full[at], phase)) {
             if (lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
+            drain<nst>(full + warp * nst, stage, phase);
             return;
         }
         uint8_t *st = ring + at * STAGE;

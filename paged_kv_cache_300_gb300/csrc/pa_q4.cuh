@@ -72,129 +72,137 @@ __device__ __forceinline__ uint32_t q4_pack_scale(const Q4Scale &s)
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// N values of a row in the type they came in: bf16 stays packed in pairs until
-// a value is needed.
-template <typename T, int N>
+// A row is held by 8 neighbouring lanes, four rows a warp: lane l has the dims
+// 64 c + 8 l .. + 7, c < NC = D / 64, in the type they came in (bf16 stays
+// packed in pairs until a value is needed).
+template <typename T, int NC>
 struct Q4Row;
-template <int N>
-struct Q4Row<float, N> {
-    float v[N];
+template <int NC>
+struct Q4Row<float, NC> {
+    float v[NC][8];
     __device__ __forceinline__ void load(const float *p)
     {
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const float4 x = __ldg(reinterpret_cast<const float4 *>(p + i));
-            v[i] = x.x;
-            v[i + 1] = x.y;
-            v[i + 2] = x.z;
-            v[i + 3] = x.w;
-        }
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(p + 64 * c + i));
+                v[c][i] = x.x;
+                v[c][i + 1] = x.y;
+                v[c][i + 2] = x.z;
+                v[c][i + 3] = x.w;
+            }
     }
-    __device__ __forceinline__ float get(int i) const { return v[i]; }
-    // extrema over 16 neighbouring lanes; NaN anywhere leaves finite false
-    __device__ __forceinline__ void extrema(float &lo, float &hi, bool &finite) const
+    __device__ __forceinline__ float2 pair(int c, int i) const { return make_float2(v[c][2 * i], v[c][2 * i + 1]); }
+    // extrema of the row; NaN where it holds one
+    __device__ __forceinline__ void extrema(float &lo, float &hi) const
     {
-        lo = hi = v[0];
-        bool ok = fabsf(v[0]) < INFINITY;
+        auto lower = [](float x, float y) {
+            float r;
+            asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+            return r;
+        };
+        auto upper = [](float x, float y) {
+            float r;
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+            return r;
+        };
+        lo = hi = v[0][0];
 #pragma unroll
-        for (int i = 1; i < N; ++i) {
-            lo = fminf(lo, v[i]);
-            hi = fmaxf(hi, v[i]);
-            ok = ok && fabsf(v[i]) < INFINITY;
+        for (int i = 1; i < 8 * NC; ++i) {
+            lo = lower(lo, v[i >> 3][i & 7]);
+            hi = upper(hi, v[i >> 3][i & 7]);
         }
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        for (int o = 4; o > 0; o >>= 1) {
+            lo = lower(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = upper(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
-        const unsigned row = 0xffffu << (threadIdx.x & 16);
-        finite = (__ballot_sync(0xffffffffu, ok) & row) == row;
     }
 };
-template <int N>
-struct Q4Row<__nv_bfloat16, N> {
-    uint32_t w[N / 2];
+template <int NC>
+struct Q4Row<__nv_bfloat16, NC> {
+    uint32_t w[NC][4];
     __device__ __forceinline__ void load(const __nv_bfloat16 *p)
     {
-        if constexpr (N == 8) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
-            w[0] = x.x;
-            w[1] = x.y;
-            w[2] = x.z;
-            w[3] = x.w;
-        } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
-            w[0] = x.x;
-            w[1] = x.y;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p + 64 * c));
+            w[c][0] = x.x;
+            w[c][1] = x.y;
+            w[c][2] = x.z;
+            w[c][3] = x.w;
         }
     }
-    __device__ __forceinline__ float get(int i) const { return i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]); }
-    // pairs at a time; then (max x, max -x) travel as one pair.  max with
-    // NaN is NaN here.
-    __device__ __forceinline__ void extrema(float &lo, float &hi, bool &finite) const
+    __device__ __forceinline__ float2 pair(int c, int i) const
+    {
+        return make_float2(bf16_lo(w[c][i]), bf16_hi(w[c][i]));
+    }
+    // pairs at a time; then (max x, max -x) travel as one pair
+    __device__ __forceinline__ void extrema(float &lo, float &hi) const
     {
         auto bf = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
         auto un = [](__nv_bfloat162 h) { return *reinterpret_cast<const uint32_t *>(&h); };
-        uint32_t a = w[0], b = w[0] ^ 0x80008000u;
+        uint32_t a = w[0][0], b = w[0][0];
 #pragma unroll
-        for (int i = 1; i < N / 2; ++i) {
-            a = un(__hmax2_nan(bf(a), bf(w[i])));
-            b = un(__hmax2_nan(bf(b), bf(w[i] ^ 0x80008000u)));
+        for (int i = 1; i < 4 * NC; ++i) {
+            a = un(__hmax2_nan(bf(a), bf(w[i >> 2][i & 3])));
+            b = un(__hmin2_nan(bf(b), bf(w[i >> 2][i & 3])));
         }
+        b ^= 0x80008000u;
         uint32_t m = un(__hmax2_nan(bf(__byte_perm(a, b, 0x5410)), bf(__byte_perm(a, b, 0x7632))));
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = un(__hmax2_nan(bf(m), bf(__shfl_xor_sync(0xffffffffu, m, o))));
+        for (int o = 4; o > 0; o >>= 1) m = un(__hmax2_nan(bf(m), bf(__shfl_xor_sync(0xffffffffu, m, o))));
         hi = bf16_lo(m);
         lo = -bf16_hi(m);
-        finite = fabsf(hi) < INFINITY && fabsf(lo) < INFINITY; // false for NaN
     }
 };
 
-// Quantises a row held by 16 neighbouring lanes, EPL = D / 16 values each (two
-// rows a warp): s is the row's scale, the result the lane's codes, 4 bits each.
-template <typename T, int EPL>
-__device__ __forceinline__ uint32_t q4_half_warp(const Q4Row<T, EPL> &x, Q4Scale &s)
+// Two fp32 numbers to a register pair, which one instruction works on.
+__device__ __forceinline__ uint64_t f32x2(float x, float y)
 {
-    float lo, hi;
-    bool finite;
-    x.extrema(lo, hi, finite);
-    s = q4_scale(lo, hi, finite);
-    // n = round-half-even((x / 16 - b / 16) * (16 / s)), which lies in 0..15: the
-    // sum with 2^23 rounds it into the low bits.  x / 16 is exact, so the first
-    // step is one rounding as a fused operation too; the product is not fused.
-    // The sums of the bits leave out 0x4b000000 (the bits of 2^23) at every
-    // step; only the first two places keep something of it.
-    uint32_t c = 0;
-#pragma unroll
-    for (int i = EPL - 1; i >= 0; --i)
-        c = c * 16u + __float_as_uint(__fadd_rn(__fmul_rn(fmaf(x.get(i), 0.0625f, -s.low16), s.inv16), 8388608.f));
-    c -= 0xfb000000u;
-    return s.inv16 > 0.f ? (EPL == 8 ? c : c & 0xffffu) : 0u;
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
 }
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x);
-template <>
-__device__ __forceinline__ float to_f32<float>(float x)
+// Quantises a row: s is its scale, c the lane's codes, 4 bits each.
+template <typename T, int NC>
+__device__ __forceinline__ void q4_quantise(const Q4Row<T, NC> &x, Q4Scale &s, uint32_t (&c)[NC])
 {
-    return x;
-}
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x)
-{
-    return __bfloat162float(x);
-}
-template <typename T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ float from_f32<float>(float x)
-{
-    return x;
-}
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x)
-{
-    return __float2bfloat16_rn(x);
+    float lo, hi;
+    x.extrema(lo, hi);
+    s = q4_scale(lo, hi, fabsf(lo) < INFINITY && fabsf(hi) < INFINITY); // false for NaN
+    // n = round-half-even((x / 16 - b / 16) * (16 / s)), which lies in 0..15: the
+    // sum with 2^23 rounds it into the low bits.  x / 16 is exact, so the first
+    // step is one rounding as a fused operation too.  The product is rounded
+    // before the sum: a packed mul, or an fma with a constant -0, is fused with
+    // the packed add behind it all the same, so it is an fma with a computed -0.
+    // The sums of the bits leave out 0x4b000000 (the bits of 2^23) at every
+    // step; only the first two places keep something of it.
+    const uint64_t sixteenth = f32x2(0.0625f, 0.0625f), low = f32x2(-s.low16, -s.low16), inv = f32x2(s.inv16, s.inv16),
+                   big = f32x2(8388608.f, 8388608.f);
+    const float zero = __fmul_rn(s.inv16, -0.f);
+    const uint64_t minus_zero = f32x2(zero, zero);
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+        uint32_t n = 0;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const float2 v = x.pair(k, i);
+            uint32_t n0, n1;
+            asm("{\n\t.reg .b64 t;\n\t"
+                "fma.rn.f32x2 t, %2, %3, %4;\n\t"
+                "fma.rn.f32x2 t, t, %5, %7;\n\t"
+                "add.rn.f32x2 t, t, %6;\n\t"
+                "mov.b64 {%0, %1}, t;\n\t}"
+                : "=r"(n0), "=r"(n1)
+                : "l"(f32x2(v.x, v.y)), "l"(sixteenth), "l"(low), "l"(inv), "l"(big),
+                  "l"(minus_zero));
+            n = (n * 16u + n1) * 16u + n0;
+        }
+        c[k] = s.inv16 > 0.f ? n - 0xfb000000u : 0u;
+    }
 }
 
 // Four consecutive elements, rounded once.
