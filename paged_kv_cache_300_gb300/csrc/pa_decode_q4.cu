@@ -287,7 +287,7 @@ __device__ __forceinline__ int seq_blocks(int L, long long cap, int bs, bool *ok
 
 // A CTA's range holds at least this many tokens of its heads: below that,
 // more CTAs cost more in partials than they save.
-constexpr int kMinTokens = 128;
+constexpr int kMinTokens = 256;
 // What the start and end of a sequence cost a warp, in tokens of its head.
 constexpr int kSeqTokens = 200;
 // Parts of a sequence that its last CTA joins, at most (see make_plan).
