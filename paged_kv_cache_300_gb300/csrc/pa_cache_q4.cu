@@ -32,7 +32,8 @@ constexpr int kAhead = 2;
 // head a warp, and a large chunk reads its slots once for all heads.
 constexpr int kMinWarps = 4096;
 template <int D, typename T>
-__global__ void __launch_bounds__(kThreads, 5) update_q4_kernel(const CacheQ4Args a, const int heads, const int bs_shift)
+__global__ void __launch_bounds__(kThreads, 5)
+    update_q4_kernel(const CacheQ4Args a, const int heads, const int bs_shift)
 {
     constexpr int NC = D / 64;
     const int lane = threadIdx.x & 31, l = lane & 7;

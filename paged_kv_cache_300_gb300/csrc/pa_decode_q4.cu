@@ -28,17 +28,25 @@
 //    keeps all its bits); fp32 operands run as a sum of two f16 numbers.
 //  * p s is rounded to f16 (half a step 2^-11; the sum of p is not rounded).
 //    Its reference m follows the maximum of x + log2(s), so that p s, not p, is
-//    at most 2^14; it moves only when p s would pass that, which leaves 23 bits
-//    or more below the largest term before f16 loses bits of a weight.
+//    at most 2^14; it moves only when p s would pass that, and then
+//    leaves it at 2^9.  So a weight keeps f16's 11 bits down to 2^-23 of the
+//    largest one, and is off by 2^-34 of that at most below.
 //
 // Work.  HBM-bound on (D + 8) / 2D bytes an element.  One stage is 32 or 64
-// tokens of one kv head: up to four records, each one bulk copy.  A CTA has up
-// to 8 warps, TW of them sharing the tokens of each of HS kv heads; each
-// resolves its part of the block table and fills its own ring.
+// tokens of one kv head: up to four records, each one bulk copy.  An SM has one
+// CTA of 16 warps, TW of them sharing the tokens of each of HS kv heads; each
+// resolves its part of the block table and fills its own ring of two stages.
 // The flat list of (head group, sequence, block) is cut into equal ranges, one
 // per CTA (every CTA derives them from cache_seqlens); a sequence cut by a
 // range's border leaves partials (acc, m, l) that its last CTA joins in
 // logical order.  The warps of a head join in shared memory first.
+//
+// What bounds it (bf16; algorithmic bytes over time, a copy runs at 6.8 TB/s):
+//   96 sequences of 4K-16K, 64/8 heads x 128    1068 MB  175 us  6.1 TB/s  HBM; SMs end 5-8% apart
+//   256 of 512-4096, 32/8 x 128                   648 MB  116 us  5.6 TB/s  the same
+//   1024 of 257-768, 32/32 x 64                  1237 MB  235 us  5.2 TB/s  a sequence's ends, per head
+//   64 of 512-4096, 32/8 x 128                    164 MB   42 us  3.9 TB/s  start 5-7 us, join 4-5 us
+//   one of 5000, 32/8 x 128                       5.5 MB   14 us            latency: start, walk, join
 #include "pa_internal.h"
 #include "pa_q4.cuh"
 
@@ -49,8 +57,13 @@ namespace pa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+// One CTA of 16 warps an SM: a warp takes up to 128 registers and up to 9 KB of
+// ring.  With two CTAs of 8 warps, three slots a warp and twice the partials, 96
+// long sequences took 183 us (175), 64 shorter ones 44.2 (42.0).
 constexpr int kMaxWarps = 16;
-constexpr int kSlots = 2; // of a warp's ring
+// Slots of a warp's ring: 74 to 147 KB in flight an SM, which is more than HBM's
+// latency needs.  More slots leave less L1 and were slower.
+constexpr int kSlots = 2;
 // Largest weight p s before the reference moves (2^14), and the log2 of the
 // largest one after it has moved.
 constexpr float kWeightMax = 16384.f, kWeightNew = 9.f;
@@ -120,7 +133,8 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t m, uint32_t x)
 // Codes as they come out of a mask are f16 subnormals.  The tensor cores align
 // a subnormal's product by the smallest exponent, so it keeps some 17 bits of
 // the 24: plenty beside bf16 operands, too few for fp32 ones, whose codes are
-// made normal numbers first (times 2^14, exact).
+// made normal numbers first (times 2^14, exact): the largest error against 64
+// bits went from 5e-6 to 8e-7, and 64 fp32 sequences from 56 to 59 us.
 template <bool F32>
 __device__ __forceinline__ uint32_t operand(uint32_t codes)
 {
@@ -286,11 +300,17 @@ __device__ __forceinline__ int seq_blocks(int L, long long cap, int bs, bool *ok
 }
 
 // A CTA's range holds at least this many tokens of its heads: below that,
-// more CTAs cost more in partials than they save.
+// more CTAs cost more in partials than they save.  With 128, 256 and 512 a
+// sequence of 300 tokens takes 11.9, 11.2 and 11.0 us, one of 2500 13.5, 12.8
+// and 14.2, eight of 300 to 900 19.8, 19.3 and 20.9.
 constexpr int kMinTokens = 256;
-// What the start and end of a sequence cost a warp, in tokens of its head.
+// What the start and end of a sequence cost a warp, in tokens of its head: with
+// 0, 200 and 400, 64 sequences of 512 to 4096 take 51.4, 42.4 and 42.4 us, 256 of
+// them 122.2, 116.1 and 122.5, 96 of 4K to 16K 175.0, 169.3 and 174.7.
 constexpr int kSeqTokens = 200;
-// Parts of a sequence that its last CTA joins, at most (see make_plan).
+// Parts of a sequence that its last CTA joins, about (see make_plan).  With 4, 8
+// and 16, 16 sequences of 512 to 4096 take 26.6, 25.8 and 27.1 us, eight of 20K to
+// 40K 54.7, 53.2 and 53.7.
 constexpr int kMaxParts = 8;
 
 // Quantise the new token's rows of kv head kvh, K in lanes 0-7 and V in 8-15,
@@ -1275,7 +1295,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 }
 
 constexpr int kMaxDev = 64;
-constexpr size_t kSmemPerCta = 210 * 1024; // one CTA an SM, beside its static arrays
+constexpr size_t kSmemPerCta = 210 * 1024; // of 227, beside the static arrays
 
 template <int D, int R>
 size_t smem_bytes(int ncw, int tw, int group)
@@ -1352,8 +1372,10 @@ int plan_and_launch(const DecodeQ4Args *a, int batch, int num_kv_heads, int grou
 }
 
 // Copies of the head group in the products' columns: as many as fit, up to
-// the tiles of a stage.  Four (64-token stages) for head_dim 64 only: at 128
-// two such stages a warp would not leave room for a second CTA on the SM.
+// the tiles of a stage.  1024 sequences with D 64 and one head a kv head: 235 us
+// with four copies, 274 with two.  256 sequences with D 128 and four heads a kv
+// head: 116 us with two, 122 with none.  Four copies (64-token stages) are for
+// head_dim 64 only: at 128 their rings would not fit 16 warps.
 template <int D, int BS, typename T>
 int by_copies(const DecodeQ4Args *a, int batch, int num_kv_heads, int group, size_t have, size_t *need, cudaStream_t s)
 {
