@@ -161,7 +161,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 // Wait for a barrier's phase without giving the thread up: an unsuccessful
 // try_wait suspends it for microseconds on this GPU, many times the waits met
-// here (a copy's rest, a neighbour's shuffles).  The limit is about a second.
+// here (a copy's rest, a neighbour's shuffles).  The limit is about a second.  A
+// warp that gives up leaves: all its copies were under way before the wait began,
+// so each has had the limit too.
 __device__ __forceinline__ bool spin_wait(uint64_t *bar, uint32_t parity)
 {
     for (uint32_t i = 0; i < (1u << 25); ++i) {
@@ -188,17 +190,6 @@ __device__ __forceinline__ bool group_sync(uint64_t *bar, int warps, uint32_t &p
     const bool ok = spin_wait(bar, phase);
     phase ^= 1;
     return __all_sync(kFull, ok);
-}
-
-// Before a warp that gave up leaves: the copies into its ring have ended, or
-// the wait for them has.
-template <int NST>
-__device__ __noinline__ void drain(uint64_t *bars, int stage, uint32_t phase)
-{
-    for (int i = 0; i < NST; ++i) {
-        const int at = (stage + i) % NST;
-        spin_wait(&bars[at], phase ^ (stage + i >= NST));
-    }
 }
 
 template <int N>
@@ -833,10 +824,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     uint32_t phase = 0, gphase = 0;
     auto sync = [&] {
         const bool ok = group_sync(&s_group[ch], tw, gphase);
-        if (!ok) {
-            if (lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
-            drain<nst>(full + warp * nst, stage, phase);
-        }
+        if (!ok && lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
         return ok;
     };
     int left = (int)(u1 - u0); // units whose segments have not ended here
@@ -907,7 +895,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         flags = cf >> 8;
         if (!spin_wait(&full[at], phase)) {
             if (lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
-            drain<nst>(full + warp * nst, stage, phase);
             return;
         }
         uint8_t *st = ring + at * STAGE;
