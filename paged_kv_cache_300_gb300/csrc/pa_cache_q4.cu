@@ -18,11 +18,12 @@ constexpr int kThreads = 256;
 // words, each token's lanes writing half of them; a lone token writes its halves
 // of the words.
 //
-// What bounds it: reading the chunk (5/4 of its bytes move in all) on one side,
-// instructions on the other.  33K rows of 8 bf16 heads x 128 dims (174 MB): 34
-// us, 5.1 TB/s.  With 16 lanes a row, a pair's rows one after the other, it was
-// 44 us and 289 instructions for four rows of 128; now 176, because a row's scale
-// is computed once for 16 elements a lane and arithmetic goes in pairs.
+// What bounds it: moving the bytes (a bf16 chunk's, and a quarter of them again)
+// on one side, instructions on the other.  33K rows of 8 bf16 heads x 128 dims
+// (174 MB): 33 us, 5.3 TB/s.  With 16 lanes a row, a pair's rows one after the
+// other, it was 44 us and 289 instructions for four rows of 128; now 173, because
+// a row's scale is computed once for 16 elements a lane and arithmetic goes in
+// pairs.
 constexpr int kRows = 16;
 // Heads whose rows are held or on their way.  The same chunk with the read-back
 // behind it: 82 us with 1 (no loads beside the sums), 76 with 2, 75 with 3.
