@@ -508,15 +508,22 @@ def _q4_workspace(index, stream, sizes):
         _q4_sizes[key] = nbytes
     if nbytes == 0:
         return None  # sizes the call refuses, or an empty batch
+    if stream is None and torch.cuda.current_device() == index:
+        return _q4_stream_workspace(index, nbytes, 4 * sizes[0] * sizes[2])
+    with torch.cuda.device(index), torch.cuda.stream(stream):  # None: the device's current stream
+        return _q4_stream_workspace(index, nbytes, 4 * sizes[0] * sizes[2])
+
+
+def _q4_stream_workspace(index, nbytes, counter_bytes):
+    """_q4_workspace on the current stream of device `index`, the current one."""
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
-        ws[:4 * sizes[0] * sizes[2]].zero_()
+        ws[:counter_bytes].zero_()
         return ws
-    handle = _current_raw_stream(index) if stream is None else stream.cuda_stream
+    handle = _current_raw_stream(index)
     ws = _q4_workspaces.get((index, handle))
     if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(stream):  # None: the current stream
-            ws = torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=f"cuda:{index}")
         _q4_workspaces[(index, handle)] = ws
     return ws
 

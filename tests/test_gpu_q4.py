@@ -438,6 +438,33 @@ def test_two_captured_graphs_replay_at_once():
         assert torch.equal(out, w)
 
 
+def test_capture_over_two_streams():
+    """A call captured on a stream that is not the current one has a workspace
+    of the graph's too, and leaves none of it to later calls on that stream."""
+    c = make(27, [3000, 100, 2600], 8, 2, 128, 16, BF16)
+    want = _decode(c)[0]
+    a, b = _dev(c), _dev(c)
+    outs = [torch.zeros_like(a["q"]) for _ in range(3)]
+    side = torch.cuda.Stream()
+    call = lambda g, out, **kw: pa.pa_decode_q4(  # noqa: E731
+        g["q"], g["pool"], g["table"], g["lens"], g["k_new"], g["v_new"], out, **kw)
+    held = dict(pa._q4_workspaces)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        call(b, outs[1], stream=side)
+        call(a, outs[0])
+        torch.cuda.current_stream().wait_stream(side)
+    assert pa._q4_workspaces == held
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    call(b, outs[2], stream=side)
+    side.synchronize()
+    for out in outs:
+        assert torch.equal(out, want)
+
+
 def test_one_workspace_for_calls_of_different_sizes():
     cases = [make(30, [900, 20], 8, 2, 128, 16, BF16), make(31, list(range(0, 900, 9)), 16, 16, 64, 32, F32),
              make(32, [6000], 8, 1, 128, 32, BF16)]
