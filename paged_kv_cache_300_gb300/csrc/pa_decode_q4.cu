@@ -42,9 +42,9 @@
 // logical order.  The warps of a head join in shared memory first.
 //
 // What bounds it (bf16; algorithmic bytes over time, a copy runs at 6.8 TB/s):
-//   96 sequences of 4K-16K, 64/8 heads x 128    1068 MB  175 us  6.1 TB/s  HBM; SMs end 5-8% apart
+//   96 sequences of 4K-16K, 64/8 heads x 128    1068 MB  176 us  6.1 TB/s  HBM; SMs end 5-8% apart
 //   256 of 512-4096, 32/8 x 128                   648 MB  116 us  5.6 TB/s  the same
-//   1024 of 257-768, 32/32 x 64                  1237 MB  235 us  5.2 TB/s  a sequence's ends, per head
+//   1024 of 257-768, 32/32 x 64                  1237 MB  228 us  5.4 TB/s  a sequence's ends, per head
 //   64 of 512-4096, 32/8 x 128                    164 MB   42 us  3.9 TB/s  start 5-7 us, join 4-5 us
 //   one of 5000, 32/8 x 128                       5.5 MB   14 us            latency: start, walk, join
 #include "pa_internal.h"
@@ -80,7 +80,7 @@ enum { kLast = 1, kAppend = 2, kBad = 4, kWhole = 8 };
 // segment's last stage only.
 struct alignas(16) Meta {
     int b, hg, len, cnt;       // sequence, head group, cache_seqlens[b], tokens | flags << 8
-    int blocks, nblk, sb, pad; // blocks of the segment and of the sequence, blocks before the sequence
+    int blocks, nblk, sb, blk; // blocks of the segment and of the sequence, blocks before the sequence; its new token's block
 };
 
 // A warp's loader, in shared memory, where it costs the sums no registers.
@@ -214,11 +214,12 @@ struct QWords;
 template <int N>
 struct QWords<__nv_bfloat16, N> {
     uint4 w[N / 8];
+    template <bool SHARED>
     __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool ok)
     {
 #pragma unroll
         for (int i = 0; i < N / 8; ++i)
-            w[i] = ok ? __ldg(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
+            w[i] = ok ? load16<SHARED>(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
     }
     __device__ __forceinline__ float get(int i) const
     {
@@ -230,11 +231,12 @@ struct QWords<__nv_bfloat16, N> {
 template <int N>
 struct QWords<float, N> {
     float4 w[N / 4];
+    template <bool SHARED>
     __device__ __forceinline__ void load(const float *p, bool ok)
     {
 #pragma unroll
         for (int i = 0; i < N / 4; ++i)
-            w[i] = ok ? __ldg(reinterpret_cast<const float4 *>(p) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            w[i] = ok ? load16<SHARED>(reinterpret_cast<const float4 *>(p) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     __device__ __forceinline__ float get(int i) const
     {
@@ -304,19 +306,40 @@ constexpr int kSeqTokens = 200;
 // 40K 54.7, 53.2 and 53.7.
 constexpr int kMaxParts = 8;
 
-// Quantise the new token's rows of kv head kvh, K in lanes 0-7 and V in 8-15,
-// and write them into the pool and into the staged record (token t of the
-// record at `rec`).
-template <int D, int BS, typename T>
-__device__ __noinline__ void append(const DecodeQ4Args &a, int b, int kvh, int L, int t, uint8_t *rec)
+// A slot of a ring: a stage's records and behind them, where 16 warps' slots leave
+// the room, the head's rows of q (with a segment's first stage) and its new rows
+// (with the stage that takes them).  They come with the stage's copies and spare a
+// warp two trips to L2 at every sequence, on which 16 warps with sequences of equal
+// length wait at the same time: 1024 sequences of 257 to 768 tokens, 32 heads of
+// either kind, 235 -> 228 us.
+template <int D, int R, typename T>
+struct Slot {
+    static constexpr bool with_q = D == 64, with_new = D == 64 || R == 2;
+    static constexpr int tokens = 16 * (R < 2 ? 2 : R), row = D * (int)sizeof(T);
+    static constexpr int q = tokens * (D + 8); // where q starts
+    static constexpr int k_new = q + (with_q ? 8 / R * row : 0);
+    static constexpr int v_new = k_new + (with_new ? row : 0);
+    static constexpr int bytes = v_new + (with_new ? row : 0);
+};
+
+// Quantise the new token's rows of the warp's head, K in lanes 0-7 and V in 8-15,
+// and write them into the pool and into the stage at `st`, whose last token it is
+// (cnt tokens; `mt` is its note).
+template <int D, int BS, int R, typename T>
+__device__ __noinline__ void append(const DecodeQ4Args &a, const Meta &mt, int hs, int ch, int cnt, uint8_t *st)
 {
     constexpr int NC = D / 64;
+    using S = Slot<D, R, T>;
     const int lane = threadIdx.x & 31, l = lane & 7;
     const bool value = lane & 8;
-    const size_t src = ((size_t)b * a.num_kv_heads + kvh) * D + l * 8;
+    const int kvh = mt.hg * hs + ch, blk = mt.blk, t = (cnt - 1) % BS;
+    uint8_t *rec = st + (cnt - 1) / BS * q4_record_bytes(D, BS);
+    const size_t src = ((size_t)mt.b * a.num_kv_heads + kvh) * D + l * 8;
     Q4Row<T, NC> x;
-    x.load(static_cast<const T *>(value ? a.v_new : a.k_new) + src);
-    const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks_per_seq + L / BS);
+    if constexpr (S::with_new)
+        x.template load<true>(reinterpret_cast<const T *>(st + (value ? S::v_new : S::k_new)) + l * 8);
+    else
+        x.template load<false>(static_cast<const T *>(value ? a.v_new : a.k_new) + src);
     Q4Scale s;
     uint32_t c[NC];
     q4_quantise(x, s, c);
@@ -460,9 +483,11 @@ __device__ __forceinline__ void copy_async_wait()
 
 // The loader's slower steps: everything but a stage of whole blocks inside a
 // segment.  Not inlined, so that its registers do not weigh on the sums.
-template <int D, int BS, int SB, typename T>
+template <int D, int BS, int R, typename T>
 struct Loader {
+    using S = Slot<D, R, T>;
     static constexpr int REC = q4_record_bytes(D, BS);
+    static constexpr int SB = S::tokens / BS; // blocks of a stage
 
     // fetch the entries of the warp's blocks o0.. of a segment into window w
     static __device__ __forceinline__ void fetch(const DecodeQ4Args &a, LoadState &ld, int w, int b, bool ok, int j0,
@@ -484,12 +509,12 @@ struct Loader {
     {
         const int lane = threadIdx.x & 31;
         const size_t row = (size_t)b * a.num_kv_heads + kvh;
-        for (int o = lane * 128; o < a.group * D * (int)sizeof(T); o += 32 * 128)
+        for (int o = lane * 128; !S::with_q && o < a.group * S::row; o += 32 * 128)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(a.q) +
-                                                          row * a.group * D * sizeof(T) + o));
-        if (ends && lane < 2)
+                                                          row * a.group * S::row + o));
+        if (!S::with_new && ends && lane < 2)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                static_cast<const char *>(lane ? a.v_new : a.k_new) + row * D * sizeof(T)));
+                static_cast<const char *>(lane ? a.v_new : a.k_new) + row * S::row));
     }
     // start of the segment (b, hg) from block j0 on, with `rem` units left;
     // len2 has been fetched
@@ -556,26 +581,36 @@ struct Loader {
         if (here && ok && !valid) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
         const int loads = __popc(__ballot_sync(kFull, valid));
         const bool last = li == lend;
+        const int pos0 = blk0 * BS, kvh = hg * hs + ch;
+        const bool takes = ok && loads == blocks && blocks > 0 && len < pos0 + blocks * BS; // the new token
+        const int tail = __shfl_sync(kFull, p, (blocks - 1) & 31);
         if (lane == 0) {
-            const int pos0 = blk0 * BS;
             const int cnt = blocks > 0 && ok ? min(blocks * BS, len - pos0 + 1) : 0;
             int flags = last ? kLast : 0;
             if (loads < blocks || !ok) flags |= kBad;
-            if (ok && loads == blocks && blocks > 0 && len < pos0 + blocks * BS) flags |= kAppend;
+            if (takes) flags |= kAppend;
             if (j0 == 0 && je == nblk) flags |= kWhole;
             int4 *mt = reinterpret_cast<int4 *>(meta);
             mt[0] = make_int4(b, hg, len, cnt | flags << 8);
-            mt[1] = make_int4(je - j0, nblk, sb, 0);
-            if (loads > 0)
-                mbar_arrive_expect_tx(bar, loads * REC);
+            mt[1] = make_int4(je - j0, nblk, sb, tail);
+            uint32_t bytes = loads * REC;
+            if (S::with_q && li == 0) bytes += a.group * S::row;
+            if (S::with_new && takes) bytes += 2 * S::row;
+            if (bytes > 0)
+                mbar_arrive_expect_tx(bar, bytes);
             else
                 mbar_arrive(bar);
         }
         __syncwarp();
+        const size_t row = (size_t)b * a.num_kv_heads + kvh;
+        if (S::with_q && lane == 31 && li == 0)
+            bulk_load(dst + S::q, static_cast<const char *>(a.q) + row * a.group * S::row, a.group * S::row, bar);
+        if (S::with_new && lane >= 29 && lane < 31 && takes)
+            bulk_load(dst + (lane == 29 ? S::k_new : S::v_new),
+                      static_cast<const char *>(lane == 29 ? a.k_new : a.v_new) + row * S::row, S::row, bar);
         if (valid)
             bulk_load(dst + lane * REC,
-                      static_cast<const uint8_t *>(a.kv_cache) + ((size_t)p * a.num_kv_heads + hg * hs + ch) * REC, REC,
-                      bar);
+                      static_cast<const uint8_t *>(a.kv_cache) + ((size_t)p * a.num_kv_heads + kvh) * REC, REC, bar);
         bool switched = false;
         if (last) {
             const int rem = rem0 - (je - j0);
@@ -632,7 +667,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     constexpr int NTILE = R < 2 ? 2 : R;            // 16-token tiles of a stage
     constexpr int ST = 16 * NTILE;                  // tokens of a stage
     constexpr int SB = ST / BS;                     // blocks of a stage
-    constexpr int STAGE = ST * (D + 8);             // bytes
+    using S = Slot<D, R, T>;
     constexpr int KW = D / 32;                      // words of a lane's row part
     constexpr int MT = D / 16;                      // 16-dim tiles of the output
     constexpr int DL = D / 8;                       // output dims of a lane
@@ -659,7 +694,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     const long long cap = (long long)mbps * BS;
     // rings of the consumers, barriers, metadata, join buffers
     uint8_t *ring = smem;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + (size_t)ncw * nst * STAGE);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + (size_t)ncw * nst * S::bytes);
     Meta *meta = reinterpret_cast<Meta *>(full + ((ncw * nst + 1) & ~1));
     float *join = reinterpret_cast<float *>(meta + ncw * nst);
 
@@ -762,10 +797,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     // Every warp fills its own ring: it issues a stage's copies as soon as it
     // has used the slot up, so no other warp and no second barrier is waited
     // for.
-    using L = Loader<D, BS, SB, T>;
+    using L = Loader<D, BS, R, T>;
     LoadState &ld = s_load[warp];
     auto issue = [&](int at) {
-        const uint32_t dst = smem_u32(ring + at * STAGE);
+        const uint32_t dst = smem_u32(ring + at * S::bytes);
         const int e = ld.e;
         if (e < ld.elim) { // SB whole blocks inside a segment
             if (elect_one()) {
@@ -838,9 +873,18 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             l0 = l1 = lo0 = lo1 = 0.f;
             const int g = r % CW;
             QWords<T, KW * 8> qw;
-            qw.load(static_cast<const T *>(a.q) +
-                        ((size_t)meta[at].b * Hq + (size_t)(meta[at].hg * hs + ch) * G + g) * D + c * (KW * 8),
-                    g < G);
+            if constexpr (S::with_q) {
+                if (!spin_wait(&full[at], phase)) {
+                    if (lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
+                    return;
+                }
+                qw.template load<true>(reinterpret_cast<const T *>(ring + at * S::bytes + S::q) + g * D + c * (KW * 8), g < G);
+            } else {
+                qw.template load<false>(static_cast<const T *>(a.q) +
+                                            ((size_t)meta[at].b * Hq + (size_t)(meta[at].hg * hs + ch) * G + g) * D +
+                                            c * (KW * 8),
+                                        g < G);
+            }
             float amax = 0.f, sum = 0.f;
 #pragma unroll
             for (int i = 0; i < KW * 8; ++i) {
@@ -897,14 +941,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             if (lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
             return;
         }
-        uint8_t *st = ring + at * STAGE;
+        uint8_t *st = ring + at * S::bytes;
         int cnt = ST;
         if (cf != ST) { // not SB whole blocks inside a segment
             bad |= (flags & kBad) != 0;
             cnt = (flags & kBad) ? 0 : cf & 255;
             if (flags & kAppend)
-                append<D, BS, T>(a, meta[at].b, meta[at].hg * hs + ch, meta[at].len, (cnt - 1) % BS,
-                                 st + (cnt - 1) / BS * REC);
+                append<D, BS, R, T>(a, meta[at], hs, ch, cnt, st);
         }
         if (cnt > 0) {
             // ---- products of the tiles, one chain each
@@ -1284,11 +1327,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 constexpr int kMaxDev = 64;
 constexpr size_t kSmemPerCta = 210 * 1024; // of 227, beside the static arrays
 
-template <int D, int R>
+template <int D, int R, typename T>
 size_t smem_bytes(int ncw, int tw, int group)
 {
-    const int stage_tokens = 16 * (R < 2 ? 2 : R);
-    return (size_t)ncw * kSlots * (stage_tokens * (D + 8) + 8 + sizeof(Meta)) + 8 +
+    return (size_t)ncw * kSlots * (Slot<D, R, T>::bytes + 8 + sizeof(Meta)) + 8 +
            (tw > 1 ? (size_t)ncw * group * D * 4 : 0);
 }
 
@@ -1311,9 +1353,9 @@ int make_plan(int batch, int num_kv_heads, int group, Plan *p)
     for (int h = 2; h <= kMaxWarps && h <= num_kv_heads; ++h)
         if (num_kv_heads % h == 0 && (long long)kMaxParts * batch * num_kv_heads >= (long long)p->ctas * h) hs = h;
     const int tw = kMaxWarps / hs, ncw = hs * tw;
-    static_assert(kMaxWarps * (kSlots * (16 * (R < 2 ? 2 : R) * (D + 8) + 8 + sizeof(Meta)) + 8 / R * D * 4) + 8 <=
+    static_assert(kMaxWarps * (kSlots * (Slot<D, R, T>::bytes + 8 + sizeof(Meta)) + 8 / R * D * 4) + 8 <=
                   kSmemPerCta, "a full CTA's rings and join buffers fit");
-    p->smem = smem_bytes<D, R>(ncw, tw, group);
+    p->smem = smem_bytes<D, R, T>(ncw, tw, group);
     static int raised[kMaxDev];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return PA_ERR_DEVICE;
@@ -1360,9 +1402,10 @@ int plan_and_launch(const DecodeQ4Args *a, int batch, int num_kv_heads, int grou
 
 // Copies of the head group in the products' columns: as many as fit, up to
 // the tiles of a stage.  1024 sequences with D 64 and one head a kv head: 235 us
-// with four copies, 274 with two.  256 sequences with D 128 and four heads a kv
-// head: 116 us with two, 122 with none.  Four copies (64-token stages) are for
-// head_dim 64 only: at 128 their rings would not fit 16 warps.
+// with four copies, 274 with two, q and the new rows not in the slots yet.  256
+// sequences with D 128 and four heads a kv head: 116 us with two, 122 with none.
+// Four copies (64-token stages) are for head_dim 64 only: at 128 their rings
+// would not fit 16 warps.
 template <int D, int BS, typename T>
 int by_copies(const DecodeQ4Args *a, int batch, int num_kv_heads, int group, size_t have, size_t *need, cudaStream_t s)
 {

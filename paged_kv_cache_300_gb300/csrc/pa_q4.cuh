@@ -72,6 +72,16 @@ __device__ __forceinline__ uint32_t q4_pack_scale(const Q4Scale &s)
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// 16 bytes of global memory that nothing writes meanwhile, or of shared memory.
+template <bool SHARED, typename V>
+__device__ __forceinline__ V load16(const V *p)
+{
+    if constexpr (SHARED)
+        return *p;
+    else
+        return __ldg(p);
+}
+
 // A row is held by 8 neighbouring lanes, four rows a warp: lane l has the dims
 // 64 c + 8 l .. + 7, c < NC = D / 64, in the type they came in (bf16 stays
 // packed in pairs until a value is needed).
@@ -80,13 +90,14 @@ struct Q4Row;
 template <int NC>
 struct Q4Row<float, NC> {
     float v[NC][8];
+    template <bool SHARED = false>
     __device__ __forceinline__ void load(const float *p)
     {
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
-                const float4 x = __ldg(reinterpret_cast<const float4 *>(p + 64 * c + i));
+                const float4 x = load16<SHARED>(reinterpret_cast<const float4 *>(p + 64 * c + i));
                 v[c][i] = x.x;
                 v[c][i + 1] = x.y;
                 v[c][i + 2] = x.z;
@@ -123,11 +134,12 @@ struct Q4Row<float, NC> {
 template <int NC>
 struct Q4Row<__nv_bfloat16, NC> {
     uint32_t w[NC][4];
+    template <bool SHARED = false>
     __device__ __forceinline__ void load(const __nv_bfloat16 *p)
     {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p + 64 * c));
+            const uint4 x = load16<SHARED>(reinterpret_cast<const uint4 *>(p + 64 * c));
             w[c][0] = x.x;
             w[c][1] = x.y;
             w[c][2] = x.z;
