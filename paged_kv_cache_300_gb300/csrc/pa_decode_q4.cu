@@ -43,7 +43,7 @@
 //
 // What bounds it (bf16; algorithmic bytes over time, a copy runs at 6.8 TB/s):
 //   96 sequences of 4K-16K, 64/8 heads x 128    1068 MB  176 us  6.1 TB/s  HBM; SMs end 5-8% apart
-//   256 of 512-4096, 32/8 x 128                   648 MB  116 us  5.6 TB/s  the same
+//   256 of 512-4096, 32/8 x 128                   648 MB  114 us  5.7 TB/s  the same
 //   1024 of 257-768, 32/32 x 64                  1237 MB  228 us  5.4 TB/s  a sequence's ends, per head
 //   64 of 512-4096, 32/8 x 128                    164 MB   42 us  3.9 TB/s  start 5-7 us, join 4-5 us
 //   one of 5000, 32/8 x 128                       5.5 MB   14 us            latency: start, walk, join
