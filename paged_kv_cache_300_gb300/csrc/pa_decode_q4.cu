@@ -26,8 +26,19 @@
 //    instruction), the products come in both signs and the cuts cancel.
 //  * q is scaled by a power of two per head into f16's range (a bf16 number
 //    keeps all its bits); fp32 operands run as a sum of two f16 numbers.
-//  * p s is rounded to f16 (half a step 2^-11; the sum of p is not rounded).
-//    Its reference m follows the maximum of x + log2(s), so that p s, not p, is
+//  * p s is rounded to f16 (half a step 2^-11; the sums of p and of p b are not
+//    rounded), and what the rounding leaves is not dropped where that is cheap.
+//    With fp32 operands, and where the heads stand in the columns more than once,
+//    the rest goes along as a second f16 number, in the second case in a copy whose
+//    columns would be zero for that tile, so it costs no product: 2^-22 of a weight.
+//    bf16 groups of 5 to 8 heads fill the columns; a second pass of products took
+//    96 long sequences from 176.5 to 206 us.  There the rest is applied to the
+//    middle code: sum w n is off by sum (w' - w) (n - 7.5) instead of
+//    sum (w' - w) n.  Distance to 64 bits, beside 1.663e-3 (64 sequences, two
+//    copies), 1.657e-3 (1024, four) and 1.657e-3 (96, none) of the result's own
+//    rounding: with w' alone 1.756, 1.733 and 1.755e-3 (42.0, 228.7 and 176.5 us),
+//    now 1.663, 1.657 and 1.671e-3 (42.3, 233.6 and 178.5 us).
+//  * The reference m of p s follows the maximum of x + log2(s), so that p s, not p, is
 //    at most 2^14; it moves only when p s would pass that, and then
 //    leaves it at 2^9.  So a weight keeps f16's 11 bits down to 2^-23 of the
 //    largest one, and is off by 2^-34 of that at most below.
@@ -656,7 +667,8 @@ struct Loader {
 // query heads stands in them R times, and copy `rep` of a score belongs to
 // tile `rep` of R: every lane then turns the scores of its own tile into
 // weights (1 / R of the work), the weights of a tile are left in its own copy
-// (the others are masked to zero), and the copies' sums are added at the end.
+// (bf16: what their rounding left in the neighbouring one; the others are masked to
+// zero), and the copies' sums are added at the end.
 // R = 1 has two tiles a stage as well, and every lane works on both.
 template <int D, int BS, int R, typename T>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1)
@@ -848,7 +860,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     auto tile_at = [](int t, int row_bytes) { return BS == 16 ? t * REC : (t >> 1) * REC + (t & 1) * 16 * row_bytes; };
     const uint32_t s_off = q4_scale_offset(D, BS) + r * 8;
     T *outp = static_cast<T *>(a.out);
-    const float odd15 = (r & 1) ? 15.f : 0.f; // rows r and r + 8 are tokens of r's parity
+    // rows r and r + 8 are tokens of r's parity
+    constexpr bool SECOND = F32 || R > 1; // the weights as two f16 numbers
+    const float base = SECOND ? (r & 1) ? 15.f : 0.f : 7.5f;
+    const float centre = (r & 1) ? 7.5f : -7.5f;
     const uint32_t odd_sign = (r & 1) ? 0x80008000u : 0u;
 
     uint32_t qh[KW][2][2], ql[F32 ? KW : 1][2][2];
@@ -1002,7 +1017,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                 for (int k = 0; k < 2; ++k) {
                     const float ks = bf16_lo(sc[k][0]), kl = bf16_hi(sc[k][0]);
                     vst[t][k] = bf16_lo(sc[k][1]);
-                    vlo[t][k] = fmaf(vst[t][k], odd15, bf16_hi(sc[k][1]));
+                    vlo[t][k] = fmaf(vst[t][k], base, bf16_hi(sc[k][1]));
                     if constexpr (F32) {
                         // around the middle code, where the two terms do not cancel
                         const float mid = fmaf(ks, 7.5f, kl);
@@ -1074,7 +1089,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                     }
             }
             // ---- weights, their sums, and the values' B operand
-            uint32_t wh[XT][2], wl[F32 ? XT : 1][2];
+            uint32_t wh[XT][2], wl[SECOND ? XT : 1][2];
 #pragma unroll
             for (int t = 0; t < XT; ++t)
 #pragma unroll
@@ -1086,10 +1101,15 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                     lo1 = fmaf(p1, vlo[t][k], lo1);
                     const float w0 = p0 * vst[t][k], w1 = p1 * vst[t][k];
                     const uint32_t pk = pack_f16(w0, w1);
+                    const __half2 h = *reinterpret_cast<const __half2 *>(&pk);
                     wh[t][k] = movmatrix_trans(pk ^ odd_sign);
-                    if constexpr (F32) {
-                        const __half2 h = *reinterpret_cast<const __half2 *>(&pk);
+                    if constexpr (SECOND) {
                         wl[t][k] = movmatrix_trans(pack_f16(w0 - __low2float(h), w1 - __high2float(h)) ^ odd_sign);
+                        // to the columns of the neighbouring copy
+                        if constexpr (!F32) wl[t][k] = __shfl_xor_sync(kFull, wl[t][k], 4 * CW);
+                    } else { // an even token's 7.5 w - 7.5 w', an odd one's 7.5 w + 7.5 w'
+                        lo0 = fmaf(__low2float(h), centre, lo0);
+                        lo1 = fmaf(__high2float(h), centre, lo1);
                     }
                 }
             // ---- O^T += V^T (p s)^T
@@ -1106,7 +1126,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                     for (int k = 0; k < 2; ++k) {
                         const bool own = R == 1 || brep == tile;
                         bh[tt][k] = own ? wh[R == 1 ? tt : 0][k] : 0u;
-                        if constexpr (F32) bl[tt][k] = own ? wl[R == 1 ? tt : 0][k] : 0u;
+                        if constexpr (F32)
+                            bl[tt][k] = own ? wl[R == 1 ? tt : 0][k] : 0u;
+                        else if constexpr (SECOND)
+                            bh[tt][k] = brep == (tile ^ 1) ? wl[0][k] : bh[tt][k];
                     }
                 }
 #pragma unroll

@@ -543,3 +543,39 @@ def test_serving_steps(d, bs, hq, hkv):
     used = sum(-(-h // bs) for h in hist)
     assert count.item() == nb - used
     assert np.unique(np.concatenate([table[r].cpu().numpy()[:-(-hist[r] // bs)] for r in range(b)])).size == used
+
+
+# ------------------------------------------------------------------ exactness
+@pytest.mark.parametrize("d,bs,hq,hkv,left", [(128, 16, 32, 8, 2.0 ** -13), (128, 32, 6, 3, 2.0 ** -13),
+                                              (64, 32, 16, 16, 2.0 ** -13), (64, 16, 16, 4, 2.0 ** -13),
+                                              (128, 16, 64, 8, 2.1e-4), (64, 32, 40, 8, 2.1e-4)])
+def test_decode_bf16_is_off_by_little_but_its_own_rounding(d, bs, hq, hkv, left):
+    """The 2-norm of the error is h, that of the reference's own rounding to
+    bf16, and beside it e, what the sums before the rounding are off by:
+    sqrt(h^2 + e^2), the two being independent.
+
+    Up to 4 heads a kv head: weights are sums of two f16 numbers (2^-22), and a
+    score is off by 2^-17 of its largest product, 15 s max|q| scale <= 15 x 0.4 x
+    5 x 0.125 < 4, in each of up to 8 steps that add up as roots: < 2^-13 of p, and
+    as much of the result at most.
+
+    5 to 8: a weight m 2^k, 1 <= m < 2, is off by an even spread over +-2^-11 2^k,
+    2^-11 / (m sqrt(3)) of itself in the root mean square, and 1 / m^2 is
+    (1 - 1/4) / (2 log 2) = 0.54 on average over logarithms that are spread evenly:
+    2.1e-4.  That meets s (n - 7.5), which is no larger than the spread of the
+    values that the result is a mean of.
+
+    The two meet in 2 e h over the root of 16384 elements, 0.3% of h^2 for e = 0.2 h.
+    """
+    c = make(40 + d + hq, [1100 + 37 * i for i in range(max(4, 16384 // (hq * d)))], hq, hkv, d, bs, BF16)
+    codes = c["pool"][:, :, :bs * d]  # middle codes are more frequent than those at the ends, as in normal data
+    more = np.random.default_rng(hq).integers(0, 256, codes.shape, dtype=np.uint8)
+    codes[:] = ((codes & 15) + (more & 15)) // 2 | ((codes >> 4) + (more >> 4)) // 2 << 4
+    out, _, _, _, err = _decode(c)
+    assert err == 0
+    ref, _ = q4.decode(_f32(c["q"]), c["pool"], c["table"], c["lens"], _f32(c["k_new"]), _f32(c["v_new"]), bs)
+    ref = torch.from_numpy(ref)
+    size = ref.norm()
+    h = float((ref.to(BF16).double() - ref).norm() / size)
+    got = float((out.cpu().double() - ref).norm() / size)
+    assert got <= (h * h + left * left) ** 0.5 * 1.002, (got, h)
