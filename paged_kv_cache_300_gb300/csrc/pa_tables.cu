@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a)
                 a.seqlens_k[b] = s_len[b];
             }
         }
-        for (int i = cta * kThreads + tid; i < a.total_slots; i += ncta * kThreads) a.slot_map[i] = -1;
+        // (the last step of a slot map of nearly 2^31 entries passes 32 bits)
+        for (long long i = cta * kThreads + tid; i < a.total_slots; i += ncta * kThreads) a.slot_map[i] = -1;
         return;
     }
 

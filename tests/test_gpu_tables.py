@@ -171,3 +171,26 @@ def test_captured_step_advances_lengths_and_stack_in_place():
         assert np.array_equal(g_len.cpu().numpy(), lens) and nf.item() == count
         assert np.array_equal(outs[1].cpu().numpy(), cu_k)
     assert err.item() == 0
+
+
+@pytest.mark.parametrize("new,flag", [([40, 16], 0), ([40, -2], pa.DEVERR_OVERFLOW)])
+def test_the_largest_slot_map_is_filled_to_its_end_and_no_further(new, flag):
+    """2^31 - 1 slots, served and refused: the index of a thread's last step
+    does not fit 32 bits.  The map lies between other data."""
+    n, lens, bs = 2 ** 31 - 1, [16, 16], 16
+    if torch.cuda.mem_get_info()[0] < 12 * 2 ** 30:
+        pytest.skip("needs 12 GB")
+    memory = torch.full((n + 2048,), 77, dtype=torch.int32, device=DEV)
+    slots = memory[1024:1024 + n]
+    lens, new, table, free = make(4, lens, new, bs, 5)
+    t = lambda x: torch.from_numpy(np.array(x)).to(DEV)  # noqa: E731
+    err = t(np.zeros(1, dtype=np.int32))
+    nf = t(np.array([5], dtype=np.int32))
+    cu_q, _, _ = pa.pa_block_tables(t(lens), t(new), t(table), t(free), nf, slots, bs, dev_err=err)
+    assert err.item() == flag
+    tokens = int(cu_q[-1].item())
+    assert tokens == (0 if flag else 56)
+    assert (slots[:tokens] >= 0).all()
+    for at in range(tokens, n, 2 ** 28):
+        assert (slots[at:min(n, at + 2 ** 28)] == -1).all()
+    assert (memory[:1024] == 77).all() and (memory[1024 + n:] == 77).all()
