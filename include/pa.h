@@ -320,10 +320,10 @@ int pa_cache_update_q4(const void *k_chunk, const void *v_chunk, const int32_t *
  * Read back: rows [cu_seq_lens_k[r], cu_seq_lens_k[r+1]) of k_full, v_full
  * [total_k, num_kv_heads, head_dim] receive logical positions 0, 1, .. of
  * request r as values (b + n s in fp32, rounded to dtype), which pa_varlen
- * takes as they are (total_k * num_kv_heads < 2^31 - 64).  Rows behind
- * cu_seq_lens_k[batch] are left as they were.  A needed block_table entry that is no block sets
- * PA_DEVERR_BAD_BLOCK, a position beyond the table PA_DEVERR_OVERFLOW; those
- * rows are zeroed.  cu_seq_lens_k that does not start at 0, decreases or
+ * takes as they are (total_k * num_kv_heads < 2^31 - 64, total_k / block_size +
+ * batch < 2^31).  Rows behind cu_seq_lens_k[batch] are left as they were.  A
+ * needed block_table entry that is no block sets PA_DEVERR_BAD_BLOCK, a position
+ * beyond the table PA_DEVERR_OVERFLOW; those rows are zeroed.  cu_seq_lens_k that does not start at 0, decreases or
  * passes total_k sets PA_DEVERR_BAD_CU; nothing behind total_k is written.
  */
 int pa_cache_gather_q4(const void *kv_cache, const int32_t *block_table,

@@ -71,6 +71,8 @@ int pa_cache_gather_q4(const void *kv_cache, const int32_t *block_table,
     if (rc != PA_OK) return rc;
     if (batch < 0 || total_k < 0 || max_blocks_per_seq <= 0) return PA_ERR_SHAPE;
     if ((long long)total_k * num_kv_heads >= (1ll << 31) - 64) return PA_ERR_UNSUPPORTED;
+    // the grid has a CTA for every block of total_k rows and one more for every request
+    if ((long long)total_k / block_size + batch >= 1ll << 31) return PA_ERR_UNSUPPORTED;
     if (batch == 0 || total_k == 0) return PA_OK;
     if (!kv_cache || !block_table || !cu_seq_lens_k || !k_full || !v_full) return PA_ERR_NULL;
     if (!aligned(kv_cache, 16) || !aligned(k_full, 16) || !aligned(v_full, 16) || !aligned(block_table, 4) ||

@@ -172,3 +172,9 @@ def test_table_reference_worked_example():
     assert t[2].tolist() == [3, 5, 6, 2] and n == 2 and slots[-1] == 2 * 32 and lens.tolist() == [0, 33, 97]
     assert q4.block_tables([0], [200], table[:1], free, 3, 300, 32) is None  # longer than the row
     assert q4.block_tables([0, 0], [64, 64], table[:2], free, 3, 300, 32) is None  # three free blocks
+
+
+def test_gather_refuses_a_grid_past_31_bits(lib):
+    assert _gather(lib, b=2 ** 31 - 1, t=64) == -4
+    assert _gather(lib, b=2 ** 31 - 4, t=64, k=None) == -4
+    assert _gather(lib, b=2 ** 31 - 5, t=64, k=None) == -1
