@@ -429,6 +429,13 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _c_int(*sizes):
+    """Refuse sizes that the C interface's int does not hold (ctypes would cut
+    them to 32 bits)."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise ValueError(f"a size of {max(sizes)} passes 2^31 - 1")
+
+
 def pa_q4_block_bytes(num_kv_heads, head_dim, block_size) -> int:
     """Bytes of one block of the 4-bit pool; 0 for sizes it does not have."""
     return int(load().pa_q4_block_bytes(num_kv_heads, head_dim, block_size))
@@ -450,6 +457,7 @@ def pa_cache_update_q4(k_chunk, v_chunk, slot_map, kv_cache, dev_err=None, strea
     its row."""
     shape = k_chunk.shape
     t, hkv, d = shape
+    _c_int(t)
     dt = _dtype(k_chunk)
     index, nb, bs = _q4_geometry(kv_cache, hkv, d)
     if v_chunk.shape != shape or not _fits(index, k_chunk.dtype, k_chunk, v_chunk):
@@ -470,6 +478,7 @@ def pa_cache_gather_q4(kv_cache, block_table, cu_seq_lens_k, k_full, v_full, dev
     dt = _dtype(k_full)
     index, nb, bs = _q4_geometry(kv_cache, hkv, d)
     b, mb = block_table.shape
+    _c_int(tk, b, mb)
     if v_full.shape != shape or not _fits(index, k_full.dtype, k_full, v_full):
         _refuse(index, k_full.dtype, k_full=k_full, v_full=v_full)
     if cu_seq_lens_k.shape != (b + 1,) or \
@@ -552,6 +561,7 @@ def pa_decode_q4(q, kv_cache, block_table, cache_seqlens, k_new, v_new, out=None
         _refuse(index, dtype, q=q, out=out, k_new=k_new, v_new=v_new, k_stored=k_stored,
                 v_stored=v_stored)
     tb, mb = block_table.shape
+    _c_int(b, mb)
     if tb != b or cache_seqlens.shape != (b,) or \
             not _fits(index, torch.int32, block_table, cache_seqlens, dev_err):
         _refuse(index, torch.int32, block_table=block_table, cache_seqlens=cache_seqlens,
@@ -601,9 +611,11 @@ def pa_block_tables(cache_seqlens, new_lens, block_table, free_blocks, num_free,
             free_blocks.dim() != 1 or slot_map.dim() != 1 or num_free.numel() != 1 or \
             num_free_out.numel() != 1:
         raise ValueError("inconsistent shapes")
+    slots, blocks = slot_map.numel(), free_blocks.numel()
+    _c_int(b, slots, blocks, mb, block_size)
     _launch("pa_block_tables", index, stream, cache_seqlens.data_ptr(), new_lens.data_ptr(),
             block_table.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(),
             slot_map.data_ptr(), cu_seq_lens_q.data_ptr(), cu_seq_lens_k.data_ptr(),
-            seqlens_k.data_ptr(), num_free_out.data_ptr(), b, slot_map.numel(),
-            free_blocks.numel(), block_size, mb, _addr(dev_err))
+            seqlens_k.data_ptr(), num_free_out.data_ptr(), b, slots, blocks, block_size, mb,
+            _addr(dev_err))
     return cu_seq_lens_q, cu_seq_lens_k, seqlens_k

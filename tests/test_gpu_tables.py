@@ -194,3 +194,22 @@ def test_the_largest_slot_map_is_filled_to_its_end_and_no_further(new, flag):
     for at in range(tokens, n, 2 ** 28):
         assert (slots[at:min(n, at + 2 ** 28)] == -1).all()
     assert (memory[:1024] == 77).all() and (memory[1024 + n:] == 77).all()
+
+
+def test_sizes_that_do_not_fit_an_int_are_refused():
+    """2^32 entries would reach the library as 0, 2^32 + 4 as 4."""
+    if torch.cuda.mem_get_info()[0] < 20 * 2 ** 30:
+        pytest.skip("needs 20 GB")
+    big = torch.empty(2 ** 32 + 4, dtype=torch.int32, device=DEV)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    args = dict(table=i32(0, 0).view(1, 2), free=i32(0, 0, 0), slots=i32(0))
+    for name, t in (("slots", big), ("free", big), ("table", big.view(1, -1))):
+        a = {**args, name: t}
+        with pytest.raises(ValueError, match="2\\^31"):
+            pa.pa_block_tables(i32(3), i32(0), a["table"], a["free"], i32(1), a["slots"], 16)
+    rows = lambda: torch.zeros(1, 1, 64, device=DEV)  # noqa: E731
+    pool = pa.pa_q4_pool(2, 1, 64, 16)
+    with pytest.raises(ValueError, match="2\\^31"):
+        pa.pa_decode_q4(rows(), pool, big.view(1, -1), i32(0), rows(), rows())
+    with pytest.raises(ValueError, match="2\\^31"):
+        pa.pa_cache_gather_q4(pool, big.view(1, -1), i32(0, 1), rows(), rows())
