@@ -280,7 +280,9 @@ int pa_varlen_paged(const void *q, const void *k_cache, const void *v_cache,
  * stands for b + n s.  With fl = rounding to fp32 after each operation:
  *   b   = min x, rounded down to bf16
  *   r   = fl(fl(max x / 16 - b / 16) * fl(16 / 15))
- *   s   = r rounded up to bf16; 0 when r < 2^-100
+ *   s   = r rounded up to bf16; 0 when r < 2^-100; up to twice the bf16
+ *         number below while fl(b + 15 s) is larger than every bf16 number
+ *         (rows with a value near 3.4e38)
  *   n_i = round-half-even(fl(fl(x_i / 16 - b / 16) * fl(16 / s))), at most 15
  *         (0 when s = 0)
  * so |x_i - (b + n_i s)| <= s / 2 up to the fp32 roundings.  A row that

@@ -10,6 +10,9 @@ from __future__ import annotations
 import numpy as np
 
 
+BF16_MAX = (2 - 2.0 ** -7) * 2.0 ** 127
+
+
 def bf16_bits_to_f64(bits):
     return (np.asarray(bits, dtype=np.uint16).astype(np.uint32) << 16).view(np.float32).astype(np.float64)
 
@@ -34,6 +37,9 @@ def quantise(x):
     with np.errstate(over="ignore", invalid="ignore"):
         r = (hi * f(0.0625) - low * f(0.0625)) * f(16.0 / 15.0)
         step_bits = np.where(r < f(2.0 ** -100), np.uint32(0), _step_bits(r)).astype(np.uint32)
+        for _ in range(2):  # a top value that would read back as an infinity
+            top = (15 * step_bits.view(f).astype(np.float64) + low).astype(f)
+            step_bits = np.where(finite & (top > f(BF16_MAX)), step_bits - np.uint32(0x10000), step_bits)
         step = step_bits.view(f)
         some = finite & (step > 0)
         inv = f(16) / np.where(some, step, f(1))

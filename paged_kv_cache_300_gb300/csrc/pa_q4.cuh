@@ -20,6 +20,8 @@ __device__ __forceinline__ int q4_v_unit(int t, int x)
     return 2 * (p * (D / 4) + u * 8 + (x & 7)) + (t & 1);
 }
 
+constexpr float kBf16Max = 3.3895313892515355e38f; // (2 - 2^-7) 2^127
+
 // Step, low and 16 / step of a row with the given extrema.  Each operation
 // is rounded on its own (no contraction), because the codes are defined by
 // these fp32 steps.
@@ -51,6 +53,14 @@ __device__ __forceinline__ Q4Scale q4_scale(float lo, float hi, bool finite)
     r.low16 = __fmul_rn(r.low, 0.0625f);
     const float range = __fmul_rn(__fsub_rn(__fmul_rn(hi, 0.0625f), r.low16), 16.0f / 15.0f);
     r.step = range < 7.888609052210118e-31f /* 2^-100 */ ? 0.f : bf16_away(range);
+    // A top code past the largest number would read back as an infinity.  Two bf16
+    // steps less always do: 15 s is within 2^-7 of max - b, each step takes at least
+    // that much off, and the top value is then off by 30 2^-7 s < s / 2.  The 33K-row
+    // update with its read-back: 76.2 us without this, 76.7 with it.
+    if (fmaf(15.f, r.step, r.low) > kBf16Max) {
+        r.step = __uint_as_float(__float_as_uint(r.step) - 0x10000u);
+        if (fmaf(15.f, r.step, r.low) > kBf16Max) r.step = __uint_as_float(__float_as_uint(r.step) - 0x10000u);
+    }
     if (!finite || fabsf(r.low) == INFINITY) {
         r.step = r.low = __int_as_float(0x7fc00000);
         r.inv16 = 0.f;

@@ -7,6 +7,7 @@ import torch
 import paged_kv_cache_300_gb300 as pa
 from oracle import q4
 from tests.q4_util import NORM, check, decode_bound, make
+from tests.test_q4_format import edge_rows
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -86,6 +87,33 @@ def test_update_of_extreme_rows(dtype):
     for i in range(32):
         q4.write(pool, i, _f32(x[0, i]), _f32(x[1, i]), bs)
     _same_pool(got, pool, bs, d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_finite_rows_at_the_end_of_the_numbers(dtype, d):
+    """Stored as the format says, and read back without an infinity."""
+    bs, x = 16, edge_rows(dtype)
+    x = torch.cat([x, x[:, torch.arange(63, -1, -1)]], 1)[:, :d].unsqueeze(1)
+    t = len(x)
+    nb = t // bs + 1
+    pool = np.zeros((nb, 1, q4.record_bytes(d, bs)), dtype=np.uint8)
+    got = torch.from_numpy(pool).to(DEV)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    xd = x.to(DEV)
+    pa.pa_cache_update_q4(xd, xd, i32(list(range(t))), got)
+    for i in range(t):
+        q4.write(pool, i, _f32(x[i]), _f32(x[i]), bs)
+    _same_pool(got, pool, bs, d)
+    kf, vf = torch.empty_like(xd), torch.empty_like(xd)
+    pa.pa_cache_gather_q4(got, i32([list(range(nb))]), i32([0, t]), kf, vf)
+    assert torch.isfinite(kf).all() and torch.isfinite(vf).all()
+    # each row once more as the one token of a sequence
+    lens, tab = i32([0] * t), torch.arange(t, dtype=torch.int32, device=DEV).view(-1, 1)
+    alone = pa.pa_q4_pool(t, 1, d, bs)
+    ks, vs = torch.empty_like(xd), torch.empty_like(xd)
+    pa.pa_decode_q4(torch.zeros_like(xd), alone, tab, lens, xd, xd, k_stored=ks, v_stored=vs)
+    assert torch.equal(ks, kf) and torch.equal(vs, vf)
 
 
 def test_update_skips_slots_beyond_the_pool():

@@ -57,6 +57,38 @@ def test_rows_without_a_finite_low_read_as_nan(bad):
     assert np.isnan(q4.values(n, s, b)).all() and n.max() == 0
 
 
+def edge_rows(dtype):
+    """Finite rows with their largest element at the end of the numbers, and
+    their smallest from the same to its opposite."""
+    top = torch.finfo(dtype).max
+    if dtype == torch.float32:
+        tops = [top, 3.3895e38, 3.3896e38, 3.396e38, 3.4e38, 3.3e38, 3.35e38, 3.38e38]
+    else:
+        tops = [top, 3.3e38, 3.34e38, 3.36e38, 3.38e38]
+    g = torch.Generator().manual_seed(1)
+    rows = []
+    for hi in tops:
+        for low in (1.0, 0.999, 0.99, 17 / 32, 0.9, 0.5, 0.3, 0.05, 0.01, 0.0, -0.05, -0.7, -0.99):
+            x = hi * (low + (1 - low) * torch.rand(64, generator=g, dtype=torch.float64))
+            x[:2] = torch.tensor([hi * low, hi], dtype=torch.float64)
+            rows.append(x.clamp(-3.385e38, top).to(dtype))
+    return torch.stack(rows)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_finite_rows_at_the_end_of_the_numbers_read_back_finite(dtype):
+    x = edge_rows(dtype)
+    assert torch.isfinite(x).all()
+    n, s, b = q4.quantise(x.float().numpy())
+    v = q4.values(n, s, b)
+    step = q4.bf16_bits_to_f64(s)[:, None]
+    # half a step, and the three fp32 roundings of at most 16 steps in all
+    assert (np.abs(v - x.double().numpy()) <= step * (0.5 + 48 * 2.0 ** -24)).all()
+    assert (np.abs(v) <= torch.finfo(torch.float32).max).all()
+    if dtype == torch.bfloat16:
+        assert torch.isfinite(torch.from_numpy(v).to(dtype)).all()
+
+
 def test_write_then_read():
     rng = np.random.default_rng(1)
     for d, bs in ((64, 16), (128, 32)):
