@@ -78,9 +78,10 @@ constexpr int kSlots = 2;
 // Largest weight p s before the reference moves (2^14), and the log2 of the
 // largest one after it has moved.
 constexpr float kWeightMax = 16384.f, kWeightNew = 9.f;
-// Steps below 2^-80 count as 2^-80 there: p stays below 2^94 and its sums inside
-// fp32.
-constexpr float kStepFloor = 8.271806125530277e-25f;
+// Steps below 2^-80, and below 2^-24 of the row's low value (of what is summed with
+// p in its place, which is b + 15 s at most), count as that much there: p stays below 2^94, p b below 2^38, and their sums inside fp32.  (Rows of one
+// value have a step of 0.)  Such a step's codes say less than fp32 holds of b.
+constexpr float kStepFloor = 8.271806125530277e-25f, kLowPart = 5.9604644775390625e-8f;
 
 // A batch of at most this many sequences has its lengths in shared memory.
 constexpr int kMaxLens = 512;
@@ -1040,20 +1041,23 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                         }
             }
             // ---- the reference moves where a weight p s would leave its range
-            // (or p, where the step is very small)
+            // (or p b or p, where the step is very small)
+            auto size = [&](int t, int k) {
+                return fmaxf(fmaxf(vst[t][k], kStepFloor), fabsf(vlo[t][k]) * kLowPart);
+            };
             float top = 0.f;
 #pragma unroll
             for (int t = 0; t < XT; ++t)
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
-                    top = fmaxf(top, exp2_approx(fmaxf(x[t][2 * k], x[t][2 * k + 1])) * fmaxf(vst[t][k], kStepFloor));
+                    top = fmaxf(top, exp2_approx(fmaxf(x[t][2 * k], x[t][2 * k + 1])) * size(t, k));
             if (__any_sync(kFull, top > kWeightMax) || fresh) {
                 float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
                 for (int t = 0; t < XT; ++t)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float lv = log2_approx(fmaxf(vst[t][k], kStepFloor));
+                        const float lv = log2_approx(size(t, k));
                         t0 = fmaxf(t0, x[t][2 * k] + lv);
                         t1 = fmaxf(t1, x[t][2 * k + 1] + lv);
                     }

@@ -341,6 +341,26 @@ def test_decode_of_constant_rows():
     _against_reference(c)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 2), (128, 16, 2)])
+@pytest.mark.parametrize("size", [1e9, 1e12, 1e30, 3.3e38])
+@pytest.mark.parametrize("every", [1, 3])
+def test_decode_of_large_constant_rows(dtype, d, hq, hkv, size, every):
+    """Value rows of one large number (step 0), all or one in three: what they
+    weigh is held back by their size, not by their step."""
+    bs = 16
+    c = make(34, [50, 3, 700, 2000], hq, hkv, d, bs, dtype)
+    sc = np.ascontiguousarray(c["pool"][:, :, bs * d:]).view("<u2").reshape(*c["pool"].shape[:2], bs, 4).copy()
+    low = torch.tensor(size).to(BF16).view(torch.int16).item() & 0xFFFF
+    held = (sc[..., 2] & 0x7FFF) <= 0x7F80  # slots that hold a token
+    held[:, :, np.arange(bs) % every != 0] = False
+    sc[..., 2][held], sc[..., 3][held] = 0, low
+    c["pool"][:, :, bs * d:] = sc.reshape(*c["pool"].shape[:2], -1).view(np.uint8)
+    if every == 1:
+        c["v_new"][:] = size
+    _against_reference(c)
+
+
 def test_decode_zero_query_is_the_mean():
     c = make(17, [100], 2, 1, 64, 16, F32)
     c["q"].zero_()
