@@ -350,7 +350,7 @@ int pa_cache_gather_q4(const void *kv_cache, const int32_t *block_table,
  * pa_decode, and batch * max_blocks_per_seq * num_kv_heads < 2^31; every
  * pointer is device memory.  Elements of q above 2^115 may overflow.  A key or value row that is NaN
  * makes the outputs it reaches NaN, as the formula does.  Value steps below
- * 2^-80, or below 2^-24 of the low value, are weighed as the others but may lose
+ * 2^-76, or below 2^-24 of the low value, are weighed as the others but may lose
  * their codes (the low value stays).
  */
 size_t pa_decode_q4_workspace_size(int batch, int num_heads, int num_kv_heads, int head_dim,

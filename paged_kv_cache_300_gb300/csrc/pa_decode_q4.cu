@@ -75,13 +75,18 @@ constexpr int kMaxWarps = 16;
 // Slots of a warp's ring: 74 to 147 KB in flight an SM, which is more than HBM's
 // latency needs.  More slots leave less L1 and were slower.
 constexpr int kSlots = 2;
-// Largest weight p s before the reference moves (2^14), and the log2 of the
-// largest one after it has moved.
+// Weights are p s in units of 2^14 (kUnit): for the largest steps, 2^125, the largest p
+// is then 2^-102 and more, and those below 2^-24 of it, where f16 ends too, may flush to
+// zero.  (In units of 1 it was 2^-13 of it.)
+constexpr float kUnit = 6.103515625e-5f;
+// Largest weight before the reference moves (2^14), and the log2 of the largest one
+// after it has moved.
 constexpr float kWeightMax = 16384.f, kWeightNew = 9.f;
-// Steps below 2^-80, and below 2^-24 of the row's low value (of what is summed with
-// p in its place, which is b + 15 s at most), count as that much there: p stays below 2^94, p b below 2^38, and their sums inside fp32.  (Rows of one
-// value have a step of 0.)  Such a step's codes say less than fp32 holds of b.
-constexpr float kStepFloor = 8.271806125530277e-25f, kLowPart = 5.9604644775390625e-8f;
+// Steps below 2^-76, and below 2^-24 of the row's low value (of what is summed with
+// p in its place, which is b + 15 s at most), count as that much there: p stays
+// below 2^104, p b below 2^52, and their sums inside fp32.  (Rows of one value have a
+// step of 0.)  Such a step's codes say less than fp32 holds of b.
+constexpr float kStepFloor = 1.3234889800848443e-23f * kUnit, kLowPart = 5.9604644775390625e-8f * kUnit;
 
 // A batch of at most this many sequences has its lengths in shared memory.
 constexpr int kMaxLens = 512;
@@ -863,8 +868,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     T *outp = static_cast<T *>(a.out);
     // rows r and r + 8 are tokens of r's parity
     constexpr bool SECOND = F32 || R > 1; // the weights as two f16 numbers
-    const float base = SECOND ? (r & 1) ? 15.f : 0.f : 7.5f;
-    const float centre = (r & 1) ? 7.5f : -7.5f;
+    const float base = (SECOND ? (r & 1) ? 15.f : 0.f : 7.5f) / kUnit;
+    const float centre = ((r & 1) ? 7.5f : -7.5f) / kUnit;
     const uint32_t odd_sign = (r & 1) ? 0x80008000u : 0u;
 
     uint32_t qh[KW][2][2], ql[F32 ? KW : 1][2][2];
@@ -1017,7 +1022,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const float ks = bf16_lo(sc[k][0]), kl = bf16_hi(sc[k][0]);
-                    vst[t][k] = bf16_lo(sc[k][1]);
+                    vst[t][k] = bf16_lo(sc[k][1]) * kUnit;
                     vlo[t][k] = fmaf(vst[t][k], base, bf16_hi(sc[k][1]));
                     if constexpr (F32) {
                         // around the middle code, where the two terms do not cancel
@@ -1203,7 +1208,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         const int dim0 = r * DL + (R == 4 ? (rep >> 1) * (DL / 2) : 0);
 #pragma unroll
         for (int k = 0; k < DL; ++k) {
-            const float sc = (k & 1) ? kCodeScale / 16.f : kCodeScale;
+            const float sc = (k & 1) ? kCodeScale / kUnit / 16.f : kCodeScale / kUnit;
             const float v0 = acc[k >> 1][2 * (k & 1)] * sc, v1 = acc[k >> 1][2 * (k & 1) + 1] * sc;
             if constexpr (R == 1) {
                 val[k] = v0;

@@ -320,6 +320,28 @@ def test_decode_magnitudes(dtype, k_gain, v_gain, q_gain):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("group", [1, 4, 8])
+@pytest.mark.parametrize("step", [2.0 ** 110, 2.0 ** 120, 2.0 ** 123])
+def test_decode_of_the_largest_steps(dtype, group, step):
+    """One key that outweighs 4000 others by 2^18 each: together they are a
+    64th of the sum, and none of them may be lost because its value's step is
+    large.  Their lows are the opposite of the one's."""
+    d, bs, n = 128, 16, 4000
+    c = make(35, [n], group, 1, d, bs, dtype)
+    sc = np.ascontiguousarray(c["pool"][:, :, bs * d:]).view("<u2").reshape(-1, 1, bs, 4).copy()
+    bits = lambda x: torch.tensor(x).to(BF16).view(torch.int16).numpy().view("<u2")  # noqa: E731
+    sc[..., 0], sc[..., 1] = 0, 0                    # keys of zeros
+    sc[..., 2], sc[..., 3] = bits(step), bits(-2.0 * step)
+    blk = c["table"][0, 5]
+    sc[blk, 0, 7, 1] = bits(1.0)                     # the one key
+    sc[blk, 0, 7, 3] = bits(-8.0 * step)
+    c["pool"][:, :, bs * d:] = sc.reshape(*c["pool"].shape[:2], -1).view(np.uint8)
+    c["k_new"][:], c["v_new"][:] = 0, 0
+    c["q"][:] = 18 * 0.6931471805599453 / d ** 0.5    # scale q.k = 18 log 2
+    _against_reference(c)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_decode_values_of_very_different_sizes(dtype):
     """Tokens whose values differ by 2^40 in size, the large ones hardly seen."""
     c = make(15, [300, 300], 8, 2, 64, 16, dtype)
