@@ -35,7 +35,7 @@ __all__ = [
     "pa_decode_workspace_size", "pa_status_string", "pa_version", "DEVERR_BAD_BLOCK",
     "DEVERR_OVERFLOW", "DEVERR_BAD_CU", "DEVERR_TIMEOUT", "DEVERR_NO_SPACE", "pa_block_tables",
     "pa_q4_block_bytes", "pa_q4_pool", "pa_cache_update_q4", "pa_cache_gather_q4", "pa_decode_q4",
-    "pa_decode_q4_workspace_size",
+    "pa_decode_q4_workspace_size", "pa_reset_workspaces",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +48,7 @@ DEVERR_NO_SPACE = 16
 _lock = threading.Lock()
 _lib = None
 _workspaces: dict = {}
+_q4_workspaces: dict = {}
 
 
 class PAError(RuntimeError):
@@ -192,6 +193,21 @@ def _workspace(dev, nbytes):
     return ws
 
 
+def pa_reset_workspaces():
+    """Zero the workspaces kept for calls of pa_decode, pa_decode_contiguous and
+    pa_decode_q4 that were given none (in place: captured calls may use them).
+    Needed after such a call has set DEVERR_TIMEOUT: counters of the sequences
+    that were given up may be left in its workspace, and later calls would join
+    those sequences' parts too early or not at all.  Call it when no such call
+    is running; it waits for the GPU.  (A caller's own workspace is zeroed by the
+    caller; a captured pa_decode_q4 clears its counters in the graph.)"""
+    for kept in (_workspaces, _q4_workspaces):
+        for ws in list(kept.values()):
+            ws.zero_()
+            if ws.is_cuda:
+                torch.cuda.synchronize(ws.device)
+
+
 def pa_decode(q, k_cache, v_cache, block_table, cache_seqlens, k_new, v_new, out=None,
               softmax_scale: float = 0.0, workspace=None, dev_err=None, stream=None):
     """Decode step (see include/pa.h).  q [B, Hq, D]; k_cache/v_cache
@@ -200,7 +216,9 @@ def pa_decode(q, k_cache, v_cache, block_table, cache_seqlens, k_new, v_new, out
     Returns out [B, Hq, D].  q, block_table, cache_seqlens, k_new, v_new
     and out may be pinned host tensors (read and written in place; `out`
     defaults to a pinned host tensor then); the pools, workspace and
-    dev_err live on the GPU."""
+    dev_err live on the GPU.  Without a workspace the call uses one that is
+    kept for the device and stream; after DEVERR_TIMEOUT it has to be zeroed
+    with pa_reset_workspaces()."""
     dev = _check_dev(k_cache, v_cache, workspace, dev_err)
     _check_host_or_dev(dev, q, block_table, cache_seqlens, k_new, v_new, out)
     _i32(block_table, "block_table")
@@ -499,7 +517,6 @@ def pa_decode_q4_workspace_size(batch, num_heads, num_kv_heads, head_dim, block_
                                                   block_size, dt))
 
 
-_q4_workspaces: dict = {}
 _q4_sizes: dict = {}
 
 
@@ -544,7 +561,9 @@ def pa_decode_q4(q, kv_cache, block_table, cache_seqlens, k_new, v_new, out=None
     [B, Hkv, D] are quantised in place at position cache_seqlens[b] and
     q [B, Hq, D] attends over positions 0..cache_seqlens[b].  bfloat16 or
     float32.  k_stored, v_stored, when given, receive the new token as the
-    pool now holds it.  Returns out [B, Hq, D]."""
+    pool now holds it.  Without a workspace the call uses one that is kept for
+    the device and stream; after DEVERR_TIMEOUT it has to be zeroed with
+    pa_reset_workspaces().  Returns out [B, Hq, D]."""
     shape, rows = q.shape, k_new.shape
     b, hq, d = shape
     hkv = rows[1]

@@ -546,6 +546,20 @@ def test_one_workspace_for_calls_of_different_sizes():
             _against_reference(c, workspace=ws)
 
 
+def test_reset_zeroes_the_kept_workspaces():
+    """What a call that gave up may leave behind: counters that are not zero,
+    and sums of another call."""
+    c = make(36, [3000, 20, 2500], 8, 2, 128, 16, BF16)
+    want = _decode(c)[0]
+    key = torch.cuda.current_device(), torch.cuda.current_stream().cuda_stream
+    kept = pa._q4_workspaces[key]
+    for left in (1, 2, 17):
+        kept[:4 * 6].view(torch.int32).fill_(left)
+        pa.pa_reset_workspaces()
+        assert not kept.any() and pa._q4_workspaces[key] is kept
+        assert torch.equal(_decode(c)[0], want)
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("d,bs,hq,hkv", [(128, 16, 8, 2), (128, 32, 16, 8)])
 def test_serving_steps(d, bs, hq, hkv):

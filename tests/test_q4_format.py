@@ -189,6 +189,14 @@ def test_binding_refuses_what_it_cannot_take():
                            *(z(1, dtype=torch.int32),) * 3, 16)
 
 
+def test_reset_zeroes_what_is_kept(monkeypatch):
+    kept = [torch.ones(16, dtype=torch.uint8) for _ in range(3)]
+    monkeypatch.setattr(pa, "_workspaces", {(0, 0): kept[0], (0, 7): kept[1]})
+    monkeypatch.setattr(pa, "_q4_workspaces", {(0, 0): kept[2]})
+    pa.pa_reset_workspaces()
+    assert not any(t.any() for t in kept)
+
+
 def test_table_reference_worked_example():
     """Three requests of 30, 32 and 70 tokens in blocks of 32, one new token
     each: only the second needs a block; then the first ends and the third
