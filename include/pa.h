@@ -87,6 +87,7 @@ enum {
 #define PA_DEVERR_BAD_CU 4    /* cu_seq_lens not non-decreasing, or cu_seq_lens_k does not
                                  equal cache_seqlens + q lengths in pa_cache_update */
 #define PA_DEVERR_TIMEOUT 8   /* a bounded wait inside a kernel gave up */
+#define PA_LEFT_OUT INT32_MIN /* as a length: the sequence takes no part in the pa_decode_q4 call */
 #define PA_DEVERR_NO_SPACE 16 /* pa_block_tables: too few free blocks, or slot_map too short */
 
 /*
@@ -345,6 +346,9 @@ int pa_cache_gather_q4(const void *kv_cache, const int32_t *block_table,
  * values the pool now stands for at L, for a caller that uses them again in
  * this step (a later layer that shares these keys) or watches the error.
  * Left as they were where the sequence's append was refused.
+ * A sequence with cache_seqlens[b] = PA_LEFT_OUT takes no part: nothing is
+ * appended, its output rows are zeros and no error bit is set (other negative
+ * lengths are errors).
  * block_table, cache_seqlens, workspace, device errors, placement and the
  * limits num_heads / num_kv_heads <= 8, batch * num_kv_heads <= 262144 as
  * pa_decode, and batch * max_blocks_per_seq * num_kv_heads < 2^31; every
@@ -374,8 +378,8 @@ int pa_decode_q4(const void *q, void *kv_cache, const int32_t *block_table,
  *           row;
  *   n = -1  the request has ended: its blocks go back and its length becomes 0.
  *           Its row is left as it is and names blocks that others may own by
- *           now: give the row a new request before it is decoded again, or a
- *           negative length, which pa_decode_q4 refuses for that row alone.
+ *           now, so it must not be decoded with its old length: see
+ *           pa_block_tables_decode.
  * free_blocks [num_blocks] is a stack of *num_free block ids (top at the
  * end).  Ended requests push their blocks first, in order of (request,
  * logical block); then the taken blocks are popped in the same order.
@@ -399,6 +403,25 @@ int pa_block_tables(const int32_t *cache_seqlens, const int32_t *new_lens, int32
                     int32_t *cu_seq_lens_q, int32_t *cu_seq_lens_k, int32_t *seqlens_k,
                     int32_t *num_free_out, int batch, int total_slots, int num_blocks,
                     int block_size, int max_blocks_per_seq, int32_t *dev_err, void *stream);
+
+/*
+ * The same step, and the lengths for the pa_decode_q4 call behind it:
+ *   decode_lens [batch]   L where n = 1, the position of the request's one new
+ *                         token; PA_LEFT_OUT where n is anything else (nothing
+ *                         new, ended, or a chunk for pa_cache_update_q4) and for
+ *                         all requests of a refused step
+ * so that one decode over the whole batch appends and attends for the requests
+ * with a new token and leaves the blocks of the others, and of ended requests'
+ * old rows, alone.  decode_lens overlaps no other argument; NULL leaves it out
+ * (pa_block_tables).  seqlens_k may still be cache_seqlens, and the two calls be
+ * captured together.
+ */
+int pa_block_tables_decode(const int32_t *cache_seqlens, const int32_t *new_lens,
+                           int32_t *block_table, int32_t *free_blocks, const int32_t *num_free,
+                           int32_t *slot_map, int32_t *cu_seq_lens_q, int32_t *cu_seq_lens_k,
+                           int32_t *seqlens_k, int32_t *num_free_out, int32_t *decode_lens,
+                           int batch, int total_slots, int num_blocks, int block_size,
+                           int max_blocks_per_seq, int32_t *dev_err, void *stream);
 
 /* Static description of a status code (never NULL). */
 const char *pa_status_string(int status);

@@ -35,7 +35,7 @@ __all__ = [
     "pa_decode_workspace_size", "pa_status_string", "pa_version", "DEVERR_BAD_BLOCK",
     "DEVERR_OVERFLOW", "DEVERR_BAD_CU", "DEVERR_TIMEOUT", "DEVERR_NO_SPACE", "pa_block_tables",
     "pa_q4_block_bytes", "pa_q4_pool", "pa_cache_update_q4", "pa_cache_gather_q4", "pa_decode_q4",
-    "pa_decode_q4_workspace_size", "pa_reset_workspaces",
+    "pa_decode_q4_workspace_size", "PA_LEFT_OUT", "pa_reset_workspaces",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -44,6 +44,7 @@ _LIB_PATH = os.path.join(_HERE, "_lib", "libpa300.so")
 PA_F32, PA_BF16 = 0, 1
 DEVERR_BAD_BLOCK, DEVERR_OVERFLOW, DEVERR_BAD_CU, DEVERR_TIMEOUT = 1, 2, 4, 8
 DEVERR_NO_SPACE = 16
+PA_LEFT_OUT = -2**31  # as a length: the sequence takes no part in the pa_decode_q4 call
 
 _lock = threading.Lock()
 _lib = None
@@ -101,6 +102,8 @@ def load():
         lib.pa_decode_q4.restype = i
         lib.pa_block_tables.argtypes = [p] * 10 + [i] * 5 + [p, p]
         lib.pa_block_tables.restype = i
+        lib.pa_block_tables_decode.argtypes = [p] * 11 + [i] * 5 + [p, p]
+        lib.pa_block_tables_decode.restype = i
         lib.pa_status_string.argtypes = [i]
         lib.pa_status_string.restype = ctypes.c_char_p
         lib.pa_version.argtypes = []
@@ -447,11 +450,8 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _c_int(*sizes):
-    """Refuse sizes that the C interface's int does not hold (ctypes would cut
-    them to 32 bits)."""
-    if max(sizes) > 0x7FFFFFFF:
-        raise ValueError(f"a size of {max(sizes)} passes 2^31 - 1")
+def _too_large():
+    raise ValueError("a size passes 2^31 - 1")  # ctypes would cut it to 32 bits
 
 
 def pa_q4_block_bytes(num_kv_heads, head_dim, block_size) -> int:
@@ -475,7 +475,8 @@ def pa_cache_update_q4(k_chunk, v_chunk, slot_map, kv_cache, dev_err=None, strea
     its row."""
     shape = k_chunk.shape
     t, hkv, d = shape
-    _c_int(t)
+    if t > 0x7FFFFFFF:
+        _too_large()
     dt = _dtype(k_chunk)
     index, nb, bs = _q4_geometry(kv_cache, hkv, d)
     if v_chunk.shape != shape or not _fits(index, k_chunk.dtype, k_chunk, v_chunk):
@@ -496,7 +497,8 @@ def pa_cache_gather_q4(kv_cache, block_table, cu_seq_lens_k, k_full, v_full, dev
     dt = _dtype(k_full)
     index, nb, bs = _q4_geometry(kv_cache, hkv, d)
     b, mb = block_table.shape
-    _c_int(tk, b, mb)
+    if tk | b | mb > 0x7FFFFFFF:
+        _too_large()
     if v_full.shape != shape or not _fits(index, k_full.dtype, k_full, v_full):
         _refuse(index, k_full.dtype, k_full=k_full, v_full=v_full)
     if cu_seq_lens_k.shape != (b + 1,) or \
@@ -560,7 +562,8 @@ def pa_decode_q4(q, kv_cache, block_table, cache_seqlens, k_new, v_new, out=None
     """Decode step over the 4-bit pool (see include/pa.h): k_new, v_new
     [B, Hkv, D] are quantised in place at position cache_seqlens[b] and
     q [B, Hq, D] attends over positions 0..cache_seqlens[b].  bfloat16 or
-    float32.  k_stored, v_stored, when given, receive the new token as the
+    float32.  A sequence whose length is PA_LEFT_OUT takes no part (its rows of
+    out are zeros).  k_stored, v_stored, when given, receive the new token as the
     pool now holds it.  Without a workspace the call uses one that is kept for
     the device and stream; after DEVERR_TIMEOUT it has to be zeroed with
     pa_reset_workspaces().  Returns out [B, Hq, D]."""
@@ -580,7 +583,8 @@ def pa_decode_q4(q, kv_cache, block_table, cache_seqlens, k_new, v_new, out=None
         _refuse(index, dtype, q=q, out=out, k_new=k_new, v_new=v_new, k_stored=k_stored,
                 v_stored=v_stored)
     tb, mb = block_table.shape
-    _c_int(b, mb)
+    if b | mb > 0x7FFFFFFF:
+        _too_large()
     if tb != b or cache_seqlens.shape != (b,) or \
             not _fits(index, torch.int32, block_table, cache_seqlens, dev_err):
         _refuse(index, torch.int32, block_table=block_table, cache_seqlens=cache_seqlens,
@@ -600,12 +604,14 @@ def pa_decode_q4(q, kv_cache, block_table, cache_seqlens, k_new, v_new, out=None
 # ------------------------------------------------------------------ block tables
 def pa_block_tables(cache_seqlens, new_lens, block_table, free_blocks, num_free, slot_map,
                     block_size, cu_seq_lens_q=None, cu_seq_lens_k=None, seqlens_k=None,
-                    num_free_out=None, dev_err=None, stream=None):
+                    num_free_out=None, dev_err=None, stream=None, decode_lens=None):
     """One step's block tables from the requests' lengths (see include/pa.h).
     cache_seqlens, new_lens [B]; block_table [B, MB] and free_blocks
     [num_blocks] are updated in place; slot_map [any length] is filled, -1
     behind the last token.  All int32.  num_free [1] is advanced in place
-    unless num_free_out is given.  Returns (cu_seq_lens_q, cu_seq_lens_k,
+    unless num_free_out is given.  decode_lens [B], when given, receives the
+    lengths for a pa_decode_q4 call over the whole batch: those before the step
+    where one token is new, PA_LEFT_OUT elsewhere.  Returns (cu_seq_lens_q, cu_seq_lens_k,
     seqlens_k)."""
     if not block_table.is_cuda:
         raise ValueError("all tensors must live on a CUDA device")
@@ -620,21 +626,24 @@ def pa_block_tables(cache_seqlens, new_lens, block_table, free_blocks, num_free,
     if num_free_out is None:
         num_free_out = num_free
     if not _fits(index, torch.int32, cache_seqlens, new_lens, block_table, free_blocks, num_free,
-                 slot_map, cu_seq_lens_q, cu_seq_lens_k, seqlens_k, num_free_out, dev_err):
+                 slot_map, cu_seq_lens_q, cu_seq_lens_k, seqlens_k, num_free_out, decode_lens,
+                 dev_err):
         _refuse(index, torch.int32, cache_seqlens=cache_seqlens, new_lens=new_lens,
                 block_table=block_table, free_blocks=free_blocks, num_free=num_free,
                 slot_map=slot_map, cu_seq_lens_q=cu_seq_lens_q, cu_seq_lens_k=cu_seq_lens_k,
-                seqlens_k=seqlens_k, num_free_out=num_free_out, dev_err=dev_err)
+                seqlens_k=seqlens_k, num_free_out=num_free_out, decode_lens=decode_lens,
+                dev_err=dev_err)
     if cache_seqlens.shape != (b,) or new_lens.shape != (b,) or seqlens_k.shape != (b,) or \
             cu_seq_lens_q.shape != (b + 1,) or cu_seq_lens_k.shape != (b + 1,) or \
             free_blocks.dim() != 1 or slot_map.dim() != 1 or num_free.numel() != 1 or \
-            num_free_out.numel() != 1:
+            num_free_out.numel() != 1 or (decode_lens is not None and decode_lens.shape != (b,)):
         raise ValueError("inconsistent shapes")
     slots, blocks = slot_map.numel(), free_blocks.numel()
-    _c_int(b, slots, blocks, mb, block_size)
-    _launch("pa_block_tables", index, stream, cache_seqlens.data_ptr(), new_lens.data_ptr(),
+    if b | slots | blocks | mb | block_size > 0x7FFFFFFF:
+        _too_large()
+    _launch("pa_block_tables_decode", index, stream, cache_seqlens.data_ptr(), new_lens.data_ptr(),
             block_table.data_ptr(), free_blocks.data_ptr(), num_free.data_ptr(),
             slot_map.data_ptr(), cu_seq_lens_q.data_ptr(), cu_seq_lens_k.data_ptr(),
-            seqlens_k.data_ptr(), num_free_out.data_ptr(), b, slots, blocks, block_size, mb,
-            _addr(dev_err))
+            seqlens_k.data_ptr(), num_free_out.data_ptr(), _addr(decode_lens), b, slots, blocks,
+            block_size, mb, _addr(dev_err))
     return cu_seq_lens_q, cu_seq_lens_k, seqlens_k

@@ -159,6 +159,18 @@ int pa_block_tables(const int32_t *cache_seqlens, const int32_t *new_lens, int32
                     int32_t *num_free_out, int batch, int total_slots, int num_blocks,
                     int block_size, int max_blocks_per_seq, int32_t *dev_err, void *stream)
 {
+    return pa_block_tables_decode(cache_seqlens, new_lens, block_table, free_blocks, num_free, slot_map,
+                                  cu_seq_lens_q, cu_seq_lens_k, seqlens_k, num_free_out, nullptr, batch,
+                                  total_slots, num_blocks, block_size, max_blocks_per_seq, dev_err, stream);
+}
+
+int pa_block_tables_decode(const int32_t *cache_seqlens, const int32_t *new_lens,
+                           int32_t *block_table, int32_t *free_blocks, const int32_t *num_free,
+                           int32_t *slot_map, int32_t *cu_seq_lens_q, int32_t *cu_seq_lens_k,
+                           int32_t *seqlens_k, int32_t *num_free_out, int32_t *decode_lens,
+                           int batch, int total_slots, int num_blocks, int block_size,
+                           int max_blocks_per_seq, int32_t *dev_err, void *stream)
+{
     if (batch < 0 || total_slots < 0 || num_blocks <= 0 || block_size <= 0 || max_blocks_per_seq <= 0)
         return PA_ERR_SHAPE;
     if (batch > kTablesMaxBatch || (long long)num_blocks * block_size >= (1ll << 31) ||
@@ -170,7 +182,7 @@ int pa_block_tables(const int32_t *cache_seqlens, const int32_t *new_lens, int32
     for (const void *p : {(const void *)cache_seqlens, (const void *)new_lens, (const void *)block_table,
                           (const void *)free_blocks, (const void *)num_free, (const void *)slot_map,
                           (const void *)cu_seq_lens_q, (const void *)cu_seq_lens_k, (const void *)seqlens_k,
-                          (const void *)num_free_out})
+                          (const void *)num_free_out, (const void *)decode_lens})
         if (!aligned(p, 4)) return PA_ERR_SHAPE;
     TablesArgs a{};
     a.cache_seqlens = cache_seqlens;
@@ -183,6 +195,7 @@ int pa_block_tables(const int32_t *cache_seqlens, const int32_t *new_lens, int32
     a.cu_k = cu_seq_lens_k;
     a.seqlens_k = seqlens_k;
     a.num_free_out = num_free_out;
+    a.decode_lens = decode_lens;
     a.dev_err = dev_err;
     a.batch = batch;
     a.total_slots = total_slots;

@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         const int len = __ldg(a.cache_seqlens + b);
         if (cached) s_lens[b] = len;
         local += seq_blocks(len, cap, BS, &ok);
-        if (!ok && blockIdx.x == 0) flag_error(a.dev_err, PA_DEVERR_OVERFLOW);
+        if (!ok && len != PA_LEFT_OUT && blockIdx.x == 0) flag_error(a.dev_err, PA_DEVERR_OVERFLOW);
     }
     int incl = local;
 #pragma unroll

@@ -166,6 +166,7 @@ struct TablesArgs {
     int32_t *cu_k;
     int32_t *seqlens_k;
     int32_t *num_free_out;
+    int32_t *decode_lens; // or NULL
     int32_t *dev_err;
     int batch, total_slots, num_blocks, block_size, max_blocks_per_seq;
     int shift; // log2 of block_size, -1 if it is no power of two (set by the launch)

@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a)
             for (int b = tid; b < B; b += kThreads) {
                 a.cu_q[b + 1] = a.cu_k[b + 1] = 0;
                 a.seqlens_k[b] = s_len[b];
+                if (a.decode_lens) a.decode_lens[b] = PA_LEFT_OUT;
             }
         }
         // (the last step of a slot map of nearly 2^31 entries passes 32 bits)
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a)
         const int n = s_cu[b + 1] - s_cu[b];
         // an ended request's length is 0: its slice of cu_k is empty
         a.seqlens_k[b] = a.new_lens[b] < 0 ? 0 : s_len[b] + n;
+        if (a.decode_lens) a.decode_lens[b] = n == 1 ? s_len[b] : PA_LEFT_OUT;
     }
     if (cta == 0 && tid == 0) {
         a.cu_q[0] = a.cu_k[0] = 0;

@@ -663,3 +663,104 @@ def test_decode_bf16_is_off_by_little_but_its_own_rounding(d, bs, hq, hkv, left)
     h = float((ref.to(BF16).double() - ref).norm() / size)
     got = float((out.cpu().double() - ref).norm() / size)
     assert got <= (h * h + left * left) ** 0.5 * 1.002, (got, h)
+
+
+# ------------------------------------------------------------------ the step's tables and its decode
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_decode_of_sequences_left_out(dtype):
+    """No output, no append, no error; the others within their bound."""
+    c = make(50, [100, 900, 5, 40], 8, 2, 128, 16, dtype)
+    _, pool_good, ks_good, _, _ = _decode(c)
+    ref, seen = q4.decode(_f32(c["q"]), c["pool"].copy(), c["table"], c["lens"], _f32(c["k_new"]), _f32(c["v_new"]), 16)
+    bound = decode_bound(c["q"], seen, ref, dtype, 128 ** -0.5)
+    lens = c["lens"].copy()
+    for out_of in ([1], [0, 3], [0, 1, 2, 3]):
+        c["lens"] = lens.copy()
+        c["lens"][out_of] = pa.PA_LEFT_OUT
+        out, pool, ks, _, err = _decode(c)
+        assert err == 0
+        for b in range(4):
+            own = c["table"][b][c["table"][b] >= 0]
+            if b in out_of:
+                assert not out[b].any()
+                assert np.array_equal(pool.cpu().numpy()[own], c["pool"][own])
+            else:
+                # the work is cut in other places, so the sums differ by roundings
+                check(out[b:b + 1], ref[b:b + 1], bound[b:b + 1], norm=NORM[dtype])
+                assert torch.equal(ks[b], ks_good[b]) and torch.equal(pool[own], pool_good[own])
+    c["lens"][2] = -2 ** 31 + 1  # any other negative length is an error
+    assert _decode(c)[4] == pa.DEVERR_OVERFLOW
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_tables_and_decode_of_one_step(captured):
+    """Steps of a server over a fixed batch: lengths and free list in place,
+    tables and decode in one graph.  Requests pause and end, others take an ended
+    one's blocks in the same step, and its row stays empty for a while: nothing of
+    another request may change, and no step raises an error."""
+    d, bs, hq, hkv, b, mb, nb = 64, 16, 4, 2, 5, 8, 14
+    g = torch.Generator().manual_seed(5)
+    rng = np.random.default_rng(5)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    z = lambda *s: torch.zeros(*s, dtype=BF16, device=DEV)  # noqa: E731
+    pool, table = pa.pa_q4_pool(nb, hkv, d, bs), torch.full((b, mb), -1, dtype=torch.int32, device=DEV)
+    free, count, lens, new, at, err = i32(list(range(nb))), i32([nb]), i32([0] * b), i32([0] * b), i32([0] * b), i32([0])
+    slots, cu_q, cu_k = i32([0] * b), i32([0] * (b + 1)), i32([0] * (b + 1))
+    q, kn, vn, out = z(b, hq, d), z(b, hkv, d), z(b, hkv, d), z(b, hq, d)
+
+    def step():
+        pa.pa_block_tables(lens, new, table, free, count, slots, bs, cu_seq_lens_q=cu_q, cu_seq_lens_k=cu_k,
+                           seqlens_k=lens, decode_lens=at, dev_err=err)
+        pa.pa_decode_q4(q, pool, table, at, kn, vn, out, dev_err=err)
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+    hist = [0] * b
+    rows = [np.zeros((0, 2, hkv, d), dtype=np.float32) for _ in range(b)]  # every request's own tokens
+    taken_over = 0
+    for i in range(90):
+        todo = [1 if rng.random() < 0.8 else 0 for _ in range(b)]
+        for r in range(b):
+            if hist[r] == 0 and rng.random() < 0.6:
+                todo[r] = 0  # an empty row waits for its next request
+            if hist[r] > 20 and rng.random() < 0.06:
+                todo[r] = -1
+        if sum(-(-(h + max(m, 0)) // bs) for h, m in zip(hist, todo) if m >= 0) > nb:
+            todo = [0] * b
+            todo[int(np.argmax(hist))] = -1
+        xs = [torch.randn(*t.shape, generator=g).to(BF16) for t in (q, kn, vn)]
+        for t, x in zip((q, kn, vn), xs):
+            t.copy_(x)
+        new.copy_(i32(todo))
+        graph.replay() if captured else step()
+        torch.cuda.synchronize()
+        assert err.item() == 0, i
+        tab = table.cpu().numpy()
+        for r in range(b):
+            if todo[r] < 0:
+                hist[r], rows[r] = 0, rows[r][:0]
+            elif todo[r] == 1:
+                new_row = np.stack([_f32(xs[1][r]), _f32(xs[2][r])])[None]
+                rows[r] = np.concatenate([rows[r], new_row])
+                hist[r] += 1
+        assert lens.tolist() == hist
+        owned = [set(tab[r, :-(-hist[r] // bs)].tolist()) for r in range(b)]
+        taken_over += sum(hist[r] == 0 and any(o & set(tab[r].tolist()) for o in owned) for r in range(b))
+        small = np.zeros((nb, hkv, q4.record_bytes(d, bs)), dtype=np.uint8)
+        for r in range(b):
+            if todo[r] != 1:
+                assert not out[r].any()
+            for p in range(hist[r]):
+                q4.write(small, int(tab[r, p // bs]) * bs + p % bs, rows[r][p, 0], rows[r][p, 1], bs)
+        # the pool holds every living request's tokens, and the outputs are theirs
+        for r in range(b):
+            got = q4.read(pool.cpu().numpy(), tab[r], hist[r], d, bs)
+            want = q4.read(small, tab[r], hist[r], d, bs)
+            assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]), (i, r)
+            if todo[r] == 1:
+                ref, seen = q4.decode(_f32(xs[0][r:r + 1]), small, tab[r:r + 1], np.array([hist[r] - 1]),
+                                      _f32(xs[1][r:r + 1]), _f32(xs[2][r:r + 1]), bs)
+                check(out[r:r + 1], ref, decode_bound(xs[0][r:r + 1], seen, ref, BF16, d ** -0.5), (i, r))
+    assert taken_over > 10  # rows of ended requests that name another's blocks

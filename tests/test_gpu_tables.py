@@ -213,3 +213,33 @@ def test_sizes_that_do_not_fit_an_int_are_refused():
         pa.pa_decode_q4(rows(), pool, big.view(1, -1), i32(0), rows(), rows())
     with pytest.raises(ValueError, match="2\\^31"):
         pa.pa_cache_gather_q4(pool, big.view(1, -1), i32(0, 1), rows(), rows())
+
+
+def _decode_lens(lens, new):
+    return np.where(np.asarray(new) == 1, lens, pa.PA_LEFT_OUT).astype(np.int32)
+
+
+@pytest.mark.parametrize("batch,new_hi", [(1, 1), (40, 3), (1025, 1), (4097, 9), (16384, 3)])
+def test_decode_lens(batch, new_hi):
+    """Lengths before the step where one token is new; everybody else, ended
+    requests among them, is left out of the decode behind it."""
+    bs = 16
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, 300, batch).tolist()
+    new = np.where(rng.random(batch) < 0.2, -1, rng.integers(0, new_hi + 1, batch)).tolist()
+    tokens = sum(max(m, 0) for m in new)
+    lens, new, table, free = make(batch, lens, new, bs, tokens + 1)
+    out = torch.full((batch,), 5, dtype=torch.int32, device=DEV)
+    want = q4.block_tables(lens, new, table, free, tokens + 1, tokens, bs)
+    d, res = run(lens, new, table, free, tokens + 1, tokens, bs, decode_lens=out)
+    same(d, res, want)
+    assert int(d["err"].item()) == 0 and np.array_equal(out.cpu().numpy(), _decode_lens(lens, new))
+
+
+@pytest.mark.parametrize("tail", [0, 5000, 20000])
+def test_a_refused_step_leaves_everybody_out_of_the_decode(tail):
+    lens, new, table, free = make(5, [16, 40, 3], [1, 1, -1], 16, 0)
+    new[0] = 400  # longer than its row
+    out = torch.full((3,), 5, dtype=torch.int32, device=DEV)
+    d, _ = run(lens, new, table, free, 0, 401 + tail, 16, decode_lens=out)
+    assert int(d["err"].item()) & pa.DEVERR_OVERFLOW and (out == pa.PA_LEFT_OUT).all()

@@ -179,6 +179,12 @@ def test_tables_refuse_before_any_launch(lib, over, status):
     assert _tables(lib, **over) == status
 
 
+def test_tables_with_decode_lens_refuse_before_any_launch(lib):
+    p = _p(4096)
+    call = lambda **o: lib.pa_block_tables_decode(*[p] * 10, o.get("at", p), o.get("b", 2), 4, 8, 16, 4, None, None)  # noqa: E731
+    assert call(at=_p(4098)) == -3 and call(b=-1) == -3 and call(b=16385, at=None) == -4
+
+
 def test_binding_refuses_what_it_cannot_take():
     z = torch.zeros
     with pytest.raises(ValueError):  # not on a GPU
