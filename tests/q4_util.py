@@ -97,3 +97,39 @@ def check(got, ref, bound, what="", norm=None):
 # 2-norms: a bf16 result is off by its own rounding, at most half a step (2^-8)
 # of every element; for fp32 the library's own tolerance.
 NORM = {torch.bfloat16: 2.0 ** -8, torch.float32: 1e-5}
+
+
+def write_rows(pool, slots, k, v, bs):
+    """oracle.q4.write for many tokens at once: rows k, v [T, Hkv, D] into the
+    slots (in place; negative ones are skipped)."""
+    t = np.flatnonzero(slots >= 0)
+    blk, off = (slots[t] // bs)[:, None, None], slots[t] % bs
+    h, d = np.arange(k.shape[1])[None, :, None], k.shape[2]
+    for kv, x in enumerate((k, v)):
+        n, s, b = q4.quantise(x[t])
+        if kv == 0:
+            pool[blk, h, (off[:, None] * (d // 2) + np.arange(d // 2))[:, None]] = n[..., 0::2] | n[..., 1::2] << 4
+        else:
+            at = bs * d // 2 + 2 * q4.v_unit(off[:, None], np.arange(d // 4)[None], d)[:, None]
+            pool[blk, h, at] = n[..., 0::4] | n[..., 1::4] << 4
+            pool[blk, h, at + 1] = n[..., 2::4] | n[..., 3::4] << 4
+        scale = np.stack([s & 255, s >> 8, b & 255, b >> 8], -1).astype(np.uint8)
+        pool[blk, h, (bs * d + 8 * off[:, None] + 4 * kv + np.arange(4))[:, None]] = scale
+
+
+def edge_rows(dtype):
+    """Finite rows with their largest element at the end of the numbers, and
+    their smallest from the same to its opposite."""
+    top = torch.finfo(dtype).max
+    if dtype == torch.float32:
+        tops = [top, 3.3895e38, 3.3896e38, 3.396e38, 3.4e38, 3.3e38, 3.35e38, 3.38e38]
+    else:
+        tops = [top, 3.3e38, 3.34e38, 3.36e38, 3.38e38]
+    g = torch.Generator().manual_seed(1)
+    rows = []
+    for hi in tops:
+        for low in (1.0, 0.999, 0.99, 17 / 32, 0.9, 0.5, 0.3, 0.05, 0.01, 0.0, -0.05, -0.7, -0.99):
+            x = hi * (low + (1 - low) * torch.rand(64, generator=g, dtype=torch.float64))
+            x[:2] = torch.tensor([hi * low, hi], dtype=torch.float64)
+            rows.append(x.clamp(-3.385e38, top).to(dtype))
+    return torch.stack(rows)

@@ -6,8 +6,7 @@ import torch
 
 import paged_kv_cache_300_gb300 as pa
 from oracle import q4
-from tests.q4_util import NORM, check, decode_bound, make
-from tests.test_q4_format import edge_rows
+from tests.q4_util import NORM, check, decode_bound, edge_rows, make, write_rows
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -68,6 +67,55 @@ def test_update(dtype, d, bs, hkv, total):
         if s >= 0:
             q4.write(pool, int(s), _f32(x[0, i]), _f32(x[1, i]), bs)
     assert err.item() == 0
+    _same_pool(got, pool, bs, d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,bs", [(64, 32), (128, 16)])
+@pytest.mark.parametrize("total,hkv,heads", [(1700, 5, 2), (1600, 8, 3), (2600, 5, 3), (4200, 3, 3), (4099, 8, 8)])
+def test_update_with_several_heads_a_warp(dtype, d, bs, total, hkv, heads):
+    """Chunks large enough that a warp takes several heads, of which the last
+    warps have fewer: a run of slots that begins in the middle of a token pair,
+    then lone and neighbouring ones in any order, padding between."""
+    assert min(hkv, total * hkv // 4096) == heads
+    rng = np.random.default_rng(total)
+    nb = -(-total // bs) + 3
+    slots = np.arange(3, 3 + total, dtype=np.int32)
+    rest = np.setdiff1d(np.arange(nb * bs), slots[:total // 2])
+    slots[total // 2:] = rng.permutation(rest)[:total - total // 2]
+    slots[rng.random(total) < 0.1] = -1
+    g = torch.Generator().manual_seed(total)
+    x = (torch.randn(2, total, hkv, d, generator=g) * torch.exp(torch.randn(2, total, hkv, 1, generator=g))).to(dtype)
+    pool = rng.integers(0, 256, (nb, hkv, q4.record_bytes(d, bs)), dtype=np.uint8)
+    got = torch.from_numpy(pool).to(DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pa.pa_cache_update_q4(x[0].to(DEV), x[1].to(DEV), torch.from_numpy(slots).to(DEV), got, dev_err=err)
+    write_rows(pool, slots, _f32(x[0]), _f32(x[1]), bs)
+    assert err.item() == 0
+    _same_pool(got, pool, bs, d)
+
+
+def test_update_with_every_step_there_is():
+    """A row for each bf16 step above 2^-100, with values at the borders of
+    its codes and one number beside them: 16 / step has to be correctly rounded."""
+    bs, d = 32, 64
+    step = (np.arange(0x0D81, 0x7F80, dtype=np.uint32) << 16).view(np.float32).astype(np.float64)
+    step = step[15 * step < q4.BF16_MAX]
+    assert step[0] < 1.01 * 2.0 ** -100 and step[-1] > 2.0 ** 124 and len(step) == 28679
+    edge = (step[:, None] * (np.arange(15) + 0.5)).astype(np.float32)
+    up, down = np.nextafter(edge, np.float32(np.inf)), np.nextafter(edge, np.float32(0))
+    top = (15 * step * (1 - 2.0 ** -10)).astype(np.float32)[:, None]
+    more = np.random.default_rng(3).random((len(step), 17)).astype(np.float32)
+    x = np.concatenate([np.zeros_like(top), top, np.minimum(edge, top), np.minimum(up, top), down, more * top], 1)
+    n, s, _ = q4.quantise(x)
+    assert np.array_equal(q4.bf16_bits_to_f64(s), step) and n.max() == 15
+    t = len(x)
+    pool = np.zeros((-(-t // bs), 1, q4.record_bytes(d, bs)), dtype=np.uint8)
+    got = torch.from_numpy(pool).to(DEV)
+    k, v = x[:, None], np.ascontiguousarray(x[:, None, ::-1])
+    slots = np.arange(t, dtype=np.int32)
+    pa.pa_cache_update_q4(torch.from_numpy(k).to(DEV), torch.from_numpy(v).to(DEV), torch.from_numpy(slots).to(DEV), got)
+    write_rows(pool, slots, k, v, bs)
     _same_pool(got, pool, bs, d)
 
 

@@ -243,3 +243,54 @@ def test_a_refused_step_leaves_everybody_out_of_the_decode(tail):
     out = torch.full((3,), 5, dtype=torch.int32, device=DEV)
     d, _ = run(lens, new, table, free, 0, 401 + tail, 16, decode_lens=out)
     assert int(d["err"].item()) & pa.DEVERR_OVERFLOW and (out == pa.PA_LEFT_OUT).all()
+
+
+@pytest.mark.parametrize("total", [4096, 16384])
+@pytest.mark.parametrize("name", REFUSED)
+def test_a_refused_step_of_a_cluster_changes_nothing(name, total):
+    """The refused steps again with slot maps that 8 and 16 CTAs fill."""
+    lens, new, o, flag = REFUSED[name]
+    if name == "slot map short":
+        new, o = [total, 1], dict(o, spare=total // 16 + 9, total=total, wide=total // 16 + 3)
+    else:
+        o = dict(o, total=o["total"] + total)
+    _, _, table, free = make(2, [max(n, 0) for n in lens], [0, 0], 16, o["spare"], wide=o.get("wide", 8))
+    count = o.get("count", o["spare"])
+    lens, new = np.array(lens, dtype=np.int32), np.array(new, dtype=np.int32)
+    d, out = run(lens, new, table, free, count, o["total"], 16)
+    assert int(d["err"].item()) & flag
+    assert np.array_equal(d["table"].cpu().numpy(), table) and np.array_equal(d["free"].cpu().numpy(), free)
+    assert int(d["nf"].item()) == count and (d["slots"] == -1).all()
+    assert not out[0].any() and not out[1].any() and np.array_equal(out[2], lens)
+
+
+@pytest.mark.parametrize("b,total", [(4500, 4500), (200, 17000), (16384, 16384)])
+def test_captured_steps_of_a_cluster_in_place(b, total):
+    """Lengths and stack written back by 8 and 16 CTAs, every replay the next
+    step; requests pause and end."""
+    bs, steps = 16, 8
+    rng = np.random.default_rng(b)
+    lens, _, table, free = make(10, rng.integers(0, 60, b).tolist(), [1] * b, bs, b, wide=6)
+    t = lambda x: torch.from_numpy(np.array(x)).to(DEV)  # noqa: E731
+    g_len, g_new, g_tab, g_free, nf = t(lens), t(lens), t(table), t(free), t(np.array([b], dtype=np.int32))
+    slots = torch.empty(total, dtype=torch.int32, device=DEV)
+    cu = [torch.empty(b + 1, dtype=torch.int32, device=DEV) for _ in range(2)]
+    at = torch.empty(b, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_block_tables(g_len, g_new, g_tab, g_free, nf, slots, bs, cu_seq_lens_q=cu[0], cu_seq_lens_k=cu[1],
+                           seqlens_k=g_len, decode_lens=at, dev_err=err)
+    count = b
+    for _ in range(steps):
+        new = rng.choice([-1, 0, 1, 1, 1, 1], b).astype(np.int32)
+        new[lens + 1 > 6 * bs] = -1
+        g_new.copy_(t(new))
+        graph.replay()
+        before = lens
+        table, free, count, want, cu_q, cu_k, lens = q4.block_tables(lens, new, table, free, count, total, bs)
+        torch.cuda.synchronize()
+        assert err.item() == 0 and nf.item() == count
+        for got, w in ((slots, want), (g_tab, table), (g_len, lens), (cu[0], cu_q), (cu[1], cu_k),
+                       (at, _decode_lens(before, new)), (g_free[:count], free[:count])):
+            assert np.array_equal(got.cpu().numpy(), w)

@@ -10,6 +10,7 @@ import torch
 import paged_kv_cache_300_gb300 as pa
 from oracle import q4
 from paged_kv_cache_300_gb300 import _build
+from tests.q4_util import edge_rows, write_rows
 
 
 @pytest.fixture(scope="module")
@@ -57,24 +58,6 @@ def test_rows_without_a_finite_low_read_as_nan(bad):
     assert np.isnan(q4.values(n, s, b)).all() and n.max() == 0
 
 
-def edge_rows(dtype):
-    """Finite rows with their largest element at the end of the numbers, and
-    their smallest from the same to its opposite."""
-    top = torch.finfo(dtype).max
-    if dtype == torch.float32:
-        tops = [top, 3.3895e38, 3.3896e38, 3.396e38, 3.4e38, 3.3e38, 3.35e38, 3.38e38]
-    else:
-        tops = [top, 3.3e38, 3.34e38, 3.36e38, 3.38e38]
-    g = torch.Generator().manual_seed(1)
-    rows = []
-    for hi in tops:
-        for low in (1.0, 0.999, 0.99, 17 / 32, 0.9, 0.5, 0.3, 0.05, 0.01, 0.0, -0.05, -0.7, -0.99):
-            x = hi * (low + (1 - low) * torch.rand(64, generator=g, dtype=torch.float64))
-            x[:2] = torch.tensor([hi * low, hi], dtype=torch.float64)
-            rows.append(x.clamp(-3.385e38, top).to(dtype))
-    return torch.stack(rows)
-
-
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_finite_rows_at_the_end_of_the_numbers_read_back_finite(dtype):
     x = edge_rows(dtype)
@@ -100,6 +83,21 @@ def test_write_then_read():
         k, v, _, _ = q4.read(pool, row, bs + 3, d, bs)
         assert np.array_equal(k, q4.values(*q4.quantise(x[:, 0])))
         assert np.array_equal(v, q4.values(*q4.quantise(x[:, 1])))
+
+
+@pytest.mark.parametrize("d,bs", [(64, 32), (128, 16)])
+def test_write_of_many_rows(d, bs):
+    rng = np.random.default_rng(2)
+    one = rng.integers(0, 256, (6, 3, q4.record_bytes(d, bs)), dtype=np.uint8)
+    many = one.copy()
+    x = rng.standard_normal((2, 40, 3, d)).astype(np.float32)
+    slots = rng.permutation(6 * bs)[:40].astype(np.int32)
+    slots[[3, 20]] = -1
+    for i, s in enumerate(slots):
+        if s >= 0:
+            q4.write(one, int(s), x[0, i], x[1, i], bs)
+    write_rows(many, slots, x[0], x[1], bs)
+    assert np.array_equal(one, many)
 
 
 def test_block_bytes(lib):
