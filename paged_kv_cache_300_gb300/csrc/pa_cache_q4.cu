@@ -20,10 +20,10 @@ constexpr int kThreads = 256;
 //
 // What bounds it: moving the bytes (a bf16 chunk's, and a quarter of them again)
 // on one side, instructions on the other.  33K rows of 8 bf16 heads x 128 dims
-// (174 MB): 33 us, 5.3 TB/s.  With 16 lanes a row, a pair's rows one after the
-// other, it was 44 us and 289 instructions for four rows of 128; now 173, because
-// a row's scale is computed once for 16 elements a lane and arithmetic goes in
-// pairs.
+// (174 MB): 34 us, 5.1 TB/s; of fp32 (306 MB): 51 us, 6.0 TB/s.  With 16 lanes a
+// row, a pair's rows one after the other, bf16 took 44 us and 289 instructions for four
+// rows of 128; now 178, because a row's scale is computed once for 16 elements a lane
+// and arithmetic goes in pairs.
 constexpr int kRows = 16;
 // Heads whose rows are held or on their way.  The same chunk with the read-back
 // behind it: 82 us with 1 (no loads beside the sums), 76 with 2, 75 with 3.
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 5)
 
 // ------------------------------------------------------------------ gather
 // What bounds it: writing the rows.  145K rows of 8 bf16 heads x 128 dims (750
-// MB): 116 us, 6.5 TB/s, 95% of a copy's rate.  fp32, 24K rows of 6 heads x 64
+// MB): 116 us, 6.5 TB/s, 95% of a copy's rate; fp32 208 us, the same rate.  fp32, 24K rows of 6 heads x 64
 // dims (84 MB): 18 us, 4.6 TB/s; with 8 values a thread, whose two stores leave
 // every other 16 bytes to the next instruction, it was 24.5 us.
 //

@@ -7,8 +7,9 @@
 // (token, head) instead of once per element.
 //
 // Codes as matrix operands.  A nibble n at bits 0-3 of a half is the f16
-// subnormal n 2^-24, at bits 4-7 it is n 2^-20, both exact, and mma.sync
-// multiplies subnormals exactly.  So  w & 0x000f000f  and  w & 0x00f000f0  of a
+// subnormal n 2^-24, at bits 4-7 it is n 2^-20, both exact, and mma.sync takes
+// subnormals (its sums keep some 17 bits of their products: see operand()).  So
+//  w & 0x000f000f  and  w & 0x00f000f0  of a
 // word (and of w >> 8) are four operand registers: 5 instructions turn 8 codes
 // into operands, with no conversion, subtraction or scaling.  The powers of two
 // leave through q (its elements that meet the 2^-20 codes carry 2^-4) and
@@ -53,11 +54,15 @@
 // logical order.  The warps of a head join in shared memory first.
 //
 // What bounds it (bf16; algorithmic bytes over time, a copy runs at 6.8 TB/s):
-//   96 sequences of 4K-16K, 64/8 heads x 128    1068 MB  176 us  6.1 TB/s  HBM; SMs end 5-8% apart
-//   256 of 512-4096, 32/8 x 128                   648 MB  114 us  5.7 TB/s  the same
-//   1024 of 257-768, 32/32 x 64                  1237 MB  228 us  5.4 TB/s  a sequence's ends, per head
+//   96 sequences of 4K-16K, 64/8 heads x 128    1068 MB  179 us  6.0 TB/s  HBM; SMs end 5-8% apart
+//   256 of 512-4096, 32/8 x 128                   648 MB  116 us  5.6 TB/s  the same
+//   1024 of 257-768, 32/32 x 64                  1237 MB  233 us  5.3 TB/s  a sequence's ends, per head
 //   64 of 512-4096, 32/8 x 128                    164 MB   42 us  3.9 TB/s  start 5-7 us, join 4-5 us
 //   one of 5000, 32/8 x 128                       5.5 MB   14 us            latency: start, walk, join
+// fp32 runs twice the products, operands of two halves and spilled registers:
+//   96 sequences of 4K-16K, 64/8 heads x 128    1070 MB  319 us  3.4 TB/s
+//   1024 of 257-768, 32/32 x 64                  1262 MB  349 us  3.6 TB/s
+//   64 of 512-4096, 32/8 x 128                    166 MB   62 us  2.7 TB/s
 #include "pa_internal.h"
 #include "pa_q4.cuh"
 
@@ -68,11 +73,11 @@ namespace pa {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-// One CTA of 16 warps an SM: a warp takes up to 128 registers and up to 9 KB of
+// One CTA of 16 warps an SM: a warp takes up to 128 registers and 7 to 11 KB of
 // ring.  With two CTAs of 8 warps, three slots a warp and twice the partials, 96
 // long sequences took 183 us (175), 64 shorter ones 44.2 (42.0).
 constexpr int kMaxWarps = 16;
-// Slots of a warp's ring: 74 to 147 KB in flight an SM, which is more than HBM's
+// Slots of a warp's ring: 74 to 176 KB in flight an SM, which is more than HBM's
 // latency needs.  More slots leave less L1 and were slower.
 constexpr int kSlots = 2;
 // Weights are p s in units of 2^14 (kUnit): for the largest steps, 2^125, the largest p
@@ -151,7 +156,8 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t w, uint32_t m, uint32_t x)
 // a subnormal's product by the smallest exponent, so it keeps some 17 bits of
 // the 24: plenty beside bf16 operands, too few for fp32 ones, whose codes are
 // made normal numbers first (times 2^14, exact): the largest error against 64
-// bits went from 5e-6 to 8e-7, and 64 fp32 sequences from 56 to 59 us.
+// bits, over four shapes, goes from 1.6e-5 to 9e-7, and 64 fp32 sequences from 59.6 to
+// 62.4 us, 1024 short ones from 315 to 349.
 template <bool F32>
 __device__ __forceinline__ uint32_t operand(uint32_t codes)
 {
@@ -1433,9 +1439,9 @@ int plan_and_launch(const DecodeQ4Args *a, int batch, int num_kv_heads, int grou
 }
 
 // Copies of the head group in the products' columns: as many as fit, up to
-// the tiles of a stage.  1024 sequences with D 64 and one head a kv head: 235 us
-// with four copies, 274 with two, q and the new rows not in the slots yet.  256
-// sequences with D 128 and four heads a kv head: 116 us with two, 122 with none.
+// the tiles of a stage.  1024 sequences with D 64 and one head a kv head: 233 us
+// with four copies, 288 with two.  256 sequences with D 128 and four heads a kv head:
+// 116 us with two, 121.5 with none.
 // Four copies (64-token stages) are for head_dim 64 only: at 128 their rings
 // would not fit 16 warps.
 template <int D, int BS, typename T>

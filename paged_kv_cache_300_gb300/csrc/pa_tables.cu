@@ -6,12 +6,12 @@
 // (4 a slot, 20 a request); what a call costs is latency.  So one launch does
 // it all: a cluster of CTAs in which each makes all the sums for itself (no
 // traffic between CTAs), then takes its share of the requests and of the
-// slots.  Two cluster barriers order the rest: given-back blocks are on the
+// slots.  One cluster barrier orders the rest: given-back blocks are on the
 // stack before a block is taken from it, and lengths and the stack's size,
-// which may be written in place, are read by everybody before.  A small step
+// which may be written in place, have been read by everybody before they are.  A small step
 // is one CTA (kClusterSlots).  Up to 4096 requests of a token each: 8.9 us, the
 // host's time for a call; 4096 requests, 585 of them ending, with 512K new
-// tokens: 19.7 us, of which the 2.4 MB would take 0.4: the rest is the chain of
+// tokens: 20.2 us, of which the 2.4 MB would take 0.4: the rest is the chain of
 // dependent steps (lengths, sums, barrier, search, stack, store).
 #include "pa_common.cuh"
 #include "pa_internal.h"
