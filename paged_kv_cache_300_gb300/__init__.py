@@ -450,6 +450,16 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _empty(stream, shape, dtype, device):
+    """An output the caller gave no tensor for, in memory of the stream that
+    writes it: memory that the current stream has given back may still be in use
+    there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _too_large():
     raise ValueError("a size passes 2^31 - 1")  # ctypes would cut it to 32 bits
 
@@ -574,7 +584,7 @@ def pa_decode_q4(q, kv_cache, block_table, cache_seqlens, k_new, v_new, out=None
     dt = _dtype(q)
     index, nb, bs = _q4_geometry(kv_cache, hkv, d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, shape, dtype, q.device)
     if out.shape != shape or rows != (b, hkv, d) or v_new.shape != rows or \
             (k_stored is not None and k_stored.shape != rows) or \
             (v_stored is not None and v_stored.shape != rows):
@@ -618,11 +628,11 @@ def pa_block_tables(cache_seqlens, new_lens, block_table, free_blocks, num_free,
     b, mb = block_table.shape
     index = block_table.get_device()
     if cu_seq_lens_q is None:
-        cu_seq_lens_q = torch.empty(b + 1, dtype=torch.int32, device=block_table.device)
+        cu_seq_lens_q = _empty(stream, b + 1, torch.int32, block_table.device)
     if cu_seq_lens_k is None:
-        cu_seq_lens_k = torch.empty(b + 1, dtype=torch.int32, device=block_table.device)
+        cu_seq_lens_k = _empty(stream, b + 1, torch.int32, block_table.device)
     if seqlens_k is None:
-        seqlens_k = torch.empty(b, dtype=torch.int32, device=block_table.device)
+        seqlens_k = _empty(stream, b, torch.int32, block_table.device)
     if num_free_out is None:
         num_free_out = num_free
     if not _fits(index, torch.int32, cache_seqlens, new_lens, block_table, free_blocks, num_free,

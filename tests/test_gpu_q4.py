@@ -533,6 +533,36 @@ def test_decode_on_a_stream_of_its_own():
     assert torch.equal(out, want)
 
 
+def test_outputs_made_for_another_stream_take_no_memory_in_use():
+    """A tensor that the current stream has yet to read is given up; what a call
+    on a side stream allocates must not lie there."""
+    c = make(37, [700, 30], 8, 2, 128, 16, BF16)
+    g = _dev(c)
+    n = 4096
+    lens, new, free, count = (torch.zeros(k, dtype=torch.int32, device=DEV) for k in (n, n, 8, 1))
+    table = torch.full((n, 1), -1, dtype=torch.int32, device=DEV)
+    slots = torch.empty(4, dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    calls = [((2, 8, 128), BF16, lambda: pa.pa_decode_q4(g["q"], g["pool"], g["table"], g["lens"], g["k_new"],
+                                                         g["v_new"], stream=side)),
+             ((n + 1,), torch.int32, lambda: pa.pa_block_tables(lens, new, table, free, count, slots, 16, stream=side))]
+    for shape, dtype, call in calls:
+        call()  # workspaces and code are there
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        x = [torch.full(shape, 3, dtype=dtype, device=DEV) for _ in range(3)]
+        y = [torch.zeros(shape, dtype=dtype, device=DEV) for _ in range(3)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)  # a tenth of a second
+        for a, b in zip(x, y):
+            b.copy_(a)
+        del x, a
+        kept = call()
+        torch.cuda.synchronize()
+        assert all((b == 3).all() for b in y)
+        del kept
+
+
 def test_two_captured_graphs_replay_at_once():
     """Graphs captured without a workspace of their own have one each."""
     cases = [make(25 + i, [3000, 2000, 2600], 8, 2, 128, 16, BF16) for i in range(2)]
