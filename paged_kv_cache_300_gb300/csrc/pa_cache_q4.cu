@@ -264,7 +264,7 @@ int launch_after(void (*kernel)(A...), dim3 grid, cudaStream_t s, A... args)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
+    return launch_status(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 template <int D, typename T>

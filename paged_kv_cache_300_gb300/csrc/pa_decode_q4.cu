@@ -1398,9 +1398,9 @@ int make_plan(int batch, int num_kv_heads, int group, Plan *p)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return PA_ERR_DEVICE;
     if (!__atomic_load_n(&raised[dev], __ATOMIC_ACQUIRE)) {
-        if (cudaFuncSetAttribute(decode_q4_kernel<D, BS, R, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)kSmemPerCta) != cudaSuccess)
-            return PA_ERR_LAUNCH;
+        const cudaError_t e = cudaFuncSetAttribute(
+            decode_q4_kernel<D, BS, R, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemPerCta);
+        if (e != cudaSuccess) return launch_status(e);
         __atomic_store_n(&raised[dev], 1, __ATOMIC_RELEASE);
     }
     p->gm.hs = hs;
@@ -1435,7 +1435,7 @@ int plan_and_launch(const DecodeQ4Args *a, int batch, int num_kv_heads, int grou
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_q4_kernel<D, BS, R, T>, *a, p.gm) == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
+    return launch_status(cudaLaunchKernelEx(&cfg, decode_q4_kernel<D, BS, R, T>, *a, p.gm));
 }
 
 // Copies of the head group in the products' columns: as many as fit, up to

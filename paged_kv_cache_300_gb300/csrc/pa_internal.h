@@ -176,6 +176,14 @@ int tables_launch(const TablesArgs &a, cudaStream_t s);
 
 // ------------------------------------------------------------------ helpers
 int num_sms();
+// Status of a launch (or of its preparation).  The runtime keeps a failed call's
+// error until it is asked for, and a later call that asks would report it as its own.
+inline int launch_status(cudaError_t e)
+{
+    if (e == cudaSuccess) return PA_OK;
+    cudaGetLastError();
+    return PA_ERR_LAUNCH;
+}
 int encode_rows_map(CUtensorMap *map, const void *base, uint64_t rows, int heads, int head_dim,
                     int box_rows);
 int encode_unit_map(CUtensorMap *map, const void *base, uint64_t rows, int heads, int head_dim,

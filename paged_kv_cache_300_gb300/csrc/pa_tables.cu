@@ -281,10 +281,11 @@ int tables_launch(const TablesArgs &args, cudaStream_t s)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_DEVICE;
     if (!__atomic_load_n(&raised[dev], __ATOMIC_ACQUIRE)) {
-        if (cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (3 * kTablesMaxBatch + 1) * 4) != cudaSuccess ||
-            cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-            return PA_ERR_LAUNCH;
+        cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (3 * kTablesMaxBatch + 1) * 4);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return launch_status(e);
         __atomic_store_n(&raised[dev], 1, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg = {};
@@ -302,7 +303,7 @@ int tables_launch(const TablesArgs &args, cudaStream_t s)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, tables_kernel, a) == cudaSuccess ? PA_OK : PA_ERR_LAUNCH;
+    return launch_status(cudaLaunchKernelEx(&cfg, tables_kernel, a));
 }
 
 }  // namespace pa

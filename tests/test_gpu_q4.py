@@ -1,5 +1,7 @@
 """The 4-bit pool on the GPU: update, read-back and decode against the plain
 reference."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -561,6 +563,41 @@ def test_outputs_made_for_another_stream_take_no_memory_in_use():
         torch.cuda.synchronize()
         assert all((b == 3).all() for b in y)
         del kept
+
+
+def test_a_refused_launch_is_not_reported_again_by_a_later_call():
+    """Launches into a capture that has become void fail on the host.  The next
+    good call of another kind must not answer with that error."""
+    cudart = ctypes.CDLL(f"libcudart.so.{torch.version.cuda.split('.')[0]}")
+    c = make(38, [20, 30], 8, 2, 128, 16, BF16)
+    g = _dev(c)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    out, ws = torch.empty_like(g["q"]), torch.zeros(4 << 20, dtype=torch.uint8, device=DEV)
+    slots, cu, one = i32(0, 1), i32(0, 1, 2), i32(0)
+    chunk, pool = g["k_new"], torch.zeros(4, 16, 2, 128, dtype=BF16, device=DEV)
+    table, free = torch.full((2, 2), -1, dtype=torch.int32, device=DEV), i32(0, 1, 2, 3)
+    outs = dict(cu_seq_lens_q=cu.clone(), cu_seq_lens_k=cu.clone(), seqlens_k=i32(0, 0))
+    calls = [lambda s: pa.pa_cache_update_q4(chunk, chunk, slots, g["pool"], stream=s),
+             lambda s: pa.pa_cache_gather_q4(g["pool"], g["table"], cu, chunk.clone(), chunk.clone(), stream=s),
+             lambda s: pa.pa_decode_q4(g["q"], g["pool"], g["table"], g["lens"], chunk, chunk, out, workspace=ws, stream=s),
+             lambda s: pa.pa_block_tables(i32(0, 0), i32(0, 0), table, free, one, slots, 16, stream=s, **outs)]
+    good = lambda: pa.pa_cache_update(chunk, chunk, cu, i32(0, 0), i32(0, 1).view(2, 1), pool, pool)  # noqa: E731
+    for call in calls:
+        call(None)
+        torch.cuda.synchronize()
+        side, graph = torch.cuda.Stream(), ctypes.c_void_p()
+        handle = ctypes.c_void_p(side.cuda_stream)
+        assert cudart.cudaStreamBeginCapture(handle, 2) == 0  # relaxed
+        try:
+            assert cudart.cudaStreamSynchronize(handle) != 0  # voids the capture
+            cudart.cudaGetLastError()
+            with pytest.raises(pa.PAError):
+                call(side)
+        finally:
+            cudart.cudaStreamEndCapture(handle, ctypes.byref(graph))
+            cudart.cudaGetLastError()
+        good()
+    torch.cuda.synchronize()
 
 
 def test_two_captured_graphs_replay_at_once():
