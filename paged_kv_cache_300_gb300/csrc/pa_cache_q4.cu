@@ -44,9 +44,9 @@ __global__ void __launch_bounds__(kThreads, 5)
     // Rows that lead: all but the odd token of a pair whose even one stands
     // before it in the chunk, and padding.
     const int row0 = blockIdx.x * kRows, mine = row0 + (lane & (kRows - 1));
-    const int slot_l = mine < a.total ? __ldg(a.slot_map + mine) : -1;
-    const int before = mine > 0 && mine < a.total ? __ldg(a.slot_map + mine - 1) : -1;
-    const int after = mine + 1 < a.total ? __ldg(a.slot_map + mine + 1) : -1;
+    const int slot_l = mine < a.total ? a.slot_map[mine] : -1;
+    const int before = mine > 0 && mine < a.total ? a.slot_map[mine - 1] : -1;
+    const int after = mine + 1 < a.total ? a.slot_map[mine + 1] : -1;
     const bool inside = slot_l < a.num_blocks << bs_shift;
     if (!inside && lane < kRows && threadIdx.x < 32 && blockIdx.y == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
     const bool leads = lane < kRows && slot_l >= 0 && inside && !((slot_l & 1) && before == slot_l - 1);
@@ -139,7 +139,7 @@ __device__ __forceinline__ int tile_owner(const int32_t *cu, int n, int x, int b
     int lo = 0, len = n; // the answer is in [lo, lo + len)
     while (len > 1) {
         const int step = (len + 31) / 32, r = lo + lane * step;
-        const bool below = lane * step < len && (__ldg(cu + r) >> bs_shift) + r <= x;
+        const bool below = lane * step < len && (cu[r] >> bs_shift) + r <= x;
         const int last = 31 - __clz((int)(__ballot_sync(kFull, below) | 1u));
         const int end = lo + len;
         lo += last * step;
@@ -152,9 +152,9 @@ __device__ __forceinline__ int tile_owner(const int32_t *cu, int n, int x, int b
 // (one block looks at all of them).
 __device__ __forceinline__ void check_cu(const CacheQ4Args &a)
 {
-    bool bad = threadIdx.x == 0 && (__ldg(a.cu_k) != 0 || __ldg(a.cu_k + a.batch) > a.total);
+    bool bad = threadIdx.x == 0 && (a.cu_k[0] != 0 || a.cu_k[a.batch] > a.total);
     for (int b = threadIdx.x; b < a.batch; b += blockDim.x)
-        bad = bad || __ldg(a.cu_k + b + 1) < __ldg(a.cu_k + b);
+        bad = bad || a.cu_k[b + 1] < a.cu_k[b];
     if (bad) flag_error(a.dev_err, PA_DEVERR_BAD_CU);
 }
 
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kThreads) gather_q4_kernel(const CacheQ4Args a
     if (blockIdx.x == 0) check_cu(a);
     const int bs = 1 << bs_shift, hkv = a.num_kv_heads;
     const int b = tile_owner(a.cu_k, a.batch, blockIdx.x, bs_shift);
-    const int k0 = __ldg(a.cu_k + b), k1 = min(__ldg(a.cu_k + b + 1), a.total);
+    const int k0 = a.cu_k[b], k1 = min(a.cu_k[b + 1], a.total);
     const int lb = (int)blockIdx.x - (k0 >> bs_shift) - b;
     if (k0 < 0 || lb < 0 || (long long)lb << bs_shift >= k1 - k0) return; // no tile, or flagged by check_cu
     const int pos0 = lb << bs_shift, rows = min(bs, k1 - k0 - pos0);
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) gather_q4_kernel(const CacheQ4Args a
     if (lb >= a.max_blocks_per_seq) {
         if (threadIdx.x == 0) flag_error(a.dev_err, PA_DEVERR_OVERFLOW);
     } else {
-        blk = __ldg(a.block_table + (size_t)b * a.max_blocks_per_seq + lb);
+        blk = a.block_table[(size_t)b * a.max_blocks_per_seq + lb];
         if (blk < 0 || blk >= a.num_blocks) {
             if (threadIdx.x == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
             blk = -1;
@@ -221,19 +221,19 @@ __global__ void __launch_bounds__(kThreads) gather_q4_kernel(const CacheQ4Args a
             const uint8_t *kr = rec + p * D + i * (N / 2);
             const uint8_t *vr = rec + q4_v_offset(D, bs) + 2 * q4_v_unit<D>(2 * p, i * (N / 4));
             if constexpr (N == 8) {
-                kc[0] = __ldg(reinterpret_cast<const uint32_t *>(kr));
-                kc[1] = __ldg(reinterpret_cast<const uint32_t *>(kr + D / 2));
-                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(vr));
+                kc[0] = *reinterpret_cast<const uint32_t *>(kr);
+                kc[1] = *reinterpret_cast<const uint32_t *>(kr + D / 2);
+                const uint2 w = *reinterpret_cast<const uint2 *>(vr);
                 vc[0] = __byte_perm(w.x, w.y, 0x5410);
                 vc[1] = __byte_perm(w.x, w.y, 0x7632);
             } else {
-                kc[0] = __ldg(reinterpret_cast<const uint16_t *>(kr));
-                kc[1] = __ldg(reinterpret_cast<const uint16_t *>(kr + D / 2));
-                const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(vr));
+                kc[0] = *reinterpret_cast<const uint16_t *>(kr);
+                kc[1] = *reinterpret_cast<const uint16_t *>(kr + D / 2);
+                const uint32_t w = *reinterpret_cast<const uint32_t *>(vr);
                 vc[0] = w & 0xffffu;
                 vc[1] = w >> 16;
             }
-            sc = __ldg(reinterpret_cast<const uint4 *>(rec + q4_scale_offset(D, bs) + p * 16));
+            sc = *reinterpret_cast<const uint4 *>(rec + q4_scale_offset(D, bs) + p * 16);
         }
         const size_t o = (size_t)(2 * p) * row_elts + h * D + i * N;
         float v[N];

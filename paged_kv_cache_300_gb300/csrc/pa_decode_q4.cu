@@ -56,7 +56,7 @@
 // What bounds it (bf16; algorithmic bytes over time, a copy runs at 6.8 TB/s):
 //   96 sequences of 4K-16K, 64/8 heads x 128    1068 MB  179 us  6.0 TB/s  HBM; SMs end 5-8% apart
 //   256 of 512-4096, 32/8 x 128                   648 MB  116 us  5.6 TB/s  the same
-//   1024 of 257-768, 32/32 x 64                  1237 MB  233 us  5.3 TB/s  a sequence's ends, per head
+//   1024 of 257-768, 32/32 x 64                  1237 MB  234 us  5.3 TB/s  a sequence's ends, per head
 //   64 of 512-4096, 32/8 x 128                    164 MB   42 us  3.9 TB/s  start 5-7 us, join 4-5 us
 //   one of 5000, 32/8 x 128                       5.5 MB   14 us            latency: start, walk, join
 // fp32 runs twice the products, operands of two halves and spilled registers:
@@ -738,10 +738,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
     int local = 0;
     const bool cached = B <= kMaxLens;
-    auto len_of = [&](int b) { return cached ? s_lens[b] : __ldg(a.cache_seqlens + b); };
+    auto len_of = [&](int b) { return cached ? s_lens[b] : a.cache_seqlens[b]; };
     for (int b = b_lo; b < b_hi; ++b) {
         bool ok;
-        const int len = __ldg(a.cache_seqlens + b);
+        const int len = a.cache_seqlens[b];
         if (cached) s_lens[b] = len;
         local += seq_blocks(len, cap, BS, &ok);
         if (!ok && len != PA_LEFT_OUT && blockIdx.x == 0) flag_error(a.dev_err, PA_DEVERR_OVERFLOW);
@@ -1439,7 +1439,7 @@ int plan_and_launch(const DecodeQ4Args *a, int batch, int num_kv_heads, int grou
 }
 
 // Copies of the head group in the products' columns: as many as fit, up to
-// the tiles of a stage.  1024 sequences with D 64 and one head a kv head: 233 us
+// the tiles of a stage.  1024 sequences with D 64 and one head a kv head: 234 us
 // with four copies, 288 with two.  256 sequences with D 128 and four heads a kv head:
 // 116 us with two, 121.5 with none.
 // Four copies (64-token stages) are for head_dim 64 only: at 128 their rings

@@ -879,3 +879,60 @@ def test_tables_and_decode_of_one_step(captured):
                                       _f32(xs[1][r:r + 1]), _f32(xs[2][r:r + 1]), bs)
                 check(out[r:r + 1], ref, decode_bound(xs[0][r:r + 1], seen, ref, BF16, d ** -0.5), (i, r))
     assert taken_over > 10  # rows of ended requests that name another's blocks
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("b,d,bs,hq,hkv,chunk", [(3, 128, 16, 8, 2, 5), (40, 64, 32, 8, 8, 3), (600, 64, 16, 4, 2, 2)])
+def test_steps_back_to_back_are_the_steps_one_by_one(captured, b, d, bs, hq, hkv, chunk):
+    """Every call starts while the one before it runs: tables (in place), update by
+    their slots and read-back, tables and decode, 24 times without a pause, give
+    the bits that the same steps give with a pause behind every call."""
+    steps, mb = 24, -(-24 * (chunk + 2) // bs) + 1
+    nb = b * mb
+    g = torch.Generator(device=DEV).manual_seed(b)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)  # noqa: E731
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(BF16)  # noqa: E731
+    rows, most = b * chunk, b * steps * (chunk + 1)
+    k, v, q, kn, vn = rnd(steps, rows, hkv, d), rnd(steps, rows, hkv, d), rnd(steps, b, hq, d), rnd(steps, b, hkv, d), rnd(
+        steps, b, hkv, d)
+    grow = torch.randint(0, chunk + 1, (steps, b), generator=g, device=DEV).int()
+    one = torch.randint(0, 2, (steps, b), generator=g, device=DEV).int()
+    order = torch.randperm(nb, generator=g, device=DEV).int()
+    results = []
+    for pause in (True, False):
+        pool, table, free, count = pa.pa_q4_pool(nb, hkv, d, bs), i32(b, mb) - 1, order.clone(), i32(1) + nb
+        lens, at, slots, cu, ck, err = i32(b), i32(b), i32(rows), i32(b + 1), i32(b + 1), i32(1)
+        out, kf, vf = rnd(steps, b, hq, d) * 0, torch.zeros(steps, most, hkv, d, dtype=BF16, device=DEV), None
+        vf = torch.zeros_like(kf)
+        ws = torch.zeros(pa.pa_decode_q4_workspace_size(b, hq, hkv, d, bs), dtype=torch.uint8, device=DEV)
+        stop = torch.cuda.synchronize if pause else (lambda: None)
+
+        def tables(new):
+            pa.pa_block_tables(lens, new, table, free, count, slots, bs, cu_seq_lens_q=cu, cu_seq_lens_k=ck,
+                               seqlens_k=lens, decode_lens=at, dev_err=err)
+            stop()
+
+        def chain():
+            for i in range(steps):
+                tables(grow[i])
+                pa.pa_cache_update_q4(k[i], v[i], slots, pool, dev_err=err)
+                stop()
+                pa.pa_cache_gather_q4(pool, table, ck, kf[i], vf[i], dev_err=err)
+                stop()
+                tables(one[i])
+                pa.pa_decode_q4(q[i], pool, table, at, kn[i], vn[i], out[i], workspace=ws, dev_err=err)
+                stop()
+
+        if captured and not pause:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                chain()
+            graph.replay()
+        else:
+            chain()
+        torch.cuda.synchronize()
+        assert err.item() == 0
+        results.append([out, pool, table, lens, free, count, kf, vf])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+    assert torch.isfinite(results[0][0]).all() and results[0][3].float().mean() > steps
