@@ -87,8 +87,10 @@ enum {
 #define PA_DEVERR_BAD_CU 4    /* cu_seq_lens not non-decreasing, or cu_seq_lens_k does not
                                  equal cache_seqlens + q lengths in pa_cache_update */
 #define PA_DEVERR_TIMEOUT 8   /* a bounded wait inside a kernel gave up */
-#define PA_LEFT_OUT INT32_MIN /* as a length: the sequence takes no part in the pa_decode_q4 call */
 #define PA_DEVERR_NO_SPACE 16 /* pa_block_tables: too few free blocks, or slot_map too short */
+
+/* as a length of pa_decode_q4: the sequence takes no part in the call */
+#define PA_LEFT_OUT INT32_MIN
 
 /*
  * Bytes of scratch workspace pa_decode needs for these sizes on the current
@@ -281,9 +283,9 @@ int pa_varlen_paged(const void *q, const void *k_cache, const void *v_cache,
  * stands for b + n s.  With fl = rounding to fp32 after each operation:
  *   b   = min x, rounded down to bf16
  *   r   = fl(fl(max x / 16 - b / 16) * fl(16 / 15))
- *   s   = r rounded up to bf16; 0 when r < 2^-100; up to twice the bf16
- *         number below while fl(b + 15 s) is larger than every bf16 number
- *         (rows with a value near 3.4e38)
+ *   s   = r rounded up to bf16; 0 when r < 2^-100.  While fl(b + 15 s) is
+ *         larger than every bf16 number (rows with a value near 3.4e38), s is
+ *         the next lower bf16 number instead, twice at most
  *   n_i = round-half-even(fl(fl(x_i / 16 - b / 16) * fl(16 / s))), at most 15
  *         (0 when s = 0)
  * so |x_i - (b + n_i s)| <= s / 2 up to the fp32 roundings.  A row that

@@ -14,11 +14,13 @@ built, or no GPU is present, calls raise.
                      (optionally gather prefix + chunk into packed k/v)
     pa_varlen        packed variable-length attention (bf16: tcgen05)
     pa_varlen_paged  the same, reading keys through block_table from the pool
-    pa_block_tables  a step's block tables, slot map and cumulative lengths,
-                     built on the GPU from the requests' lengths
+    pa_block_tables  a step's block tables, slot map, cumulative lengths and the
+                     lengths for its decode, built on the GPU from the requests'
+                     lengths
     pa_cache_update_q4  quantise a chunk into the 4-bit pool, by slot map
     pa_cache_gather_q4  read whole sequences of the 4-bit pool back
     pa_decode_q4     the decode step over the 4-bit pool
+    pa_reset_workspaces  zero the kept workspaces after a call that gave up
 """
 from __future__ import annotations
 
