@@ -69,7 +69,7 @@ def draw(rng):
         tokens = _log_int(rng, 1, min(65536, 100_000_000 // ((hq + hkv) * d)))
         return dict(op=op, tokens=tokens, lo=rng.randint(0, 65536), hq=hq, hkv=hkv, d=d, dtype=dtype, **turn)
     if op == "append":
-        budget = _log_int(rng, 1, 100_000_000 // ((hq + 2 * hkv) * d))  # new tokens
+        budget = _log_int(rng, 1, 70_000_000 // ((hq + 2 * hkv) * d))  # new tokens
         batch = min(_log_int(rng, 1, 1024), budget)
         room = max(1, 2 * (budget // batch) - 1)
         return dict(op=op, batch=batch, lo=0, hi=_log_int(rng, 1, 4096), new_lo=rng.choice([0, 1]) if room > 1 else 1, new_hi=room,
