@@ -71,7 +71,7 @@ def draw(rng):
     if op == "append":
         budget = _log_int(rng, 1, 70_000_000 // ((hq + 2 * hkv) * d))  # new tokens
         batch = min(_log_int(rng, 1, 1024), budget)
-        room = max(1, 2 * (budget // batch) - 1)
+        room = max(1, (2 if batch > 4 else 1) * (budget // batch))
         return dict(op=op, batch=batch, lo=0, hi=_log_int(rng, 1, 4096), new_lo=rng.choice([0, 1]) if room > 1 else 1, new_hi=room,
                     hq=hq, hkv=hkv, d=d, bs=bs, bounds=rng.random() < 0.8, dtype=dtype, **turn)
     top = _log_int(rng, 3, 256)
