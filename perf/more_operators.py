@@ -81,7 +81,7 @@ def draw(rng):
         batch = min(_log_int(rng, 1, 256), max(1, blocks // 8))
         hi = min(131072, max(8, blocks // batch) * bs)
         top = min(top, hi // bs // 2)  # some of the requests have more blocks than that
-        most = max(1, 60_000_000 // (hq * (hi // bs + 1)))  # queries
+        most = max(1, 8_000_000 // (hq * (hi // bs + 1)))  # queries
     else:
         most = 130_000_000 // (hkv * d * bs * top)
         batch = min(_log_int(rng, 1, 256), most)
