@@ -425,6 +425,112 @@ int pa_block_tables_decode(const int32_t *cache_seqlens, const int32_t *new_lens
                            int batch, int total_slots, int num_blocks, int block_size,
                            int max_blocks_per_seq, int32_t *dev_err, void *stream);
 
+/*
+ * Rotary positions
+ * ----------------
+ * A row of head_dim values has rotary_dim / 2 pairs (x, y): dims (i, rotary_dim / 2 + i),
+ * or neighbours (2i, 2i + 1) where `interleaved` is not 0.  Dims from rotary_dim on pass
+ * through.  Pair i of a token belongs to axis a = pair_axis[i] (time, height, width, ...)
+ * and is turned by that axis' position p = positions[a * tokens + token]:
+ *   x' = x c - y s,  y' = y c + x s,  c = cos_sin[p][i],  s = cos_sin[p][rotary_dim / 2 + i]
+ * in fp32, rounded once to dtype.  The table holds what the model's frequencies (and their
+ * scaling) give, and is the same for all calls.
+ *   positions  [num_axes, tokens]
+ *   cos_sin    fp32 [max_position, rotary_dim], 16-byte aligned
+ *   pair_axis  HOST array of rotary_dim / 2 axes below num_axes; NULL with one axis
+ *   q, k, q_out, k_out   rows of a token are dense [heads, head_dim]; from token to token
+ *              they are *_stride elements apart (a multiple of 16 bytes; outputs at
+ *              least heads * head_dim), so that q and k can be parts of one
+ *              projection's output.  An output may be its input (same stride), and
+ *              overlaps nothing else.  q or k may be NULL with 0 heads.
+ * A position outside [0, max_position) sets PA_DEVERR_OVERFLOW; the token's rows are
+ * zeros.  rotary_dim is a multiple of 16 up to head_dim, num_axes at most 4.
+ */
+int pa_rotary(const void *q, const void *k, const int32_t *positions, const float *cos_sin,
+              void *q_out, void *k_out, int tokens, int num_heads, int num_kv_heads, int head_dim,
+              int rotary_dim, int max_position, int num_axes, const uint8_t *pair_axis,
+              int interleaved, long long q_stride, long long k_stride, long long q_out_stride,
+              long long k_out_stride, pa_dtype dtype, int32_t *dev_err, void *stream);
+
+/*
+ * pa_rotary and the append to the paged cache in one pass: q is turned into q_out, k is
+ * turned and written with v (bit for bit) to slot slot_map[token] (physical block *
+ * block_size + offset, as pa_block_tables gives them) of k_cache, v_cache.  A row whose
+ * slot is negative is padding: nothing of it is read or written, its row of q_out
+ * included.  A slot >= num_blocks * block_size sets PA_DEVERR_BAD_BLOCK, a position
+ * outside the table PA_DEVERR_OVERFLOW: the token's q_out is zeros and nothing is
+ * appended.  A slot may appear once only: two rows in one slot leave a mixture.
+ * rotary_dim 0 appends without turning (positions and cos_sin NULL; q is copied).
+ *
+ * bounds [num_blocks, num_kv_heads, 2, head_dim] of dtype, or NULL: the least
+ * ([.., 0, :]) and the largest ([.., 1, :]) value of each channel over the keys of a
+ * block, as pa_select_blocks takes them.  A token at offset 0 starts its block's bounds
+ * anew, others widen them; NaN wins.  The rows of one block have to follow one another,
+ * in order of their offsets (as pa_block_tables packs them).  Blocks that get no token
+ * are left alone.
+ */
+int pa_cache_append_rotary(const void *q, const void *k, const void *v, const int32_t *slot_map,
+                           void *k_cache, void *v_cache, void *bounds, const int32_t *positions,
+                           const float *cos_sin, void *q_out, int tokens, int num_heads,
+                           int num_kv_heads, int head_dim, int rotary_dim, int max_position,
+                           int num_axes, const uint8_t *pair_axis, int interleaved,
+                           long long q_stride, long long k_stride, long long v_stride,
+                           long long q_out_stride, int num_blocks, int block_size, pa_dtype dtype,
+                           int32_t *dev_err, void *stream);
+
+/*
+ * Block-sparse attention
+ * ----------------------
+ * Queries are packed rows [total_q, num_heads, head_dim] located by cu_seq_lens_q
+ * [batch + 1], or one of each request where cu_seq_lens_q is NULL (total_q = batch).
+ * Request r has seqlens_k[r] keys in the cache, the new tokens' among them; of its ql
+ * queries, query i sees positions 0 .. seqlens_k[r] - ql + i (none where that is
+ * negative), so blocks 0 .. that position / block_size.  Rows behind
+ * cu_seq_lens_q[batch] are left as they were.  A request whose length is PA_LEFT_OUT takes
+ * no part: its rows see nothing.
+ *
+ * pa_select_blocks: for each query and kv head the logical numbers of top_k of the
+ * visible blocks, ascending, -1 behind them where fewer are visible:
+ *   selected [total_q, num_kv_heads, top_k]
+ * The first first_blocks and the last last_blocks visible ones are always among them;
+ * the others are those of largest
+ *   score = max over the kv head's query heads g of sum_d max(q_gd, 0) hi_d + min(q_gd, 0) lo_d,
+ * which no key between the block's bounds lo, hi exceeds in its product with q_g.  The
+ * choice is that of the exact scores (ties: the lowest block), whatever the order of the
+ * sums.  A NaN ranks above all numbers; sums of |q| |bound| stay below 3e38 (a score that
+ * overflows is an infinity).  Bounds of the last block are used only where last_blocks is
+ * 0: a chunk's later tokens are in them.
+ * dtype is that of q and bounds.  first_blocks + last_blocks <= top_k;
+ * max_blocks_per_seq <= 49152; num_heads / num_kv_heads <= 8; head_dim 64 or 128.
+ * A needed block_table entry that is no block sets PA_DEVERR_BAD_BLOCK, a length beyond
+ * the table PA_DEVERR_OVERFLOW, cu_seq_lens_q that does not start at 0 or decreases behind
+ * a row's request PA_DEVERR_BAD_CU: the rows are -1.
+ */
+int pa_select_blocks(const void *q, const void *bounds, const int32_t *block_table,
+                     const int32_t *seqlens_k, const int32_t *cu_seq_lens_q, int32_t *selected,
+                     int batch, int total_q, int num_heads, int num_kv_heads, int head_dim,
+                     int num_blocks, int block_size, int max_blocks_per_seq, int top_k,
+                     int first_blocks, int last_blocks, pa_dtype dtype, int32_t *dev_err,
+                     void *stream);
+
+/*
+ * pa_sparse: out[t, h] = softmax(scale q[t, h] K^T) V over the visible positions of the
+ * logical blocks selected[t, kv head, :] (any order; negative entries and blocks behind
+ * the query count nothing, a block that appears twice counts twice).  A row that sees no
+ * position is zeros; NaN that a row sees makes its outputs NaN, an infinite value those
+ * it reaches infinite or NaN.  selected, queries and lengths as above; the caches as pa_decode,
+ * whose tokens are all written already (nothing is appended).
+ * dtype PA_BF16 or PA_F32; num_heads / num_kv_heads <= 8; head_dim 64 or 128; PA_BF16: block_size
+ * a multiple of 16.  A needed block_table entry that is no block sets PA_DEVERR_BAD_BLOCK, a length
+ * beyond the table PA_DEVERR_OVERFLOW, a bad cu_seq_lens_q PA_DEVERR_BAD_CU: the rows are
+ * zeros.  Needs no workspace; calls share nothing.
+ */
+int pa_sparse(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+              const int32_t *seqlens_k, const int32_t *cu_seq_lens_q, const int32_t *selected,
+              void *out, int batch, int total_q, int num_heads, int num_kv_heads, int head_dim,
+              int num_blocks, int block_size, int max_blocks_per_seq, int top_k, pa_dtype dtype,
+              float softmax_scale, int32_t *dev_err, void *stream);
+
 /* Static description of a status code (never NULL). */
 const char *pa_status_string(int status);
 

@@ -21,10 +21,16 @@ built, or no GPU is present, calls raise.
     pa_cache_gather_q4  read whole sequences of the 4-bit pool back
     pa_decode_q4     the decode step over the 4-bit pool
     pa_reset_workspaces  zero the kept workspaces after a call that gave up
+    pa_rotary        queries and keys turned by their positions, on one axis or several
+    pa_cache_append_rotary  the same and the append to the paged cache in one pass, with
+                     the bounds of each block's keys
+    pa_select_blocks  the blocks each query attends to, chosen by those bounds
+    pa_sparse        attention over the selected blocks of the paged cache
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -37,7 +43,8 @@ __all__ = [
     "pa_decode_workspace_size", "pa_status_string", "pa_version", "DEVERR_BAD_BLOCK",
     "DEVERR_OVERFLOW", "DEVERR_BAD_CU", "DEVERR_TIMEOUT", "DEVERR_NO_SPACE", "pa_block_tables",
     "pa_q4_block_bytes", "pa_q4_pool", "pa_cache_update_q4", "pa_cache_gather_q4", "pa_decode_q4",
-    "pa_decode_q4_workspace_size", "PA_LEFT_OUT", "pa_reset_workspaces",
+    "pa_decode_q4_workspace_size", "PA_LEFT_OUT", "pa_reset_workspaces", "pa_rotary",
+    "pa_cache_append_rotary", "pa_select_blocks", "pa_sparse",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -106,6 +113,15 @@ def load():
         lib.pa_block_tables.restype = i
         lib.pa_block_tables_decode.argtypes = [p] * 11 + [i] * 5 + [p, p]
         lib.pa_block_tables_decode.restype = i
+        n = ctypes.c_longlong
+        lib.pa_rotary.argtypes = [p] * 6 + [i] * 7 + [p, i] + [n] * 4 + [i, p, p]
+        lib.pa_rotary.restype = i
+        lib.pa_cache_append_rotary.argtypes = [p] * 10 + [i] * 7 + [p, i] + [n] * 4 + [i] * 3 + [p, p]
+        lib.pa_cache_append_rotary.restype = i
+        lib.pa_select_blocks.argtypes = [p] * 6 + [i] * 12 + [p, p]
+        lib.pa_select_blocks.restype = i
+        lib.pa_sparse.argtypes = [p] * 8 + [i] * 10 + [f, p, p]
+        lib.pa_sparse.restype = i
         lib.pa_status_string.argtypes = [i]
         lib.pa_status_string.restype = ctypes.c_char_p
         lib.pa_version.argtypes = []
@@ -659,3 +675,203 @@ def pa_block_tables(cache_seqlens, new_lens, block_table, free_blocks, num_free,
             seqlens_k.data_ptr(), num_free_out.data_ptr(), _addr(decode_lens), b, slots, blocks,
             block_size, mb, _addr(dev_err))
     return cu_seq_lens_q, cu_seq_lens_k, seqlens_k
+
+
+# ------------------------------------------------------------------ rotary positions
+@functools.lru_cache(maxsize=64)
+def _pair_axes(axes):
+    """The host array of a tuple of axes, one of each pair."""
+    if min(axes) < 0 or max(axes) > 255:
+        raise ValueError("pair_axis holds axes from 0")
+    return (ctypes.c_uint8 * len(axes))(*axes)
+
+
+def _token_rows(index, dtype, name, t, tokens, head_dim):
+    """(heads, address, elements from token to token) of rows [T, H, D] whose
+    tokens may stand apart (a part of a projection's output); (0, None, 0) for None."""
+    if t is None:
+        return 0, None, 0
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.get_device() != index:
+        raise ValueError("all tensors must be on the same CUDA device")
+    n, heads, d = t.shape
+    if n != tokens or d != head_dim:
+        raise ValueError("inconsistent shapes")
+    step, row, one = t.stride()
+    if (one != 1 and d > 1) or (row != d and heads > 1):
+        raise ValueError(f"{name}: the rows of a token must be dense")
+    return heads, t.data_ptr(), heads * d if n <= 1 else step
+
+
+def _rotary_table(index, positions, cos_sin, pair_axis, tokens):
+    """(positions, cos_sin, rotary_dim, rows of the table, axes, host array of the
+    pairs' axes), checked."""
+    if positions is None or not _fits(index, torch.int32, positions):
+        _refuse(index, torch.int32, positions=positions)
+    if cos_sin is None or cos_sin.dim() != 2 or not _fits(index, torch.float32, cos_sin):
+        _refuse(index, torch.float32, cos_sin=cos_sin)
+    rows, rot = cos_sin.shape
+    if rows > 0x7FFFFFFF:
+        _too_large()
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
+        raise ValueError("positions must be [T] or [axes, T]")
+    host = None
+    if pair_axis is not None:
+        pair_axis = tuple(pair_axis)
+        if len(pair_axis) != rot // 2 or not pair_axis:
+            raise ValueError("pair_axis must have an axis for each of the rotary_dim / 2 pairs")
+        host = _pair_axes(pair_axis)
+    return positions.data_ptr(), cos_sin.data_ptr(), rot, rows, axes, host
+
+
+def pa_rotary(q, k, positions, cos_sin, q_out=None, k_out=None, interleaved: bool = False,
+              pair_axis=None, dev_err=None, stream=None):
+    """Turn queries q [T, Hq, D] and keys k [T, Hkv, D] (one of them may be None) by
+    their positions (see include/pa.h).  bfloat16 or float32; the tokens of a tensor
+    may stand apart (slices of one projection's output).  positions [T], or
+    [axes, T] with pair_axis, a sequence of the axis of each pair; cos_sin float32
+    [max_position, rotary_dim], cosines in the first half of a row.  interleaved: pairs
+    are neighbouring dims instead of split halves.  q_out, k_out may be q, k
+    themselves.  Returns (q_out, k_out)."""
+    some = q if q is not None else k
+    if some is None or not some.is_cuda:
+        raise ValueError("q or k is needed, on a CUDA device")
+    tokens, _, d = some.shape
+    index, dtype = some.get_device(), some.dtype
+    dt = _dtype(some)
+    if tokens > 0x7FFFFFFF:
+        _too_large()
+    hq, qp, qs = _token_rows(index, dtype, "q", q, tokens, d)
+    hk, kp, ks = _token_rows(index, dtype, "k", k, tokens, d)
+    pos, table, rot, rows, axes, host = _rotary_table(index, positions, cos_sin, pair_axis, tokens)
+    if not _fits(index, torch.int32, dev_err):
+        _refuse(index, torch.int32, dev_err=dev_err)
+    if q is not None and q_out is None:
+        q_out = _empty(stream, q.shape, dtype, q.device)
+    if k is not None and k_out is None:
+        k_out = _empty(stream, k.shape, dtype, k.device)
+    ho, qo, qos = _token_rows(index, dtype, "q_out", q_out, tokens, d)
+    hko, ko, kos = _token_rows(index, dtype, "k_out", k_out, tokens, d)
+    if ho != hq or hko != hk:
+        raise ValueError("inconsistent shapes")
+    _launch("pa_rotary", index, stream, qp, kp, pos, table, qo, ko, tokens, hq, hk, d, rot, rows,
+            axes, host, interleaved, qs, ks, qos, kos, dt, _addr(dev_err))
+    return q_out, k_out
+
+
+def pa_cache_append_rotary(q, k, v, slot_map, k_cache, v_cache, positions=None, cos_sin=None,
+                           q_out=None, bounds=None, interleaved: bool = False, pair_axis=None,
+                           dev_err=None, stream=None):
+    """Turn a step's q [T, Hq, D] (or None) and k [T, Hkv, D] by their positions and put
+    k, v into the slots slot_map [T] of k_cache, v_cache [NB, bs, Hkv, D] (see
+    include/pa.h); a negative slot skips its row.  positions, cos_sin, interleaved and
+    pair_axis as pa_rotary; without them k is put as it is.  bounds [NB, Hkv, 2, D], when
+    given, keeps the least and the largest key of each block for pa_select_blocks.
+    Returns q_out."""
+    if not k_cache.is_cuda:
+        raise ValueError("all tensors must live on a CUDA device")
+    nb, bs, hkv, d = k_cache.shape
+    index, dtype, tokens = k_cache.get_device(), k_cache.dtype, k.shape[0]
+    dt = _dtype(k_cache)
+    if tokens | nb | bs > 0x7FFFFFFF:
+        _too_large()
+    if v_cache.shape != k_cache.shape or (bounds is not None and bounds.shape != (nb, hkv, 2, d)) or \
+            not _fits(index, dtype, k_cache, v_cache, bounds):
+        _refuse(index, dtype, k_cache=k_cache, v_cache=v_cache, bounds=bounds)
+    if slot_map.shape != (tokens,) or not _fits(index, torch.int32, slot_map, dev_err):
+        _refuse(index, torch.int32, slot_map=slot_map, dev_err=dev_err)
+    hq, qp, qs = _token_rows(index, dtype, "q", q, tokens, d)
+    hk, kp, ks = _token_rows(index, dtype, "k", k, tokens, d)
+    hv, vp, vs = _token_rows(index, dtype, "v", v, tokens, d)
+    if positions is None and cos_sin is None:
+        if pair_axis is not None or interleaved:
+            raise ValueError("pairs to turn need positions and cos_sin")
+        pos = table = host = None
+        rot = rows = axes = 0
+    else:
+        pos, table, rot, rows, axes, host = _rotary_table(index, positions, cos_sin, pair_axis, tokens)
+    if q is not None and q_out is None:
+        q_out = _empty(stream, q.shape, dtype, q.device)
+    ho, qo, qos = _token_rows(index, dtype, "q_out", q_out, tokens, d)
+    if hk != hkv or hv != hkv or ho != hq:
+        raise ValueError("inconsistent shapes")
+    _launch("pa_cache_append_rotary", index, stream, qp, kp, vp, slot_map.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), _addr(bounds), pos, table, qo, tokens, hq, hkv, d,
+            rot, rows, axes, host, interleaved, qs, ks, vs, qos, nb, bs, dt, _addr(dev_err))
+    return q_out
+
+
+# ------------------------------------------------------------------ block-sparse attention
+def _query_rows(index, q, block_table, seqlens_k, cu_seq_lens_q, dev_err, **more):
+    """Checks of the index tensors that both calls take; (batch, table's width)."""
+    b, mb = block_table.shape
+    if b | mb | q.shape[0] > 0x7FFFFFFF:
+        _too_large()
+    if seqlens_k.shape != (b,) or \
+            (cu_seq_lens_q.shape != (b + 1,) if cu_seq_lens_q is not None else q.shape[0] != b) or \
+            not _fits(index, torch.int32, block_table, seqlens_k, cu_seq_lens_q, dev_err, *more.values()):
+        _refuse(index, torch.int32, block_table=block_table, seqlens_k=seqlens_k,
+                cu_seq_lens_q=cu_seq_lens_q, dev_err=dev_err, **more)
+    return b, mb
+
+
+def pa_select_blocks(q, bounds, block_table, seqlens_k, top_k: int, block_size: int,
+                     first_blocks: int = 1, last_blocks: int = 1, cu_seq_lens_q=None, selected=None,
+                     dev_err=None, stream=None):
+    """The blocks each query and kv head attends to (see include/pa.h): q [Tq, Hq, D]
+    (turned already), bounds [NB, Hkv, 2, D] of the blocks' keys, block_table [B, MB],
+    seqlens_k [B] with the new tokens; cu_seq_lens_q [B + 1] locates the requests'
+    queries (None: one of each).  Returns selected [Tq, Hkv, top_k] int32: logical blocks,
+    ascending, the first first_blocks and last last_blocks visible ones always among
+    them, -1 behind the last."""
+    if not q.is_cuda:
+        raise ValueError("all tensors must live on a CUDA device")
+    tq, hq, d = q.shape
+    index, dtype = q.get_device(), q.dtype
+    dt = _dtype(q)
+    nb, hkv, two, d2 = bounds.shape
+    if two != 2 or d2 != d or not _fits(index, dtype, q, bounds):
+        _refuse(index, dtype, q=q, bounds=bounds)
+    if nb | top_k | block_size | first_blocks | last_blocks > 0x7FFFFFFF:
+        _too_large()
+    if selected is None:
+        selected = _empty(stream, (tq, hkv, top_k), torch.int32, q.device)
+    elif selected.shape != (tq, hkv, top_k):
+        raise ValueError("selected must be [Tq, Hkv, top_k]")
+    b, mb = _query_rows(index, q, block_table, seqlens_k, cu_seq_lens_q, dev_err, selected=selected)
+    _launch("pa_select_blocks", index, stream, q.data_ptr(), bounds.data_ptr(), block_table.data_ptr(),
+            seqlens_k.data_ptr(), _addr(cu_seq_lens_q), selected.data_ptr(), b, tq, hq, hkv, d, nb,
+            block_size, mb, top_k, first_blocks, last_blocks, dt, _addr(dev_err))
+    return selected
+
+
+def pa_sparse(q, k_cache, v_cache, block_table, seqlens_k, selected, cu_seq_lens_q=None, out=None,
+              softmax_scale: float = 0.0, dev_err=None, stream=None):
+    """Attention of each query over its selected blocks (see include/pa.h): q [Tq, Hq, D];
+    k_cache, v_cache [NB, bs, Hkv, D], the new tokens written already; selected
+    [Tq, Hkv, top_k] int32 logical blocks (negative: none); block_table, seqlens_k and
+    cu_seq_lens_q as pa_select_blocks.  bfloat16 or float32.  Returns out [Tq, Hq, D]."""
+    if not q.is_cuda:
+        raise ValueError("all tensors must live on a CUDA device")
+    shape = q.shape
+    tq, hq, d = shape
+    index, dtype = q.get_device(), q.dtype
+    dt = _dtype(q)
+    nb, bs, hkv, d2 = k_cache.shape
+    if out is None:
+        out = _empty(stream, shape, dtype, q.device)
+    if d2 != d or v_cache.shape != k_cache.shape or out.shape != shape or \
+            not _fits(index, dtype, q, k_cache, v_cache, out):
+        _refuse(index, dtype, q=q, k_cache=k_cache, v_cache=v_cache, out=out)
+    top_k = selected.shape[-1]
+    if selected.shape != (tq, hkv, top_k):
+        raise ValueError("selected must be [Tq, Hkv, top_k]")
+    if nb | bs | top_k > 0x7FFFFFFF:
+        _too_large()
+    b, mb = _query_rows(index, q, block_table, seqlens_k, cu_seq_lens_q, dev_err, selected=selected)
+    _launch("pa_sparse", index, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), seqlens_k.data_ptr(), _addr(cu_seq_lens_q), selected.data_ptr(),
+            out.data_ptr(), b, tq, hq, hkv, d, nb, bs, mb, top_k, dt, softmax_scale, _addr(dev_err))
+    return out

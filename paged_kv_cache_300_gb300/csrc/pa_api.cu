@@ -122,6 +122,12 @@ static int cached_map(CUtensorMap *map, int kind, const void *base, uint64_t row
     return PA_OK;
 }
 
+int cached_unit_map(CUtensorMap *map, const void *base, uint64_t rows, int heads, int head_dim, int box_rows,
+                    int box_heads)
+{
+    return cached_map(map, 1, base, rows, heads, head_dim, box_rows, box_heads);
+}
+
 // 4-D bf16 view of q [rows, heads, 128] as (64 dims, 2 halves, heads, rows);
 // one box is one 64-dim half of `pack` consecutive heads for `box_queries`
 // consecutive rows, landing in shared memory as box_queries * pack rows of

@@ -174,8 +174,65 @@ struct TablesArgs {
 constexpr int kTablesMaxBatch = 16384;
 int tables_launch(const TablesArgs &a, cudaStream_t s);
 
+// ------------------------------------------------------------------ rotary positions
+struct RotaryArgs {
+    const void *q; // or NULL: no queries
+    const void *k;
+    const void *v; // append only
+    void *q_out;
+    void *k_out; // append: the pool's keys
+    void *v_out; // append: the pool's values
+    void *bounds; // append: [num_blocks, Hkv, 2, D] or NULL
+    const int32_t *positions; // [num_axes, tokens]
+    const float *cos_sin;     // [max_position, rotary_dim]
+    const int32_t *slot_map;  // append only
+    int32_t *dev_err;
+    unsigned long long pair_axis[2]; // two bits a pair
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride; // elements from token to token
+    int tokens, num_heads, num_kv_heads, rotary_dim, max_position, num_blocks, block_size;
+};
+int rotary_launch(const RotaryArgs &a, int axes, int head_dim, bool f32, bool interleaved, bool append, cudaStream_t s);
+
+// ------------------------------------------------------------------ block-sparse attention
+struct SelectArgs {
+    const void *q;
+    const void *bounds;
+    const int32_t *block_table;
+    const int32_t *seqlens_k;
+    const int32_t *cu_q; // or NULL: query t is request t's only one
+    int32_t *selected;
+    int32_t *dev_err;
+    int batch, total_q, num_heads, num_kv_heads, group, num_blocks, block_size, max_blocks_per_seq;
+    int top_k, first, last;
+};
+// Scored blocks that one row's shared memory holds.
+constexpr int kSelectMaxBlocks = 49152;
+int select_launch(const SelectArgs &a, int head_dim, bool f32, cudaStream_t s);
+
+struct SparseArgs {
+    const void *q;
+    const void *k_cache;
+    const void *v_cache;
+    const int32_t *block_table;
+    const int32_t *seqlens_k;
+    const int32_t *cu_q; // or NULL: query t is request t's only one
+    const int32_t *selected;
+    void *out;
+    int32_t *dev_err;
+    int batch, total_q, num_heads, num_kv_heads, group, num_blocks, block_size, max_blocks_per_seq, top_k;
+    float scale_log2;
+};
+// Tokens of one copy of the bf16 kernel: block_size is a multiple of it.
+constexpr int kSparseUnit = 16;
+int sparse_bf16_launch(const SparseArgs &a, int head_dim, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                       cudaStream_t s);
+int sparse_f32_launch(const SparseArgs &a, int head_dim, cudaStream_t s);
+
 // ------------------------------------------------------------------ helpers
 int num_sms();
+// The tensor map of encode_unit_map, from the maps of recent calls where it is there.
+int cached_unit_map(CUtensorMap *map, const void *base, uint64_t rows, int heads, int head_dim, int box_rows,
+                    int box_heads);
 // Status of a launch (or of its preparation).  The runtime keeps a failed call's
 // error until it is asked for, and a later call that asks would report it as its own.
 inline int launch_status(cudaError_t e)

@@ -1,0 +1,97 @@
+// What the block-sparse kernels share: where a query row stands in its request,
+// and access to a cluster's shared memory.
+#pragma once
+
+#include "pa_common.cuh"
+
+namespace pa {
+
+// Largest r in [0, n] with cu[r] <= t, -1 if there is none; the whole warp
+// searches, 32 entries a step (one step up to 32 requests, two up to 1024).
+__device__ __forceinline__ int find_request(const int32_t *cu, int n, int t, int lane)
+{
+    int lo = 0, count = n + 1;
+    while (true) {
+        const int step = (count + 31) / 32, at = lane * step;
+        const uint32_t m = __ballot_sync(0xffffffffu, at < count && __ldg(cu + lo + at) <= t);
+        if (m == 0) return lo == 0 ? -1 : lo; // lo > 0 was a hit of the step before
+        const int hit = 31 - __clz(m);
+        lo += hit * step;
+        count = min(step, count - hit * step);
+        if (step == 1) return lo;
+    }
+}
+
+// Row t of the packed queries: its request and the last position it sees.
+struct QueryRow {
+    int req;
+    int pos;   // < 0: sees nothing
+    bool skip; // behind the last request: its outputs are left as they are
+    int err;   // PA_DEVERR_* bits
+};
+
+template <typename Args>
+__device__ __forceinline__ QueryRow query_row(const Args &a, int t, int lane)
+{
+    QueryRow q{t, -1, false, 0};
+    int back = 0; // the request's queries behind row t
+    if (a.cu_q != nullptr) {
+        q.req = find_request(a.cu_q, a.batch, t, lane);
+        if (q.req == a.batch) {
+            q.skip = true;
+            return q;
+        }
+        const int c1 = q.req >= 0 ? __ldg(a.cu_q + q.req + 1) : 0;
+        if (q.req < 0 || c1 <= t || __ldg(a.cu_q) != 0) {
+            q.err = PA_DEVERR_BAD_CU;
+            return q;
+        }
+        back = c1 - 1 - t;
+    }
+    const int kl = __ldg(a.seqlens_k + q.req);
+    if (kl == PA_LEFT_OUT) return q;
+    if (kl < 0 || (long long)kl > (long long)a.max_blocks_per_seq * a.block_size) {
+        q.err = PA_DEVERR_OVERFLOW;
+        return q;
+    }
+    q.pos = kl - 1 - back;
+    return q;
+}
+
+// ---------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Address of `p` (this CTA's shared memory) in the CTA of rank `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t x)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ float cluster_load(uint32_t addr)
+{
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+    return x;
+}
+__device__ __forceinline__ void cluster_min(uint32_t addr, uint32_t x)
+{
+    asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void cluster_max(uint32_t addr, uint32_t x)
+{
+    asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+
+}  // namespace pa
