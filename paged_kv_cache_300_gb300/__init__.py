@@ -450,12 +450,15 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _launch(name, index, stream, *args):
     """Call the library with the tensors' device current, on `stream` (default:
     that device's current stream)."""
     fn = getattr(_lib or load(), name)
     handle = _current_raw_stream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(index):
@@ -681,9 +684,12 @@ def pa_block_tables(cache_seqlens, new_lens, block_table, free_blocks, num_free,
 @functools.lru_cache(maxsize=64)
 def _pair_axes(axes):
     """The host array of a tuple of axes, one of each pair."""
-    if min(axes) < 0 or max(axes) > 255:
-        raise ValueError("pair_axis holds axes from 0")
+    if not axes or min(axes) < 0 or max(axes) > 255:
+        raise ValueError("pair_axis holds an axis from 0 for each pair")
     return (ctypes.c_uint8 * len(axes))(*axes)
+
+
+_DTYPES = {torch.bfloat16: PA_BF16, torch.float32: PA_F32}
 
 
 def _token_rows(index, dtype, name, t, tokens, head_dim):
@@ -691,38 +697,43 @@ def _token_rows(index, dtype, name, t, tokens, head_dim):
     tokens may stand apart (a part of a projection's output); (0, None, 0) for None."""
     if t is None:
         return 0, None, 0
+    n, heads, d = t.shape
+    if n == tokens and d == head_dim and t.dtype is dtype and t.get_device() == index:
+        if t.is_contiguous():
+            return heads, t.data_ptr(), heads * d
+        step, row, one = t.stride()
+        if one == 1 and (row == d or heads <= 1):
+            return heads, t.data_ptr(), step
+        raise ValueError(f"{name}: the rows of a token must be dense")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.get_device() != index:
         raise ValueError("all tensors must be on the same CUDA device")
-    n, heads, d = t.shape
-    if n != tokens or d != head_dim:
-        raise ValueError("inconsistent shapes")
-    step, row, one = t.stride()
-    if (one != 1 and d > 1) or (row != d and heads > 1):
-        raise ValueError(f"{name}: the rows of a token must be dense")
-    return heads, t.data_ptr(), heads * d if n <= 1 else step
+    raise ValueError("inconsistent shapes")
 
 
 def _rotary_table(index, positions, cos_sin, pair_axis, tokens):
     """(positions, cos_sin, rotary_dim, rows of the table, axes, host array of the
     pairs' axes), checked."""
-    if positions is None or not _fits(index, torch.int32, positions):
-        _refuse(index, torch.int32, positions=positions)
-    if cos_sin is None or cos_sin.dim() != 2 or not _fits(index, torch.float32, cos_sin):
-        _refuse(index, torch.float32, cos_sin=cos_sin)
+    if positions is None or cos_sin is None:
+        raise ValueError("positions and cos_sin are needed")
     rows, rot = cos_sin.shape
-    if rows > 0x7FFFFFFF:
+    shape = positions.shape
+    if len(shape) == 1:
+        axes, n = 1, shape[0]
+    else:
+        axes, n = shape
+    if n != tokens or not _fits(index, torch.int32, positions):
+        _refuse(index, torch.int32, positions=positions)
+    if not _fits(index, torch.float32, cos_sin):
+        _refuse(index, torch.float32, cos_sin=cos_sin)
+    if rows | axes > 0x7FFFFFFF:
         _too_large()
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
-        raise ValueError("positions must be [T] or [axes, T]")
     host = None
     if pair_axis is not None:
-        pair_axis = tuple(pair_axis)
-        if len(pair_axis) != rot // 2 or not pair_axis:
+        host = _pair_axes(tuple(pair_axis))
+        if len(host) != rot // 2:
             raise ValueError("pair_axis must have an axis for each of the rotary_dim / 2 pairs")
-        host = _pair_axes(pair_axis)
     return positions.data_ptr(), cos_sin.data_ptr(), rot, rows, axes, host
 
 
@@ -735,27 +746,31 @@ def pa_rotary(q, k, positions, cos_sin, q_out=None, k_out=None, interleaved: boo
     [max_position, rotary_dim], cosines in the first half of a row.  interleaved: pairs
     are neighbouring dims instead of split halves.  q_out, k_out may be q, k
     themselves.  Returns (q_out, k_out)."""
-    some = q if q is not None else k
-    if some is None or not some.is_cuda:
-        raise ValueError("q or k is needed, on a CUDA device")
+    some = k if q is None else q
+    if some is None:
+        raise ValueError("q or k is needed")
     tokens, _, d = some.shape
     index, dtype = some.get_device(), some.dtype
-    dt = _dtype(some)
+    if index < 0:
+        raise ValueError("all tensors must live on a CUDA device")
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        dt = _dtype(some)
     if tokens > 0x7FFFFFFF:
         _too_large()
+    if q_out is None and q is not None:
+        q_out = _empty(stream, q.shape, dtype, q.device)
+    if k_out is None and k is not None:
+        k_out = _empty(stream, k.shape, dtype, k.device)
     hq, qp, qs = _token_rows(index, dtype, "q", q, tokens, d)
     hk, kp, ks = _token_rows(index, dtype, "k", k, tokens, d)
-    pos, table, rot, rows, axes, host = _rotary_table(index, positions, cos_sin, pair_axis, tokens)
-    if not _fits(index, torch.int32, dev_err):
-        _refuse(index, torch.int32, dev_err=dev_err)
-    if q is not None and q_out is None:
-        q_out = _empty(stream, q.shape, dtype, q.device)
-    if k is not None and k_out is None:
-        k_out = _empty(stream, k.shape, dtype, k.device)
     ho, qo, qos = _token_rows(index, dtype, "q_out", q_out, tokens, d)
     hko, ko, kos = _token_rows(index, dtype, "k_out", k_out, tokens, d)
     if ho != hq or hko != hk:
         raise ValueError("inconsistent shapes")
+    pos, table, rot, rows, axes, host = _rotary_table(index, positions, cos_sin, pair_axis, tokens)
+    if dev_err is not None and not _fits(index, torch.int32, dev_err):
+        _refuse(index, torch.int32, dev_err=dev_err)
     _launch("pa_rotary", index, stream, qp, kp, pos, table, qo, ko, tokens, hq, hk, d, rot, rows,
             axes, host, interleaved, qs, ks, qos, kos, dt, _addr(dev_err))
     return q_out, k_out
@@ -770,21 +785,29 @@ def pa_cache_append_rotary(q, k, v, slot_map, k_cache, v_cache, positions=None, 
     pair_axis as pa_rotary; without them k is put as it is.  bounds [NB, Hkv, 2, D], when
     given, keeps the least and the largest key of each block for pa_select_blocks.
     Returns q_out."""
-    if not k_cache.is_cuda:
-        raise ValueError("all tensors must live on a CUDA device")
-    nb, bs, hkv, d = k_cache.shape
+    shape = k_cache.shape
+    nb, bs, hkv, d = shape
     index, dtype, tokens = k_cache.get_device(), k_cache.dtype, k.shape[0]
-    dt = _dtype(k_cache)
+    if index < 0:
+        raise ValueError("all tensors must live on a CUDA device")
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        dt = _dtype(k_cache)
     if tokens | nb | bs > 0x7FFFFFFF:
         _too_large()
-    if v_cache.shape != k_cache.shape or (bounds is not None and bounds.shape != (nb, hkv, 2, d)) or \
+    if v_cache.shape != shape or (bounds is not None and bounds.shape != (nb, hkv, 2, d)) or \
             not _fits(index, dtype, k_cache, v_cache, bounds):
         _refuse(index, dtype, k_cache=k_cache, v_cache=v_cache, bounds=bounds)
     if slot_map.shape != (tokens,) or not _fits(index, torch.int32, slot_map, dev_err):
         _refuse(index, torch.int32, slot_map=slot_map, dev_err=dev_err)
+    if q_out is None and q is not None:
+        q_out = _empty(stream, q.shape, dtype, q.device)
     hq, qp, qs = _token_rows(index, dtype, "q", q, tokens, d)
     hk, kp, ks = _token_rows(index, dtype, "k", k, tokens, d)
     hv, vp, vs = _token_rows(index, dtype, "v", v, tokens, d)
+    ho, qo, qos = _token_rows(index, dtype, "q_out", q_out, tokens, d)
+    if hk != hkv or hv != hkv or ho != hq:
+        raise ValueError("inconsistent shapes")
     if positions is None and cos_sin is None:
         if pair_axis is not None or interleaved:
             raise ValueError("pairs to turn need positions and cos_sin")
@@ -792,11 +815,6 @@ def pa_cache_append_rotary(q, k, v, slot_map, k_cache, v_cache, positions=None, 
         rot = rows = axes = 0
     else:
         pos, table, rot, rows, axes, host = _rotary_table(index, positions, cos_sin, pair_axis, tokens)
-    if q is not None and q_out is None:
-        q_out = _empty(stream, q.shape, dtype, q.device)
-    ho, qo, qos = _token_rows(index, dtype, "q_out", q_out, tokens, d)
-    if hk != hkv or hv != hkv or ho != hq:
-        raise ValueError("inconsistent shapes")
     _launch("pa_cache_append_rotary", index, stream, qp, kp, vp, slot_map.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), _addr(bounds), pos, table, qo, tokens, hq, hkv, d,
             rot, rows, axes, host, interleaved, qs, ks, vs, qos, nb, bs, dt, _addr(dev_err))
@@ -804,16 +822,16 @@ def pa_cache_append_rotary(q, k, v, slot_map, k_cache, v_cache, positions=None, 
 
 
 # ------------------------------------------------------------------ block-sparse attention
-def _query_rows(index, q, block_table, seqlens_k, cu_seq_lens_q, dev_err, **more):
+def _query_rows(index, tokens, block_table, seqlens_k, cu_seq_lens_q, dev_err, selected):
     """Checks of the index tensors that both calls take; (batch, table's width)."""
     b, mb = block_table.shape
-    if b | mb | q.shape[0] > 0x7FFFFFFF:
+    if b | mb | tokens > 0x7FFFFFFF:
         _too_large()
     if seqlens_k.shape != (b,) or \
-            (cu_seq_lens_q.shape != (b + 1,) if cu_seq_lens_q is not None else q.shape[0] != b) or \
-            not _fits(index, torch.int32, block_table, seqlens_k, cu_seq_lens_q, dev_err, *more.values()):
+            (tokens != b if cu_seq_lens_q is None else cu_seq_lens_q.shape != (b + 1,)) or \
+            not _fits(index, torch.int32, block_table, seqlens_k, cu_seq_lens_q, dev_err, selected):
         _refuse(index, torch.int32, block_table=block_table, seqlens_k=seqlens_k,
-                cu_seq_lens_q=cu_seq_lens_q, dev_err=dev_err, **more)
+                cu_seq_lens_q=cu_seq_lens_q, dev_err=dev_err, selected=selected)
     return b, mb
 
 
@@ -826,11 +844,13 @@ def pa_select_blocks(q, bounds, block_table, seqlens_k, top_k: int, block_size: 
     queries (None: one of each).  Returns selected [Tq, Hkv, top_k] int32: logical blocks,
     ascending, the first first_blocks and last last_blocks visible ones always among
     them, -1 behind the last."""
-    if not q.is_cuda:
-        raise ValueError("all tensors must live on a CUDA device")
     tq, hq, d = q.shape
     index, dtype = q.get_device(), q.dtype
-    dt = _dtype(q)
+    if index < 0:
+        raise ValueError("all tensors must live on a CUDA device")
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        dt = _dtype(q)
     nb, hkv, two, d2 = bounds.shape
     if two != 2 or d2 != d or not _fits(index, dtype, q, bounds):
         _refuse(index, dtype, q=q, bounds=bounds)
@@ -840,7 +860,7 @@ def pa_select_blocks(q, bounds, block_table, seqlens_k, top_k: int, block_size: 
         selected = _empty(stream, (tq, hkv, top_k), torch.int32, q.device)
     elif selected.shape != (tq, hkv, top_k):
         raise ValueError("selected must be [Tq, Hkv, top_k]")
-    b, mb = _query_rows(index, q, block_table, seqlens_k, cu_seq_lens_q, dev_err, selected=selected)
+    b, mb = _query_rows(index, tq, block_table, seqlens_k, cu_seq_lens_q, dev_err, selected)
     _launch("pa_select_blocks", index, stream, q.data_ptr(), bounds.data_ptr(), block_table.data_ptr(),
             seqlens_k.data_ptr(), _addr(cu_seq_lens_q), selected.data_ptr(), b, tq, hq, hkv, d, nb,
             block_size, mb, top_k, first_blocks, last_blocks, dt, _addr(dev_err))
@@ -853,24 +873,27 @@ def pa_sparse(q, k_cache, v_cache, block_table, seqlens_k, selected, cu_seq_lens
     k_cache, v_cache [NB, bs, Hkv, D], the new tokens written already; selected
     [Tq, Hkv, top_k] int32 logical blocks (negative: none); block_table, seqlens_k and
     cu_seq_lens_q as pa_select_blocks.  bfloat16 or float32.  Returns out [Tq, Hq, D]."""
-    if not q.is_cuda:
-        raise ValueError("all tensors must live on a CUDA device")
-    shape = q.shape
+    shape, pool = q.shape, k_cache.shape
     tq, hq, d = shape
     index, dtype = q.get_device(), q.dtype
-    dt = _dtype(q)
-    nb, bs, hkv, d2 = k_cache.shape
+    if index < 0:
+        raise ValueError("all tensors must live on a CUDA device")
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        dt = _dtype(q)
+    nb, bs, hkv, d2 = pool
     if out is None:
         out = _empty(stream, shape, dtype, q.device)
-    if d2 != d or v_cache.shape != k_cache.shape or out.shape != shape or \
-            not _fits(index, dtype, q, k_cache, v_cache, out):
+    elif out.shape != shape:
+        raise ValueError("inconsistent shapes")
+    if d2 != d or v_cache.shape != pool or not _fits(index, dtype, q, k_cache, v_cache, out):
         _refuse(index, dtype, q=q, k_cache=k_cache, v_cache=v_cache, out=out)
-    top_k = selected.shape[-1]
-    if selected.shape != (tq, hkv, top_k):
+    rows, heads, top_k = selected.shape
+    if rows != tq or heads != hkv:
         raise ValueError("selected must be [Tq, Hkv, top_k]")
     if nb | bs | top_k > 0x7FFFFFFF:
         _too_large()
-    b, mb = _query_rows(index, q, block_table, seqlens_k, cu_seq_lens_q, dev_err, selected=selected)
+    b, mb = _query_rows(index, tq, block_table, seqlens_k, cu_seq_lens_q, dev_err, selected)
     _launch("pa_sparse", index, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_table.data_ptr(), seqlens_k.data_ptr(), _addr(cu_seq_lens_q), selected.data_ptr(),
             out.data_ptr(), b, tq, hq, hkv, d, nb, bs, mb, top_k, dt, softmax_scale, _addr(dev_err))

@@ -25,7 +25,8 @@ __device__ __forceinline__ int find_request(const int32_t *cu, int n, int t, int
 // Row t of the packed queries: its request and the last position it sees.
 struct QueryRow {
     int req;
-    int pos;   // < 0: sees nothing
+    int pos;   // < 0: sees nothing (the rows behind it may, but for the same error or left-out request)
+    int left;  // the request's queries from row t on
     bool skip; // behind the last request: its outputs are left as they are
     int err;   // PA_DEVERR_* bits
 };
@@ -33,7 +34,7 @@ struct QueryRow {
 template <typename Args>
 __device__ __forceinline__ QueryRow query_row(const Args &a, int t, int lane)
 {
-    QueryRow q{t, -1, false, 0};
+    QueryRow q{t, -(1 << 30), 1, false, 0};
     int back = 0; // the request's queries behind row t
     if (a.cu_q != nullptr) {
         q.req = find_request(a.cu_q, a.batch, t, lane);
@@ -47,6 +48,7 @@ __device__ __forceinline__ QueryRow query_row(const Args &a, int t, int lane)
             return q;
         }
         back = c1 - 1 - t;
+        q.left = c1 - t;
     }
     const int kl = __ldg(a.seqlens_k + q.req);
     if (kl == PA_LEFT_OUT) return q;

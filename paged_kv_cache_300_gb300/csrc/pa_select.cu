@@ -9,22 +9,28 @@
 // Scores.  Bound by the bytes of the bounds (2 D elements a block and head, 1 / bs
 // of the keys and values).  In bf16 the operands are exact and the sum is a
 // product of [q+, q-] with [hi, lo]: mma.sync m16n8k16 with 16 blocks on M and the
-// heads on N.  The order of the sum over d is free, so a lane's 16-byte load of a
-// row is two k-steps' fragments as it stands: bounds go from memory to the tensor
-// cores without shared memory, 8 KB a warp in flight.  A row is one CTA's; with
-// few rows a cluster's, whose CTAs score a share each and store the scores in
-// the first one's shared memory.
+// heads, of several tokens where there are fewer than 8, on N.  The order of the sum
+// over d is free, so a lane's 16-byte load of a row is two k-steps' fragments as it
+// stands: bounds go from memory to the tensor cores without shared memory, 8 KB a
+// warp in flight.  A CTA takes a tile of neighbouring tokens (one, for decode) and a kv
+// head, and reads the bounds once for all of the tile's tokens of a request.  With few
+// rows a cluster takes a row; its CTAs score a share each and store the scores in the
+// first one's shared memory.
 //
 // Choice.  The answer is that of the exact scores, ties to the lowest block,
 // whatever the order of the sums in fp32.  The k-th largest of the fp32 scores, t,
 // is found by histograms; with every score off by at most E, blocks above t + 2 E
 // are in and blocks below t - 2 E out for certain.  Where those between are more
-// than the places left, their scores are made again in 64 bits, as differences
-// from t, and chosen among by the same histograms.
+// than the places left, their scores are made again to some 60 bits, as differences
+// from t, and chosen among by the same histograms.  A warp chooses for a token of a tile;
+// all warps together for the only token.
 //   E: an m16n8k16 step is taken to be off by at most 2^-22 of the magnitudes it adds
-//   (|accumulator| + |products|); D / 16 steps a chain: E < 2^-22 (D / 16 + 2) S with S = sum |q||b|
-//   <= L1(q) max|b|.  2^-17 L1(q) max|b| is 3 times that.  (fp32: D / 16 + 5 roundings
-//   of 2^-24 a lane's share.)
+//   (|accumulator| + |products|); D / 16 steps a chain: E < 2^-22 (D / 16 + 2) S with S >=
+//   sum |q||b| of every head and block.  S is the largest over the blocks of sum_d u_d max(|lo_d|, |hi_d|),
+//   u the |q| of a head or, for tiles of tokens, the largest |q| of all their heads (one column more).  (fp32: D / 16 + 5
+//   roundings of 2^-24, within the same.)  L1(q) max|b| costs no product but is several times
+//   as much, and then every other row needs exact scores, which take longer than all the rest.
+#include <limits.h>
 #include <type_traits>
 
 #include "pa_common.cuh"
@@ -36,8 +42,9 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBins = 2048, kBinBits = 11;
-constexpr int kGroup = 8; // most query heads of a kv head
+constexpr int kGroup = 8;   // most query heads of a kv head
+constexpr int kTile = 16;   // most tokens of a CTA
+constexpr int kPad = 64;    // bytes behind a staged q row: neighbouring rows on other banks
 
 // Order-preserving map of floats to integers; a NaN is above everything, 0 is no float's.
 __device__ __forceinline__ uint32_t key_of(float x)
@@ -81,40 +88,51 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) // the other on
     asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t abs2(uint32_t x) { return x & 0x7fff7fffu; }
 
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(float x) { return x; }
 
-// What the CTAs of a row tell its first one.
-struct Shared {
-    uint32_t least, most; // of the keys
-    uint32_t mag;         // largest |bound| of blocks whose score is finite (bits of a float >= 0)
-    uint32_t bad;         // a needed table entry is no block
-    uint32_t bin, above, listed, result;
+// ------------------------------------------------------------------ the choice
+// Shared memory of W warps that choose together.
+template <int W>
+struct Choice {
+    static constexpr int BITS = W == 1 ? 8 : 11, BINS = 1 << BITS;
+    uint32_t bin, above, in, listed, result;
     uint32_t list[32];
-    uint32_t warp[kWarps];
-    uint32_t count[kWarps][2];
-    uint32_t hist[kBins];
+    float exact[32];
+    uint32_t warp[W][2];
+    uint32_t hist[BINS];
 };
 
-// The need-th largest of the keys in [lo, hi] (need >= 1, at most as many as there are).
-__device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint32_t need, uint32_t lo, uint32_t hi,
-                                                Shared &sh)
+template <int W>
+__device__ __forceinline__ void choice_sync()
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int PER = kBins / kThreads;
-    while (lo < hi) { // at most three times: 11 bits each
-        const int bits = 32 - __clz(hi - lo), shift = max(bits - kBinBits, 0);
-        for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
-        if (tid == 0) sh.listed = 0;
+    if (W == 1)
+        __syncwarp();
+    else
         __syncthreads();
-        for (int i = tid; i < n; i += kThreads) {
+}
+
+// The need-th largest of the keys in [lo, hi] (need >= 1, at most as many as there are).
+// `tid` counts the threads of the W warps.
+template <int W>
+__device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint32_t need, uint32_t lo, uint32_t hi,
+                                                Choice<W> &sh, int tid)
+{
+    constexpr int T = 32 * W, PER = Choice<W>::BINS / T;
+    const int lane = tid & 31, warp = tid >> 5;
+    while (lo < hi) { // at most four times
+        const int bits = 32 - __clz(hi - lo), shift = max(bits - Choice<W>::BITS, 0);
+        for (int i = tid; i < Choice<W>::BINS; i += T) sh.hist[i] = 0;
+        if (tid == 0) sh.listed = 0;
+        choice_sync<W>();
+#pragma unroll 4
+        for (int i = tid; i < n; i += T) {
             const uint32_t k = key[i];
             if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1u);
         }
-        __syncthreads();
+        choice_sync<W>();
         // sums from the top bin down: thread t has bins PER * t ..
         uint32_t bin[PER], sum = 0;
 #pragma unroll
@@ -125,33 +143,37 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint
             const uint32_t x = __shfl_down_sync(kFull, incl, o);
             if (lane + o < 32) incl += x;
         }
-        if (lane == 0) sh.warp[warp] = incl;
-        __syncthreads();
         uint32_t above = incl - sum;
-        for (int w = warp + 1; w < kWarps; ++w) above += sh.warp[w];
+        if (W > 1) {
+            if (lane == 0) sh.warp[warp][0] = incl;
+            choice_sync<W>();
+#pragma unroll
+            for (int w = 1; w < W; ++w) above += w > warp ? sh.warp[w][0] : 0;
+        }
         if (above < need && need <= above + sum) { // one thread
+#pragma unroll
             for (int i = PER - 1; i >= 0; --i) {
-                if (need <= above + bin[i]) {
+                if (above < need && need <= above + bin[i]) {
                     sh.bin = tid * PER + i;
                     sh.above = above;
-                    sh.result = bin[i];
-                    break;
+                    sh.in = bin[i];
                 }
                 above += bin[i];
             }
         }
-        __syncthreads();
-        const uint32_t in = sh.result;
+        choice_sync<W>();
+        const uint32_t in = sh.in;
         need -= sh.above;
         lo += sh.bin << shift;
         if (shift == 0) return lo; // a bin is one key
         hi = min(hi, lo + ((1u << shift) - 1));
         if (in <= 32) { // few enough to look at one by one
-            for (int i = tid; i < n; i += kThreads) {
+#pragma unroll 4
+            for (int i = tid; i < n; i += T) {
                 const uint32_t k = key[i];
                 if (k >= lo && k <= hi) sh.list[atomicAdd(&sh.listed, 1u)] = k;
             }
-            __syncthreads();
+            choice_sync<W>();
             if (warp == 0) {
                 const uint32_t k = lane < in ? sh.list[lane] : 0;
                 uint32_t more = 0, same = 0;
@@ -162,88 +184,254 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint
                 }
                 if (lane < in && more < need && need <= more + same) sh.result = k;
             }
-            __syncthreads();
+            choice_sync<W>();
             return sh.result;
         }
-        __syncthreads();
+        choice_sync<W>();
     }
     return lo;
 }
 
-// The row's score of one block in 64 bits; the warp's lanes share the channels.
+// A sum of floats kept as three: what rounding leaves at each level goes to the next
+// (the error-free sum of two numbers, Knuth), so the whole is off by some 2^-60 of the
+// magnitudes.  64-bit arithmetic would do, but this GPU has little: 2 us a block here.
+struct Sum3 {
+    float a = 0.f, b = 0.f, c = 0.f;
+    static __device__ __forceinline__ float two_sum(float x, float y, float &left)
+    {
+        const float s = x + y, t = s - x;
+        left = (x - (s - t)) + (y - t);
+        return s;
+    }
+    __device__ __forceinline__ void add(float x)
+    {
+        float e, f;
+        a = two_sum(a, x, e);
+        b = two_sum(b, e, f);
+        c += f;
+    }
+    __device__ __forceinline__ double value() const { return (double)a + ((double)b + (double)c); }
+};
+
+// The row's score of one block, exact to the last bits of a double, in all lanes.  Four
+// lanes share a head.
 template <typename T, int D>
 __device__ __forceinline__ double exact_score(const T *q, const T *bounds, int G, int lane)
 {
-    double best = 0;
-    for (int g = 0; g < G; ++g) {
-        double s = 0;
+    const int g = lane >> 2;
+    Sum3 sum;
+    if (g < G) {
+        constexpr int N = D / 32;
+        T x[N][8], lo[N][8], hi[N][8];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const int d = i * 32 + lane;
-            const float x = to_float(q[(size_t)g * D + d]);
-            // one of the two factors is 0
-            s += (double)x * (double)to_float(bounds[x > 0.f ? D + d : d]);
-        }
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-        best = g == 0 || s > best ? s : best;
+            for (int j = 0; j < (int)sizeof(T) / 2; ++j) {
+                const int d = i * 32 + (lane & 3) * 8;
+                reinterpret_cast<uint4 *>(x[i])[j] = reinterpret_cast<const uint4 *>(q + (size_t)g * D + d)[j];
+                reinterpret_cast<uint4 *>(lo[i])[j] = reinterpret_cast<const uint4 *>(bounds + d)[j];
+                reinterpret_cast<uint4 *>(hi[i])[j] = reinterpret_cast<const uint4 *>(bounds + D + d)[j];
+            }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float u = to_float(x[i][j]), v = u > 0.f ? to_float(hi[i][j]) : to_float(lo[i][j]); // the other product is 0
+                const float p = u * v;
+                sum.add(p);
+                if (sizeof(T) == 4) sum.add(fmaf(u, v, -p)); // (bf16 products are exact)
+            }
     }
-    return best;
+    double s = sum.value();
+    s += __shfl_xor_sync(kFull, s, 1);
+    s += __shfl_xor_sync(kFull, s, 2);
+    for (int k = 1; k < G; ++k) { // the largest, to lane 0 and from there to all
+        const double x = __shfl_sync(kFull, s, 4 * k);
+        if (lane == 0 && x > s) s = x;
+    }
+    return __shfl_sync(kFull, s, 0);
 }
 
-// What one warp has of the row's keys.
-struct Range {
-    uint32_t least = 0xffffffffu, most = 0;
-    float mag = 0.f;
-    __device__ __forceinline__ void take(uint32_t k, float score, float m)
-    {
-        least = min(least, k);
-        most = max(most, k);
-        if (fabsf(score) < INFINITY) mag = fmaxf(mag, m);
-    }
+// What a row's choice is made from.
+template <typename T>
+struct Row {
+    const T *q;           // of the row's G heads
+    const T *bounds;      // of the kv head
+    const int32_t *table; // of the scored blocks
+    int n, first;         // scored blocks, the logical number of the first of them
+    int need;             // to be chosen
+    float width;          // 2 E
 };
 
-template <int D>
-__device__ __forceinline__ void score_blocks(const SelectArgs &a, const __nv_bfloat16 *q, const int32_t *table, int h,
-                                             int j0, int n, int first, int stride, int lane, uint32_t keys, Range &range,
-                                             float &l1, bool &bad)
+// Writes the `need` of the row's n scored blocks with the largest scores to out, ascending.
+// `key` holds the scores.
+template <typename T, int D, int W>
+__device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *out, const SelectArgs &a, Choice<W> &sh, int tid)
+{
+    const int lane = tid & 31, warp = tid >> 5, n = r.n, need = r.need;
+    uint32_t least = 0xffffffffu, most = 0;
+#pragma unroll 4
+    for (int i = tid; i < n; i += 32 * W) { // scores to keys
+        const uint32_t k = key_of(__uint_as_float(key[i]));
+        key[i] = k;
+        least = min(least, k);
+        most = max(most, k);
+    }
+    least = __reduce_min_sync(kFull, least);
+    most = __reduce_max_sync(kFull, most);
+    choice_sync<1>();
+    if (W > 1) {
+        if (lane == 0) {
+            sh.warp[warp][0] = least;
+            sh.warp[warp][1] = most;
+        }
+        choice_sync<W>();
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            least = min(least, sh.warp[w][0]);
+            most = max(most, sh.warp[w][1]);
+        }
+        choice_sync<W>();
+    }
+    // keys above `high` are in, and `quota` of those from `low` to `high`
+    uint32_t low = kth_largest<W>(key, n, need, least, most, sh, tid), high = low;
+    const float cut = value_of(low);
+    const bool blurred = fabsf(cut) < INFINITY && r.width > 0.f && r.width < INFINITY;
+    if (blurred) {
+        low = key_of(cut - r.width);
+        high = key_of(cut + r.width);
+    }
+    // each warp has a run of a multiple of 32 keys, so that places follow from counts
+    const int per = ((n + 32 * W - 1) / (32 * W)) * 32, i0 = warp * per, i1 = min(n, i0 + per);
+    int sure = 0, open = 0, sure_before = 0, open_before = 0;
+    for (int pass = 0;; ++pass) {
+        int mine_sure = 0, mine_open = 0;
+#pragma unroll 4
+        for (int i = i0 + lane; i < i1; i += 32) {
+            const uint32_t k = key[i];
+            mine_sure += k > high;
+            mine_open += k >= low && k <= high;
+        }
+        mine_sure = __reduce_add_sync(kFull, mine_sure);
+        mine_open = __reduce_add_sync(kFull, mine_open);
+        if (W > 1) {
+            if (lane == 0) {
+                sh.warp[warp][0] = mine_sure;
+                sh.warp[warp][1] = mine_open;
+            }
+            choice_sync<W>();
+            sure = open = sure_before = open_before = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                if (w == warp) {
+                    sure_before = sure;
+                    open_before = open;
+                }
+                sure += sh.warp[w][0];
+                open += sh.warp[w][1];
+            }
+        } else {
+            sure = mine_sure;
+            open = mine_open;
+        }
+        if (pass > 0 || !blurred || sure + open == need) break;
+        // more blocks than places within the error of the scores: again and exactly,
+        // as the difference from the cut (a float holds it to 2^-40 of the scores)
+        if (open <= 32) { // as good as always: a few
+            if (tid == 0) sh.listed = 0;
+            choice_sync<W>();
+            for (int i = i0 + lane; i < i1; i += 32)
+                if (key[i] >= low && key[i] <= high) sh.list[atomicAdd(&sh.listed, 1u)] = i;
+            choice_sync<W>();
+            for (int c = warp; c < open; c += W) {
+                const T *bounds = r.bounds + (size_t)__ldg(r.table + sh.list[c]) * a.num_kv_heads * 2 * D;
+                const float x = (float)(exact_score<T, D>(r.q, bounds, a.group, lane) - (double)cut);
+                if (lane == 0) sh.exact[c] = x;
+            }
+            choice_sync<W>();
+            if (tid < open) {
+                int before = 0;
+                for (int c = 0; c < open; ++c)
+                    before += sh.exact[c] > sh.exact[tid] || (sh.exact[c] == sh.exact[tid] && sh.list[c] < sh.list[tid]);
+                key[sh.list[tid]] = before < need - sure ? 0xffffffffu : 0u;
+            }
+            choice_sync<W>();
+            low = high; // none is left there
+            continue;
+        }
+        for (int i = i0 + lane; i - lane < i1; i += 32) {
+            const uint32_t k = i < i1 ? key[i] : 0;
+            uint32_t todo = __ballot_sync(kFull, i < i1 && k >= low && k <= high);
+            uint32_t now = k > high ? 0xffffffffu : 0u;
+            while (todo) {
+                const int b = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const T *bounds = r.bounds + (size_t)__ldg(r.table + (i - lane) + b) * a.num_kv_heads * 2 * D;
+                const uint32_t exact = key_of((float)(exact_score<T, D>(r.q, bounds, a.group, lane) - (double)cut));
+                if (lane == b) now = exact;
+            }
+            if (i < i1) key[i] = now;
+        }
+        choice_sync<W>();
+        low = high = kth_largest<W>(key, n, need - sure, 1u, 0xfffffffeu, sh, tid);
+        choice_sync<W>();
+    }
+    const int quota = need - sure;
+    int place = sure_before + min(open_before, quota), ties = open_before;
+#pragma unroll 4
+    for (int i = i0 + lane; i - lane < i1; i += 32) {
+        const uint32_t k = i < i1 ? key[i] : 0;
+        const uint32_t eq = __ballot_sync(kFull, i < i1 && k >= low && k <= high), below = (1u << lane) - 1;
+        const bool in = i < i1 && (k > high || (((eq >> lane) & 1) && ties + __popc(eq & below) < quota));
+        const uint32_t chosen = __ballot_sync(kFull, in);
+        if (in) out[place + __popc(chosen & below)] = r.first + i;
+        place += __popc(chosen);
+        ties += __popc(eq);
+    }
+}
+
+// ------------------------------------------------------------------ the scores
+// What a warp scores: blocks 0 .. n - 1 of a request's row of the table from `table` on, for
+// the heads of `tokens` tokens, whose rows of q stand in shared memory ([token][heads' power
+// of two], rows of D elements and kPad bytes, 0 where there is no head; behind them the
+// largest |q| of all; what else is in the last 8 rows goes to columns that nobody reads).  Scores go to shared memory at `keys`, `stride` bytes a token.
+struct Scoring {
+    const int32_t *table;
+    int head, n, tokens, heads_log2;
+    uint32_t q, keys, stride;
+};
+
+__device__ __forceinline__ uint4 load_shared(uint32_t addr)
+{
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr));
+    return x;
+}
+
+template <int D, bool ONE>
+__device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring &s, int first, int step, int lane, float &mag,
+                                             int &bad, const __nv_bfloat16 *)
 {
     constexpr int NC = D / 32; // 16-byte pieces of a row per lane
-    const int g = lane >> 2, c = (lane & 3) * 8, G = a.group;
-    uint4 qp[NC], qn[NC];
-    float mine = 0.f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (g < G) x = *reinterpret_cast<const uint4 *>(q + (size_t)g * D + i * 32 + c);
-        qp[i] = make_uint4(max_nan2(x.x, 0), max_nan2(x.y, 0), max_nan2(x.z, 0), max_nan2(x.w, 0));
-        qn[i] = make_uint4(min_nan2(x.x, 0), min_nan2(x.y, 0), min_nan2(x.z, 0), min_nan2(x.w, 0));
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mine += fabsf(low_bf16(w[j])) + fabsf(high_bf16(w[j]));
-    }
-    mine += __shfl_xor_sync(kFull, mine, 1);
-    mine += __shfl_xor_sync(kFull, mine, 2);
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) mine = fmaxf(mine, __shfl_xor_sync(kFull, mine, o));
-    l1 = mine;
-
-    const __nv_bfloat16 *bounds = static_cast<const __nv_bfloat16 *>(a.bounds) + (size_t)h * 2 * D + c;
+    constexpr int ROW = 2 * D + kPad;
+    const int g = lane >> 2, c = lane & 3, n = s.n;
+    const int per_log2 = 3 - s.heads_log2; // tokens of 8 columns
+    const int groups = (s.tokens + (1 << per_log2) - 1) >> per_log2;
+    const __nv_bfloat16 *bounds = static_cast<const __nv_bfloat16 *>(a.bounds) + (size_t)s.head * 2 * D + c * 8;
     const size_t block = (size_t)a.num_kv_heads * 2 * D;
     const int tiles = (n + 15) / 16;
-    const int col = 2 * (lane & 3);
+    // the lane's entry of a tile's 16 blocks (a row behind the last reads block 0 and is left out)
     auto entry_of = [&](int tile) {
         const int j = tile * 16 + (lane & 15);
-        return tile < tiles && j < n ? __ldg(table + j0 + j) : 0;
+        const int e = tile < tiles && j < n ? __ldg(s.table + j) : 0;
+        const bool wrong = e < 0 || e >= a.num_blocks;
+        if (wrong) bad = min(bad, j);
+        return wrong ? 0 : e;
     };
     int entry = entry_of(first);
-    for (int tile = first; tile < tiles; tile += stride) {
-        const bool wrong = entry < 0 || entry >= a.num_blocks;
-        bad |= wrong;
-        const int at = wrong ? 0 : entry; // (a row behind the last reads block 0 and is left out)
-        entry = entry_of(tile + stride);
-        const __nv_bfloat16 *r0 = bounds + (size_t)__shfl_sync(kFull, at, g) * block;
-        const __nv_bfloat16 *r1 = bounds + (size_t)__shfl_sync(kFull, at, g + 8) * block;
+    for (int tile = first; tile < tiles; tile += step) {
+        const __nv_bfloat16 *r0 = bounds + (size_t)__shfl_sync(kFull, entry, g) * block;
+        const __nv_bfloat16 *r1 = bounds + (size_t)__shfl_sync(kFull, entry, g + 8) * block;
         uint4 lo[NC][2], hi[NC][2];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -252,271 +440,348 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const __nv_bfl
             hi[i][0] = __ldg(reinterpret_cast<const uint4 *>(r0 + D + i * 32));
             hi[i][1] = __ldg(reinterpret_cast<const uint4 *>(r1 + D + i * 32));
         }
-        float sh[4] = {0.f, 0.f, 0.f, 0.f}, sl[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t m0 = 0, m1 = 0;
-        const uint32_t abs2 = 0x7fff7fffu;
+        entry = entry_of(tile + step);
+        {   // S, of each head where there are 8 columns at most, else of the largest |q|
+            float m[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t q = s.q + (uint32_t)(ONE ? g : s.tokens << s.heads_log2) * ROW + c * 16;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            mma_bf16_16816(sh, hi[i][0].x, hi[i][1].x, hi[i][0].y, hi[i][1].y, qp[i].x, qp[i].y);
-            mma_bf16_16816(sl, lo[i][0].x, lo[i][1].x, lo[i][0].y, lo[i][1].y, qn[i].x, qn[i].y);
-            mma_bf16_16816(sh, hi[i][0].z, hi[i][1].z, hi[i][0].w, hi[i][1].w, qp[i].z, qp[i].w);
-            mma_bf16_16816(sl, lo[i][0].z, lo[i][1].z, lo[i][0].w, lo[i][1].w, qn[i].z, qn[i].w);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t &m = k ? m1 : m0;
-                m = max2(m, max2(max2(hi[i][k].x & abs2, hi[i][k].y & abs2), max2(hi[i][k].z & abs2, hi[i][k].w & abs2)));
-                m = max2(m, max2(max2(lo[i][k].x & abs2, lo[i][k].y & abs2), max2(lo[i][k].z & abs2, lo[i][k].w & abs2)));
+            for (int i = 0; i < NC; ++i) {
+                const uint4 u = load_shared(q + i * 64);
+                mma_bf16_16816(m, max2(abs2(hi[i][0].x), abs2(lo[i][0].x)), max2(abs2(hi[i][1].x), abs2(lo[i][1].x)),
+                               max2(abs2(hi[i][0].y), abs2(lo[i][0].y)), max2(abs2(hi[i][1].y), abs2(lo[i][1].y)), abs2(u.x), abs2(u.y));
+                mma_bf16_16816(m, max2(abs2(hi[i][0].z), abs2(lo[i][0].z)), max2(abs2(hi[i][1].z), abs2(lo[i][1].z)),
+                               max2(abs2(hi[i][0].w), abs2(lo[i][0].w)), max2(abs2(hi[i][1].w), abs2(lo[i][1].w)), abs2(u.z), abs2(u.w));
             }
+            // (infinities and NaN do not count: the scores are none either)
+            const bool both = ONE && 2 * c + 1 < a.group;
+            if (!ONE || 2 * c < a.group) {
+                if (tile * 16 + g < n && m[0] < INFINITY) mag = fmaxf(mag, m[0]);
+                if (tile * 16 + g + 8 < n && m[2] < INFINITY) mag = fmaxf(mag, m[2]);
+            }
+            if (both && tile * 16 + g < n && m[1] < INFINITY) mag = fmaxf(mag, m[1]);
+            if (both && tile * 16 + g + 8 < n && m[3] < INFINITY) mag = fmaxf(mag, m[3]);
         }
+        // GB groups of 8 columns at a time: 2 GB chains of products
+        auto group = [&](int grp, auto count) {
+            constexpr int GB = decltype(count)::value;
+            float sh[GB][4], sl[GB][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) { // rows g and g + 8
-            float s = col < G ? sh[2 * k] + sl[2 * k] : -INFINITY;
-            if (col + 1 < G) s = max_nan(s, sh[2 * k + 1] + sl[2 * k + 1]);
-            const uint32_t mw = k ? m1 : m0;
-            float m = fmaxf(low_bf16(mw), high_bf16(mw));
+            for (int b = 0; b < GB; ++b)
 #pragma unroll
-            for (int o = 1; o < 4; o <<= 1) {
-                s = max_nan(s, __shfl_xor_sync(kFull, s, o));
-                m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-            }
-            const int j = tile * 16 + g + 8 * k;
-            if (j < n) {
-                const uint32_t key = key_of(s);
-                range.take(key, s, m);
-                if ((lane & 3) == 0) cluster_store(keys + 4 * j, key);
-            }
-        }
+                for (int k = 0; k < 4; ++k) sh[b][k] = sl[b][k] = 0.f;
+            const uint32_t q = s.q + (uint32_t)(grp * 8 + g) * ROW + c * 16;
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+#pragma unroll
+                for (int b = 0; b < GB; ++b) {
+                    const uint4 x = load_shared(q + b * 8 * ROW + i * 64);
+                    mma_bf16_16816(sh[b], hi[i][0].x, hi[i][1].x, hi[i][0].y, hi[i][1].y, max_nan2(x.x, 0), max_nan2(x.y, 0));
+                    mma_bf16_16816(sl[b], lo[i][0].x, lo[i][1].x, lo[i][0].y, lo[i][1].y, min_nan2(x.x, 0), min_nan2(x.y, 0));
+                    mma_bf16_16816(sh[b], hi[i][0].z, hi[i][1].z, hi[i][0].w, hi[i][1].w, max_nan2(x.z, 0), max_nan2(x.w, 0));
+                    mma_bf16_16816(sl[b], lo[i][0].z, lo[i][1].z, lo[i][0].w, lo[i][1].w, min_nan2(x.z, 0), min_nan2(x.w, 0));
+                }
+            // columns 2c and 2c + 1: heads of the same token unless a token has one column
+            const int mask = (1 << s.heads_log2) - 1, h0 = (2 * c) & mask, h1 = (2 * c + 1) & mask;
+#pragma unroll
+            for (int b = 0; b < GB; ++b)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) { // rows g and g + 8
+                    const int j = tile * 16 + g + 8 * k;
+                    float x = h0 < a.group ? sh[b][2 * k] + sl[b][2 * k] : -INFINITY;
+                    const float y = h1 < a.group ? sh[b][2 * k + 1] + sl[b][2 * k + 1] : -INFINITY;
+                    const int token = ((grp + b) << per_log2) + ((2 * c) >> s.heads_log2);
+                    if (s.heads_log2 == 0) {
+                        if (j < n && token < s.tokens) cluster_store(s.keys + token * s.stride + 4 * j, __float_as_uint(x));
+                        if (j < n && token + 1 < s.tokens) cluster_store(s.keys + (token + 1) * s.stride + 4 * j, __float_as_uint(y));
+                        continue;
+                    }
+                    x = max_nan(x, y);
+                    if (s.heads_log2 > 1) x = max_nan(x, __shfl_xor_sync(kFull, x, 1));
+                    if (s.heads_log2 > 2) x = max_nan(x, __shfl_xor_sync(kFull, x, 2));
+                    if (j < n && token < s.tokens && h0 == 0) cluster_store(s.keys + token * s.stride + 4 * j, __float_as_uint(x));
+                }
+        };
+        int grp = 0;
+        if (!ONE)
+            for (; grp + 1 < groups; grp += 2) group(grp, std::integral_constant<int, 2>());
+        if (grp < groups) group(grp, std::integral_constant<int, 1>());
     }
 }
 
 // fp32: a warp scores kBatch blocks at a time, its lanes share the channels.
-template <int D>
-__device__ __forceinline__ void score_blocks(const SelectArgs &a, const float *q, const int32_t *table, int h, int j0,
-                                             int n, int first, int stride, int lane, uint32_t keys, Range &range, float &l1,
-                                             bool &bad)
+template <int D, bool ONE>
+__device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring &s, int first, int step, int lane, float &mag,
+                                             int &bad, const float *)
 {
     constexpr int E = D / 32, kBatch = 4;
-    const int G = a.group;
-    float x[kGroup][E];
-    l1 = 0.f;
-#pragma unroll
-    for (int g = 0; g < kGroup; ++g) {
-        float mine = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            x[g][i] = g < G ? q[(size_t)g * D + lane * E + i] : 0.f;
-            mine += fabsf(x[g][i]);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
-        l1 = fmaxf(l1, mine);
-    }
+    constexpr int ROW = 4 * D + kPad;
     using Vec = typename std::conditional<E == 4, float4, float2>::type;
-    const float *bounds = static_cast<const float *>(a.bounds) + (size_t)h * 2 * D + lane * E;
+    const int n = s.n;
+    const float *bounds = static_cast<const float *>(a.bounds) + (size_t)s.head * 2 * D + lane * E;
     const size_t block = (size_t)a.num_kv_heads * 2 * D;
     const int tiles = (n + kBatch - 1) / kBatch;
-    for (int tile = first; tile < tiles; tile += stride) {
+    auto row_of = [&](int r, float(&x)[E]) {
+        const uint32_t at = s.q + (uint32_t)r * ROW + lane * E * 4;
+        if constexpr (E == 4)
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(at));
+        else
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "r"(at));
+    };
+    for (int tile = first; tile < tiles; tile += step) {
         float lo[kBatch][E], hi[kBatch][E];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int j = tile * kBatch + b;
-            int e = j < n ? __ldg(table + j0 + j) : 0;
+            int e = j < n ? __ldg(s.table + j) : 0;
             if (e < 0 || e >= a.num_blocks) {
-                bad = true;
+                bad = min(bad, j);
                 e = 0;
             }
             *reinterpret_cast<Vec *>(lo[b]) = __ldg(reinterpret_cast<const Vec *>(bounds + (size_t)e * block));
             *reinterpret_cast<Vec *>(hi[b]) = __ldg(reinterpret_cast<const Vec *>(bounds + (size_t)e * block + D));
         }
+        float u[E];
+        row_of(s.tokens << s.heads_log2, u);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int j = tile * kBatch + b;
-            float s[kGroup], m = 0.f;
+            float m = 0.f;
 #pragma unroll
-            for (int g = 0; g < kGroup; ++g) s[g] = 0.f;
+            for (int i = 0; i < E; ++i) m = fmaf(u[i], fmaxf(fabsf(lo[b][i]), fabsf(hi[b][i])), m);
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                m = fmaxf(m, fmaxf(fabsf(lo[b][i]), fabsf(hi[b][i])));
+            for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(kFull, m, o);
+            if (tile * kBatch + b < n && m < INFINITY) mag = fmaxf(mag, m);
+        }
+        for (int t = 0; t < s.tokens; ++t) {
+            float best[kBatch];
 #pragma unroll
-                for (int g = 0; g < kGroup; ++g)
-                    if (g < G) s[g] = fmaf(max_nan(x[g][i], 0.f), hi[b][i], fmaf(min_nan(x[g][i], 0.f), lo[b][i], s[g]));
+            for (int b = 0; b < kBatch; ++b) best[b] = -INFINITY;
+            for (int g = 0; g < a.group; ++g) {
+                float x[E], p[kBatch];
+                row_of((t << s.heads_log2) + g, x);
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    p[b] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        p[b] = fmaf(max_nan(x[i], 0.f), hi[b][i], fmaf(min_nan(x[i], 0.f), lo[b][i], p[b]));
+                }
+                // the four sums together: lanes of a quarter end up with one of them
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float give = lane & 16 ? p[i] : p[i + 2], keep = lane & 16 ? p[i + 2] : p[i];
+                    p[i] = keep + __shfl_xor_sync(kFull, give, 16);
+                }
+                const float give = lane & 8 ? p[0] : p[1], keep = lane & 8 ? p[1] : p[0];
+                float z = keep + __shfl_xor_sync(kFull, give, 8);
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
+                best[0] = max_nan(best[0], z);
             }
-            float best = -INFINITY;
-#pragma unroll
-            for (int g = 0; g < kGroup; ++g) {
-                if (g >= G) break;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s[g] += __shfl_xor_sync(kFull, s[g], o);
-                best = max_nan(best, s[g]);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-            if (j < n) {
-                const uint32_t key = key_of(best);
-                range.take(key, best, m);
-                if (lane == 0) cluster_store(keys + 4 * j, key);
-            }
+            const int j = tile * kBatch + (lane >> 3); // the quarter's block
+            if (j < n && (lane & 7) == 0) cluster_store(s.keys + t * s.stride + 4 * j, __float_as_uint(best[0]));
         }
     }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a, int ctas)
+// Tile `unit` of those that the requests' queries make up, `tile` rows each but the last of
+// a request: rows [first, first + count) of the packed queries.  count 0: none.  With
+// cumulative lengths that are none, err, and the unit-th tile of all rows.
+struct TileRows {
+    int first, count, err;
+};
+__device__ __forceinline__ TileRows tile_rows(const SelectArgs &a, int unit, int tile, int lane)
 {
-    extern __shared__ uint32_t key[];
+    TileRows r{0, 0, __ldg(a.cu_q) != 0 ? PA_DEVERR_BAD_CU : 0};
+    int before = 0;
+    bool bad = false;
+#pragma unroll 2
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const int c0 = b < a.batch ? __ldg(a.cu_q + b) : 0, c1 = b < a.batch ? __ldg(a.cu_q + b + 1) : 0;
+        bad |= c1 < c0;
+        const int mine = c1 > c0 ? (c1 - c0 + tile - 1) / tile : 0;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kFull, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const uint32_t hit = __ballot_sync(kFull, unit >= before + incl - mine && unit < before + incl);
+        if (hit) {
+            const int from = __ffs(hit) - 1, t = c0 + (unit - (before + incl - mine)) * tile;
+            r.first = __shfl_sync(kFull, t, from);
+            r.count = __shfl_sync(kFull, min(tile, c1 - t), from);
+        }
+        before += __shfl_sync(kFull, incl, 31);
+    }
+    if (r.err || __any_sync(kFull, bad)) {
+        r.err = PA_DEVERR_BAD_CU;
+        r.first = unit * tile;
+        r.count = max(0, min(tile, a.total_q - r.first));
+    } else if (r.first + r.count > a.total_q) {
+        r.count = max(0, a.total_q - r.first);
+    }
+    return r;
+}
+
+struct Shared {
+    uint32_t mag; // S, the bits of a float >= 0
+    int bad;      // the first scored block whose table entry is none
+};
+
+// TILE = 1: one token a CTA, or a cluster of `ctas`.  Otherwise up to `tile` tokens of one
+// request a CTA.
+template <typename T, int D, int TILE>
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a, int ctas, int tile, int heads_log2)
+{
+    constexpr int W = TILE == 1 ? kWarps : 1; // warps that choose together
+    constexpr int ROW = (int)sizeof(T) * D + kPad;
+    extern __shared__ uint32_t keys[]; // [tile][max_blocks_per_seq], then the rows of q
     __shared__ Shared sh;
+    __shared__ Choice<W> choice[kWarps / W];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = ctas > 1 ? (int)cluster_rank() : 0;
+    const bool cluster = TILE == 1 && ctas > 1;
+    const int rank = cluster ? (int)cluster_rank() : 0;
     if (tid == 0) {
-        sh.least = 0xffffffffu;
-        sh.most = sh.mag = sh.bad = 0;
+        sh.mag = 0;
+        sh.bad = INT_MAX;
     }
     __syncwarp();
     grid_dep_trigger();
-    if (ctas > 1)
-        cluster_arrive();
-    else
-        __syncthreads();
+    if (cluster) cluster_arrive();
     grid_dep_wait();
 
-    const int row = blockIdx.x / ctas, t = row / a.num_kv_heads, h = row % a.num_kv_heads;
-    const QueryRow at = query_row(a, t, lane);
-    int32_t *out = a.selected + (size_t)row * a.top_k;
-    const int seen = at.pos < 0 ? 0 : at.pos / a.block_size + 1;
-    const int need = a.top_k - a.first - a.last;
-    // nothing to choose (the same for all CTAs of the row)
-    if (at.skip || seen <= a.top_k || need == 0) {
-        if (rank == 0 && !at.skip) {
-            if (at.err && tid == 0) flag_error(a.dev_err, at.err);
-            for (int i = tid; i < a.top_k; i += kThreads)
-                out[i] = seen > a.top_k ? (i < a.first ? i : seen - a.top_k + i) : i < seen ? i : -1;
-        }
-        if (ctas > 1) cluster_wait();
-        return;
-    }
-    const int32_t *table = a.block_table + (size_t)at.req * a.max_blocks_per_seq;
-    const T *q = static_cast<const T *>(a.q) + ((size_t)t * a.num_heads + (size_t)h * a.group) * D;
-    const int j0 = a.first, n = seen - a.first - a.last;
-
-    if (ctas > 1) cluster_wait(); // the first CTA's shared memory is there
-    Range range;
-    float l1 = 0.f;
-    bool bad = false;
-    score_blocks<D>(a, q, table, h, j0, n, rank * kWarps + warp, ctas * kWarps, lane, cluster_addr(key, 0), range, l1, bad);
-    range.least = __reduce_min_sync(kFull, range.least);
-    range.most = __reduce_max_sync(kFull, range.most);
-    const uint32_t mag = __reduce_max_sync(kFull, __float_as_uint(range.mag));
-    bad = __any_sync(kFull, bad);
-    if (lane == 0 && range.most != 0) { // the warp has scored a block
-        cluster_min(cluster_addr(&sh.least, 0), range.least);
-        cluster_max(cluster_addr(&sh.most, 0), range.most);
-        cluster_max(cluster_addr(&sh.mag, 0), mag);
-        if (bad) cluster_max(cluster_addr(&sh.bad, 0), 1u);
-    }
-    __syncwarp();
-    if (ctas > 1) {
-        cluster_arrive();
-        cluster_wait();
-        if (rank != 0) return;
+    const int unit = TILE == 1 ? (int)(blockIdx.x / ctas) : (int)blockIdx.x;
+    const int h = unit % a.num_kv_heads; // heads of a tile side by side
+    int t = unit / a.num_kv_heads, count = 1;
+    QueryRow at;
+    if (TILE == 1) {
+        at = query_row(a, t, lane);
     } else {
-        __syncthreads();
-    }
-    if (sh.bad) {
-        if (tid == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
-        for (int i = tid; i < a.top_k; i += kThreads) out[i] = -1;
-        return;
-    }
-
-    // ---- the choice: keys above `high` are in, `quota` of those from `low` to `high`
-    uint32_t low = kth_largest(key, n, need, sh.least, sh.most, sh), high = low;
-    const float cut = value_of(low), width = l1 * __uint_as_float(sh.mag) * 0x1p-16f;
-    const bool blurred = fabsf(cut) < INFINITY && width > 0.f && width < INFINITY;
-    if (blurred) {
-        low = key_of(cut - width);
-        high = key_of(cut + width);
-    }
-    // each warp has a run of 32 keys' multiples, so that places follow from counts
-    const int per = ((n + kThreads - 1) / kThreads) * 32, i0 = warp * per, i1 = min(n, i0 + per);
-    int sure = 0, open = 0, sure_before = 0, open_before = 0;
-    for (int pass = 0;; ++pass) {
-        int mine_sure = 0, mine_open = 0;
-        for (int i = i0 + lane; i - lane < i1; i += 32) {
-            const uint32_t k = i < i1 ? key[i] : 0;
-            mine_sure += __popc(__ballot_sync(kFull, i < i1 && k > high));
-            mine_open += __popc(__ballot_sync(kFull, i < i1 && k >= low && k <= high));
+        const TileRows r = tile_rows(a, t, tile, lane);
+        if (r.count == 0) return;
+        t = r.first;
+        count = r.count;
+        at = query_row(a, t, lane);
+        if (r.err) {
+            at.pos = -(1 << 30);
+            at.err = r.err;
+            at.skip = false;
         }
+    }
+    const int cap = a.max_blocks_per_seq, need = a.top_k - a.first - a.last;
+    const int last_seen = at.pos + count - 1 < 0 ? 0 : (at.pos + count - 1) / a.block_size + 1; // by the last token
+    const bool nothing = at.skip || last_seen <= a.top_k || need == 0; // to be scored
+    if (nothing) {
+        if (cluster) cluster_wait();
+    } else {
+        uint8_t *q_rows = reinterpret_cast<uint8_t *>(keys + (size_t)tile * cap + (-(size_t)tile * cap & 3));
+        const T *q = static_cast<const T *>(a.q) + ((size_t)t * a.num_heads + (size_t)h * a.group) * D;
+        Scoring s;
+        s.table = a.block_table + (size_t)at.req * cap + a.first;
+        s.head = h;
+        s.n = last_seen - a.first - a.last;
+        s.tokens = count;
+        s.heads_log2 = heads_log2;
+        s.q = smem_u32(q_rows);
+        s.keys = TILE == 1 ? cluster_addr(keys, 0) : smem_u32(keys);
+        s.stride = cap * 4;
+        // rows of q, 16 bytes a thread; then the largest |q| of each channel
+        constexpr int PIECES = (int)sizeof(T) * D / 16;
+        const int rows = count << heads_log2;
+        for (int i = tid; i < rows * PIECES; i += kThreads) {
+            const int r = i / PIECES, p = i % PIECES, g = r & ((1 << heads_log2) - 1), tk = r >> heads_log2;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (g < a.group) x = reinterpret_cast<const uint4 *>(q + ((size_t)tk * a.num_heads + g) * D)[p];
+            *reinterpret_cast<uint4 *>(q_rows + (size_t)r * ROW + p * 16) = x;
+        }
+        __syncthreads();
+        if (TILE > 1 || sizeof(T) == 4) {
+            if (tid < D) {
+                float u = 0.f;
+                for (int r = 0; r < rows; ++r) { // (a head with an infinity has no finite score)
+                    const float x = fabsf(to_float(reinterpret_cast<const T *>(q_rows + (size_t)r * ROW)[tid]));
+                    if (x < INFINITY) u = fmaxf(u, x);
+                }
+                T *env = reinterpret_cast<T *>(q_rows + (size_t)rows * ROW);
+                if constexpr (sizeof(T) == 2)
+                    env[tid] = __float2bfloat16_rn(u);
+                else
+                    env[tid] = u;
+            }
+            __syncthreads();
+        }
+        if (cluster) cluster_wait(); // the first CTA's shared memory is there
+        float mag = 0.f;
+        int bad = INT_MAX;
+        score_blocks<D, TILE == 1>(a, s, rank * kWarps + warp, ctas * kWarps, lane, mag, bad, q);
+        const uint32_t most = __reduce_max_sync(kFull, __float_as_uint(mag));
+        bad = __reduce_min_sync(kFull, bad);
         if (lane == 0) {
-            sh.count[warp][0] = mine_sure;
-            sh.count[warp][1] = mine_open;
+            cluster_max(cluster_addr(&sh.mag, 0), most);
+            if (bad != INT_MAX) cluster_min(cluster_addr(&sh.bad, 0), (uint32_t)bad);
         }
-        __syncthreads();
-        sure = open = sure_before = open_before = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == warp) {
-                sure_before = sure;
-                open_before = open;
-            }
-            sure += sh.count[w][0];
-            open += sh.count[w][1];
+        __syncwarp();
+        if (cluster) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            __syncthreads();
         }
-        if (pass > 0 || !blurred || sure + open == need) break;
-        // more blocks than places within the error of the scores: again in 64 bits,
-        // as the difference from the cut (a float holds it to 2^-40 of the scores)
-        for (int i = i0 + lane; i - lane < i1; i += 32) {
-            const uint32_t k = i < i1 ? key[i] : 0;
-            uint32_t todo = __ballot_sync(kFull, i < i1 && k >= low && k <= high);
-            uint32_t now = k > high ? 0xffffffffu : 0u;
-            while (todo) {
-                const int b = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const int e = __ldg(table + j0 + (i - lane) + b);
-                const T *bounds = static_cast<const T *>(a.bounds) + ((size_t)e * a.num_kv_heads + h) * 2 * D;
-                const uint32_t k64 = key_of((float)(exact_score<T, D>(q, bounds, a.group, lane) - (double)cut));
-                if (lane == b) now = k64;
-            }
-            if (i < i1) key[i] = now;
-        }
-        __syncthreads();
-        low = high = kth_largest(key, n, need - sure, 1u, 0xfffffffeu, sh);
-        __syncthreads();
     }
-    const int quota = need - sure;
-    int place = a.first + sure_before + min(open_before, quota), ties = open_before;
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
-        const uint32_t k = i < i1 ? key[i] : 0;
-        const uint32_t eq = __ballot_sync(kFull, i < i1 && k >= low && k <= high);
-        const uint32_t below = (1u << lane) - 1;
-        const bool in = i < i1 && (k > high || (((eq >> lane) & 1) && ties + __popc(eq & below) < quota));
-        const uint32_t chosen = __ballot_sync(kFull, in);
-        if (in) out[place + __popc(chosen & below)] = j0 + i;
-        place += __popc(chosen);
-        ties += __popc(eq);
+    if (rank != 0 || at.skip) return;
+    const int bad_block = nothing ? INT_MAX : sh.bad;
+    if (tid == 0 && (at.err || bad_block != INT_MAX)) flag_error(a.dev_err, at.err ? at.err : PA_DEVERR_BAD_BLOCK);
+    // the tokens' outputs, by W warps each
+    for (int i = warp / W; i < count; i += kWarps / W) {
+        const int seen = at.pos + i < 0 ? 0 : (at.pos + i) / a.block_size + 1;
+        int32_t *out = a.selected + ((size_t)(t + i) * a.num_kv_heads + h) * a.top_k;
+        const int wt = W == 1 ? lane : tid;
+        if (seen <= a.top_k) {
+            for (int k = wt; k < a.top_k; k += 32 * W) out[k] = k < seen ? k : -1;
+            continue;
+        }
+        const int n = seen - a.first - a.last;
+        const bool failed = bad_block < n; // (not for entries that only later tokens need)
+        for (int k = wt; k < a.first + a.last; k += 32 * W) {
+            const int to = k < a.first ? k : k + need;
+            out[to] = failed ? -1 : k < a.first ? k : seen - a.top_k + to;
+        }
+        if (failed)
+            for (int k = wt; k < need; k += 32 * W) out[a.first + k] = -1;
+        if (failed || need == 0) continue;
+        Row<T> r;
+        r.q = static_cast<const T *>(a.q) + ((size_t)(t + i) * a.num_heads + (size_t)h * a.group) * D;
+        r.bounds = static_cast<const T *>(a.bounds) + (size_t)h * 2 * D;
+        r.table = a.block_table + (size_t)at.req * cap + a.first;
+        r.n = n;
+        r.first = a.first;
+        r.need = need;
+        // 2 E, and the rounding of S
+        r.width = (sizeof(T) == 2 ? (D / 16 + 2) * 0x1.02p-21f : (D / 16 + 6) * 0x1.02p-23f) * __uint_as_float(sh.mag);
+        choose<T, D, W>(keys + (size_t)i * cap, r, out + a.first, a, choice[W == 1 ? warp : 0], wt);
     }
-    for (int i = tid; i < a.first; i += kThreads) out[i] = i;
-    for (int i = tid; i < a.last; i += kThreads) out[a.top_k - a.last + i] = seen - a.last + i;
 }
 
-template <typename T, int D>
-int launch(const SelectArgs &a, cudaStream_t s)
+template <typename T, int D, int TILE>
+int launch(const SelectArgs &a, int ctas, int tile, int heads_log2, size_t smem, cudaStream_t s)
 {
-    const size_t smem = (size_t)a.max_blocks_per_seq * 4;
     static int raised[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_DEVICE;
     if (!__atomic_load_n(&raised[dev], __ATOMIC_ACQUIRE)) {
-        cudaError_t e = cudaFuncSetAttribute(select_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSelectMaxBlocks * 4);
+        cudaError_t e = cudaFuncSetAttribute(select_kernel<T, D, TILE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSelectMaxBlocks * 4 + 16 + (kGroup + 1) * ((int)sizeof(T) * D + kPad));
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(select_kernel<T, D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            e = cudaFuncSetAttribute(select_kernel<T, D, TILE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return launch_status(e);
         __atomic_store_n(&raised[dev], 1, __ATOMIC_RELEASE);
     }
-    const long long rows = (long long)a.total_q * a.num_kv_heads;
-    // few rows: as many CTAs a row as fit the GPU beside one another
-    int ctas = 1;
-    while (ctas < 16 && rows * ctas * 2 <= 2 * num_sms() && a.max_blocks_per_seq > 16 * kWarps * ctas) ctas *= 2;
+    // tiles do not pass the end of a request: one more for each
+    const long long tiles = TILE == 1 ? a.total_q : a.total_q / tile + (long long)a.batch;
+    if (tiles * a.num_kv_heads * ctas >= 1ll << 31) return PA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(rows * ctas));
+    cfg.gridDim = dim3((unsigned)(tiles * a.num_kv_heads * ctas));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -529,15 +794,36 @@ int launch(const SelectArgs &a, cudaStream_t s)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, select_kernel<T, D>, a, ctas));
+    return launch_status(cudaLaunchKernelEx(&cfg, select_kernel<T, D, TILE>, a, ctas, tile, heads_log2));
+}
+
+template <typename T, int D>
+int launch_tile(const SelectArgs &a, cudaStream_t s)
+{
+    const long long rows = (long long)a.total_q * a.num_kv_heads;
+    const int heads_log2 = a.group > 4 ? 3 : a.group > 2 ? 2 : a.group > 1 ? 1 : 0;
+    const size_t row = sizeof(T) * D + kPad;
+    auto smem_of = [&](int tile) { return (size_t)tile * a.max_blocks_per_seq * 4 + 16 + ((size_t)(((tile << heads_log2) + 7) & ~7) + 1) * row; };
+    // Chunks: the tile with the most tokens that leaves every SM two CTAs, fits two of
+    // them, and holds no more tokens than requests have on average.
+    int tile = 1;
+    if (a.cu_q != nullptr)
+        while (tile < kTile && (a.total_q + 2 * tile - 1) / (2 * tile) * (long long)a.num_kv_heads >= num_sms() &&
+               smem_of(2 * tile) <= 100 * 1024 && a.total_q >= 2ll * tile * a.batch)
+            tile *= 2;
+    if (tile > 1) return launch<T, D, kTile>(a, 1, tile, heads_log2, smem_of(tile), s);
+    // Few rows: as many CTAs a row as fit the GPU beside one another.
+    int ctas = 1;
+    while (ctas < 16 && rows * ctas * 2 <= 2 * num_sms() && a.max_blocks_per_seq > 16 * kWarps * ctas) ctas *= 2;
+    return launch<T, D, 1>(a, ctas, 1, heads_log2, smem_of(1), s);
 }
 
 }  // namespace
 
 int select_launch(const SelectArgs &a, int head_dim, bool f32, cudaStream_t s)
 {
-    if (f32) return head_dim == 64 ? launch<float, 64>(a, s) : launch<float, 128>(a, s);
-    return head_dim == 64 ? launch<__nv_bfloat16, 64>(a, s) : launch<__nv_bfloat16, 128>(a, s);
+    if (f32) return head_dim == 64 ? launch_tile<float, 64>(a, s) : launch_tile<float, 128>(a, s);
+    return head_dim == 64 ? launch_tile<__nv_bfloat16, 64>(a, s) : launch_tile<__nv_bfloat16, 128>(a, s);
 }
 
 }  // namespace pa

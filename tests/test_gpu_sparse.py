@@ -89,6 +89,46 @@ def test_select_for_chunks(dtype, d, bs, hq, hkv, top):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,bs,hq,hkv,first,last", [(64, 16, 32, 8, 1, 1), (128, 16, 24, 24, 0, 2), (64, 32, 36, 18, 2, 0), (128, 16, 48, 16, 1, 1),
+                                                    (64, 16, 40, 8, 1, 1), (128, 32, 64, 8, 0, 0)])
+@pytest.mark.parametrize("tokens", [800, 210])
+def test_select_for_tiles_of_tokens(dtype, d, bs, hq, hkv, first, last, tokens):
+    """Enough tokens a request for CTAs that take up to 16 of them: requests that end
+    inside a tile, single tokens between, queries before the first key, rows whose blocks
+    all fit, one request with a bad entry, rows behind the last request; heads in every
+    packing of eight columns."""
+    top = 9
+    part = tokens // 5
+    new = [part + 3, 0, 1, 2 * part, 17, part - 21, 16]
+    lens = [60 * bs + 5, 40, 33 * bs, 2 * part - 5, 21 * bs - 1, 25 * bs + part, 50 * bs]
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    blocks = [-(-n // bs) for n in lens]
+    nb = sum(blocks)
+    table = _table(np.random.default_rng(1), blocks, max(blocks) + 1, nb)
+    bounds = _bounds(5, nb, hkv, d, dtype)
+    q = torch.randn(int(cu[-1]) + 5, hq, d, generator=torch.Generator().manual_seed(8)).to(dtype)
+    want = _want(q, bounds, table, i32(lens), top, bs, first, last, torch.from_numpy(cu))
+    broken = table.clone()
+    broken[6, 20] = nb + 7
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = _select(q, bounds, broken, i32(lens), top, bs, first, last, torch.from_numpy(cu), err)
+    assert err.item() == pa.DEVERR_BAD_BLOCK
+    assert np.array_equal(got[:cu[6]], want[:cu[6]])
+    assert (got[cu[6]:cu[7]] == -1).all() and (got[cu[7]:] == -9).all()
+    # an entry that only a request's later tokens need fails theirs alone
+    broken = table.clone()
+    broken[5, 30] = -1
+    got = _select(q, bounds, broken, i32(lens), top, bs, first, last, torch.from_numpy(cu), err)
+    rows = np.array([r == 5 and p // bs - last >= 30 for r, p in ref.query_positions(lens, cu)])
+    assert (bs == 32 or part < 60 or rows.any()) and not rows.all()
+    assert (got[:cu[7]][rows] == -1).all() and np.array_equal(got[:cu[7]][~rows], want[:cu[7]][~rows])
+    for bad in ([1] + cu[1:].tolist(), cu[:3].tolist() + [cu[-1] + 3] + cu[4:].tolist()):
+        err.zero_()
+        got = _select(q, bounds, table, i32(lens), top, bs, first, last, i32(bad), err)
+        assert err.item() == pa.DEVERR_BAD_CU
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_select_among_equal_and_nearly_equal_scores(dtype):
     """Blocks whose scores are equal (ties: the lowest block) or differ by less than the
     rounding of an fp32 sum; the exact scores decide."""
