@@ -501,7 +501,8 @@ int pa_cache_append_rotary(const void *q, const void *k, const void *v, const in
  * overflows is an infinity).  Bounds of the last block are used only where last_blocks is
  * 0: a chunk's later tokens are in them.
  * dtype is that of q and bounds.  first_blocks + last_blocks <= top_k;
- * max_blocks_per_seq <= 49152; num_heads / num_kv_heads <= 8; head_dim 64 or 128.
+ * max_blocks_per_seq <= 49152; top_k at most 2^20; num_heads / num_kv_heads <= 8; head_dim 64 or 128;
+ * total_q * num_kv_heads < 2^27.
  * A needed block_table entry that is no block sets PA_DEVERR_BAD_BLOCK, a length beyond
  * the table PA_DEVERR_OVERFLOW, cu_seq_lens_q that does not start at 0 or decreases behind
  * a row's request PA_DEVERR_BAD_CU: the rows are -1.
@@ -521,7 +522,8 @@ int pa_select_blocks(const void *q, const void *bounds, const int32_t *block_tab
  * it reaches infinite or NaN.  selected, queries and lengths as above; the caches as pa_decode,
  * whose tokens are all written already (nothing is appended).
  * dtype PA_BF16 or PA_F32; num_heads / num_kv_heads <= 8; head_dim 64 or 128; PA_BF16: block_size
- * a multiple of 16.  A needed block_table entry that is no block sets PA_DEVERR_BAD_BLOCK, a length
+ * a multiple of 16; top_k at most 2^20, top_k * block_size < 2^30,
+ * total_q * num_kv_heads < 2^27.  A needed block_table entry that is no block sets PA_DEVERR_BAD_BLOCK, a length
  * beyond the table PA_DEVERR_OVERFLOW, a bad cu_seq_lens_q PA_DEVERR_BAD_CU: the rows are
  * zeros.  Needs no workspace; calls share nothing.
  */

@@ -196,6 +196,7 @@ int pa_sparse(const void *q, const void *k_cache, const void *v_cache, const int
                               max_blocks_per_seq, top_k, dtype);
     if (rc != PA_OK) return rc;
     if (dtype == PA_BF16 && block_size % kSparseUnit != 0) return PA_ERR_UNSUPPORTED;
+    if ((long long)top_k * block_size >= 1ll << 30) return PA_ERR_UNSUPPORTED; // tokens of a list in 32 bits
     if (batch == 0 || total_q == 0) return PA_OK;
     if (!q || !k_cache || !v_cache || !block_table || !seqlens_k || !selected || !out) return PA_ERR_NULL;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(block_table, 4) ||

@@ -87,6 +87,12 @@ __device__ __forceinline__ float cluster_load(uint32_t addr)
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
     return x;
 }
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr)
+{
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr) : "memory");
+    return x;
+}
 __device__ __forceinline__ void cluster_min(uint32_t addr, uint32_t x)
 {
     asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");

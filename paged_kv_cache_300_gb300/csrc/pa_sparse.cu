@@ -34,49 +34,80 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kGroup = 8; // most query heads of a kv head
-constexpr int kList = 64; // list entries that a warp looks up at a time
+constexpr int kList = 64; // units that a warp looks up at a time
+// How far a score may pass the reference of its row's weights (log2): weights up to 2^8,
+// as exact as those up to 1.
+constexpr float kSlack = 8.f;
+constexpr int kUnitF32 = 8; // tokens of a unit of the fp32 kernel
 
 // One row's partial results in shared memory: [kGroup][D] accumulators, [kGroup]
 // maxima (log2 domain), [kGroup] sums; a negative sum marks a row that failed.
 template <int D>
-struct Part {
+struct alignas(16) Part {
     float acc[kGroup][D];
     float m[kGroup], l[kGroup];
 };
 
-// Join of `count` partials for head g, channel d: the weights, the sum, the value.
+// Join of partials for four channels of a head.
 struct Joined {
-    float acc = 0.f, m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, l = 0.f;
     bool bad = false;
-    __device__ __forceinline__ void add(float x, float xm, float xl)
+    __device__ __forceinline__ void add(const float4 &x, float xm, float xl)
     {
         bad |= xl < 0.f;
         const float mn = fmaxf(m, xm), mu = mn == -INFINITY ? 0.f : mn;
         const float wa = exp2_approx(m - mu), wb = exp2_approx(xm - mu);
-        acc = acc * wa + x * wb;
+        acc.x = acc.x * wa + x.x * wb;
+        acc.y = acc.y * wa + x.y * wb;
+        acc.z = acc.z * wa + x.z * wb;
+        acc.w = acc.w * wa + x.w * wb;
         l = l * wa + xl * wb;
         m = mn;
     }
+    __device__ __forceinline__ float4 value() const
+    {
+        if (bad || l == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);
+        const float i = 1.f / l;
+        return make_float4(acc.x * i, acc.y * i, acc.z * i, acc.w * i);
+    }
 };
 
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void put(float *p, float x) { *p = x; }
-
-// Joins the CTA's kWarps partials, then the cluster's, and writes the row.
-template <typename T, int D>
-__device__ __forceinline__ void finish_row(Part<D> *parts, Part<D> *cta, T *out, int G, int ctas, int rank)
+__device__ __forceinline__ void put(__nv_bfloat16 *p, const float4 &x)
 {
-    const int tid = threadIdx.x;
-    __syncthreads();
-    for (int e = tid; e < G * D; e += kThreads) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+}
+__device__ __forceinline__ void put(float *p, const float4 &x) { *reinterpret_cast<float4 *>(p) = x; }
+
+// Threads of a row's W warps: all of the CTA's, or a group of them.
+template <int W>
+__device__ __forceinline__ void row_sync(int group)
+{
+    if constexpr (W == kWarps)
+        __syncthreads();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * W) : "memory");
+}
+
+// Joins the partials of the row's W warps, `step` bytes apart, then the cluster's, and writes
+// the row.  `tid` counts the row's threads.
+template <typename T, int D, int W>
+__device__ __forceinline__ void finish_row(const void *parts, int step, Part<D> *cta, T *out, int G, int ctas, int rank, int tid,
+                                           int group)
+{
+    row_sync<W>(group);
+    for (int e = tid * 4; e < G * D; e += W * 128) {
         const int g = e / D, d = e % D;
         Joined j;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) j.add(parts[w].acc[g][d], parts[w].m[g], parts[w].l[g]);
+        for (int w = 0; w < W; ++w) {
+            const Part<D> *p = reinterpret_cast<const Part<D> *>(static_cast<const uint8_t *>(parts) + w * step);
+            j.add(*reinterpret_cast<const float4 *>(&p->acc[g][d]), p->m[g], p->l[g]);
+        }
         if (ctas == 1) {
-            put(out + e, j.bad || j.l == 0.f ? 0.f : j.acc / j.l);
+            put(out + e, j.value());
         } else {
-            cta->acc[g][d] = j.acc;
+            *reinterpret_cast<float4 *>(&cta->acc[g][d]) = j.acc;
             if (d == 0) {
                 cta->m[g] = j.m;
                 cta->l[g] = j.bad ? -1.f : j.l;
@@ -87,13 +118,24 @@ __device__ __forceinline__ void finish_row(Part<D> *parts, Part<D> *cta, T *out,
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-    for (int e = rank * kThreads + tid; e < G * D; e += ctas * kThreads) {
+    for (int e = (rank * kThreads + tid) * 4; e < G * D; e += ctas * kThreads * 4) {
         const int g = e / D, d = e % D;
         Joined j;
-        for (int c = 0; c < ctas; ++c)
-            j.add(cluster_load(cluster_addr(&cta->acc[g][d], c)), cluster_load(cluster_addr(&cta->m[g], c)),
-                  cluster_load(cluster_addr(&cta->l[g], c)));
-        put(out + e, j.bad || j.l == 0.f ? 0.f : j.acc / j.l);
+        for (int c0 = 0; c0 < ctas; c0 += 4) { // the loads of four CTAs in flight
+            float4 x[4];
+            float m[4], l[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int from = min(c0 + c, ctas - 1);
+                x[c] = cluster_load4(cluster_addr(&cta->acc[g][d], from));
+                m[c] = cluster_load(cluster_addr(&cta->m[g], from));
+                l[c] = cluster_load(cluster_addr(&cta->l[g], from));
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c0 + c < ctas) j.add(x[c], m[c], l[c]);
+        }
+        put(out + e, j.value());
     }
     __syncwarp();
     cluster_arrive(); // the others' shared memory stays until all have read it
@@ -101,30 +143,45 @@ __device__ __forceinline__ void finish_row(Part<D> *parts, Part<D> *cta, T *out,
 }
 
 // A row that sees nothing, or was refused: zeros.  The same for all CTAs of the row.
-template <typename T>
-__device__ __forceinline__ void zero_row(T *out, int elements, int rank)
+template <typename T, int W>
+__device__ __forceinline__ void zero_row(T *out, int elements, int rank, int tid)
 {
     if (rank != 0) return;
-    for (int e = threadIdx.x; e < elements; e += kThreads) put(out + e, 0.f);
+    for (int e = tid * 4; e < elements; e += W * 128) put(out + e, make_float4(0.f, 0.f, 0.f, 0.f));
 }
 
-// The warp's next kList list entries from `e0`, one in `stride`: those that are visible,
-// as (first row in the pool, logical block), in list order; their count.
-__device__ __forceinline__ int look_up(const SparseArgs &a, const int32_t *list, const int32_t *table, int e0, int stride,
-                                       int last_block, int lane, int2 *items, bool &bad)
+// Units of UNIT tokens that a row's list makes up, `per_block` of them an entry.  The warp's
+// next kList of them from `u0`, one in `stride`: those with a visible position, as (first row
+// in the pool, first position); their count.
+template <int UNIT>
+__device__ __forceinline__ int look_up(const SparseArgs &a, const int32_t *list, const int32_t *table, int u0, int stride,
+                                       int units, int per_block, int pos, int lane, int2 *items, bool &bad)
 {
     int count = 0;
+    const int last_block = pos / a.block_size;
+    int2 found[kList / 32];
+    bool use[kList / 32];
 #pragma unroll
     for (int k = 0; k < kList / 32; ++k) {
-        const long long e = e0 + (long long)(k * 32 + lane) * stride;
-        int lb = -1, phys = 0;
-        if (e < a.top_k) lb = __ldg(list + e);
-        const bool use = lb >= 0 && lb <= last_block;
-        if (use) phys = __ldg(table + lb);
-        const bool wrong = use && (phys < 0 || phys >= a.num_blocks);
+        const long long u = u0 + (long long)(k * 32 + lane) * stride;
+        const int e = u < units ? (int)u / per_block : 0, part = u < units ? (int)u - e * per_block : 0;
+        const int lb = u < units ? __ldg(list + e) : -1;
+        found[k] = make_int2(part * UNIT, lb);
+    }
+#pragma unroll
+    for (int k = 0; k < kList / 32; ++k) {
+        const int lb = found[k].y, part = found[k].x;
+        use[k] = lb >= 0 && lb <= last_block && (long long)lb * a.block_size + part <= pos;
+        const int phys = use[k] ? __ldg(table + lb) : 0;
+        const bool wrong = use[k] && (phys < 0 || phys >= a.num_blocks);
         bad |= wrong;
-        const uint32_t m = __ballot_sync(kFull, use && !wrong);
-        if (use && !wrong) items[count + __popc(m & ((1u << lane) - 1))] = make_int2(phys * a.block_size, lb);
+        use[k] &= !wrong;
+        found[k] = make_int2(phys * a.block_size + part, lb * a.block_size + part);
+    }
+#pragma unroll
+    for (int k = 0; k < kList / 32; ++k) {
+        const uint32_t m = __ballot_sync(kFull, use[k]);
+        if (use[k]) items[count + __popc(m & ((1u << lane) - 1))] = found[k];
         count += __popc(m);
     }
     __syncwarp();
@@ -143,13 +200,14 @@ struct Ring {
     static constexpr int SLAB = kSparseUnit * 128;  // 16 rows x 64 dims
     static constexpr int HALF = KB * SLAB;          // K (or V) of a unit
     static constexpr int UNIT = 2 * HALF;
-    static constexpr int STAGES = D == 128 ? 3 : 6; // 24 KB a warp, 96 KB a CTA, two CTAs an SM
+    static constexpr int STAGES = D == 128 ? 2 : 4; // 16 KB a warp, 64 KB a CTA, three CTAs an SM
     static constexpr int BYTES = kWarps * STAGES * UNIT;
     static_assert(sizeof(Part<D>) <= STAGES * UNIT, "a warp's partial takes the place of its ring");
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+// W warps a row: kWarps / W rows a CTA, or a cluster of `ctas` for one row (W = kWarps).
+template <int D, int W>
+__global__ void __launch_bounds__(kThreads, 3)
     sparse_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const SparseArgs a,
                        int ctas)
 {
@@ -174,14 +232,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     grid_dep_trigger();
     grid_dep_wait();
 
-    const int row = blockIdx.x / ctas, t = row / a.num_kv_heads, h = row % a.num_kv_heads, G = a.group;
+    const int group = warp / W, tr = tid % (32 * W);
+    const int row = W == kWarps ? (int)(blockIdx.x / ctas) : (int)blockIdx.x * (kWarps / W) + group;
+    const int t = row / a.num_kv_heads, h = row % a.num_kv_heads, G = a.group;
+    if (W < kWarps && t >= a.total_q) return;
     const QueryRow at = query_row(a, t, lane);
     if (at.skip) return;
     const size_t off = ((size_t)t * a.num_heads + (size_t)h * G) * D;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + off;
     if (at.pos < 0) {
-        if (at.err && rank == 0 && tid == 0) flag_error(a.dev_err, at.err);
-        zero_row(out, G * D, rank);
+        if (at.err && rank == 0 && tr == 0) flag_error(a.dev_err, at.err);
+        zero_row<__nv_bfloat16, W>(out, G * D, rank, tr);
         return;
     }
     const int32_t *list = a.selected + (size_t)row * a.top_k;
@@ -207,17 +268,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int mi = lane >> 3, mr = lane & 7;
     const int k_toff = (mi & 1) * 8 + mr, k_doff = (mi >> 1) * 8; // ldmatrix A = K
     const int v_toff = (mi >> 1) * 8 + mr, v_doff = (mi & 1) * 8; // ldmatrix.trans A = V^T
-    const int upb = a.block_size / kSparseUnit;                   // units a block
-    const int stride = ctas * kWarps;
+    const int upb = a.block_size / kSparseUnit, all = a.top_k * upb; // units a block, and of the list
+    const int stride = ctas * W;
     int2 *items = lists[warp];
     int stage = 0;
     uint32_t phase = 0;
 
     bool stuck = false; // a wait gave up: the row fails
-    for (int e0 = rank * kWarps + warp; e0 < a.top_k && !stuck; e0 += kList * stride) {
-        const int units = look_up(a, list, table, e0, stride, at.pos / a.block_size, lane, items, bad) * upb;
-        auto request = [&](int u, int s) { // lane 0
-            const int r0 = items[u / upb].x + (u % upb) * kSparseUnit;
+    for (int u0 = rank * W + warp % W; u0 < all && !stuck; u0 += kList * stride) {
+        const int units = look_up<kSparseUnit>(a, list, table, u0, stride, all, upb, at.pos, lane, items, bad);
+        const int2 item0 = items[lane], item1 = items[lane + 32]; // (from `units` on: leftovers)
+        auto request = [&](int r0, int s) { // lane 0
             const uint32_t dst = smem_u32(ring + s * R::UNIT);
             mbar_arrive_expect_tx(&bar[s], R::UNIT);
             tma_load_3d(dst, &tm_k, &bar[s], 0, r0, h * R::KB);
@@ -225,24 +286,25 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         if (lane == 0)
             for (int u = 0, s = stage; u < min(units, R::STAGES); ++u) {
-                request(u, s);
+                request(items[u].x, s);
                 s = s + 1 == R::STAGES ? 0 : s + 1;
             }
         __syncwarp();
         for (int u = 0; u < units; ++u) {
-            if (!mbar_wait(&bar[stage], phase)) {
-                if (lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
+            // the unit's first position, the next request's row
+            const int pos0 = __shfl_sync(kFull, u < 32 ? item0.y : item1.y, u & 31);
+            const int ahead = u + R::STAGES, r0 = __shfl_sync(kFull, ahead < 32 ? item0.x : item1.x, ahead & 31);
+            if (!__all_sync(kFull, mbar_wait(&bar[stage], phase))) {
                 stuck = true;
                 break;
             }
-            const int pos0 = items[u / upb].y * a.block_size + (u % upb) * kSparseUnit; // of the unit's first token
             uint8_t *kst = ring + stage * R::UNIT, *vst = kst + R::HALF;
-            const int live = min(at.pos - pos0 + 1, kSparseUnit); // tokens that the query sees
+            const int live = min(at.pos - pos0 + 1, kSparseUnit); // tokens that the query sees, from 1
             if (live < kSparseUnit) {
-                const int r0 = max(live, 0), chunks = (kSparseUnit - r0) * 8;
+                const int chunks = (kSparseUnit - live) * 8;
                 for (int ci = lane; ci < chunks * R::KB; ci += 32) {
                     const int slab = ci / chunks, rem = ci % chunks;
-                    *reinterpret_cast<uint4 *>(vst + slab * R::SLAB + (r0 + rem / 8) * 128 + (rem % 8) * 16) =
+                    *reinterpret_cast<uint4 *>(vst + slab * R::SLAB + (live + rem / 8) * 128 + (rem % 8) * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
@@ -258,40 +320,45 @@ __global__ void __launch_bounds__(kThreads, 2)
                 ldsm_x4(kbase + (d >> 6) * R::SLAB + sw128_offset(k_toff, d & 63), r0, r1, r2, r3);
                 mma_bf16_16816(ks & 1 ? s2 : s, r0, r1, r2, r3, qf[ks][0], qf[ks][1]);
             }
-            // ---- mask, scale (log2 domain), online softmax
-            float t0 = -INFINITY, t1 = -INFINITY;
+            // ---- scale (log2 domain), mask
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool vis = trow + ((i >> 1) << 3) < live;
-                s[i] = vis ? (s[i] + s2[i]) * a.scale_log2 : -INFINITY;
-                if (i & 1)
-                    t1 = fmaxf(t1, s[i]);
-                else
-                    t0 = fmaxf(t0, s[i]);
-            }
+            for (int i = 0; i < 4; ++i) s[i] = (s[i] + s2[i]) * a.scale_log2;
+            if (live < kSparseUnit) {
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                t0 = fmaxf(t0, __shfl_xor_sync(kFull, t0, o));
-                t1 = fmaxf(t1, __shfl_xor_sync(kFull, t1, o));
+                for (int i = 0; i < 4; ++i)
+                    if (trow + ((i >> 1) << 3) >= live) s[i] = -INFINITY;
             }
-            const float mn0 = fmaxf(m0, t0), mn1 = fmaxf(m1, t1);
-            const float mu0 = mn0 == -INFINITY ? 0.f : mn0, mu1 = mn1 == -INFINITY ? 0.f : mn1;
-            const float al0 = exp2_approx(m0 - mu0), al1 = exp2_approx(m1 - mu1);
-            m0 = mn0;
-            m1 = mn1;
+            // ---- the reference of the weights follows the maximum when that has grown by
+            // more than 2^kSlack: no maximum over the lanes and no rescaling for most units
+            const bool grown = fmaxf(s[0], s[2]) > m0 + kSlack || fmaxf(s[1], s[3]) > m1 + kSlack;
+            if (__any_sync(kFull, grown)) {
+                float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    t0 = fmaxf(t0, __shfl_xor_sync(kFull, t0, o));
+                    t1 = fmaxf(t1, __shfl_xor_sync(kFull, t1, o));
+                }
+                t0 = fmaxf(m0, t0), t1 = fmaxf(m1, t1);
+                const float al0 = t0 == -INFINITY ? 1.f : exp2_approx(m0 - t0), al1 = t1 == -INFINITY ? 1.f : exp2_approx(m1 - t1);
+                m0 = t0;
+                m1 = t1;
+                l0 *= al0;
+                l1 *= al1;
+#pragma unroll
+                for (int dm = 0; dm < KS; ++dm) {
+                    acc[dm][0] *= al0;
+                    acc[dm][1] *= al1;
+                    acc[dm][2] *= al0;
+                    acc[dm][3] *= al1;
+                }
+            }
+            const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
             s[0] = exp2_approx(s[0] - mu0);
             s[1] = exp2_approx(s[1] - mu1);
             s[2] = exp2_approx(s[2] - mu0);
             s[3] = exp2_approx(s[3] - mu1);
-            l0 = l0 * al0 + (s[0] + s[2]);
-            l1 = l1 * al1 + (s[1] + s[3]);
-#pragma unroll
-            for (int dm = 0; dm < KS; ++dm) {
-                acc[dm][0] *= al0;
-                acc[dm][1] *= al1;
-                acc[dm][2] *= al0;
-                acc[dm][3] *= al1;
-            }
+            l0 += s[0] + s[2];
+            l1 += s[1] + s[3];
             // ---- O^T[channel, head] += V^T P^T, a weight as the sum of two bf16 numbers
             const uint32_t w0 = pack_bf16(s[0], s[1]), w1 = pack_bf16(s[2], s[3]);
             const uint32_t b0 = movmatrix_trans(w0), b1 = movmatrix_trans(w1);
@@ -305,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mma_bf16_16816(acc[dm], r0, r1, r2, r3, c0, c1);
             }
             __syncwarp(); // every lane has read the slot
-            if (lane == 0 && u + R::STAGES < units) request(u + R::STAGES, stage);
+            if (lane == 0 && ahead < units) request(r0, stage);
             if (++stage == R::STAGES) {
                 stage = 0;
                 phase ^= 1;
@@ -320,9 +387,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     bad = __any_sync(kFull, bad);
     if (bad && lane == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
+    if (stuck && lane == 0) flag_error(a.dev_err, PA_DEVERR_TIMEOUT);
     bad |= stuck;
-    Part<D> *part = reinterpret_cast<Part<D> *>(smem) + warp;
-    __syncthreads(); // partials lie closer than rings: all rings have been read
+    Part<D> *part = reinterpret_cast<Part<D> *>(ring);
     const int g0 = 2 * (lane & 3);
 #pragma unroll
     for (int dm = 0; dm < KS; ++dm)
@@ -335,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         part->l[g0] = bad ? -1.f : l0;
         part->l[g0 + 1] = bad ? -1.f : l1;
     }
-    finish_row<__nv_bfloat16, D>(reinterpret_cast<Part<D> *>(smem), &cta_part, out, G, ctas, rank);
+    finish_row<__nv_bfloat16, D, W>(smem + group * W * R::STAGES * R::UNIT, R::STAGES * R::UNIT, &cta_part, out, G, ctas, rank, tr,
+                                    group);
 }
 
 // ------------------------------------------------------------------ fp32
@@ -379,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
     float *out = static_cast<float *>(a.out) + off;
     if (at.pos < 0) {
         if (at.err && rank == 0 && tid == 0) flag_error(a.dev_err, at.err);
-        zero_row(out, G * D, rank);
+        zero_row<float, kWarps>(out, G * D, rank, tid);
         return;
     }
     const int32_t *list = a.selected + (size_t)row * a.top_k;
@@ -399,13 +467,14 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
     const float *kc = static_cast<const float *>(a.k_cache) + (size_t)h * D + lane * E;
     const float *vc = static_cast<const float *>(a.v_cache) + (size_t)h * D + lane * E;
     const size_t rowlen = (size_t)a.num_kv_heads * D;
-    const int stride = ctas * kWarps, bs = a.block_size;
+    const int upb = (a.block_size + kUnitF32 - 1) / kUnitF32, all = a.top_k * upb, stride = ctas * kWarps;
     int2 *items = lists[warp];
-    for (int e0 = rank * kWarps + warp; e0 < a.top_k; e0 += kList * stride) {
-        const int count = look_up(a, list, table, e0, stride, at.pos / bs, lane, items, bad);
+    for (int u0 = rank * kWarps + warp; u0 < all; u0 += kList * stride) {
+        const int count = look_up<kUnitF32>(a, list, table, u0, stride, all, upb, at.pos, lane, items, bad);
         for (int it = 0; it < count; ++it) {
             const int2 item = items[it];
-            const int live = min(at.pos - item.y * bs + 1, bs); // >= 1
+            // up to the query, the end of the unit and of the block
+            const int live = min(min(at.pos - item.y + 1, kUnitF32), a.block_size - item.y % a.block_size);
             for (int t0 = 0; t0 < live; t0 += kBatch) {
                 float k[kBatch][E], v[kBatch][E], s[kBatch];
 #pragma unroll
@@ -416,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
 #pragma unroll
                     for (int i = 0; i < E; ++i) v[b][i] = t0 + b < live ? v[b][i] : 0.f;
                 }
-                float most = m;
+                float most = -INFINITY;
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
                     float dot[kGroup];
@@ -430,10 +499,19 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
                     if (t0 + b >= live) s[b] = -INFINITY;
                     most = fmaxf(most, s[b]);
                 }
-                const float mu = most == -INFINITY ? 0.f : most;
-                const float al = exp2f(m - mu);
-                m = most;
-                l *= al;
+                if (__any_sync(kFull, most > m + kSlack)) { // as in bf16
+                    most = fmaxf(most, m);
+                    const float al = most == -INFINITY ? 1.f : exp2f(m - most);
+                    m = most;
+                    l *= al;
+#pragma unroll
+                    for (int g = 0; g < kGroup; ++g) {
+                        const float w = __shfl_sync(kFull, al, 4 * g);
+#pragma unroll
+                        for (int i = 0; i < E; ++i) acc[g][i] *= w;
+                    }
+                }
+                const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
                     s[b] = exp2f(s[b] - mu);
@@ -442,9 +520,6 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
 #pragma unroll
                 for (int g = 0; g < kGroup; ++g) {
                     if (g >= G) break;
-                    const float w = __shfl_sync(kFull, al, 4 * g);
-#pragma unroll
-                    for (int i = 0; i < E; ++i) acc[g][i] *= w;
 #pragma unroll
                     for (int b = 0; b < kBatch; ++b) {
                         const float p = __shfl_sync(kFull, s[b], 4 * g);
@@ -465,21 +540,28 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
         part.m[lane / 4] = m;
         part.l[lane / 4] = bad ? -1.f : l;
     }
-    finish_row<float, D>(parts, &cta_part, out, G, ctas, rank);
+    finish_row<float, D, kWarps>(parts, sizeof(Part<D>), &cta_part, out, G, ctas, rank, tid, 0);
 }
 
-// CTAs a row.  Enough of them for every SM to have a few, while each has work for
-// its warps (a block and more).
-int ctas_of(const SparseArgs &a)
+// How a row is split.  Few rows: a cluster of CTAs each, enough of them for every SM to have a
+// few CTAs while each has work for its warps (a unit and more).  Many (`pairs` an SM and more):
+// two warps a row instead of four, which spend less on beginning and joining rows.  64 blocks of
+// 16 tokens, four warps and two, us: head_dim 128, 896 rows 34.7 and 32.2, 1616 rows 58.8 and 51.8, 7000 rows
+// 213 and 194; head_dim 64, 3000 rows 79.4 and 82.6, 7000 rows 170 and 156.
+struct Split {
+    int ctas, warps;
+};
+Split split_of(const SparseArgs &a, int unit, int pairs)
 {
-    const long long rows = (long long)a.total_q * a.num_kv_heads;
-    int ctas = 1;
-    while (ctas < 16 && rows * ctas * 2 <= 4 * num_sms() && a.top_k > 2 * kWarps * ctas) ctas *= 2;
-    return ctas;
+    const long long rows = (long long)a.total_q * a.num_kv_heads, units = (long long)a.top_k * ((a.block_size + unit - 1) / unit);
+    Split s{1, kWarps};
+    while (s.ctas < 16 && rows * s.ctas * 2 <= 4 * num_sms() && units > 2 * kWarps * s.ctas) s.ctas *= 2;
+    if (pairs > 0 && rows >= (long long)pairs * num_sms()) s.warps = 2;
+    return s;
 }
 
 template <typename Kernel, typename... A>
-int launch(Kernel kernel, int *raised, size_t smem, const SparseArgs &a, cudaStream_t s, const A &...args)
+int launch(Kernel kernel, int *raised, size_t smem, const Split &split, const SparseArgs &a, cudaStream_t s, const A &...args)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_DEVICE;
@@ -489,9 +571,9 @@ int launch(Kernel kernel, int *raised, size_t smem, const SparseArgs &a, cudaStr
         if (e != cudaSuccess) return launch_status(e);
         __atomic_store_n(&raised[dev], 1, __ATOMIC_RELEASE);
     }
-    const int ctas = ctas_of(a);
+    const long long rows = (long long)a.total_q * a.num_kv_heads, per_cta = kWarps / split.warps;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.total_q * a.num_kv_heads * ctas));
+    cfg.gridDim = dim3((unsigned)((rows + per_cta - 1) / per_cta * split.ctas));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -499,28 +581,42 @@ int launch(Kernel kernel, int *raised, size_t smem, const SparseArgs &a, cudaStr
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.x = split.ctas;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, kernel, args..., a, ctas));
+    cfg.numAttrs = split.ctas > 1 ? 2 : 1;
+    return launch_status(cudaLaunchKernelEx(&cfg, kernel, args..., a, split.ctas));
+}
+
+template <int D, int W>
+int launch_bf16(const SparseArgs &a, const Split &split, const CUtensorMap &tm_k, const CUtensorMap &tm_v, cudaStream_t s)
+{
+    static int raised[64];
+    return launch(sparse_bf16_kernel<D, W>, raised, Ring<D>::BYTES + 1024, split, a, s, tm_k, tm_v);
+}
+
+template <int D>
+int launch_bf16(const SparseArgs &a, const CUtensorMap &tm_k, const CUtensorMap &tm_v, cudaStream_t s)
+{
+    const Split split = split_of(a, kSparseUnit, D == 128 ? 6 : 40);
+    if (split.warps == 2) return launch_bf16<D, 2>(a, split, tm_k, tm_v, s);
+    return launch_bf16<D, kWarps>(a, split, tm_k, tm_v, s);
 }
 
 }  // namespace
 
 int sparse_bf16_launch(const SparseArgs &a, int head_dim, const CUtensorMap &tm_k, const CUtensorMap &tm_v, cudaStream_t s)
 {
-    static int raised64[64], raised128[64];
-    if (head_dim == 64) return launch(sparse_bf16_kernel<64>, raised64, Ring<64>::BYTES + 1024, a, s, tm_k, tm_v);
-    return launch(sparse_bf16_kernel<128>, raised128, Ring<128>::BYTES + 1024, a, s, tm_k, tm_v);
+    return head_dim == 64 ? launch_bf16<64>(a, tm_k, tm_v, s) : launch_bf16<128>(a, tm_k, tm_v, s);
 }
 
 int sparse_f32_launch(const SparseArgs &a, int head_dim, cudaStream_t s)
 {
     static int raised64[64], raised128[64];
-    if (head_dim == 64) return launch(sparse_f32_kernel<64>, raised64, 0, a, s);
-    return launch(sparse_f32_kernel<128>, raised128, 0, a, s);
+    const Split split = split_of(a, kUnitF32, 0);
+    if (head_dim == 64) return launch(sparse_f32_kernel<64>, raised64, 0, split, a, s);
+    return launch(sparse_f32_kernel<128>, raised128, 0, split, a, s);
 }
 
 }  // namespace pa

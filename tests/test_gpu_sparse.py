@@ -320,6 +320,37 @@ def test_sparse_for_every_split(dtype, rows, top):
     _check(got[:1], c, q[:1], sel)
 
 
+@pytest.mark.parametrize("d,hkv,rows", [(128, 1, 913), (128, 3, 307), (64, 8, 761), (64, 5, 1217)])
+def test_sparse_of_many_rows(d, hkv, rows):
+    """Two rows a CTA: an odd number of them, lists of different lengths side by side,
+    rows without anything, a bad entry in one, rows behind the last request."""
+    assert rows * hkv >= (6 if d == 128 else 40) * 152 and rows % 2 == 1
+    bs, lens = 16, [90, 333, 17, 0]
+    c = make_cache(11, lens, hkv, d, bs, BF16, width=21)
+    pick = np.arange(rows) % 4
+    big = dict(c, table=c["table"][pick].clone(), lens=c["lens"][pick].clone())
+    q = torch.randn(rows, 2 * hkv, d, generator=torch.Generator().manual_seed(1)).to(BF16)
+    sel = _random_choice(np.random.default_rng(5), [lens[i] for i in pick], hkv, bs, 9)
+    sel[4:8, 0] = -1
+    big["table"][1, :] = -1  # the second request's first row
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = _attend(big, q, sel, dev_err=err)
+    assert err.item() == pa.DEVERR_BAD_BLOCK and (got[1] == 0).all() and (got[3::4] == 0).all()
+    rest = np.setdiff1d(np.arange(rows)[:40], [1])
+    _check(got[rest], dict(big, table=big["table"][rest], lens=big["lens"][rest]), q[rest], sel[rest])
+    last = np.arange(rows - 9, rows)
+    _check(got[last], dict(big, table=big["table"][last], lens=big["lens"][last]), q[last], sel[last])
+    # the same rows as packed queries of one request: all see its last positions
+    n = rows - 2
+    one = dict(c, table=c["table"][1:2], lens=i32([n + 20 * bs]))
+    one["table"] = torch.nn.functional.pad(one["table"], (0, n // bs + 2), value=0)
+    sel2 = np.tile(_random_choice(np.random.default_rng(6), [300], hkv, bs, 9), (rows, 1, 1))
+    out = torch.full(q.shape, 3.0, dtype=BF16, device=DEV)
+    got = _attend(one, q, sel2, cu=np.array([0, n], dtype=np.int32), out=out)
+    assert (got[n:] == 3).all()
+    _check(got[:30], dict(one, lens=i32([n + 20 * bs - n + 30])), q[:30], sel2[:30], cu=np.array([0, 30], dtype=np.int32))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_sparse_of_a_list_beyond_one_look_up(dtype):
     d, bs, top = 64, 16, 16 * 4 * 64 * 2 + 77  # three look-ups of sixteen CTAs' warps

@@ -72,7 +72,7 @@ def test_select_refusals(lib, over, status):  # noqa: F811
 @pytest.mark.parametrize("over,status", [
     (dict(dtype=2), -2), (dict(batch=-1), -3), (dict(tq=1), -3), (dict(hq=7), -3), (dict(hq=18), -4), (dict(d=96), -4), (dict(top=-4), -3),
     (dict(bs=24), -4), (dict(bs=8), -4), (dict(nb=1 << 27), -4), (dict(kc=None), -1), (dict(out=None), -1), (dict(vc=P(4104)), -3),
-    (dict(selected=P(4098)), -3), (dict(batch=0, tq=0, q=None), 0),
+    (dict(selected=P(4098)), -3), (dict(batch=0, tq=0, q=None), 0), (dict(top=1 << 20, bs=1 << 10), -4), (dict(top=(1 << 20) + 1), -4),
 ])
 def test_sparse_refusals(lib, over, status):  # noqa: F811
     order = "q kc vc table lens cu selected out batch tq hq hkv d nb bs mb top dtype scale err stream".split()
