@@ -27,7 +27,9 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
-constexpr int kHeads = 4; // heads of a thread group: their loads are in flight together
+// Heads of a thread group: their loads are in flight together, 32 bytes each and lane.
+template <typename T>
+constexpr int kHeadsOf = 8 / (int)sizeof(T);
 constexpr int kMaxAxes = 4;
 // Rows of a CTA that keeps bounds: the tokens whose runs it takes.
 constexpr int kTileTokens = 16;
@@ -261,16 +263,17 @@ __device__ __forceinline__ void load_angles(const RotaryArgs &a, const Lane &l, 
     }
 }
 
-// kHeads heads of one token: turned (TURN) or copied.  `zero` writes zeros.
+// kHeadsOf heads of one token: turned (TURN) or copied.  `zero` writes zeros.
 template <typename T, int D, bool PAIRS, bool TURN>
 __device__ __forceinline__ void move_heads(const T *src, T *dst, int heads, const Lane &l, const Angles &w, bool zero)
 {
-    Chunks<T> x[kHeads];
+    constexpr int N = kHeadsOf<T>;
+    Chunks<T> x[N];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i)
+    for (int i = 0; i < N; ++i)
         if (i < heads) x[i] = load_chunks(src + i * D, l.c0, l.c1);
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
+    for (int i = 0; i < N; ++i) {
         if (i >= heads) break;
         if (TURN && l.turns) turn<T, PAIRS>(x[i], w);
         if (zero) x[i] = Chunks<T>{};
@@ -278,13 +281,14 @@ __device__ __forceinline__ void move_heads(const T *src, T *dst, int heads, cons
     }
 }
 
-// Thread groups of D / 16 lanes take (token, kHeads heads): first the queries',
-// then (kRotary, kAppend) the keys'.  kAppendBounds: CTAs from `q_ctas` on take the
-// runs of tokens of one block that begin in their TILE tokens, a warp one head of one.
+// Thread groups of D / 16 lanes take (token, kHeadsOf heads): first the queries',
+// then (kRotary, kAppend) the keys'.  kAppendBounds: `run_ctas` CTAs, spread among the
+// others (their chains of dependent loads need company), take the runs of tokens of one block
+// that begin in their TILE tokens, a warp one head of one.
 template <typename T, int D, bool PAIRS, Mode MODE, int TILE>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, int axes, unsigned q_ctas)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rotary_kernel(const RotaryArgs a, int axes, unsigned run_ctas)
 {
-    constexpr int LPR = D / 16;
+    constexpr int LPR = D / 16, kHeads = kHeadsOf<T>;
     grid_dep_trigger();
     grid_dep_wait();
     const Lane l = lane_of<D, PAIRS>(a, threadIdx.x);
@@ -294,9 +298,12 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
     Angles w{};
     int pos[kMaxAxes];
 
-    if (MODE != kAppendBounds || blockIdx.x < q_ctas) {
+    const unsigned every = MODE == kAppendBounds ? gridDim.x / run_ctas : 1, turns = blockIdx.x / every;
+    const bool runs = MODE == kAppendBounds && turns * every == blockIdx.x && turns < run_ctas;
+    if (!runs) {
         const int gq = (hq + kHeads - 1) / kHeads, gk = MODE == kAppendBounds ? 0 : (hkv + kHeads - 1) / kHeads;
-        const long long item = (long long)blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+        const unsigned cta = MODE == kAppendBounds ? blockIdx.x - min(turns + 1, run_ctas) : blockIdx.x;
+        const long long item = (long long)cta * (kThreads / LPR) + threadIdx.x / LPR;
         const long long nq = (long long)a.tokens * gq;
         const bool is_q = item < nq;
         const long long it = is_q ? item : item - nq;
@@ -329,11 +336,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
     }
 
     if constexpr (MODE == kAppendBounds) {
-        constexpr int NG = 32 / LPR;               // tokens of a warp at once
-        constexpr int U = sizeof(T) == 2 ? 2 : 1;  // and of a lane (registers)
+        constexpr int NG = 32 / LPR; // tokens of a warp at once
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane / LPR;
         const int bs = a.block_size;
-        const int t0 = (int)(blockIdx.x - q_ctas) * TILE;
+        const int t0 = (int)turns * TILE;
         // a run begins where the block differs from the row's before
         int mine = -1, before = -1;
         if (lane < TILE && t0 + lane < a.tokens) {
@@ -365,36 +371,25 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
                 const int len = others ? __ffs(others) - 1 : 32;
                 if (h == 0 && lane < len && !(here && ok))
                     flag_error(a.dev_err, (here ? 0 : PA_DEVERR_BAD_BLOCK) | (ok ? 0 : PA_DEVERR_OVERFLOW));
-                for (int r0 = 0; r0 < len; r0 += NG * U) {
-                    Chunks<T> kx[U], vx[U];
-                    Angles aw[U];
-                    long long at[U];
+                for (int r0 = 0; r0 < len; r0 += NG) {
+                    const int r = r0 + group, from = min(r, 31);
+                    const int sl = __shfl_sync(kFull, s, from);
+                    const bool good = __shfl_sync(kFull, (int)ok, from) && r < len && here;
+                    int p[kMaxAxes];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int r = r0 + u * NG + group, from = min(r, 31);
-                        const int sl = __shfl_sync(kFull, s, from);
-                        const bool good = __shfl_sync(kFull, (int)ok, from) && r < len && here;
-                        int p[kMaxAxes];
-#pragma unroll
-                        for (int i = 0; i < kMaxAxes; ++i) p[i] = i < axes ? __shfl_sync(kFull, pos[i], from) : 0;
-                        at[u] = -1;
-                        if (good) {
-                            const long long t = base + r;
-                            at[u] = ((long long)sl * hkv + h) * D;
-                            kx[u] = load_chunks(k + t * a.k_stride + h * D, l.c0, l.c1);
-                            vx[u] = load_chunks(v + t * a.v_stride + h * D, l.c0, l.c1);
-                            if (l.turns) load_angles(a, l, p, aw[u]);
-                        }
+                    for (int i = 0; i < kMaxAxes; ++i) p[i] = i < axes ? __shfl_sync(kFull, pos[i], from) : 0;
+                    if (!good) continue;
+                    const long long t = base + r, at = ((long long)sl * hkv + h) * D;
+                    Chunks<T> x = load_chunks(k + t * a.k_stride + h * D, l.c0, l.c1);
+                    const Chunks<T> y = load_chunks(v + t * a.v_stride + h * D, l.c0, l.c1);
+                    if (l.turns) {
+                        load_angles(a, l, p, w);
+                        turn<T, PAIRS>(x, w);
                     }
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        if (at[u] < 0) continue;
-                        if (l.turns) turn<T, PAIRS>(kx[u], aw[u]);
-                        store_chunks(kc + at[u], l.c0, l.c1, kx[u]);
-                        store_chunks(vc + at[u], l.c0, l.c1, vx[u]);
-                        b.add(kx[u], kx[u]);
-                        any = true;
-                    }
+                    store_chunks(kc + at, l.c0, l.c1, x);
+                    store_chunks(vc + at, l.c0, l.c1, y);
+                    b.add(x, x);
+                    any = true;
                 }
                 if (len < 32) break;
             }
@@ -408,7 +403,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
 }
 
 template <typename T, int D, bool PAIRS, Mode MODE, int TILE>
-int launch(const RotaryArgs &a, int axes, long long q_ctas, long long ctas, cudaStream_t s)
+int launch(const RotaryArgs &a, int axes, long long run_ctas, long long ctas, cudaStream_t s)
 {
     if (ctas >= 1ll << 31) return PA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
@@ -420,25 +415,27 @@ int launch(const RotaryArgs &a, int axes, long long q_ctas, long long ctas, cuda
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, rotary_kernel<T, D, PAIRS, MODE, TILE>, a, axes, (unsigned)q_ctas));
+    return launch_status(cudaLaunchKernelEx(&cfg, rotary_kernel<T, D, PAIRS, MODE, TILE>, a, axes, (unsigned)run_ctas));
 }
 
 template <typename T, int D, bool PAIRS>
 int launch_mode(const RotaryArgs &a, int axes, bool append, cudaStream_t s)
 {
+    constexpr int kHeads = kHeadsOf<T>;
     const long long per_cta = kThreads / (D / 16);
     const long long gq = (a.num_heads + kHeads - 1) / kHeads, gk = (a.num_kv_heads + kHeads - 1) / kHeads;
     const long long nq = a.tokens * gq, nk = a.tokens * gk;
     if (!append || a.bounds == nullptr) {
         const long long ctas = (nq + nk + per_cta - 1) / per_cta;
-        return append ? launch<T, D, PAIRS, kAppend, 1>(a, axes, ctas, ctas, s)
-                      : launch<T, D, PAIRS, kRotary, 1>(a, axes, ctas, ctas, s);
+        return append ? launch<T, D, PAIRS, kAppend, 1>(a, axes, 0, ctas, s)
+                      : launch<T, D, PAIRS, kRotary, 1>(a, axes, 0, ctas, s);
     }
     const long long qc = (nq + per_cta - 1) / per_cta;
     // Few tokens are mostly runs of their own: a CTA for each.  With many, most
     // are inside a run that one CTA of the tile takes.
-    if (a.tokens <= kTileTokens * num_sms()) return launch<T, D, PAIRS, kAppendBounds, 1>(a, axes, qc, qc + a.tokens, s);
-    return launch<T, D, PAIRS, kAppendBounds, kTileTokens>(a, axes, qc, qc + (a.tokens + kTileTokens - 1) / kTileTokens, s);
+    if (a.tokens <= kTileTokens * num_sms()) return launch<T, D, PAIRS, kAppendBounds, 1>(a, axes, a.tokens, qc + a.tokens, s);
+    const long long runs = (a.tokens + kTileTokens - 1) / kTileTokens;
+    return launch<T, D, PAIRS, kAppendBounds, kTileTokens>(a, axes, runs, runs + qc, s);
 }
 
 }  // namespace
