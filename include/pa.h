@@ -465,7 +465,8 @@ int pa_rotary(const void *q, const void *k, const int32_t *positions, const floa
  * bounds [num_blocks, num_kv_heads, 2, head_dim] of dtype, or NULL: the least
  * ([.., 0, :]) and the largest ([.., 1, :]) value of each channel over the keys of a
  * block, as pa_select_blocks takes them.  A token at offset 0 starts its block's bounds
- * anew, others widen them; NaN wins.  The rows of one block have to follow one another,
+ * anew, others widen them; NaN wins.  (Tokens that are taken back and written again leave
+ * bounds that may be wider than need be, until the block starts anew.)  The rows of one block have to follow one another,
  * in order of their offsets (as pa_block_tables packs them).  Blocks that get no token
  * are left alone.
  */
@@ -497,8 +498,8 @@ int pa_cache_append_rotary(const void *q, const void *k, const void *v, const in
  *   score = max over the kv head's query heads g of sum_d max(q_gd, 0) hi_d + min(q_gd, 0) lo_d,
  * which no key between the block's bounds lo, hi exceeds in its product with q_g.  The
  * choice is that of the exact scores (ties: the lowest block), whatever the order of the
- * sums.  A NaN ranks above all numbers; sums of |q| |bound| stay below 3e38 (a score that
- * overflows is an infinity).  Bounds of the last block are used only where last_blocks is
+ * sums (as long as the sums of |q| |bound| lie between 1e-30 and 3e38; a score that overflows
+ * is an infinity).  A NaN ranks above all numbers.  Bounds of the last block are used only where last_blocks is
  * 0: a chunk's later tokens are in them.
  * dtype is that of q and bounds.  first_blocks + last_blocks <= top_k;
  * max_blocks_per_seq <= 49152; top_k at most 2^20; num_heads / num_kv_heads <= 8; head_dim 64 or 128;

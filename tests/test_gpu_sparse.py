@@ -1,5 +1,9 @@
 """pa_select_blocks and pa_sparse on the GPU against the plain reference, and the step
 that they and pa_cache_append_rotary make up."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -532,6 +536,33 @@ def test_a_captured_step_replays_on_new_inputs():
         assert torch.equal(sel, want_sel) and torch.equal(out, want)
         assert torch.equal(s["k"].nan_to_num(9.0), fresh["k"].nan_to_num(9.0))
         assert torch.equal(s["bounds"].nan_to_num(9.0), fresh["bounds"].nan_to_num(9.0))
+
+
+_FIRST_CALL_CAPTURED = """
+import torch
+import paged_kv_cache_300_gb300 as pa
+from tests.test_gpu_sparse import F32, BF16, _step, _step_args
+for dtype in (BF16, F32):
+    s, fresh = _step_args(dtype), _step_args(dtype)
+    q, k = s["qkv"][:, :4], s["qkv"][:, 4:6]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, sel = _step(s)
+        turned = pa.pa_rotary(q, k, s["pos"], s["angles"])
+    for _ in range(2):
+        graph.replay()
+    want, want_sel = _step(fresh)
+    assert torch.equal(sel, want_sel) and torch.equal(out, want)
+    assert all(torch.equal(a, b) for a, b in zip(turned, pa.pa_rotary(q, k, s["pos"], s["angles"])))
+print("captured first")
+"""
+
+
+def test_the_first_call_of_a_process_can_be_captured():
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALL_CAPTURED], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr[-2000:]
 
 
 def test_on_another_stream_and_several_at_once():
