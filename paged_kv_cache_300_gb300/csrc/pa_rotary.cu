@@ -19,6 +19,8 @@
 // turn, keep the extrema of the rounded keys in registers and join them by
 // shuffles; a run that begins inside a block widens the bounds that are there.
 // No atomics: the result does not depend on any order.
+#include <type_traits>
+
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
@@ -31,8 +33,6 @@ constexpr int kThreads = 256;
 template <typename T>
 constexpr int kHeadsOf = 8 / (int)sizeof(T);
 constexpr int kMaxAxes = 4;
-// Rows of a CTA that keeps bounds: the tokens whose runs it takes.
-constexpr int kTileTokens = 16;
 
 enum Mode { kRotary, kAppend, kAppendBounds };
 
@@ -284,7 +284,7 @@ __device__ __forceinline__ void move_heads(const T *src, T *dst, int heads, cons
 // Thread groups of D / 16 lanes take (token, kHeadsOf heads): first the queries',
 // then (kRotary, kAppend) the keys'.  kAppendBounds: `run_ctas` CTAs, spread among the
 // others (their chains of dependent loads need company), take the runs of tokens of one block
-// that begin in their TILE tokens, a warp one head of one.
+// that begin in TILE tokens, a warp one head of them.
 template <typename T, int D, bool PAIRS, Mode MODE, int TILE>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rotary_kernel(const RotaryArgs a, int axes, unsigned run_ctas)
 {
@@ -339,7 +339,11 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rotary_kerne
         constexpr int NG = 32 / LPR; // tokens of a warp at once
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane / LPR;
         const int bs = a.block_size;
-        const int t0 = (int)turns * TILE;
+        // a warp has one head of the runs that begin in TILE tokens
+        const long long unit = (long long)turns * (kThreads / 32) + warp;
+        const int h = (int)(unit % hkv);
+        if (unit / hkv * TILE >= a.tokens) return;
+        const int t0 = (int)(unit / hkv) * TILE;
         // a run begins where the block differs from the row's before
         int mine = -1, before = -1;
         if (lane < TILE && t0 + lane < a.tokens) {
@@ -347,10 +351,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rotary_kerne
             before = t0 + lane > 0 ? a.slot_map[t0 + lane - 1] : -1;
         }
         const bool lead = mine >= 0 && (before < 0 || before / bs != mine / bs);
-        const uint32_t leads = __ballot_sync(kFull, lead);
-        const int items = __popc(leads) * hkv;
-        for (int it = warp; it < items; it += kThreads / 32) {
-            const int h = it % hkv, t1 = t0 + (int)__fns(leads, 0, it / hkv + 1);
+        for (uint32_t leads = __ballot_sync(kFull, lead); leads; leads &= leads - 1) {
+            const int t1 = t0 + __ffs(leads) - 1;
             const int slot1 = __shfl_sync(kFull, mine, t1 - t0);
             const int block = slot1 / bs;
             const bool here = block < a.num_blocks;
@@ -431,11 +433,19 @@ int launch_mode(const RotaryArgs &a, int axes, bool append, cudaStream_t s)
                       : launch<T, D, PAIRS, kRotary, 1>(a, axes, 0, ctas, s);
     }
     const long long qc = (nq + per_cta - 1) / per_cta;
-    // Few tokens are mostly runs of their own: a CTA for each.  With many, most
-    // are inside a run that one CTA of the tile takes.
-    if (a.tokens <= kTileTokens * num_sms()) return launch<T, D, PAIRS, kAppendBounds, 1>(a, axes, a.tokens, qc + a.tokens, s);
-    const long long runs = (a.tokens + kTileTokens - 1) / kTileTokens;
-    return launch<T, D, PAIRS, kAppendBounds, kTileTokens>(a, axes, runs, runs + qc, s);
+    // Few tokens are mostly runs of their own: a warp for each and head.  Of many, most are
+    // inside a run that begins before them, and a warp looks at several.  Looking at 1, 4 and 16, us
+    // (tokens x kv heads, D = 128): 1024 x 8 of 1024 requests 11.7, 13.7, 35.2; 2051 x 16 of 316 19.0, 13.6, 17.1; 4096 x 8 of
+    // as many 44.9, 42.0, 54.3; 5685 x 8 of 8 34.2, 30.1, 28.1; 33116 x 8 of 32 199, 145, 131.
+    const long long warps = (long long)a.tokens * a.num_kv_heads, wave = 24ll * num_sms();
+    auto go = [&](auto tile) {
+        constexpr int TILE = decltype(tile)::value;
+        const long long units = (a.tokens + TILE - 1) / TILE * (long long)a.num_kv_heads;
+        const long long runs = (units + kThreads / 32 - 1) / (kThreads / 32);
+        return launch<T, D, PAIRS, kAppendBounds, TILE>(a, axes, runs, runs + qc, s);
+    };
+    if (warps <= 3 * wave) return go(std::integral_constant<int, 1>());
+    return warps <= 12 * wave ? go(std::integral_constant<int, 4>()) : go(std::integral_constant<int, 16>());
 }
 
 }  // namespace

@@ -30,6 +30,7 @@
 //   u the |q| of a head or, for tiles of tokens, the largest |q| of all their heads (one column more).  (fp32: D / 16 + 5
 //   roundings of 2^-24, within the same.)  L1(q) max|b| costs no product but is several times
 //   as much, and then every other row needs exact scores, which take longer than all the rest.
+#include <algorithm>
 #include <limits.h>
 #include <type_traits>
 
@@ -509,11 +510,11 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
 }
 
 // fp32: a warp scores kBatch blocks at a time, its lanes share the channels.
-template <int D, bool ONE>
-__device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring &s, int first, int step, int lane, float &mag,
-                                             int &bad, const float *)
+template <int D, int kBatch>
+__device__ __forceinline__ void score_blocks_f32(const SelectArgs &a, const Scoring &s, int first, int step, int lane, float &mag,
+                                             int &bad)
 {
-    constexpr int E = D / 32, kBatch = 4;
+    constexpr int E = D / 32;
     constexpr int ROW = 4 * D + kPad;
     using Vec = typename std::conditional<E == 4, float4, float2>::type;
     const int n = s.n;
@@ -552,9 +553,7 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
             if (tile * kBatch + b < n && m < INFINITY) mag = fmaxf(mag, m);
         }
         for (int t = 0; t < s.tokens; ++t) {
-            float best[kBatch];
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) best[b] = -INFINITY;
+            float best = -INFINITY;
             for (int g = 0; g < a.group; ++g) {
                 float x[E], p[kBatch];
                 row_of((t << s.heads_log2) + g, x);
@@ -565,22 +564,36 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
                     for (int i = 0; i < E; ++i)
                         p[b] = fmaf(max_nan(x[i], 0.f), hi[b][i], fmaf(min_nan(x[i], 0.f), lo[b][i], p[b]));
                 }
-                // the four sums together: lanes of a quarter end up with one of them
+                // the kBatch sums together: 32 / kBatch neighbouring lanes end up with one of them
+                int mask = 16;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float give = lane & 16 ? p[i] : p[i + 2], keep = lane & 16 ? p[i + 2] : p[i];
-                    p[i] = keep + __shfl_xor_sync(kFull, give, 16);
-                }
-                const float give = lane & 8 ? p[0] : p[1], keep = lane & 8 ? p[1] : p[0];
-                float z = keep + __shfl_xor_sync(kFull, give, 8);
+                for (int half = kBatch / 2; half >= 1; half /= 2, mask /= 2)
 #pragma unroll
-                for (int o = 4; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
-                best[0] = max_nan(best[0], z);
+                    for (int i = 0; i < half; ++i) {
+                        const float give = lane & mask ? p[i] : p[i + half], keep = lane & mask ? p[i + half] : p[i];
+                        p[i] = keep + __shfl_xor_sync(kFull, give, mask);
+                    }
+                float z = p[0];
+#pragma unroll
+                for (; mask >= 1; mask /= 2) z += __shfl_xor_sync(kFull, z, mask);
+                best = max_nan(best, z);
             }
-            const int j = tile * kBatch + (lane >> 3); // the quarter's block
-            if (j < n && (lane & 7) == 0) cluster_store(s.keys + t * s.stride + 4 * j, __float_as_uint(best[0]));
+            const int j = tile * kBatch + lane / (32 / kBatch); // these lanes' block
+            if (j < n && lane % (32 / kBatch) == 0) cluster_store(s.keys + t * s.stride + 4 * j, __float_as_uint(best));
         }
     }
+}
+
+// Eight blocks at a time (8 KB in flight a warp at D = 128) for a token alone where every warp has two
+// such, else four (and three CTAs an SM instead of two).
+template <int D, bool ONE>
+__device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring &s, int first, int step, int lane, float &mag,
+                                             int &bad, const float *)
+{
+    if (ONE && s.n >= 16 * step)
+        score_blocks_f32<D, 8>(a, s, first, step, lane, mag, bad);
+    else
+        score_blocks_f32<D, 4>(a, s, first, step, lane, mag, bad);
 }
 
 // Tile `unit` of those that the requests' queries make up, `tile` rows each but the last of
@@ -630,9 +643,9 @@ struct Shared {
 };
 
 // TILE = 1: one token a CTA, or a cluster of `ctas`.  Otherwise up to `tile` tokens of one
-// request a CTA.
+// request.
 template <typename T, int D, int TILE>
-__global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a, int ctas, int tile, int heads_log2)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) select_kernel(const SelectArgs a, int ctas, int tile, int heads_log2)
 {
     constexpr int W = TILE == 1 ? kWarps : 1; // warps that choose together
     constexpr int ROW = (int)sizeof(T) * D + kPad;
@@ -640,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a,
     __shared__ Shared sh;
     __shared__ Choice<W> choice[kWarps / W];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const bool cluster = TILE == 1 && ctas > 1;
+    const bool cluster = ctas > 1;
     const int rank = cluster ? (int)cluster_rank() : 0;
     if (tid == 0) {
         sh.mag = 0;
@@ -651,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a,
     if (cluster) cluster_arrive();
     grid_dep_wait();
 
-    const int unit = TILE == 1 ? (int)(blockIdx.x / ctas) : (int)blockIdx.x;
+    const int unit = (int)(blockIdx.x / ctas);
     const int h = unit % a.num_kv_heads; // heads of a tile side by side
     int t = unit / a.num_kv_heads, count = 1;
     QueryRow at;
@@ -659,7 +672,10 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a,
         at = query_row(a, t, lane);
     } else {
         const TileRows r = tile_rows(a, t, tile, lane);
-        if (r.count == 0) return;
+        if (r.count == 0) {
+            if (cluster) cluster_wait();
+            return;
+        }
         t = r.first;
         count = r.count;
         at = query_row(a, t, lane);
@@ -684,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const SelectArgs a,
         s.tokens = count;
         s.heads_log2 = heads_log2;
         s.q = smem_u32(q_rows);
-        s.keys = TILE == 1 ? cluster_addr(keys, 0) : smem_u32(keys);
+        s.keys = cluster_addr(keys, 0);
         s.stride = cap * 4;
         // rows of q, 16 bytes a thread; then the largest |q| of each channel
         constexpr int PIECES = (int)sizeof(T) * D / 16;
@@ -804,17 +820,20 @@ int launch_tile(const SelectArgs &a, cudaStream_t s)
     const int heads_log2 = a.group > 4 ? 3 : a.group > 2 ? 2 : a.group > 1 ? 1 : 0;
     const size_t row = sizeof(T) * D + kPad;
     auto smem_of = [&](int tile) { return (size_t)tile * a.max_blocks_per_seq * 4 + 16 + ((size_t)(((tile << heads_log2) + 7) & ~7) + 1) * row; };
-    // Chunks: the tile with the most tokens that leaves every SM two CTAs, fits two of
-    // them, and holds no more tokens than requests have on average.
+    // Chunks: tiles of as many tokens as requests have on average, and shared memory holds twice an SM.
     int tile = 1;
     if (a.cu_q != nullptr)
-        while (tile < kTile && (a.total_q + 2 * tile - 1) / (2 * tile) * (long long)a.num_kv_heads >= num_sms() &&
-               smem_of(2 * tile) <= 100 * 1024 && a.total_q >= 2ll * tile * a.batch)
-            tile *= 2;
-    if (tile > 1) return launch<T, D, kTile>(a, 1, tile, heads_log2, smem_of(tile), s);
-    // Few rows: as many CTAs a row as fit the GPU beside one another.
-    int ctas = 1;
-    while (ctas < 16 && rows * ctas * 2 <= 2 * num_sms() && a.max_blocks_per_seq > 16 * kWarps * ctas) ctas *= 2;
+        while (tile < kTile && smem_of(2 * tile) <= 100 * 1024 && a.total_q >= 2ll * tile * a.batch) tile *= 2;
+    auto units_of = [&](int t) { return t == 1 ? rows : (a.total_q / t + (long long)a.batch) * a.num_kv_heads; };
+    // .. or of half as many, where those fill the GPU by themselves and these do not (462 tokens of 3
+    // requests, 5 kv heads: tiles of 16 25 us, of 8 19 us; 485 of 5, 8 kv heads: 56 and 59).
+    const long long fill = 2ll * num_sms(), half = units_of(tile / 2 + (tile == 1));
+    if (tile > 1 && units_of(tile) < 3 * fill / 4 && half >= 3 * fill / 4 && half <= fill) tile /= 2;
+    // Few rows or tiles: a cluster of CTAs each, as many as are resident at a time (two an SM)
+    // while each warp has a tile of 16 blocks.
+    const long long fit = std::min<long long>(fill / units_of(tile), (a.max_blocks_per_seq + 16 * kWarps - 1) / (16 * kWarps));
+    const int ctas = fit <= 1 ? 1 : fit <= 8 ? (int)fit : fit >= 16 ? 16 : 8; // (9 to 15 are slower than 8)
+    if (tile > 1) return launch<T, D, kTile>(a, ctas, tile, heads_log2, smem_of(tile), s);
     return launch<T, D, 1>(a, ctas, 1, heads_log2, smem_of(1), s);
 }
 

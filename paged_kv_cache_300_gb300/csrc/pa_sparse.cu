@@ -22,6 +22,7 @@
 //
 // fp32.  Lanes share the channels; a warp has the rows of kBatch tokens in registers
 // at a time, products by FMA, expf.
+#include <algorithm>
 #include <type_traits>
 
 #include "pa_common.cuh"
@@ -543,8 +544,8 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
     finish_row<float, D, kWarps>(parts, sizeof(Part<D>), &cta_part, out, G, ctas, rank, tid, 0);
 }
 
-// How a row is split.  Few rows: a cluster of CTAs each, enough of them for every SM to have a
-// few CTAs while each has work for its warps (a unit and more).  Many (`pairs` an SM and more):
+// How a row is split.  Few rows: a cluster of CTAs each, up to four CTAs an SM in all, while each warp
+// has two units.  Many (`pairs` an SM and more):
 // two warps a row instead of four, which spend less on beginning and joining rows.  64 blocks of
 // 16 tokens, four warps and two, us: head_dim 128, 896 rows 34.7 and 32.2, 1616 rows 58.8 and 51.8, 7000 rows
 // 213 and 194; head_dim 64, 3000 rows 79.4 and 82.6, 7000 rows 170 and 156.
@@ -555,7 +556,8 @@ Split split_of(const SparseArgs &a, int unit, int pairs)
 {
     const long long rows = (long long)a.total_q * a.num_kv_heads, units = (long long)a.top_k * ((a.block_size + unit - 1) / unit);
     Split s{1, kWarps};
-    while (s.ctas < 16 && rows * s.ctas * 2 <= 4 * num_sms() && units > 2 * kWarps * s.ctas) s.ctas *= 2;
+    const long long fit = std::min<long long>(4ll * num_sms() / rows, (units + 2 * kWarps - 1) / (2 * kWarps));
+    s.ctas = fit <= 1 ? 1 : fit <= 8 ? (int)fit : fit >= 16 && rows * 16 <= 2 * num_sms() ? 16 : 8; // (9 to 15 are slower than 8)
     if (pairs > 0 && rows >= (long long)pairs * num_sms()) s.warps = 2;
     return s;
 }

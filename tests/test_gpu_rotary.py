@@ -197,15 +197,16 @@ def test_append(dtype, d, rot, style, kind, bs, with_bounds):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("d,bs", [(128, 16), (64, 32), (64, 100)])
-def test_append_of_a_long_chunk(dtype, d, bs):
-    """Enough tokens for CTAs that take the runs of sixteen rows; runs of more than 32."""
+@pytest.mark.parametrize("d,bs,hkv", [(128, 16, 16), (64, 32, 5), (64, 100, 16), (64, 16, 2), (128, 100, 5)])
+def test_append_of_a_long_chunk(dtype, d, bs, hkv):
+    """Enough rows for warps that look at one, four and sixteen tokens for the runs that begin
+    there; runs of more than 32."""
     rng = np.random.default_rng(9)
     new = [int(n) for n in rng.integers(1, 500, 13)] + [1] * 40
     lens = [int(n) for n in rng.integers(0, 70, len(new))]
     slots, nb = _slots(lens, new, bs, rng)
-    t, hkv = len(slots), 3
-    assert t > 16 * 152
+    t = len(slots)
+    assert {2: 0, 5: 3, 16: 12}[hkv] * 24 * 152 < t * hkv <= {2: 3, 5: 12, 16: 1000}[hkv] * 24 * 152
     slots[rng.random(t) < 0.002] = -1
     for i in range(1, t):  # padding only between requests or blocks: rows of a block follow one another
         if slots[i - 1] < 0 and slots[i] >= 0 and slots[i] % bs:

@@ -133,6 +133,30 @@ def test_select_for_tiles_of_tokens(dtype, d, bs, hq, hkv, first, last, tokens):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("batch,hkv,part", [(3, 2, 25), (2, 1, 70), (5, 3, 4)])
+def test_select_for_tiles_on_clusters(dtype, batch, hkv, part):
+    """Few tiles of tokens over long contexts: a cluster of CTAs for each, in which the first
+    chooses; tiles that hold nothing among them."""
+    d, bs, top = 64, 16, 40
+    new = [part - 3 * r % 4 for r in range(batch)]
+    new[-1] = 0 if batch > 2 else new[-1]
+    lens = [(300 + 90 * r) * bs - 5 for r in range(batch)]
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    blocks = [-(-n // bs) for n in lens]
+    nb = sum(blocks)
+    table = _table(np.random.default_rng(1), blocks, 900, nb)
+    bounds = _bounds(5, nb, hkv, d, dtype)
+    q = torch.randn(int(cu[-1]) + 2, 4 * hkv, d, generator=torch.Generator().manual_seed(8)).to(dtype)
+    got = _select(q, bounds, table, i32(lens), top, bs, cu=torch.from_numpy(cu))
+    want = _want(q, bounds, table, i32(lens), top, bs, cu=torch.from_numpy(cu))
+    assert np.array_equal(got[:cu[-1]], want[:cu[-1]]) and (got[cu[-1]:] == -9).all()
+    table[0, 100] = -1
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = _select(q, bounds, table, i32(lens), top, bs, cu=torch.from_numpy(cu), dev_err=err)
+    assert err.item() == pa.DEVERR_BAD_BLOCK and (got[:cu[1]] == -1).all() and np.array_equal(got[cu[1]:cu[-1]], want[cu[1]:cu[-1]])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_select_among_equal_and_nearly_equal_scores(dtype):
     """Blocks whose scores are equal (ties: the lowest block) or differ by less than the
     rounding of an fp32 sum; the exact scores decide."""
@@ -197,7 +221,7 @@ def test_select_from_as_many_blocks_as_there_can_be(dtype, d, n, top):
     assert np.array_equal(_select(q, bounds, table, lens, top, bs), _want(q, bounds, table, lens, top, bs))
 
 
-@pytest.mark.parametrize("rows", [1, 4, 9, 19, 38, 76, 200])
+@pytest.mark.parametrize("rows", [1, 4, 9, 19, 28, 38, 45, 60, 76, 100, 200])
 def test_select_is_the_same_for_every_split(rows):
     """As many CTAs a row as the number of rows allows: one to sixteen of them."""
     d, bs, n, top = 64, 16, 700, 50
@@ -309,7 +333,7 @@ def test_sparse_lists_of_any_kind(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("rows,top", [(1, 300), (3, 129), (10, 64), (40, 64), (150, 64), (400, 40)])
+@pytest.mark.parametrize("rows,top", [(1, 300), (3, 129), (10, 64), (28, 300), (40, 64), (90, 64), (120, 40), (150, 64), (200, 40), (400, 40)])
 def test_sparse_for_every_split(dtype, rows, top):
     """One to sixteen CTAs a row; lists longer than a warp looks up at once."""
     d, bs = 64, 16
