@@ -115,7 +115,19 @@ __device__ __forceinline__ void choice_sync()
         __syncthreads();
 }
 
-// The need-th largest of the keys in [lo, hi] (need >= 1, at most as many as there are).
+// f(key, its index) for four neighbouring keys of a row in shared memory (16-byte aligned, n rounded
+// up to 4 of them, 0 behind the last).
+template <typename F>
+__device__ __forceinline__ void each4(const uint32_t *key, int i, const F &f)
+{
+    const uint4 k = *reinterpret_cast<const uint4 *>(key + i);
+    f(k.x, i);
+    f(k.y, i + 1);
+    f(k.z, i + 2);
+    f(k.w, i + 3);
+}
+
+// The need-th largest of the keys in [lo, hi] (need >= 1, at most as many as there are; lo >= 1).
 // `tid` counts the threads of the W warps.
 template <int W>
 __device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint32_t need, uint32_t lo, uint32_t hi,
@@ -128,11 +140,11 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint
         for (int i = tid; i < Choice<W>::BINS; i += T) sh.hist[i] = 0;
         if (tid == 0) sh.listed = 0;
         choice_sync<W>();
-#pragma unroll 4
-        for (int i = tid; i < n; i += T) {
-            const uint32_t k = key[i];
-            if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1u);
-        }
+#pragma unroll 2
+        for (int i = 4 * tid; i < n; i += 4 * T)
+            each4(key, i, [&](uint32_t k, int) {
+                if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1u);
+            });
         choice_sync<W>();
         // sums from the top bin down: thread t has bins PER * t ..
         uint32_t bin[PER], sum = 0;
@@ -169,11 +181,11 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint
         if (shift == 0) return lo; // a bin is one key
         hi = min(hi, lo + ((1u << shift) - 1));
         if (in <= 32) { // few enough to look at one by one
-#pragma unroll 4
-            for (int i = tid; i < n; i += T) {
-                const uint32_t k = key[i];
-                if (k >= lo && k <= hi) sh.list[atomicAdd(&sh.listed, 1u)] = k;
-            }
+#pragma unroll 2
+            for (int i = 4 * tid; i < n; i += 4 * T)
+                each4(key, i, [&](uint32_t k, int) {
+                    if (k >= lo && k <= hi) sh.list[atomicAdd(&sh.listed, 1u)] = k;
+                });
             choice_sync<W>();
             if (warp == 0) {
                 const uint32_t k = lane < in ? sh.list[lane] : 0;
@@ -271,12 +283,15 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
 {
     const int lane = tid & 31, warp = tid >> 5, n = r.n, need = r.need;
     uint32_t least = 0xffffffffu, most = 0;
-#pragma unroll 4
-    for (int i = tid; i < n; i += 32 * W) { // scores to keys
-        const uint32_t k = key_of(__uint_as_float(key[i]));
-        key[i] = k;
-        least = min(least, k);
-        most = max(most, k);
+#pragma unroll 2
+    for (int i = 4 * tid; i < n; i += 128 * W) { // scores to keys
+        uint32_t k[4];
+        each4(key, i, [&](uint32_t x, int j) {
+            k[j - i] = j < n ? key_of(__uint_as_float(x)) : 0u;
+            if (j < n) least = min(least, k[j - i]);
+            most = max(most, k[j - i]);
+        });
+        *reinterpret_cast<uint4 *>(key + i) = make_uint4(k[0], k[1], k[2], k[3]);
     }
     least = __reduce_min_sync(kFull, least);
     most = __reduce_max_sync(kFull, most);
@@ -302,17 +317,17 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
         low = key_of(cut - r.width);
         high = key_of(cut + r.width);
     }
-    // each warp has a run of a multiple of 32 keys, so that places follow from counts
-    const int per = ((n + 32 * W - 1) / (32 * W)) * 32, i0 = warp * per, i1 = min(n, i0 + per);
+    // each warp has a run of a multiple of 128 keys, so that places follow from counts
+    const int per = ((n + 128 * W - 1) / (128 * W)) * 128, i0 = warp * per, i1 = min(n, i0 + per);
     int sure = 0, open = 0, sure_before = 0, open_before = 0;
     for (int pass = 0;; ++pass) {
         int mine_sure = 0, mine_open = 0;
-#pragma unroll 4
-        for (int i = i0 + lane; i < i1; i += 32) {
-            const uint32_t k = key[i];
-            mine_sure += k > high;
-            mine_open += k >= low && k <= high;
-        }
+#pragma unroll 2
+        for (int i = i0 + 4 * lane; i < i1; i += 128)
+            each4(key, i, [&](uint32_t k, int) {
+                mine_sure += k > high;
+                mine_open += k >= low && k <= high;
+            });
         mine_sure = __reduce_add_sync(kFull, mine_sure);
         mine_open = __reduce_add_sync(kFull, mine_open);
         if (W > 1) {
@@ -378,16 +393,43 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
         choice_sync<W>();
     }
     const int quota = need - sure;
+    const uint32_t below = (1u << lane) - 1;
     int place = sure_before + min(open_before, quota), ties = open_before;
-#pragma unroll 4
-    for (int i = i0 + lane; i - lane < i1; i += 32) {
-        const uint32_t k = i < i1 ? key[i] : 0;
-        const uint32_t eq = __ballot_sync(kFull, i < i1 && k >= low && k <= high), below = (1u << lane) - 1;
-        const bool in = i < i1 && (k > high || (((eq >> lane) & 1) && ties + __popc(eq & below) < quota));
-        const uint32_t chosen = __ballot_sync(kFull, in);
-        if (in) out[place + __popc(chosen & below)] = r.first + i;
-        place += __popc(chosen);
-        ties += __popc(eq);
+    for (int i = i0 + 4 * lane; i - 4 * lane < i1; i += 128) {
+        bool in[4] = {false, false, false, false}, eq[4] = {false, false, false, false};
+        if (i < i1)
+            each4(key, i, [&](uint32_t k, int j) {
+                in[j - i] = k > high;
+                eq[j - i] = k >= low && k <= high;
+            });
+        if (open == quota) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) in[u] |= eq[u];
+        } else { // the first `quota` of the open ones
+            uint32_t m[4];
+            int rank = ties;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                m[u] = __ballot_sync(kFull, eq[u]);
+                rank += __popc(m[u] & below);
+                ties += __popc(m[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                in[u] |= eq[u] && rank < quota;
+                rank += eq[u];
+            }
+        }
+        int to = place;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t m = __ballot_sync(kFull, in[u]);
+            to += __popc(m & below);
+            place += __popc(m);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (in[u]) out[to++] = r.first + i + u;
     }
 }
 
@@ -649,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
 {
     constexpr int W = TILE == 1 ? kWarps : 1; // warps that choose together
     constexpr int ROW = (int)sizeof(T) * D + kPad;
-    extern __shared__ uint32_t keys[]; // [tile][max_blocks_per_seq], then the rows of q
+    extern __shared__ __align__(16) uint32_t keys[]; // [tile][max_blocks_per_seq, a multiple of 4], then the rows of q
     __shared__ Shared sh;
     __shared__ Choice<W> choice[kWarps / W];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -685,13 +727,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
             at.skip = false;
         }
     }
-    const int cap = a.max_blocks_per_seq, need = a.top_k - a.first - a.last;
+    const int cap = a.max_blocks_per_seq, row_keys = (cap + 3) & ~3, need = a.top_k - a.first - a.last;
     const int last_seen = at.pos + count - 1 < 0 ? 0 : (at.pos + count - 1) / a.block_size + 1; // by the last token
     const bool nothing = at.skip || last_seen <= a.top_k || need == 0; // to be scored
     if (nothing) {
         if (cluster) cluster_wait();
     } else {
-        uint8_t *q_rows = reinterpret_cast<uint8_t *>(keys + (size_t)tile * cap + (-(size_t)tile * cap & 3));
+        uint8_t *q_rows = reinterpret_cast<uint8_t *>(keys + (size_t)tile * row_keys);
         const T *q = static_cast<const T *>(a.q) + ((size_t)t * a.num_heads + (size_t)h * a.group) * D;
         Scoring s;
         s.table = a.block_table + (size_t)at.req * cap + a.first;
@@ -701,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         s.heads_log2 = heads_log2;
         s.q = smem_u32(q_rows);
         s.keys = cluster_addr(keys, 0);
-        s.stride = cap * 4;
+        s.stride = row_keys * 4;
         // rows of q, 16 bytes a thread; then the largest |q| of each channel
         constexpr int PIECES = (int)sizeof(T) * D / 16;
         const int rows = count << heads_log2;
@@ -775,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         r.need = need;
         // 2 E, and the rounding of S
         r.width = (sizeof(T) == 2 ? (D / 16 + 2) * 0x1.02p-21f : (D / 16 + 6) * 0x1.02p-23f) * __uint_as_float(sh.mag);
-        choose<T, D, W>(keys + (size_t)i * cap, r, out + a.first, a, choice[W == 1 ? warp : 0], wt);
+        choose<T, D, W>(keys + (size_t)i * row_keys, r, out + a.first, a, choice[W == 1 ? warp : 0], wt);
     }
 }
 
@@ -819,7 +861,7 @@ int launch_tile(const SelectArgs &a, cudaStream_t s)
     const long long rows = (long long)a.total_q * a.num_kv_heads;
     const int heads_log2 = a.group > 4 ? 3 : a.group > 2 ? 2 : a.group > 1 ? 1 : 0;
     const size_t row = sizeof(T) * D + kPad;
-    auto smem_of = [&](int tile) { return (size_t)tile * a.max_blocks_per_seq * 4 + 16 + ((size_t)(((tile << heads_log2) + 7) & ~7) + 1) * row; };
+    auto smem_of = [&](int tile) { return (size_t)tile * ((a.max_blocks_per_seq + 3) & ~3) * 4 + ((size_t)(((tile << heads_log2) + 7) & ~7) + 1) * row; };
     // Chunks: tiles of as many tokens as requests have on average, and shared memory holds twice an SM.
     int tile = 1;
     if (a.cu_q != nullptr)
