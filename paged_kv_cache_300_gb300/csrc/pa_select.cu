@@ -44,7 +44,7 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kGroup = 8;   // most query heads of a kv head
-constexpr int kTile = 16;   // most tokens of a CTA
+constexpr int kTile = 16;   // most tokens of a CTA: a warp chooses for two
 constexpr int kPad = 64;    // bytes behind a staged q row: neighbouring rows on other banks
 
 // Order-preserving map of floats to integers; a NaN is above everything, 0 is no float's.
@@ -867,10 +867,10 @@ int launch_tile(const SelectArgs &a, cudaStream_t s)
     if (a.cu_q != nullptr)
         while (tile < kTile && smem_of(2 * tile) <= 100 * 1024 && a.total_q >= 2ll * tile * a.batch) tile *= 2;
     auto units_of = [&](int t) { return t == 1 ? rows : (a.total_q / t + (long long)a.batch) * a.num_kv_heads; };
-    // .. or of half as many, where those fill the GPU by themselves and these do not (462 tokens of 3
-    // requests, 5 kv heads: tiles of 16 25 us, of 8 19 us; 485 of 5, 8 kv heads: 56 and 59).
-    const long long fill = 2ll * num_sms(), half = units_of(tile / 2 + (tile == 1));
-    if (tile > 1 && units_of(tile) < 3 * fill / 4 && half >= 3 * fill / 4 && half <= fill) tile /= 2;
+    const long long fill = 2ll * num_sms();
+    // .. 16 only where there are several for every place: they read the bounds half as often, but take longer
+    // (565 tokens, 8 kv heads: 53.4 us, with 8 51.3; 4885 tokens: 326 and 382).
+    if (tile == kTile && units_of(tile) < 2 * fill) tile /= 2;
     // Few rows or tiles: a cluster of CTAs each, as many as are resident at a time (two an SM)
     // while each warp has a tile of 16 blocks.
     const long long fit = std::min<long long>(fill / units_of(tile), (a.max_blocks_per_seq + 16 * kWarps - 1) / (16 * kWarps));

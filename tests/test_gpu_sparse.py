@@ -95,7 +95,7 @@ def test_select_for_chunks(dtype, d, bs, hq, hkv, top):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("d,bs,hq,hkv,first,last", [(64, 16, 32, 8, 1, 1), (128, 16, 24, 24, 0, 2), (64, 32, 36, 18, 2, 0), (128, 16, 48, 16, 1, 1),
                                                     (64, 16, 40, 8, 1, 1), (128, 32, 64, 8, 0, 0)])
-@pytest.mark.parametrize("tokens", [800, 210])
+@pytest.mark.parametrize("tokens", [800, 210, 1500])
 def test_select_for_tiles_of_tokens(dtype, d, bs, hq, hkv, first, last, tokens):
     """Enough tokens a request for CTAs that take up to 16 of them: requests that end
     inside a tile, single tokens between, queries before the first key, rows whose blocks
@@ -133,7 +133,7 @@ def test_select_for_tiles_of_tokens(dtype, d, bs, hq, hkv, first, last, tokens):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("batch,hkv,part", [(3, 2, 25), (2, 1, 70), (5, 3, 4)])
+@pytest.mark.parametrize("batch,hkv,part", [(3, 2, 25), (2, 1, 70), (5, 3, 4), (2, 2, 9)])
 def test_select_for_tiles_on_clusters(dtype, batch, hkv, part):
     """Few tiles of tokens over long contexts: a cluster of CTAs for each, in which the first
     chooses; tiles that hold nothing among them."""
