@@ -30,6 +30,11 @@
 //   u the |q| of a head or, for tiles of tokens, the largest |q| of all their heads (one column more).  (fp32: D / 16 + 5
 //   roundings of 2^-24, within the same.)  L1(q) max|b| costs no product but is several times
 //   as much, and then every other row needs exact scores, which take longer than all the rest.
+//
+// Measured (one GB300): 96 requests of 4096 to 32768 tokens, 64 / 8 heads of 128, 128 of their blocks of 16: 87.5 us
+// for 451 MB; 7 TB/s while all CTAs score, less where some choose (4 us a row) and while the last rows end (20 us).
+// 565 tokens of 5 chunks, 32 / 8 heads, 64 of up to 750 blocks: 49 us, bound by the latency of two CTAs an SM (the tensor
+// pipe is 12% busy, issue slots 31%): half of it scores, half chooses.  One token of 313 blocks 6.7 us.
 #include <algorithm>
 #include <limits.h>
 #include <type_traits>
