@@ -505,8 +505,8 @@ int pa_cache_append_rotary(const void *q, const void *k, const void *v, const in
  * max_blocks_per_seq <= 49152; top_k at most 2^20; num_heads / num_kv_heads <= 8; head_dim 64 or 128;
  * total_q * num_kv_heads < 2^27.
  * A needed block_table entry that is no block sets PA_DEVERR_BAD_BLOCK, a length beyond
- * the table PA_DEVERR_OVERFLOW, cu_seq_lens_q that does not start at 0 or decreases behind
- * a row's request PA_DEVERR_BAD_CU: the rows are -1.
+ * the table PA_DEVERR_OVERFLOW: the rows are -1.  cu_seq_lens_q that does not start at 0 or
+ * decreases sets PA_DEVERR_BAD_CU; rows are then -1, left as they were or another request's.
  */
 int pa_select_blocks(const void *q, const void *bounds, const int32_t *block_table,
                      const int32_t *seqlens_k, const int32_t *cu_seq_lens_q, int32_t *selected,
@@ -525,8 +525,8 @@ int pa_select_blocks(const void *q, const void *bounds, const int32_t *block_tab
  * dtype PA_BF16 or PA_F32; num_heads / num_kv_heads <= 8; head_dim 64 or 128; PA_BF16: block_size
  * a multiple of 16; top_k at most 2^20, top_k * block_size < 2^30,
  * total_q * num_kv_heads < 2^27.  A needed block_table entry that is no block sets PA_DEVERR_BAD_BLOCK, a length
- * beyond the table PA_DEVERR_OVERFLOW, a bad cu_seq_lens_q PA_DEVERR_BAD_CU: the rows are
- * zeros.  Needs no workspace; calls share nothing.
+ * beyond the table PA_DEVERR_OVERFLOW: the rows are zeros; a bad cu_seq_lens_q as above.
+ * Needs no workspace; calls share nothing.
  */
 int pa_sparse(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
               const int32_t *seqlens_k, const int32_t *cu_seq_lens_q, const int32_t *selected,

@@ -250,8 +250,8 @@ __device__ __forceinline__ void load_angles(const RotaryArgs &a, const Lane &l, 
         const float *row = a.cos_sin + (size_t)p * a.rotary_dim + 8 * l.c;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float4 c = __ldg(reinterpret_cast<const float4 *>(row) + j);
-            const float4 s = __ldg(reinterpret_cast<const float4 *>(row + half) + j);
+            const float4 c = reinterpret_cast<const float4 *>(row)[j];
+            const float4 s = reinterpret_cast<const float4 *>(row + half)[j];
             w.c[4 * j] = c.x, w.c[4 * j + 1] = c.y, w.c[4 * j + 2] = c.z, w.c[4 * j + 3] = c.w;
             w.s[4 * j] = s.x, w.s[4 * j + 1] = s.y, w.s[4 * j + 2] = s.z, w.s[4 * j + 3] = s.w;
         }
@@ -262,8 +262,8 @@ __device__ __forceinline__ void load_angles(const RotaryArgs &a, const Lane &l, 
         const uint32_t ax = (l.axes >> (2 * i)) & 3u;
         const int p = ax == 0 ? pos[0] : ax == 1 ? pos[1] : ax == 2 ? pos[2] : pos[3];
         const float *at = a.cos_sin + (size_t)p * a.rotary_dim + 8 * l.c + i;
-        w.c[i] = __ldg(at);
-        w.s[i] = __ldg(at + half);
+        w.c[i] = *at;
+        w.s[i] = at[half];
     }
 }
 

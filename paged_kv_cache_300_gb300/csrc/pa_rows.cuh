@@ -6,20 +6,34 @@
 
 namespace pa {
 
-// Largest r in [0, n] with cu[r] <= t, -1 if there is none; the whole warp
-// searches, 32 entries a step (one step up to 32 requests, two up to 1024).
-__device__ __forceinline__ int find_request(const int32_t *cu, int n, int t, int lane)
+// All of these read with ordinary loads what the kernel before may have written: a launch with
+// programmatic dependence begins while that one runs, when read-only loads may keep old lines.
+
+// Largest r in [0, n] with value(r) <= t, -1 if there is none; value does not decrease.  The whole
+// warp searches, 32 values a step (one step up to 32 of them, two up to 1024).
+template <typename Value>
+__device__ __forceinline__ int find_last(const Value &value, int n, long long t, int lane)
 {
     int lo = 0, count = n + 1;
     while (true) {
         const int step = (count + 31) / 32, at = lane * step;
-        const uint32_t m = __ballot_sync(0xffffffffu, at < count && __ldg(cu + lo + at) <= t);
+        const uint32_t m = __ballot_sync(0xffffffffu, at < count && value(lo + at) <= t);
         if (m == 0) return lo == 0 ? -1 : lo; // lo > 0 was a hit of the step before
         const int hit = 31 - __clz(m);
         lo += hit * step;
         count = min(step, count - hit * step);
         if (step == 1) return lo;
     }
+}
+
+// The first CTA's threads look over the cumulative lengths.
+template <typename Args>
+__device__ __forceinline__ void check_lengths(const Args &a)
+{
+    if (a.cu_q == nullptr || blockIdx.x != 0) return;
+    bool bad = threadIdx.x == 0 && a.cu_q[0] != 0;
+    for (int i = threadIdx.x; i < a.batch; i += blockDim.x) bad |= a.cu_q[i + 1] < a.cu_q[i];
+    if (bad) flag_error(a.dev_err, PA_DEVERR_BAD_CU);
 }
 
 // Row t of the packed queries: its request and the last position it sees.
@@ -37,20 +51,20 @@ __device__ __forceinline__ QueryRow query_row(const Args &a, int t, int lane)
     QueryRow q{t, -(1 << 30), 1, false, 0};
     int back = 0; // the request's queries behind row t
     if (a.cu_q != nullptr) {
-        q.req = find_request(a.cu_q, a.batch, t, lane);
+        q.req = find_last([&](int r) { return (long long)a.cu_q[r]; }, a.batch, t, lane);
         if (q.req == a.batch) {
             q.skip = true;
             return q;
         }
-        const int c1 = q.req >= 0 ? __ldg(a.cu_q + q.req + 1) : 0;
-        if (q.req < 0 || c1 <= t || __ldg(a.cu_q) != 0) {
+        const int c1 = q.req >= 0 ? a.cu_q[q.req + 1] : 0;
+        if (q.req < 0 || c1 <= t || a.cu_q[0] != 0) {
             q.err = PA_DEVERR_BAD_CU;
             return q;
         }
         back = c1 - 1 - t;
         q.left = c1 - t;
     }
-    const int kl = __ldg(a.seqlens_k + q.req);
+    const int kl = a.seqlens_k[q.req];
     if (kl == PA_LEFT_OUT) return q;
     if (kl < 0 || (long long)kl > (long long)a.max_blocks_per_seq * a.block_size) {
         q.err = PA_DEVERR_OVERFLOW;

@@ -365,7 +365,7 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
                 if (key[i] >= low && key[i] <= high) sh.list[atomicAdd(&sh.listed, 1u)] = i;
             choice_sync<W>();
             for (int c = warp; c < open; c += W) {
-                const T *bounds = r.bounds + (size_t)__ldg(r.table + sh.list[c]) * a.num_kv_heads * 2 * D;
+                const T *bounds = r.bounds + (size_t)r.table[sh.list[c]] * a.num_kv_heads * 2 * D;
                 const float x = (float)(exact_score<T, D>(r.q, bounds, a.group, lane) - (double)cut);
                 if (lane == 0) sh.exact[c] = x;
             }
@@ -387,7 +387,7 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
             while (todo) {
                 const int b = __ffs(todo) - 1;
                 todo &= todo - 1;
-                const T *bounds = r.bounds + (size_t)__ldg(r.table + (i - lane) + b) * a.num_kv_heads * 2 * D;
+                const T *bounds = r.bounds + (size_t)r.table[(i - lane) + b] * a.num_kv_heads * 2 * D;
                 const uint32_t exact = key_of((float)(exact_score<T, D>(r.q, bounds, a.group, lane) - (double)cut));
                 if (lane == b) now = exact;
             }
@@ -471,7 +471,7 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
     // the lane's entry of a tile's 16 blocks (a row behind the last reads block 0 and is left out)
     auto entry_of = [&](int tile) {
         const int j = tile * 16 + (lane & 15);
-        const int e = tile < tiles && j < n ? __ldg(s.table + j) : 0;
+        const int e = tile < tiles && j < n ? s.table[j] : 0;
         const bool wrong = e < 0 || e >= a.num_blocks;
         if (wrong) bad = min(bad, j);
         return wrong ? 0 : e;
@@ -483,10 +483,10 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
         uint4 lo[NC][2], hi[NC][2];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            lo[i][0] = __ldg(reinterpret_cast<const uint4 *>(r0 + i * 32));
-            lo[i][1] = __ldg(reinterpret_cast<const uint4 *>(r1 + i * 32));
-            hi[i][0] = __ldg(reinterpret_cast<const uint4 *>(r0 + D + i * 32));
-            hi[i][1] = __ldg(reinterpret_cast<const uint4 *>(r1 + D + i * 32));
+            lo[i][0] = *reinterpret_cast<const uint4 *>(r0 + i * 32);
+            lo[i][1] = *reinterpret_cast<const uint4 *>(r1 + i * 32);
+            hi[i][0] = *reinterpret_cast<const uint4 *>(r0 + D + i * 32);
+            hi[i][1] = *reinterpret_cast<const uint4 *>(r1 + D + i * 32);
         }
         entry = entry_of(tile + step);
         {   // S, of each head where there are 8 columns at most, else of the largest |q|
@@ -580,13 +580,13 @@ __device__ __forceinline__ void score_blocks_f32(const SelectArgs &a, const Scor
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int j = tile * kBatch + b;
-            int e = j < n ? __ldg(s.table + j) : 0;
+            int e = j < n ? s.table[j] : 0;
             if (e < 0 || e >= a.num_blocks) {
                 bad = min(bad, j);
                 e = 0;
             }
-            *reinterpret_cast<Vec *>(lo[b]) = __ldg(reinterpret_cast<const Vec *>(bounds + (size_t)e * block));
-            *reinterpret_cast<Vec *>(hi[b]) = __ldg(reinterpret_cast<const Vec *>(bounds + (size_t)e * block + D));
+            *reinterpret_cast<Vec *>(lo[b]) = *reinterpret_cast<const Vec *>(bounds + (size_t)e * block);
+            *reinterpret_cast<Vec *>(hi[b]) = *reinterpret_cast<const Vec *>(bounds + (size_t)e * block + D);
         }
         float u[E];
         row_of(s.tokens << s.heads_log2, u);
@@ -643,45 +643,24 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
         score_blocks_f32<D, 4>(a, s, first, step, lane, mag, bad);
 }
 
-// Tile `unit` of those that the requests' queries make up, `tile` rows each but the last of
-// a request: rows [first, first + count) of the packed queries.  count 0: none.  With
-// cumulative lengths that are none, err, and the unit-th tile of all rows.
+// Tile `unit` of the packed queries: rows [first, first + count) of one request, `tile` of them but at
+// its end; count 0: none.  Request r, with rows c0 to c1, has the tiles c0 / tile + r up to
+// c1 / tile + r: one more than it may need, and found without the sums of those before.
 struct TileRows {
-    int first, count, err;
+    int first, count;
 };
 __device__ __forceinline__ TileRows tile_rows(const SelectArgs &a, int unit, int tile, int lane)
 {
-    TileRows r{0, 0, __ldg(a.cu_q) != 0 ? PA_DEVERR_BAD_CU : 0};
-    int before = 0;
-    bool bad = false;
-#pragma unroll 2
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        const int b = b0 + lane;
-        const int c0 = b < a.batch ? __ldg(a.cu_q + b) : 0, c1 = b < a.batch ? __ldg(a.cu_q + b + 1) : 0;
-        bad |= c1 < c0;
-        const int mine = c1 > c0 ? (c1 - c0 + tile - 1) / tile : 0;
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(kFull, incl, o);
-            if (lane >= o) incl += x;
-        }
-        const uint32_t hit = __ballot_sync(kFull, unit >= before + incl - mine && unit < before + incl);
-        if (hit) {
-            const int from = __ffs(hit) - 1, t = c0 + (unit - (before + incl - mine)) * tile;
-            r.first = __shfl_sync(kFull, t, from);
-            r.count = __shfl_sync(kFull, min(tile, c1 - t), from);
-        }
-        before += __shfl_sync(kFull, incl, 31);
+    if (a.cu_q[0] != 0) { // no row has a request: all are refused
+        const long long t = (long long)unit * tile;
+        return {(int)min(t, (long long)a.total_q), (int)max(0ll, min((long long)tile, a.total_q - t))};
     }
-    if (r.err || __any_sync(kFull, bad)) {
-        r.err = PA_DEVERR_BAD_CU;
-        r.first = unit * tile;
-        r.count = max(0, min(tile, a.total_q - r.first));
-    } else if (r.first + r.count > a.total_q) {
-        r.count = max(0, a.total_q - r.first);
-    }
-    return r;
+    const int r = find_last([&](int i) { return (long long)a.cu_q[i] / tile + i; }, a.batch, unit, lane);
+    if (r < 0 || r >= a.batch) return {0, 0};
+    const int c0 = a.cu_q[r], c1 = min(a.cu_q[r + 1], a.total_q);
+    const long long first = c0 + (long long)(unit - (c0 / tile + r)) * tile;
+    if (c0 < 0 || first < c0 || first >= c1) return {0, 0};
+    return {(int)first, min(tile, c1 - (int)first)};
 }
 
 struct Shared {
@@ -710,6 +689,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
     grid_dep_trigger();
     if (cluster) cluster_arrive();
     grid_dep_wait();
+    check_lengths(a);
+    __syncwarp();
 
     const int unit = (int)(blockIdx.x / ctas);
     const int h = unit % a.num_kv_heads; // heads of a tile side by side
@@ -726,11 +707,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         t = r.first;
         count = r.count;
         at = query_row(a, t, lane);
-        if (r.err) {
-            at.pos = -(1 << 30);
-            at.err = r.err;
-            at.skip = false;
-        }
     }
     const int cap = a.max_blocks_per_seq, row_keys = (cap + 3) & ~3, need = a.top_k - a.first - a.last;
     const int last_seen = at.pos + count - 1 < 0 ? 0 : (at.pos + count - 1) / a.block_size + 1; // by the last token

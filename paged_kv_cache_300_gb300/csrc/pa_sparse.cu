@@ -171,14 +171,14 @@ __device__ __forceinline__ int look_up(const SparseArgs &a, const int32_t *list,
     for (int k = 0; k < kList / 32; ++k) {
         const long long u = u0 + (long long)(k * 32 + lane) * stride;
         const int e = u < units ? (int)u / per_block : 0, part = u < units ? (int)u - e * per_block : 0;
-        const int lb = u < units ? __ldg(list + e) : -1;
+        const int lb = u < units ? list[e] : -1;
         found[k] = make_int2(part * UNIT, lb);
     }
 #pragma unroll
     for (int k = 0; k < kList / 32; ++k) {
         const int lb = found[k].y, part = found[k].x;
         use[k] = lb >= 0 && lb <= last_block && (long long)lb * a.block_size + part <= pos;
-        const int phys = use[k] ? __ldg(table + lb) : 0;
+        const int phys = use[k] ? table[lb] : 0;
         const bool wrong = use[k] && (phys < 0 || phys >= a.num_blocks);
         bad |= wrong;
         use[k] &= !wrong;
@@ -237,6 +237,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     __syncwarp();
     grid_dep_trigger();
     grid_dep_wait();
+    check_lengths(a);
+    // what the kernel before has stored in the caches is read by copies
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    __syncwarp();
 
     const int group = warp / W, tr = tid % (32 * W);
     const int row = W == kWarps ? (int)(blockIdx.x / ctas) : (int)blockIdx.x * (kWarps / W) + group;
@@ -446,6 +450,8 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
     const int rank = ctas > 1 ? (int)cluster_rank() : 0;
     grid_dep_trigger();
     grid_dep_wait();
+    check_lengths(a);
+    __syncwarp();
     const int row = blockIdx.x / ctas, t = row / a.num_kv_heads, h = row % a.num_kv_heads, G = a.group;
     const QueryRow at = query_row(a, t, lane);
     if (at.skip) return;

@@ -128,8 +128,31 @@ def test_select_for_tiles_of_tokens(dtype, d, bs, hq, hkv, first, last, tokens):
     assert (got[:cu[7]][rows] == -1).all() and np.array_equal(got[:cu[7]][~rows], want[:cu[7]][~rows])
     for bad in ([1] + cu[1:].tolist(), cu[:3].tolist() + [cu[-1] + 3] + cu[4:].tolist()):
         err.zero_()
-        got = _select(q, bounds, table, i32(lens), top, bs, first, last, i32(bad), err)
-        assert err.item() == pa.DEVERR_BAD_CU
+        _select(q, bounds, table, i32(lens), top, bs, first, last, i32(bad), err)
+        assert err.item() & pa.DEVERR_BAD_CU  # (rows may be taken for another request's, and fail as such)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("batch,most", [(75, 9), (1100, 6), (40, 60)])
+def test_select_for_tiles_of_many_requests(dtype, batch, most):
+    """More requests than a warp looks at in one step; with nothing, one token or chunks, and
+    a token behind the last that belongs to none."""
+    d, bs, top, hkv = 64, 16, 4, 2
+    rng = np.random.default_rng(batch)
+    new = rng.integers(0, most + 1, batch)
+    new[rng.random(batch) < 0.1] = 0
+    lens = new + rng.integers(0, 300, batch)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    assert cu[-1] >= 2 * batch
+    nb = 500
+    table = torch.from_numpy(rng.integers(0, nb, (batch, 25)).astype(np.int32))
+    bounds = _bounds(5, nb, hkv, d, dtype)
+    q = torch.randn(int(cu[-1]) + 1, 6, d, generator=torch.Generator().manual_seed(8)).to(dtype)
+    lens = torch.from_numpy(lens.astype(np.int32))
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = _select(q, bounds, table, lens, top, bs, cu=torch.from_numpy(cu), dev_err=err)
+    assert err.item() == 0 and (got[-1] == -9).all()
+    assert np.array_equal(got[:-1], _want(q, bounds, table, lens, top, bs, cu=torch.from_numpy(cu))[:-1])
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
