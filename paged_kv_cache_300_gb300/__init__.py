@@ -723,9 +723,11 @@ def _rotary_table(index, positions, cos_sin, pair_axis, tokens):
         axes, n = 1, shape[0]
     else:
         axes, n = shape
-    if n != tokens or not _fits(index, torch.int32, positions):
+    if n != tokens or positions.dtype is not torch.int32 or positions.get_device() != index or \
+            not positions.is_contiguous():
         _refuse(index, torch.int32, positions=positions)
-    if not _fits(index, torch.float32, cos_sin):
+    if cos_sin.dtype is not torch.float32 or cos_sin.get_device() != index or \
+            not cos_sin.is_contiguous():
         _refuse(index, torch.float32, cos_sin=cos_sin)
     if rows | axes > 0x7FFFFFFF:
         _too_large()
@@ -753,6 +755,10 @@ def pa_rotary(q, k, positions, cos_sin, q_out=None, k_out=None, interleaved: boo
     index, dtype = some.get_device(), some.dtype
     if index < 0:
         raise ValueError("all tensors must live on a CUDA device")
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return pa_rotary(q, k, positions, cos_sin, q_out, k_out, interleaved, pair_axis, dev_err,
+                             stream)
     dt = _DTYPES.get(dtype)
     if dt is None:
         dt = _dtype(some)
@@ -771,8 +777,12 @@ def pa_rotary(q, k, positions, cos_sin, q_out=None, k_out=None, interleaved: boo
     pos, table, rot, rows, axes, host = _rotary_table(index, positions, cos_sin, pair_axis, tokens)
     if dev_err is not None and not _fits(index, torch.int32, dev_err):
         _refuse(index, torch.int32, dev_err=dev_err)
-    _launch("pa_rotary", index, stream, qp, kp, pos, table, qo, ko, tokens, hq, hk, d, rot, rows,
-            axes, host, interleaved, qs, ks, qos, kos, dt, _addr(dev_err))
+    rc = (_lib or load()).pa_rotary(
+        qp, kp, pos, table, qo, ko, tokens, hq, hk, d, rot, rows, axes, host, interleaved, qs, ks, qos,
+        kos, dt, None if dev_err is None else dev_err.data_ptr(),
+        _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise PAError("pa_rotary", rc)
     return q_out, k_out
 
 
@@ -790,6 +800,10 @@ def pa_cache_append_rotary(q, k, v, slot_map, k_cache, v_cache, positions=None, 
     index, dtype, tokens = k_cache.get_device(), k_cache.dtype, k.shape[0]
     if index < 0:
         raise ValueError("all tensors must live on a CUDA device")
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return pa_cache_append_rotary(q, k, v, slot_map, k_cache, v_cache, positions, cos_sin, q_out,
+                                          bounds, interleaved, pair_axis, dev_err, stream)
     dt = _DTYPES.get(dtype)
     if dt is None:
         dt = _dtype(k_cache)
@@ -815,9 +829,13 @@ def pa_cache_append_rotary(q, k, v, slot_map, k_cache, v_cache, positions=None, 
         rot = rows = axes = 0
     else:
         pos, table, rot, rows, axes, host = _rotary_table(index, positions, cos_sin, pair_axis, tokens)
-    _launch("pa_cache_append_rotary", index, stream, qp, kp, vp, slot_map.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), _addr(bounds), pos, table, qo, tokens, hq, hkv, d,
-            rot, rows, axes, host, interleaved, qs, ks, vs, qos, nb, bs, dt, _addr(dev_err))
+    rc = (_lib or load()).pa_cache_append_rotary(
+        qp, kp, vp, slot_map.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        None if bounds is None else bounds.data_ptr(), pos, table, qo, tokens, hq, hkv, d, rot, rows, axes,
+        host, interleaved, qs, ks, vs, qos, nb, bs, dt, None if dev_err is None else dev_err.data_ptr(),
+        _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise PAError("pa_cache_append_rotary", rc)
     return q_out
 
 
@@ -851,6 +869,10 @@ def pa_select_blocks(q, bounds, block_table, seqlens_k, top_k: int, block_size: 
     dt = _DTYPES.get(dtype)
     if dt is None:
         dt = _dtype(q)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return pa_select_blocks(q, bounds, block_table, seqlens_k, top_k, block_size, first_blocks,
+                                    last_blocks, cu_seq_lens_q, selected, dev_err, stream)
     nb, hkv, two, d2 = bounds.shape
     if two != 2 or d2 != d or not _fits(index, dtype, q, bounds):
         _refuse(index, dtype, q=q, bounds=bounds)
@@ -861,9 +883,14 @@ def pa_select_blocks(q, bounds, block_table, seqlens_k, top_k: int, block_size: 
     elif selected.shape != (tq, hkv, top_k):
         raise ValueError("selected must be [Tq, Hkv, top_k]")
     b, mb = _query_rows(index, tq, block_table, seqlens_k, cu_seq_lens_q, dev_err, selected)
-    _launch("pa_select_blocks", index, stream, q.data_ptr(), bounds.data_ptr(), block_table.data_ptr(),
-            seqlens_k.data_ptr(), _addr(cu_seq_lens_q), selected.data_ptr(), b, tq, hq, hkv, d, nb,
-            block_size, mb, top_k, first_blocks, last_blocks, dt, _addr(dev_err))
+    rc = (_lib or load()).pa_select_blocks(
+        q.data_ptr(), bounds.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(),
+        None if cu_seq_lens_q is None else cu_seq_lens_q.data_ptr(), selected.data_ptr(), b, tq, hq, hkv, d,
+        nb, block_size, mb, top_k, first_blocks, last_blocks, dt,
+        None if dev_err is None else dev_err.data_ptr(),
+        _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise PAError("pa_select_blocks", rc)
     return selected
 
 
@@ -881,6 +908,10 @@ def pa_sparse(q, k_cache, v_cache, block_table, seqlens_k, selected, cu_seq_lens
     dt = _DTYPES.get(dtype)
     if dt is None:
         dt = _dtype(q)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return pa_sparse(q, k_cache, v_cache, block_table, seqlens_k, selected, cu_seq_lens_q, out,
+                             softmax_scale, dev_err, stream)
     nb, bs, hkv, d2 = pool
     if out is None:
         out = _empty(stream, shape, dtype, q.device)
@@ -894,7 +925,12 @@ def pa_sparse(q, k_cache, v_cache, block_table, seqlens_k, selected, cu_seq_lens
     if nb | bs | top_k > 0x7FFFFFFF:
         _too_large()
     b, mb = _query_rows(index, tq, block_table, seqlens_k, cu_seq_lens_q, dev_err, selected)
-    _launch("pa_sparse", index, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            block_table.data_ptr(), seqlens_k.data_ptr(), _addr(cu_seq_lens_q), selected.data_ptr(),
-            out.data_ptr(), b, tq, hq, hkv, d, nb, bs, mb, top_k, dt, softmax_scale, _addr(dev_err))
+    rc = (_lib or load()).pa_sparse(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(),
+        None if cu_seq_lens_q is None else cu_seq_lens_q.data_ptr(), selected.data_ptr(), out.data_ptr(), b,
+        tq, hq, hkv, d, nb, bs, mb, top_k, dt, softmax_scale,
+        None if dev_err is None else dev_err.data_ptr(),
+        _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise PAError("pa_sparse", rc)
     return out
