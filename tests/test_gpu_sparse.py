@@ -320,6 +320,17 @@ def test_sparse_for_single_tokens(dtype, d, bs, hq, hkv, top):
     assert (got[5] == 0).all()
 
 
+@pytest.mark.parametrize("d,bs", [(64, 1), (64, 7), (128, 20), (64, 33)])
+def test_sparse_with_blocks_of_any_size_in_fp32(d, bs):
+    """Blocks that are no whole number of the kernel's units of tokens."""
+    lens = [1, bs, 5 * bs + 1, 30 * bs, 17 * bs + bs // 2, 9]
+    c = make_cache(bs, lens, 2, d, bs, F32)
+    q = torch.randn(len(lens), 6, d, generator=torch.Generator().manual_seed(d)).to(F32)
+    for top in (2, 40):
+        sel = _random_choice(np.random.default_rng(top), lens, 2, bs, top)
+        _check(_attend(c, q, sel), c, q, sel)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("d,bs,hq,hkv", [(128, 16, 8, 2), (64, 32, 7, 1), (128, 16, 3, 3)])
 def test_sparse_for_chunks(dtype, d, bs, hq, hkv):
