@@ -95,17 +95,9 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, uint32_t x)
 {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
 }
-__device__ __forceinline__ float cluster_load(uint32_t addr)
+__device__ __forceinline__ void cluster_store4(uint32_t addr, const float4 &x)
 {
-    float x;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
-    return x;
-}
-__device__ __forceinline__ float4 cluster_load4(uint32_t addr)
-{
-    float4 x;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr) : "memory");
-    return x;
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
 }
 __device__ __forceinline__ void cluster_min(uint32_t addr, uint32_t x)
 {

@@ -109,7 +109,7 @@ struct Choice {
     uint32_t list[32];
     float exact[32];
     uint32_t warp[W][2];
-    uint32_t hist[BINS];
+    alignas(16) uint32_t hist[BINS];
 };
 
 template <int W>
@@ -135,17 +135,26 @@ __device__ __forceinline__ void each4(const uint32_t *key, int i, const F &f)
 
 // The need-th largest of the keys in [lo, hi] (need >= 1, at most as many as there are; lo >= 1).
 // `tid` counts the threads of the W warps.
+// `cleared`: the histogram and the list are empty already, for all threads to see.
+template <int W>
+__device__ __forceinline__ void clear(Choice<W> &sh, int tid)
+{
+    for (int i = 4 * tid; i < Choice<W>::BINS; i += 128 * W) *reinterpret_cast<uint4 *>(&sh.hist[i]) = make_uint4(0, 0, 0, 0);
+    if (tid == 0) sh.listed = 0;
+}
 template <int W>
 __device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint32_t need, uint32_t lo, uint32_t hi,
-                                                Choice<W> &sh, int tid)
+                                                Choice<W> &sh, int tid, bool cleared)
 {
     constexpr int T = 32 * W, PER = Choice<W>::BINS / T;
     const int lane = tid & 31, warp = tid >> 5;
     while (lo < hi) { // at most four times
         const int bits = 32 - __clz(hi - lo), shift = max(bits - Choice<W>::BITS, 0);
-        for (int i = tid; i < Choice<W>::BINS; i += T) sh.hist[i] = 0;
-        if (tid == 0) sh.listed = 0;
-        choice_sync<W>();
+        if (!cleared) {
+            clear(sh, tid);
+            choice_sync<W>();
+        }
+        cleared = false;
 #pragma unroll 2
         for (int i = 4 * tid; i < n; i += 4 * T)
             each4(key, i, [&](uint32_t k, int) {
@@ -155,7 +164,11 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint
         // sums from the top bin down: thread t has bins PER * t ..
         uint32_t bin[PER], sum = 0;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) sum += bin[i] = sh.hist[tid * PER + i];
+        for (int i = 0; i < PER; i += 4) {
+            const uint4 b = *reinterpret_cast<const uint4 *>(&sh.hist[tid * PER + i]);
+            bin[i] = b.x, bin[i + 1] = b.y, bin[i + 2] = b.z, bin[i + 3] = b.w;
+            sum += b.x + b.y + b.z + b.w;
+        }
         uint32_t incl = sum; // of this thread and the lanes above
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -289,6 +302,7 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
 {
     const int lane = tid & 31, warp = tid >> 5, n = r.n, need = r.need;
     uint32_t least = 0xffffffffu, most = 0;
+    clear(sh, tid);
 #pragma unroll 2
     for (int i = 4 * tid; i < n; i += 128 * W) { // scores to keys
         uint32_t k[4];
@@ -316,7 +330,7 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
         choice_sync<W>();
     }
     // keys above `high` are in, and `quota` of those from `low` to `high`
-    uint32_t low = kth_largest<W>(key, n, need, least, most, sh, tid), high = low;
+    uint32_t low = kth_largest<W>(key, n, need, least, most, sh, tid, true), high = low;
     const float cut = value_of(low);
     const bool blurred = fabsf(cut) < INFINITY && r.width > 0.f && r.width < INFINITY;
     if (blurred) {
@@ -395,7 +409,7 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
             if (i < i1) key[i] = now;
         }
         choice_sync<W>();
-        low = high = kth_largest<W>(key, n, need - sure, 1u, 0xfffffffeu, sh, tid);
+        low = high = kth_largest<W>(key, n, need - sure, 1u, 0xfffffffeu, sh, tid, false);
         choice_sync<W>();
     }
     const int quota = need - sure;

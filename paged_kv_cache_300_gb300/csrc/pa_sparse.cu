@@ -95,15 +95,25 @@ __device__ __forceinline__ void row_sync(int group)
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * W) : "memory");
 }
 
-// Joins the partials of the row's W warps, `step` bytes apart, then the cluster's, and writes
-// the row.  `tid` counts the row's threads.
+// What the CTAs of a cluster send one of them: their partials of its share of the channels.
+template <int D>
+struct alignas(16) Inbox {
+    float4 acc[kGroup * D / 4 + 16]; // [CTA][share]
+    float m[16][kGroup], l[16][kGroup];
+};
+
+// Joins the partials of the row's W warps, `step` bytes apart, and writes the row; in a cluster
+// each CTA sends its partial, a share of the channels to each, and joins what it is sent (one barrier;
+// reading the others' partials took another and two round trips).  `tid` counts the row's threads.
 template <typename T, int D, int W>
-__device__ __forceinline__ void finish_row(const void *parts, int step, Part<D> *cta, T *out, int G, int ctas, int rank, int tid,
+__device__ __forceinline__ void finish_row(const void *parts, int step, Inbox<D> *inbox, T *out, int G, int ctas, int rank, int tid,
                                            int group)
 {
+    const int share = (G * D / 4 + ctas - 1) / ctas; // four channels each
     row_sync<W>(group);
-    for (int e = tid * 4; e < G * D; e += W * 128) {
-        const int g = e / D, d = e % D;
+    if (ctas > 1) cluster_wait(); // all CTAs have begun
+    for (int f = tid; f < G * D / 4; f += W * 32) {
+        const int g = f * 4 / D, d = f * 4 % D;
         Joined j;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
@@ -111,41 +121,28 @@ __device__ __forceinline__ void finish_row(const void *parts, int step, Part<D> 
             j.add(*reinterpret_cast<const float4 *>(&p->acc[g][d]), p->m[g], p->l[g]);
         }
         if (ctas == 1) {
-            put(out + e, j.value());
-        } else {
-            *reinterpret_cast<float4 *>(&cta->acc[g][d]) = j.acc;
-            if (d == 0) {
-                cta->m[g] = j.m;
-                cta->l[g] = j.bad ? -1.f : j.l;
-            }
+            put(out + 4 * f, j.value());
+            continue;
+        }
+        const int to = f / share;
+        cluster_store4(cluster_addr(&inbox->acc[rank * share + f - to * share], to), j.acc);
+        if (d / 4 < ctas) { // one of the head's threads for each CTA
+            cluster_store(cluster_addr(&inbox->m[rank][g], d / 4), __float_as_uint(j.m));
+            cluster_store(cluster_addr(&inbox->l[rank][g], d / 4), __float_as_uint(j.bad ? -1.f : j.l));
         }
     }
     if (ctas == 1) return;
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-    for (int e = (rank * kThreads + tid) * 4; e < G * D; e += ctas * kThreads * 4) {
-        const int g = e / D, d = e % D;
+    for (int i = tid; i < share; i += kThreads) {
+        const int f = rank * share + i;
+        if (f >= G * D / 4) break;
+        const int g = f * 4 / D;
         Joined j;
-        for (int c0 = 0; c0 < ctas; c0 += 4) { // the loads of four CTAs in flight
-            float4 x[4];
-            float m[4], l[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int from = min(c0 + c, ctas - 1);
-                x[c] = cluster_load4(cluster_addr(&cta->acc[g][d], from));
-                m[c] = cluster_load(cluster_addr(&cta->m[g], from));
-                l[c] = cluster_load(cluster_addr(&cta->l[g], from));
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c0 + c < ctas) j.add(x[c], m[c], l[c]);
-        }
-        put(out + e, j.value());
+        for (int c = 0; c < ctas; ++c) j.add(inbox->acc[c * share + i], inbox->m[c][g], inbox->l[c][g]);
+        put(out + 4 * f, j.value());
     }
-    __syncwarp();
-    cluster_arrive(); // the others' shared memory stays until all have read it
-    cluster_wait();
 }
 
 // A row that sees nothing, or was refused: zeros.  The same for all CTAs of the row.
@@ -223,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t bars[kWarps][R::STAGES];
     __shared__ int2 lists[kWarps][kList];
-    __shared__ Part<D> cta_part;
+    __shared__ Inbox<D> inbox;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = ctas > 1 ? (int)cluster_rank() : 0;
     uint8_t *ring = smem + warp * R::STAGES * R::UNIT;
@@ -236,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     __syncwarp();
     grid_dep_trigger();
+    if (ctas > 1) cluster_arrive();
     grid_dep_wait();
     check_lengths(a);
     // what the kernel before has stored in the caches is read by copies
@@ -247,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int t = row / a.num_kv_heads, h = row % a.num_kv_heads, G = a.group;
     if (W < kWarps && t >= a.total_q) return;
     const QueryRow at = query_row(a, t, lane);
+    if (ctas > 1 && (at.skip || at.pos < 0)) cluster_wait(); // (the same for the whole cluster)
     if (at.skip) return;
     const size_t off = ((size_t)t * a.num_heads + (size_t)h * G) * D;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + off;
@@ -412,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         part->l[g0] = bad ? -1.f : l0;
         part->l[g0 + 1] = bad ? -1.f : l1;
     }
-    finish_row<__nv_bfloat16, D, W>(smem + group * W * R::STAGES * R::UNIT, R::STAGES * R::UNIT, &cta_part, out, G, ctas, rank, tr,
+    finish_row<__nv_bfloat16, D, W>(smem + group * W * R::STAGES * R::UNIT, R::STAGES * R::UNIT, &inbox, out, G, ctas, rank, tr,
                                     group);
 }
 
@@ -444,16 +443,18 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
     constexpr int E = D / 32, kBatch = 4; // channels a lane, tokens at a time
     using Vec = typename std::conditional<E == 4, float4, float2>::type;
     __shared__ Part<D> parts[kWarps];
-    __shared__ Part<D> cta_part;
+    __shared__ Inbox<D> inbox;
     __shared__ int2 lists[kWarps][kList];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = ctas > 1 ? (int)cluster_rank() : 0;
     grid_dep_trigger();
+    if (ctas > 1) cluster_arrive();
     grid_dep_wait();
     check_lengths(a);
     __syncwarp();
     const int row = blockIdx.x / ctas, t = row / a.num_kv_heads, h = row % a.num_kv_heads, G = a.group;
     const QueryRow at = query_row(a, t, lane);
+    if (ctas > 1 && (at.skip || at.pos < 0)) cluster_wait(); // (the same for the whole cluster)
     if (at.skip) return;
     const size_t off = ((size_t)t * a.num_heads + (size_t)h * G) * D;
     float *out = static_cast<float *>(a.out) + off;
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
         part.m[lane / 4] = m;
         part.l[lane / 4] = bad ? -1.f : l;
     }
-    finish_row<float, D, kWarps>(parts, sizeof(Part<D>), &cta_part, out, G, ctas, rank, tid, 0);
+    finish_row<float, D, kWarps>(parts, sizeof(Part<D>), &inbox, out, G, ctas, rank, tid, 0);
 }
 
 // How a row is split.  Few rows: a cluster of CTAs each, up to four CTAs an SM in all, while each warp
