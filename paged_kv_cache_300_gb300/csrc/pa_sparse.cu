@@ -20,13 +20,15 @@
 // are zeroed in shared memory, so that what an unused slot holds (even NaN) meets a
 // weight of 0 as a zero.
 //
-// fp32.  Lanes share the channels; a warp has the rows of kBatch tokens in registers
-// at a time, products by FMA, exp2f.
+// fp32.  Lanes share the channels, four each; a warp has the rows of kTokens tokens in
+// registers at a time, products by FMA, exp2f.  Rows of up to four heads have a kernel of
+// their own, whose smaller state leaves room for twice the tokens and takes fewer shuffles
+// (64 requests, 8 kv heads of 128, 64 blocks of 16, 537 MB: 4 heads each 86 us, 111 in the kernel for 8; 8 heads each 123).
 //
-// Measured (one GB300): 96 requests, 64 / 8 heads of 128, 128 blocks of 16 tokens each: 122 us for 805 MB, 6.6 TB/s (97% of a
+// Measured (one GB300): 96 requests, 64 / 8 heads of 128, 128 blocks of 16 tokens each: 120 us for 805 MB, 6.7 TB/s (99% of a
 // copy).  565 tokens of 5 chunks, 32 / 8 heads, 64 blocks each: 125 us for 2.4 GB out of L2 (164 MB of it from DRAM), 19 TB/s;
-// tensor pipe 36%, issue slots 41%.  One token of 64 blocks: 5.7 us, of which the loop is 0.8 and the join of 8 CTAs 2.7.
-// fp32, 13 requests, 12 / 3 heads of 64, 17 blocks of 32: 9.9 us.
+// tensor pipe 36%, issue slots 41%.  One token of 64 blocks: 5.2 us, of which the loop is 0.8 and the join of 8 CTAs 1.9.
+// fp32, 13 requests, 12 / 3 heads of 64, 17 blocks of 32: 6.3 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -44,7 +46,9 @@ constexpr int kList = 64; // units that a warp looks up at a time
 // How far a score may pass the reference of its row's weights (log2): weights up to 2^8,
 // as exact as those up to 1.
 constexpr float kSlack = 8.f;
-constexpr int kUnitF32 = 8; // tokens of a unit of the fp32 kernel
+// Tokens of a unit of the fp32 kernel: 4 KB of K.  (64 channels, 1200 rows of 64 blocks of 16: units of 16 tokens 103 us, of 8 137;
+// with blocks of 8, where a unit is half a load, 4000 rows 264 and 235.)
+constexpr int unit_f32(int d) { return 1024 / d; }
 
 // One row's partial results in shared memory: [kGroup][D] accumulators, [kGroup]
 // maxima (log2 domain), [kGroup] sums; a negative sum marks a row that failed.
@@ -416,36 +420,38 @@ __global__ void __launch_bounds__(kThreads, 3)
 }
 
 // ------------------------------------------------------------------ fp32
-// The sums of v[0..7] over the warp's lanes: lane l gets head l / 4's in one pass of
-// 9 shuffles (halving the heads a lane holds at each of the first three).
-__device__ __forceinline__ float sum_heads(float (&v)[kGroup], int lane)
+// The sums of v[0..H-1] over L lanes, powers of two: lane l of them gets head
+// l / (L / H)'s (the heads a lane holds are halved until one is left).
+template <int H, int L>
+__device__ __forceinline__ float sum_heads(float (&v)[H], int lane)
 {
+    int o = L / 2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float give = lane & 16 ? v[i] : v[i + 4], keep = lane & 16 ? v[i + 4] : v[i];
-        v[i] = keep + __shfl_xor_sync(kFull, give, 16);
-    }
+    for (int n = H / 2; n > 0; n /= 2, o /= 2) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float give = lane & 8 ? v[i] : v[i + 2], keep = lane & 8 ? v[i + 2] : v[i];
-        v[i] = keep + __shfl_xor_sync(kFull, give, 8);
+        for (int i = 0; i < n; ++i) {
+            const float give = lane & o ? v[i] : v[i + n], keep = lane & o ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(kFull, give, o);
+        }
     }
-    const float give = lane & 4 ? v[0] : v[1], keep = lane & 4 ? v[1] : v[0];
-    float x = keep + __shfl_xor_sync(kFull, give, 4);
-    x += __shfl_xor_sync(kFull, x, 2);
-    x += __shfl_xor_sync(kFull, x, 1);
+    float x = v[0];
+#pragma unroll
+    for (; o > 0; o /= 2) x += __shfl_xor_sync(kFull, x, o);
     return x;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArgs a, int ctas)
+// H: heads that a row has room for.  A lane has four channels, so the warp has one token of
+// 128 channels or two of 64 side by side, each side with a softmax state of its own (lanes of two
+// channels shuffle and broadcast twice as often: 64 requests, 8 heads on each of 8 kv heads of 64, 86 us and 67).
+template <int D, int H>
+__global__ void __launch_bounds__(kThreads, 4) sparse_f32_kernel(const SparseArgs a, int ctas)
 {
-    constexpr int E = D / 32, kBatch = 4; // channels a lane, tokens at a time
-    using Vec = typename std::conditional<E == 4, float4, float2>::type;
+    constexpr int kUnit = unit_f32(D), L = D / 4, kSides = 32 / L, kLanes = L / H; // lanes a token, and of them a head
+    constexpr int kTokens = 4096 / (H * D), kBatch = kTokens / kSides; // at a time: of the warp, of a side
     __shared__ Part<D> parts[kWarps];
     __shared__ Inbox<D> inbox;
     __shared__ int2 lists[kWarps][kList];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, side = lane / L, sub = lane % L;
     const int rank = ctas > 1 ? (int)cluster_rank() : 0;
     grid_dep_trigger();
     if (ctas > 1) cluster_arrive();
@@ -465,51 +471,51 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
     }
     const int32_t *list = a.selected + (size_t)row * a.top_k;
     const int32_t *table = a.block_table + (size_t)at.req * a.max_blocks_per_seq;
-    const float *q = static_cast<const float *>(a.q) + off + lane * E;
-    float x[kGroup][E], acc[kGroup][E];
+    const float *q = static_cast<const float *>(a.q) + off + sub * 4;
+    float x[H][4], acc[H][4];
 #pragma unroll
-    for (int g = 0; g < kGroup; ++g)
+    for (int g = 0; g < H; ++g)
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
+        for (int i = 0; i < 4; ++i) {
             x[g][i] = g < G ? q[(size_t)g * D + i] : 0.f;
             acc[g][i] = 0.f;
         }
-    // softmax state of head lane / 4, in the log2 domain
+    // softmax state of head sub / kLanes of the side's tokens, in the log2 domain
     float m = -INFINITY, l = 0.f;
     bool bad = false;
-    const float *kc = static_cast<const float *>(a.k_cache) + (size_t)h * D + lane * E;
-    const float *vc = static_cast<const float *>(a.v_cache) + (size_t)h * D + lane * E;
+    const float *kc = static_cast<const float *>(a.k_cache) + (size_t)h * D + sub * 4;
+    const float *vc = static_cast<const float *>(a.v_cache) + (size_t)h * D + sub * 4;
     const size_t rowlen = (size_t)a.num_kv_heads * D;
-    const int upb = (a.block_size + kUnitF32 - 1) / kUnitF32, all = a.top_k * upb, stride = ctas * kWarps;
+    const int upb = (a.block_size + kUnit - 1) / kUnit, all = a.top_k * upb, stride = ctas * kWarps;
     int2 *items = lists[warp];
     for (int u0 = rank * kWarps + warp; u0 < all; u0 += kList * stride) {
-        const int count = look_up<kUnitF32>(a, list, table, u0, stride, all, upb, at.pos, lane, items, bad);
+        const int count = look_up<kUnit>(a, list, table, u0, stride, all, upb, at.pos, lane, items, bad);
         for (int it = 0; it < count; ++it) {
             const int2 item = items[it];
             // up to the query, the end of the unit and of the block
-            const int live = min(min(at.pos - item.y + 1, kUnitF32), a.block_size - item.y % a.block_size);
-            for (int t0 = 0; t0 < live; t0 += kBatch) {
-                float k[kBatch][E], v[kBatch][E], s[kBatch];
+            const int live = min(min(at.pos - item.y + 1, kUnit), a.block_size - item.y % a.block_size);
+            for (int t0 = 0; t0 < live; t0 += kTokens) {
+                float k[kBatch][4], v[kBatch][4], s[kBatch];
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
-                    const size_t r = (size_t)(item.x + min(t0 + b, live - 1)) * rowlen;
-                    *reinterpret_cast<Vec *>(k[b]) = *reinterpret_cast<const Vec *>(kc + r);
-                    *reinterpret_cast<Vec *>(v[b]) = *reinterpret_cast<const Vec *>(vc + r);
+                    const size_t r = (size_t)(item.x + min(t0 + b * kSides + side, live - 1)) * rowlen;
+                    *reinterpret_cast<float4 *>(k[b]) = *reinterpret_cast<const float4 *>(kc + r);
+                    *reinterpret_cast<float4 *>(v[b]) = *reinterpret_cast<const float4 *>(vc + r);
 #pragma unroll
-                    for (int i = 0; i < E; ++i) v[b][i] = t0 + b < live ? v[b][i] : 0.f;
+                    for (int i = 0; i < 4; ++i) v[b][i] = t0 + b * kSides + side < live ? v[b][i] : 0.f;
                 }
                 float most = -INFINITY;
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
-                    float dot[kGroup];
+                    float dot[H];
 #pragma unroll
-                    for (int g = 0; g < kGroup; ++g) {
+                    for (int g = 0; g < H; ++g) {
                         dot[g] = 0.f;
 #pragma unroll
-                        for (int i = 0; i < E; ++i) dot[g] = fmaf(x[g][i], k[b][i], dot[g]);
+                        for (int i = 0; i < 4; ++i) dot[g] = fmaf(x[g][i], k[b][i], dot[g]);
                     }
-                    s[b] = sum_heads(dot, lane) * a.scale_log2;
-                    if (t0 + b >= live) s[b] = -INFINITY;
+                    s[b] = sum_heads<H, L>(dot, lane) * a.scale_log2;
+                    if (t0 + b * kSides + side >= live) s[b] = -INFINITY;
                     most = fmaxf(most, s[b]);
                 }
                 if (__any_sync(kFull, most > m + kSlack)) { // as in bf16
@@ -518,10 +524,10 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
                     m = most;
                     l *= al;
 #pragma unroll
-                    for (int g = 0; g < kGroup; ++g) {
-                        const float w = __shfl_sync(kFull, al, 4 * g);
+                    for (int g = 0; g < H; ++g) {
+                        const float w = __shfl_sync(kFull, al, side * L + kLanes * g);
 #pragma unroll
-                        for (int i = 0; i < E; ++i) acc[g][i] *= w;
+                        for (int i = 0; i < 4; ++i) acc[g][i] *= w;
                     }
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
@@ -531,13 +537,13 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
                     l += s[b];
                 }
 #pragma unroll
-                for (int g = 0; g < kGroup; ++g) {
+                for (int g = 0; g < H; ++g) {
                     if (g >= G) break;
 #pragma unroll
                     for (int b = 0; b < kBatch; ++b) {
-                        const float p = __shfl_sync(kFull, s[b], 4 * g);
+                        const float p = __shfl_sync(kFull, s[b], side * L + kLanes * g);
 #pragma unroll
-                        for (int i = 0; i < E; ++i) acc[g][i] = fmaf(p, v[b][i], acc[g][i]);
+                        for (int i = 0; i < 4; ++i) acc[g][i] = fmaf(p, v[b][i], acc[g][i]);
                     }
                 }
             }
@@ -545,13 +551,30 @@ __global__ void __launch_bounds__(kThreads, 3) sparse_f32_kernel(const SparseArg
     }
     bad = __any_sync(kFull, bad);
     if (bad && lane == 0) flag_error(a.dev_err, PA_DEVERR_BAD_BLOCK);
-    Part<D> &part = parts[warp];
+    if (kSides == 2) {
+        const float most = fmaxf(m, __shfl_xor_sync(kFull, m, 16)), al = most == -INFINITY ? 1.f : exp2f(m - most);
+        m = most;
+        l *= al;
+        l += __shfl_xor_sync(kFull, l, 16);
 #pragma unroll
-    for (int g = 0; g < kGroup; ++g)
-        *reinterpret_cast<Vec *>(&part.acc[g][lane * E]) = *reinterpret_cast<Vec *>(acc[g]);
-    if (lane % 4 == 0) {
-        part.m[lane / 4] = m;
-        part.l[lane / 4] = bad ? -1.f : l;
+        for (int g = 0; g < H; ++g) {
+            const float w = __shfl_sync(kFull, al, side * L + kLanes * g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[g][i] *= w;
+                acc[g][i] += __shfl_xor_sync(kFull, acc[g][i], 16);
+            }
+        }
+    }
+    Part<D> &part = parts[warp];
+    if (side == 0) {
+#pragma unroll
+        for (int g = 0; g < H; ++g)
+            *reinterpret_cast<float4 *>(&part.acc[g][sub * 4]) = *reinterpret_cast<float4 *>(acc[g]);
+        if (sub % kLanes == 0) {
+            part.m[sub / kLanes] = m;
+            part.l[sub / kLanes] = bad ? -1.f : l;
+        }
     }
     finish_row<float, D, kWarps>(parts, sizeof(Part<D>), &inbox, out, G, ctas, rank, tid, 0);
 }
@@ -618,6 +641,13 @@ int launch_bf16(const SparseArgs &a, const CUtensorMap &tm_k, const CUtensorMap 
     return launch_bf16<D, kWarps>(a, split, tm_k, tm_v, s);
 }
 
+template <int D, int H>
+int launch_f32(const SparseArgs &a, const Split &split, cudaStream_t s)
+{
+    static int raised[64];
+    return launch(sparse_f32_kernel<D, H>, raised, 0, split, a, s);
+}
+
 }  // namespace
 
 int sparse_bf16_launch(const SparseArgs &a, int head_dim, const CUtensorMap &tm_k, const CUtensorMap &tm_v, cudaStream_t s)
@@ -627,10 +657,9 @@ int sparse_bf16_launch(const SparseArgs &a, int head_dim, const CUtensorMap &tm_
 
 int sparse_f32_launch(const SparseArgs &a, int head_dim, cudaStream_t s)
 {
-    static int raised64[64], raised128[64];
-    const Split split = split_of(a, kUnitF32, 0);
-    if (head_dim == 64) return launch(sparse_f32_kernel<64>, raised64, 0, split, a, s);
-    return launch(sparse_f32_kernel<128>, raised128, 0, split, a, s);
+    const Split split = split_of(a, unit_f32(head_dim), 0);
+    if (a.group <= 4) return head_dim == 64 ? launch_f32<64, 4>(a, split, s) : launch_f32<128, 4>(a, split, s);
+    return head_dim == 64 ? launch_f32<64, kGroup>(a, split, s) : launch_f32<128, kGroup>(a, split, s);
 }
 
 }  // namespace pa
