@@ -45,26 +45,12 @@ struct QueryRow {
     int err;   // PA_DEVERR_* bits
 };
 
+// The same for the row with `back` queries of its request `req` behind it.
 template <typename Args>
-__device__ __forceinline__ QueryRow query_row(const Args &a, int t, int lane)
+__device__ __forceinline__ QueryRow request_row(const Args &a, int req, int back)
 {
-    QueryRow q{t, -(1 << 30), 1, false, 0};
-    int back = 0; // the request's queries behind row t
-    if (a.cu_q != nullptr) {
-        q.req = find_last([&](int r) { return (long long)a.cu_q[r]; }, a.batch, t, lane);
-        if (q.req == a.batch) {
-            q.skip = true;
-            return q;
-        }
-        const int c1 = q.req >= 0 ? a.cu_q[q.req + 1] : 0;
-        if (q.req < 0 || c1 <= t || a.cu_q[0] != 0) {
-            q.err = PA_DEVERR_BAD_CU;
-            return q;
-        }
-        back = c1 - 1 - t;
-        q.left = c1 - t;
-    }
-    const int kl = a.seqlens_k[q.req];
+    QueryRow q{req, -(1 << 30), back + 1, false, 0};
+    const int kl = a.seqlens_k[req];
     if (kl == PA_LEFT_OUT) return q;
     if (kl < 0 || (long long)kl > (long long)a.max_blocks_per_seq * a.block_size) {
         q.err = PA_DEVERR_OVERFLOW;
@@ -72,6 +58,24 @@ __device__ __forceinline__ QueryRow query_row(const Args &a, int t, int lane)
     }
     q.pos = kl - 1 - back;
     return q;
+}
+
+template <typename Args>
+__device__ __forceinline__ QueryRow query_row(const Args &a, int t, int lane)
+{
+    if (a.cu_q == nullptr) return request_row(a, t, 0);
+    QueryRow q{t, -(1 << 30), 1, false, 0};
+    q.req = find_last([&](int r) { return (long long)a.cu_q[r]; }, a.batch, t, lane);
+    if (q.req == a.batch) {
+        q.skip = true;
+        return q;
+    }
+    const int c1 = q.req >= 0 ? a.cu_q[q.req + 1] : 0;
+    if (q.req < 0 || c1 <= t || a.cu_q[0] != 0) {
+        q.err = PA_DEVERR_BAD_CU;
+        return q;
+    }
+    return request_row(a, q.req, c1 - 1 - t);
 }
 
 // ---------------------------------------------------------------- clusters

@@ -9,7 +9,7 @@
 // Scores.  Bound by the bytes of the bounds (2 D elements a block and head, 1 / bs
 // of the keys and values).  In bf16 the operands are exact and the sum is a
 // product of [q+, q-] with [hi, lo]: mma.sync m16n8k16 with 16 blocks on M and the
-// heads, of several tokens where there are fewer than 8, on N.  The order of the sum
+// heads, of several tokens where there are fewer than 8, on N (or 8 tokens, head after head).  The order of the sum
 // over d is free, so a lane's 16-byte load of a row is two k-steps' fragments as it
 // stands: bounds go from memory to the tensor cores without shared memory, 8 KB a
 // warp in flight.  A CTA takes a tile of neighbouring tokens (one, for decode) and a kv
@@ -34,8 +34,9 @@
 //
 // Measured (one GB300): 96 requests of 4096 to 32768 tokens, 64 / 8 heads of 128, 128 of their blocks of 16: 87.5 us
 // for 451 MB; 7 TB/s while all CTAs score, less where some choose (4 us a row) and while the last rows end (20 us).
-// 565 tokens of 5 chunks, 32 / 8 heads, 64 of up to 750 blocks: 49 us, bound by the latency of two CTAs an SM (the tensor
-// pipe is 12% busy, issue slots 31%): half of it scores, half chooses.  One token of 313 blocks 6.7 us.
+// 565 tokens of 5 chunks, 32 / 8 heads, 64 of up to 750 blocks: 43 us (49 with the heads of a token on neighbouring
+// columns), bound by the latency of two CTAs an SM (the products alone, 8 cycles each, are 8 us): some 24 us score, the rest
+// chooses, 4 of it by exact scores.  One token of 313 blocks 6.6 us.
 #include <algorithm>
 #include <limits.h>
 #include <type_traits>
@@ -89,13 +90,14 @@ __device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b)
     asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) // the other one of a NaN
+__device__ __forceinline__ uint32_t abs2(uint32_t x) { return x & 0x7fff7fffu; }
+// The larger magnitude; the other one of a NaN.
+__device__ __forceinline__ uint32_t most2(uint32_t a, uint32_t b)
 {
     uint32_t r;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
+    asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return abs2(r);
 }
-__device__ __forceinline__ uint32_t abs2(uint32_t x) { return x & 0x7fff7fffu; }
 
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -245,14 +247,14 @@ struct Sum3 {
     __device__ __forceinline__ double value() const { return (double)a + ((double)b + (double)c); }
 };
 
-// The row's score of one block, exact to the last bits of a double, in all lanes.  Four
-// lanes share a head.
+// The row's score of a block, exact to the last bits of a double.  Four lanes share a head, and neighbouring
+// `lanes` of them, a power of two, a block: `bounds` is theirs (null: none) and the score, in the first of them.
 template <typename T, int D>
-__device__ __forceinline__ double exact_score(const T *q, const T *bounds, int G, int lane)
+__device__ __forceinline__ double exact_score(const T *q, const T *bounds, int G, int lanes, int lane)
 {
-    const int g = lane >> 2;
+    const int g = (lane & (lanes - 1)) >> 2;
     Sum3 sum;
-    if (g < G) {
+    if (g < G && bounds != nullptr) {
         constexpr int N = D / 32;
         T x[N][8], lo[N][8], hi[N][8];
 #pragma unroll
@@ -277,11 +279,11 @@ __device__ __forceinline__ double exact_score(const T *q, const T *bounds, int G
     double s = sum.value();
     s += __shfl_xor_sync(kFull, s, 1);
     s += __shfl_xor_sync(kFull, s, 2);
-    for (int k = 1; k < G; ++k) { // the largest, to lane 0 and from there to all
-        const double x = __shfl_sync(kFull, s, 4 * k);
-        if (lane == 0 && x > s) s = x;
+    for (int k = 1; k < G; ++k) { // the largest
+        const double x = __shfl_down_sync(kFull, s, 4 * k);
+        if (g == 0 && x > s) s = x;
     }
-    return __shfl_sync(kFull, s, 0);
+    return s;
 }
 
 // What a row's choice is made from.
@@ -296,9 +298,9 @@ struct Row {
 };
 
 // Writes the `need` of the row's n scored blocks with the largest scores to out, ascending.
-// `key` holds the scores.
+// `key` holds the scores; `heads` is a.group rounded up to a power of two.
 template <typename T, int D, int W>
-__device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *out, const SelectArgs &a, Choice<W> &sh, int tid)
+__device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *out, const SelectArgs &a, int heads, Choice<W> &sh, int tid)
 {
     const int lane = tid & 31, warp = tid >> 5, n = r.n, need = r.need;
     uint32_t least = 0xffffffffu, most = 0;
@@ -379,10 +381,12 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
             for (int i = i0 + lane; i < i1; i += 32)
                 if (key[i] >= low && key[i] <= high) sh.list[atomicAdd(&sh.listed, 1u)] = i;
             choice_sync<W>();
-            for (int c = warp; c < open; c += W) {
-                const T *bounds = r.bounds + (size_t)r.table[sh.list[c]] * a.num_kv_heads * 2 * D;
-                const float x = (float)(exact_score<T, D>(r.q, bounds, a.group, lane) - (double)cut);
-                if (lane == 0) sh.exact[c] = x;
+            const int lanes = 4 * heads, blocks = 32 / lanes; // of a block, of a warp
+            for (int c0 = warp * blocks; c0 < open; c0 += W * blocks) {
+                const int c = c0 + lane / lanes;
+                const T *bounds = c < open ? r.bounds + (size_t)r.table[sh.list[c]] * a.num_kv_heads * 2 * D : nullptr;
+                const float x = (float)(exact_score<T, D>(r.q, bounds, a.group, lanes, lane) - (double)cut);
+                if (c < open && lane % lanes == 0) sh.exact[c] = x;
             }
             choice_sync<W>();
             if (tid < open) {
@@ -403,8 +407,8 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
                 const int b = __ffs(todo) - 1;
                 todo &= todo - 1;
                 const T *bounds = r.bounds + (size_t)r.table[(i - lane) + b] * a.num_kv_heads * 2 * D;
-                const uint32_t exact = key_of((float)(exact_score<T, D>(r.q, bounds, a.group, lane) - (double)cut));
-                if (lane == b) now = exact;
+                const double score = __shfl_sync(kFull, exact_score<T, D>(r.q, bounds, a.group, 32, lane), 0);
+                if (lane == b) now = key_of((float)(score - (double)cut));
             }
             if (i < i1) key[i] = now;
         }
@@ -510,10 +514,10 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 const uint4 u = load_shared(q + i * 64);
-                mma_bf16_16816(m, max2(abs2(hi[i][0].x), abs2(lo[i][0].x)), max2(abs2(hi[i][1].x), abs2(lo[i][1].x)),
-                               max2(abs2(hi[i][0].y), abs2(lo[i][0].y)), max2(abs2(hi[i][1].y), abs2(lo[i][1].y)), abs2(u.x), abs2(u.y));
-                mma_bf16_16816(m, max2(abs2(hi[i][0].z), abs2(lo[i][0].z)), max2(abs2(hi[i][1].z), abs2(lo[i][1].z)),
-                               max2(abs2(hi[i][0].w), abs2(lo[i][0].w)), max2(abs2(hi[i][1].w), abs2(lo[i][1].w)), abs2(u.z), abs2(u.w));
+                mma_bf16_16816(m, most2(hi[i][0].x, lo[i][0].x), most2(hi[i][1].x, lo[i][1].x),
+                               most2(hi[i][0].y, lo[i][0].y), most2(hi[i][1].y, lo[i][1].y), abs2(u.x), abs2(u.y));
+                mma_bf16_16816(m, most2(hi[i][0].z, lo[i][0].z), most2(hi[i][1].z, lo[i][1].z),
+                               most2(hi[i][0].w, lo[i][0].w), most2(hi[i][1].w, lo[i][1].w), abs2(u.z), abs2(u.w));
             }
             // (infinities and NaN do not count: the scores are none either)
             const bool both = ONE && 2 * c + 1 < a.group;
@@ -568,6 +572,97 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
         if (!ONE)
             for (; grp + 1 < groups; grp += 2) group(grp, std::integral_constant<int, 2>());
         if (grp < groups) group(grp, std::integral_constant<int, 1>());
+    }
+}
+
+// Tiles of eight tokens or more: a column is a token, and the heads take their turns, so that the largest
+// of a token's is found without a word between lanes.  Rows of q [head][tokens rounded up to 8].
+template <int D>
+__device__ __forceinline__ void score_tokens(const SelectArgs &a, const Scoring &s, int first, int step, int lane, float &mag, int &bad)
+{
+    constexpr int NC = D / 32; // 16-byte pieces of a row per lane
+    constexpr int ROW = 2 * D + kPad;
+    const int g = lane >> 2, c = lane & 3, n = s.n, G = a.group;
+    const __nv_bfloat16 *bounds = static_cast<const __nv_bfloat16 *>(a.bounds) + (size_t)s.head * 2 * D + c * 8;
+    const size_t block = (size_t)a.num_kv_heads * 2 * D;
+    const int tiles = (n + 15) / 16;
+    const uint32_t of_head = (uint32_t)((s.tokens + 7) & ~7) * ROW; // bytes of a head's rows
+    auto entry_of = [&](int tile) {
+        const int j = tile * 16 + (lane & 15);
+        const int e = tile < tiles && j < n ? s.table[j] : 0;
+        const bool wrong = e < 0 || e >= a.num_blocks;
+        if (wrong) bad = min(bad, j);
+        return wrong ? 0 : e;
+    };
+    int entry = entry_of(first);
+    for (int tile = first; tile < tiles; tile += step) {
+        const __nv_bfloat16 *r0 = bounds + (size_t)__shfl_sync(kFull, entry, g) * block;
+        const __nv_bfloat16 *r1 = bounds + (size_t)__shfl_sync(kFull, entry, g + 8) * block;
+        uint4 lo[NC][2], hi[NC][2];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            lo[i][0] = *reinterpret_cast<const uint4 *>(r0 + i * 32);
+            lo[i][1] = *reinterpret_cast<const uint4 *>(r1 + i * 32);
+            hi[i][0] = *reinterpret_cast<const uint4 *>(r0 + D + i * 32);
+            hi[i][1] = *reinterpret_cast<const uint4 *>(r1 + D + i * 32);
+        }
+        entry = entry_of(tile + step);
+        const int j0 = tile * 16 + g;
+        {   // S, of the largest |q|
+            float m[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint32_t q = s.q + (uint32_t)G * of_head + c * 16;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const uint4 u = load_shared(q + i * 64);
+                mma_bf16_16816(m, most2(hi[i][0].x, lo[i][0].x), most2(hi[i][1].x, lo[i][1].x), most2(hi[i][0].y, lo[i][0].y),
+                               most2(hi[i][1].y, lo[i][1].y), u.x, u.y);
+                mma_bf16_16816(m, most2(hi[i][0].z, lo[i][0].z), most2(hi[i][1].z, lo[i][1].z), most2(hi[i][0].w, lo[i][0].w),
+                               most2(hi[i][1].w, lo[i][1].w), u.z, u.w);
+            }
+            // (infinities and NaN do not count: the scores are none either)
+            if (j0 < n && m[0] < INFINITY) mag = fmaxf(mag, m[0]);
+            if (j0 + 8 < n && m[2] < INFINITY) mag = fmaxf(mag, m[2]);
+        }
+        for (int t0 = 0; t0 < s.tokens; t0 += 8) {
+            float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            // GB heads at a time: 2 GB chains of products
+            auto heads = [&](uint32_t q, auto count) {
+                constexpr int GB = decltype(count)::value;
+                float sh[GB][4], sl[GB][4];
+#pragma unroll
+                for (int b = 0; b < GB; ++b)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sh[b][k] = sl[b][k] = 0.f;
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+#pragma unroll
+                    for (int b = 0; b < GB; ++b) {
+                        const uint4 x = load_shared(q + b * of_head + i * 64);
+                        mma_bf16_16816(sh[b], hi[i][0].x, hi[i][1].x, hi[i][0].y, hi[i][1].y, max_nan2(x.x, 0), max_nan2(x.y, 0));
+                        mma_bf16_16816(sl[b], lo[i][0].x, lo[i][1].x, lo[i][0].y, lo[i][1].y, min_nan2(x.x, 0), min_nan2(x.y, 0));
+                        mma_bf16_16816(sh[b], hi[i][0].z, hi[i][1].z, hi[i][0].w, hi[i][1].w, max_nan2(x.z, 0), max_nan2(x.w, 0));
+                        mma_bf16_16816(sl[b], lo[i][0].z, lo[i][1].z, lo[i][0].w, lo[i][1].w, min_nan2(x.z, 0), min_nan2(x.w, 0));
+                    }
+#pragma unroll
+                for (int b = 0; b < GB; ++b)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) best[k] = max_nan(best[k], sh[b][k] + sl[b][k]);
+            };
+            uint32_t q = s.q + (uint32_t)(t0 + g) * ROW + c * 16;
+            int h = 0;
+            for (; h + 1 < G; h += 2, q += 2 * of_head) heads(q, std::integral_constant<int, 2>());
+            if (h < G) heads(q, std::integral_constant<int, 1>());
+            // blocks g and g + 8 of columns 2c and 2c + 1
+            const uint32_t to = s.keys + (t0 + 2 * c) * s.stride + 4 * j0;
+            if (t0 + 2 * c < s.tokens) {
+                if (j0 < n) cluster_store(to, __float_as_uint(best[0]));
+                if (j0 + 8 < n) cluster_store(to + 32, __float_as_uint(best[2]));
+            }
+            if (t0 + 2 * c + 1 < s.tokens) {
+                if (j0 < n) cluster_store(to + s.stride, __float_as_uint(best[1]));
+                if (j0 + 8 < n) cluster_store(to + s.stride + 32, __float_as_uint(best[3]));
+            }
+        }
     }
 }
 
@@ -663,19 +758,28 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
 // c1 / tile + r: one more than it may need, and found without the sums of those before.
 struct TileRows {
     int first, count;
+    QueryRow at; // the first of them
 };
 __device__ __forceinline__ TileRows tile_rows(const SelectArgs &a, int unit, int tile, int lane)
 {
-    if (a.cu_q[0] != 0) { // no row has a request: all are refused
-        const long long t = (long long)unit * tile;
-        return {(int)min(t, (long long)a.total_q), (int)max(0ll, min((long long)tile, a.total_q - t))};
-    }
+    TileRows t{0, 0, {0, -(1 << 30), 0, false, 0}};
+    const int c_first = a.cu_q[0];
     const int r = find_last([&](int i) { return (long long)a.cu_q[i] / tile + i; }, a.batch, unit, lane);
-    if (r < 0 || r >= a.batch) return {0, 0};
-    const int c0 = a.cu_q[r], c1 = min(a.cu_q[r + 1], a.total_q);
+    if (c_first != 0) { // no row has a request: all are refused
+        t.first = (int)min((long long)unit * tile, (long long)a.total_q);
+        t.count = (int)min(tile, a.total_q - t.first);
+        t.at.err = PA_DEVERR_BAD_CU;
+        return t;
+    }
+    if (r < 0 || r >= a.batch) return t;
+    const int c0 = a.cu_q[r], c1 = a.cu_q[r + 1], end = min(c1, a.total_q);
+    t.at = request_row(a, r, 0);
     const long long first = c0 + (long long)(unit - (c0 / tile + r)) * tile;
-    if (c0 < 0 || first < c0 || first >= c1) return {0, 0};
-    return {(int)first, min(tile, c1 - (int)first)};
+    if (c0 < 0 || first < c0 || first >= end) return t;
+    t.first = (int)first;
+    t.count = min(tile, end - t.first);
+    if (t.at.pos > -(1 << 30)) t.at.pos -= c1 - 1 - t.first;
+    return t;
 }
 
 struct Shared {
@@ -690,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
 {
     constexpr int W = TILE == 1 ? kWarps : 1; // warps that choose together
     constexpr int ROW = (int)sizeof(T) * D + kPad;
+    constexpr bool WIDE = sizeof(T) == 2 && TILE == kTile;
     extern __shared__ __align__(16) uint32_t keys[]; // [tile][max_blocks_per_seq, a multiple of 4], then the rows of q
     __shared__ Shared sh;
     __shared__ Choice<W> choice[kWarps / W];
@@ -721,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         }
         t = r.first;
         count = r.count;
-        at = query_row(a, t, lane);
+        at = r.at;
     }
     const int cap = a.max_blocks_per_seq, row_keys = (cap + 3) & ~3, need = a.top_k - a.first - a.last;
     const int last_seen = at.pos + count - 1 < 0 ? 0 : (at.pos + count - 1) / a.block_size + 1; // by the last token
@@ -742,11 +847,12 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         s.stride = row_keys * 4;
         // rows of q, 16 bytes a thread; then the largest |q| of each channel
         constexpr int PIECES = (int)sizeof(T) * D / 16;
-        const int rows = count << heads_log2;
+        const int wide = (count + 7) & ~7, rows = WIDE ? a.group * wide : count << heads_log2;
         for (int i = tid; i < rows * PIECES; i += kThreads) {
-            const int r = i / PIECES, p = i % PIECES, g = r & ((1 << heads_log2) - 1), tk = r >> heads_log2;
+            const int r = i / PIECES, p = i % PIECES;
+            const int g = WIDE ? r / wide : r & ((1 << heads_log2) - 1), tk = WIDE ? r - g * wide : r >> heads_log2;
             uint4 x = make_uint4(0, 0, 0, 0);
-            if (g < a.group) x = reinterpret_cast<const uint4 *>(q + ((size_t)tk * a.num_heads + g) * D)[p];
+            if (g < a.group && tk < count) x = reinterpret_cast<const uint4 *>(q + ((size_t)tk * a.num_heads + g) * D)[p];
             *reinterpret_cast<uint4 *>(q_rows + (size_t)r * ROW + p * 16) = x;
         }
         __syncthreads();
@@ -768,7 +874,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         if (cluster) cluster_wait(); // the first CTA's shared memory is there
         float mag = 0.f;
         int bad = INT_MAX;
-        score_blocks<D, TILE == 1>(a, s, rank * kWarps + warp, ctas * kWarps, lane, mag, bad, q);
+        if constexpr (WIDE)
+            score_tokens<D>(a, s, rank * kWarps + warp, ctas * kWarps, lane, mag, bad);
+        else
+            score_blocks<D, TILE == 1>(a, s, rank * kWarps + warp, ctas * kWarps, lane, mag, bad, q);
         const uint32_t most = __reduce_max_sync(kFull, __float_as_uint(mag));
         bad = __reduce_min_sync(kFull, bad);
         if (lane == 0) {
@@ -813,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         r.need = need;
         // 2 E, and the rounding of S
         r.width = (sizeof(T) == 2 ? (D / 16 + 2) * 0x1.02p-21f : (D / 16 + 6) * 0x1.02p-23f) * __uint_as_float(sh.mag);
-        choose<T, D, W>(keys + (size_t)i * row_keys, r, out + a.first, a, choice[W == 1 ? warp : 0], wt);
+        choose<T, D, W>(keys + (size_t)i * row_keys, r, out + a.first, a, 1 << heads_log2, choice[W == 1 ? warp : 0], wt);
     }
 }
 
@@ -865,12 +974,14 @@ int launch_tile(const SelectArgs &a, cudaStream_t s)
     auto units_of = [&](int t) { return t == 1 ? rows : (a.total_q / t + (long long)a.batch) * a.num_kv_heads; };
     const long long fill = 2ll * num_sms();
     // .. 16 only where there are several for every place: they read the bounds half as often, but take longer
-    // (565 tokens, 8 kv heads: 53.4 us, with 8 51.3; 4885 tokens: 326 and 382).
+    // (8 kv heads, 565 tokens of 5 requests: 45.9 us, with 8 43.6; 4096 of 2: 283 and 323).
     if (tile == kTile && units_of(tile) < 2 * fill) tile /= 2;
     // Few rows or tiles: a cluster of CTAs each, as many as are resident at a time (two an SM)
     // while each warp has a tile of 16 blocks.
     const long long fit = std::min<long long>(fill / units_of(tile), (a.max_blocks_per_seq + 16 * kWarps - 1) / (16 * kWarps));
     const int ctas = fit <= 1 ? 1 : fit <= 8 ? (int)fit : fit >= 16 ? 16 : 8; // (9 to 15 are slower than 8)
+    if constexpr (sizeof(T) == 2)
+        if (tile > 1 && tile < 8) return launch<T, D, 4>(a, ctas, tile, heads_log2, smem_of(tile), s);
     if (tile > 1) return launch<T, D, kTile>(a, ctas, tile, heads_log2, smem_of(tile), s);
     return launch<T, D, 1>(a, ctas, 1, heads_log2, smem_of(1), s);
 }
