@@ -200,7 +200,7 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint
         need -= sh.above;
         lo += sh.bin << shift;
         if (shift == 0) return lo; // a bin is one key
-        hi = min(hi, lo + ((1u << shift) - 1));
+        hi = lo + min(hi - lo, (1u << shift) - 1); // (lo + 2^shift may pass 2^32)
         if (in <= 32) { // few enough to look at one by one
 #pragma unroll 2
             for (int i = 4 * tid; i < n; i += 4 * T)
@@ -279,6 +279,8 @@ __device__ __forceinline__ double exact_score(const T *q, const T *bounds, int G
     double s = sum.value();
     s += __shfl_xor_sync(kFull, s, 1);
     s += __shfl_xor_sync(kFull, s, 2);
+    // A head with an infinite q is -infinity where the row's fp32 score is finite; its sum above is NaN.
+    if (!(s > -INFINITY)) s = -INFINITY;
     for (int k = 1; k < G; ++k) { // the largest
         const double x = __shfl_down_sync(kFull, s, 4 * k);
         if (g == 0 && x > s) s = x;

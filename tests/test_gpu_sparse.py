@@ -233,6 +233,69 @@ def test_select_with_nan_and_infinite_bounds(dtype):
     assert np.array_equal(_select(q, bounds, table, lens, top, bs), _want(q, bounds, table, lens, top, bs))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens", [1, 19])
+@pytest.mark.parametrize("nans", [1, 3, 20, 40, 300])
+def test_select_where_the_last_chosen_is_nan(dtype, tokens, nans):
+    """The keys of NaN are the largest 32-bit numbers: nothing is added to them."""
+    d, bs, n, hkv = 64, 16, 600, 2
+    bounds = _bounds(1, n, hkv, d, dtype)
+    table = torch.randperm(n, generator=torch.Generator().manual_seed(2)).int().view(1, n)
+    some = np.random.default_rng(nans).permutation(n)[:nans]
+    bounds[some, 0, 0, 2] = float("nan")
+    bounds[some, 1, 1, 60] = float("inf")
+    q = torch.randn(tokens, 6, d, generator=torch.Generator().manual_seed(1)).to(dtype)
+    lens, cu = i32([n * bs - 3]), i32([0, tokens])
+    for top in (2 + nans // 2, 3 + nans // 2, nans, nans + 1, nans + 2, nans + 3, nans + 9):
+        if top >= 2:
+            assert np.array_equal(_select(q, bounds, table, lens, top, bs, cu=cu), _want(q, bounds, table, lens, top, bs, cu=cu)), top
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens", [1, 19])
+@pytest.mark.parametrize("head", [0, 2])
+@pytest.mark.parametrize("step", [2.0 ** -14, 2.0 ** -9])
+def test_select_of_close_scores_beside_an_infinite_head(dtype, tokens, head, step):
+    """A head whose scores are all minus infinity takes nothing from the others, whose
+    scores are in doubt."""
+    d, bs, n, hkv = 64, 16, 500, 2
+    bounds = torch.full((n, hkv, 2, d), 4.0)
+    bounds[:, :, :, :2] = _bounds(3, n, hkv, d, F32)[:, :, :, :2] * step
+    bounds[:, :, :, 7] = -1
+    bounds = bounds.to(dtype)
+    table = torch.randperm(n, generator=torch.Generator().manual_seed(2)).int().view(1, n)
+    q = (torch.randn(tokens, 6, d, generator=torch.Generator().manual_seed(1)).abs() * 3 + 2).to(dtype)
+    q[:, head, 7] = float("inf")
+    lens, cu = i32([n * bs - 3]), i32([0, tokens])
+    for top in (5, 40, 300):
+        assert np.array_equal(_select(q, bounds, table, lens, top, bs, cu=cu), _want(q, bounds, table, lens, top, bs, cu=cu)), top
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 6, 2), (128, 8, 1), (64, 2, 2), (128, 10, 2)])
+def test_select_for_tiles_with_nan_infinite_and_close_scores(dtype, d, hq, hkv):
+    """The same in tiles of tokens, with heads of every number; scores of a narrow band, few and
+    many of them in doubt."""
+    bs, n, tokens = 16, 500, 43
+    bounds = _bounds(1, n, hkv, d, dtype)
+    table = torch.randperm(n, generator=torch.Generator().manual_seed(2)).int().view(1, n)
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(tokens, hq, d, generator=g).to(dtype)
+    lens, cu = i32([n * bs - 3]), i32([0, tokens])
+    bounds[7, 0, 1, 3], bounds[50, hkv - 1, 0, 9] = float("nan"), float("nan")
+    bounds[12, 0, 1, :], bounds[13, hkv - 1, 1, 4], bounds[60, 0, 0, 5] = float("inf"), float("inf"), -float("inf")
+    q[3, 1], q[9, 0, 5], q[20, hq - 1, 6] = 0, float("nan"), float("inf")
+    for top in (5, 90):
+        assert np.array_equal(_select(q, bounds, table, lens, top, bs, cu=cu), _want(q, bounds, table, lens, top, bs, cu=cu))
+    for step in (2.0 ** -14, 2.0 ** -9):
+        close = torch.full((n, hkv, 2, d), 4.0)
+        close[:, :, :, :2] = _bounds(3, n, hkv, d, F32)[:, :, :, :2] * step
+        close = close.to(dtype)
+        q = (torch.randn(tokens, hq, d, generator=g).abs() * 3 + 2).to(dtype)
+        for top in (40, 300):
+            assert np.array_equal(_select(q, close, table, lens, top, bs, cu=cu), _want(q, close, table, lens, top, bs, cu=cu))
+
+
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (F32, 64)])
 @pytest.mark.parametrize("n,top", [(49152, 1000), (20000, 19999), (49150, 3)])
 def test_select_from_as_many_blocks_as_there_can_be(dtype, d, n, top):
