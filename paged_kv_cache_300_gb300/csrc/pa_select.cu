@@ -32,7 +32,7 @@
 //   roundings of 2^-24.)  L1(q) max|b| costs no product but is some 8 times as much, and then many rows
 //   need exact scores (one request: 13.1 us instead of 6.4).
 //
-// Measured (one GB300): 96 requests of 4096 to 32768 tokens, 64 / 8 heads of 128, 128 of their blocks of 16: 87.5 us
+// Measured (one GB300): 96 requests of 4096 to 32768 tokens, 64 / 8 heads of 128, 128 of their blocks of 16: 83 us
 // for 451 MB; 7 TB/s while all CTAs score, less where some choose (4 us a row) and while the last rows end (20 us).
 // 565 tokens of 5 chunks, 32 / 8 heads, 64 of up to 750 blocks: 43 us (49 with the heads of a token on neighbouring
 // columns), bound by the latency of two CTAs an SM (the products alone, 8 cycles each, are 8 us): some 24 us score, the rest
@@ -497,19 +497,35 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
         if (wrong) bad = min(bad, j);
         return wrong ? 0 : e;
     };
+    const __nv_bfloat16 *r0, *r1;
+    uint4 lo[NC][2], hi[NC][2];
+    auto load = [&](int i) {
+        lo[i][0] = *reinterpret_cast<const uint4 *>(r0 + i * 32);
+        lo[i][1] = *reinterpret_cast<const uint4 *>(r1 + i * 32);
+        hi[i][0] = *reinterpret_cast<const uint4 *>(r0 + D + i * 32);
+        hi[i][1] = *reinterpret_cast<const uint4 *>(r1 + D + i * 32);
+    };
     int entry = entry_of(first);
-    for (int tile = first; tile < tiles; tile += step) {
-        const __nv_bfloat16 *r0 = bounds + (size_t)__shfl_sync(kFull, entry, g) * block;
-        const __nv_bfloat16 *r1 = bounds + (size_t)__shfl_sync(kFull, entry, g + 8) * block;
-        uint4 lo[NC][2], hi[NC][2];
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            lo[i][0] = *reinterpret_cast<const uint4 *>(r0 + i * 32);
-            lo[i][1] = *reinterpret_cast<const uint4 *>(r1 + i * 32);
-            hi[i][0] = *reinterpret_cast<const uint4 *>(r0 + D + i * 32);
-            hi[i][1] = *reinterpret_cast<const uint4 *>(r1 + D + i * 32);
-        }
+    auto rows_of = [&](int tile) { // and looks up the one after it
+        r0 = bounds + (size_t)__shfl_sync(kFull, entry, g) * block;
+        r1 = bounds + (size_t)__shfl_sync(kFull, entry, g + 8) * block;
         entry = entry_of(tile + step);
+    };
+    if (ONE && first < tiles) {
+        rows_of(first);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) load(i);
+    }
+    for (int tile = first; tile < tiles; tile += step) {
+        // One token has one pass of products, behind each of which the next tile's bounds take its place (96 requests:
+        // 86.0 us without, 83.1); with several the registers do not suffice for that.
+        const bool more = ONE && tile + step < tiles;
+        if (ONE) rows_of(tile + step);
+        if (!ONE) {
+            rows_of(tile);
+#pragma unroll
+            for (int i = 0; i < NC; ++i) load(i);
+        }
         {   // S, of each head where there are 8 columns at most, else of the largest |q|
             float m[4] = {0.f, 0.f, 0.f, 0.f};
             const uint32_t q = s.q + (uint32_t)(ONE ? g : s.tokens << s.heads_log2) * ROW + c * 16;
@@ -540,7 +556,7 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
                 for (int k = 0; k < 4; ++k) sh[b][k] = sl[b][k] = 0.f;
             const uint32_t q = s.q + (uint32_t)(grp * 8 + g) * ROW + c * 16;
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
+            for (int i = 0; i < NC; ++i) {
 #pragma unroll
                 for (int b = 0; b < GB; ++b) {
                     const uint4 x = load_shared(q + b * 8 * ROW + i * 64);
@@ -549,6 +565,8 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
                     mma_bf16_16816(sh[b], hi[i][0].z, hi[i][1].z, hi[i][0].w, hi[i][1].w, max_nan2(x.z, 0), max_nan2(x.w, 0));
                     mma_bf16_16816(sl[b], lo[i][0].z, lo[i][1].z, lo[i][0].w, lo[i][1].w, min_nan2(x.z, 0), min_nan2(x.w, 0));
                 }
+                if (ONE && more) load(i);
+            }
             // columns 2c and 2c + 1: heads of the same token unless a token has one column
             const int mask = (1 << s.heads_log2) - 1, h0 = (2 * c) & mask, h1 = (2 * c + 1) & mask;
 #pragma unroll
