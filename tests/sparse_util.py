@@ -59,14 +59,14 @@ def attend_bound(ref, info, d, dtype):
     """Largest error of pa_sparse, per element of ref [Tq, Hq, D].
 
     A score is a sum of d exact products in fp32, taken as d / 16 matrix steps and 2 joins
-    (bf16) or d / 32 fmas and 5 joins (fp32), each off by at most 2^-23 of
+    (bf16) or 4 fmas and 4 or 5 joins (fp32), each off by at most 2^-23 of
     Z = scale sum |q||k| (2^-24 for a rounding), and is scaled once: 16 * 2^-23 Z covers both.
     Its exponent is off by 2^-22 (ex2) and 2^-24 of the argument, at most 3 Z: together
     e = (16 + 2) 2^-23 Z + 2^-22.  Every weight moves by a factor within exp(+-e), the output
     by 2 e A with A = max |v|.  bf16 weights are two bf16 numbers: off by 2^-16.
     Sums over n positions: 2^-23 for each 16 and for each unit's rescaling, and the
-    joins of up to 64 partials (two weights of 2^-22 and three roundings each, A
-    bounds all): (n / 4 + 64 * 6) 2^-23 A.  The result is rounded once."""
+    joins of partials, at most 64 one after another (of a warp's two sides, of 4 warps, of 16 CTAs:
+    two weights of 2^-22 and three roundings each, A bounds all): (n / 4 + 64 * 6) 2^-23 A.  The result is rounded once."""
     tq, hq, _ = ref.shape
     hkv = info.shape[1]
     z, a, n = (np.repeat(info[:, :, i], hq // hkv, axis=1)[:, :, None] for i in range(3))
