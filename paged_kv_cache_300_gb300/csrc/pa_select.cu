@@ -23,7 +23,7 @@
 // are in and blocks below t - 2 E out for certain.  Where those between are more
 // than the places left, their scores are made again to some 60 bits, as differences
 // from t, and chosen among by the same histograms.  A warp chooses for a token of a tile;
-// all warps together for the only token.
+// the warps that scored it for a token alone: all of the CTA's, or with many rows 4, 2 or one.
 //   E: an m16n8k16 step is taken to be off by at most 2^-22 of the magnitudes it adds
 //   (|accumulator| + |products|; a chain of 8 steps, which this allows 2^-18.7 of its magnitudes, was
 //   off by 2^-19.75 at most in 2.5 million sums of each of five kinds); D / 16 steps a chain: E < 2^-22 (D / 16 + 2) S with S >=
@@ -106,7 +106,7 @@ __device__ __forceinline__ float to_float(float x) { return x; }
 // Shared memory of W warps that choose together.
 template <int W>
 struct Choice {
-    static constexpr int BITS = W == 1 ? 8 : 11, BINS = 1 << BITS;
+    static constexpr int BITS = W == 1 ? 8 : W == 2 ? 9 : W == 4 ? 10 : 11, BINS = 1 << BITS; // 8 bins a thread
     uint32_t bin, above, in, listed, result;
     uint32_t list[32];
     float exact[32];
@@ -114,13 +114,14 @@ struct Choice {
     alignas(16) uint32_t hist[BINS];
 };
 
+// Of the calling thread's W neighbouring warps.
 template <int W>
 __device__ __forceinline__ void choice_sync()
 {
     if (W == 1)
         __syncwarp();
     else
-        __syncthreads();
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / (32 * W)), "n"(32 * W) : "memory");
 }
 
 // f(key, its index) for four neighbouring keys of a row in shared memory (16-byte aligned, n rounded
@@ -807,21 +808,23 @@ struct Shared {
     int bad;      // the first scored block whose table entry is none
 };
 
-// TILE = 1: one token a CTA, or a cluster of `ctas`.  Otherwise up to `tile` tokens of one
-// request.
-template <typename T, int D, int TILE>
+// TILE = 1: W warps a row, or (W = kWarps) a cluster of `ctas`.  Otherwise up to `tile` tokens of one
+// request, scored by all warps, a warp choosing for each (W = 1).
+template <typename T, int D, int TILE, int W>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) select_kernel(const SelectArgs a, int ctas, int tile, int heads_log2)
 {
-    constexpr int W = TILE == 1 ? kWarps : 1; // warps that choose together
+    constexpr int SW = TILE == 1 ? W : kWarps; // warps that score together
     constexpr int ROW = (int)sizeof(T) * D + kPad;
     constexpr bool WIDE = sizeof(T) == 2 && TILE == kTile;
-    extern __shared__ __align__(16) uint32_t keys[]; // [tile][max_blocks_per_seq, a multiple of 4], then the rows of q
-    __shared__ Shared sh;
+    extern __shared__ __align__(16) uint32_t smem[]; // of each SW warps: keys [tile][max_blocks_per_seq, a multiple of 4], then the rows of q
+    __shared__ Shared shared[kWarps / SW];
     __shared__ Choice<W> choice[kWarps / W];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = warp / SW, st = tid % (32 * SW); // the warps that score together, the thread of them
+    Shared &sh = shared[group];
     const bool cluster = ctas > 1;
     const int rank = cluster ? (int)cluster_rank() : 0;
-    if (tid == 0) {
+    if (st == 0) {
         sh.mag = 0;
         sh.bad = INT_MAX;
     }
@@ -832,7 +835,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
     check_lengths(a);
     __syncwarp();
 
-    const int unit = (int)(blockIdx.x / ctas);
+    const int unit = (int)(blockIdx.x / ctas) * (kWarps / SW) + group;
+    if (SW < kWarps && unit >= (long long)a.total_q * a.num_kv_heads) return;
     const int h = unit % a.num_kv_heads; // heads of a tile side by side
     int t = unit / a.num_kv_heads, count = 1;
     QueryRow at;
@@ -849,6 +853,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         at = r.at;
     }
     const int cap = a.max_blocks_per_seq, row_keys = (cap + 3) & ~3, need = a.top_k - a.first - a.last;
+    uint32_t *keys = smem + (SW < kWarps ? (size_t)group * (row_keys + 9 * ROW / 4) : 0);
     const int last_seen = at.pos + count - 1 < 0 ? 0 : (at.pos + count - 1) / a.block_size + 1; // by the last token
     const bool nothing = at.skip || last_seen <= a.top_k || need == 0; // to be scored
     if (nothing) {
@@ -868,36 +873,36 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         // rows of q, 16 bytes a thread; then the largest |q| of each channel
         constexpr int PIECES = (int)sizeof(T) * D / 16;
         const int wide = (count + 7) & ~7, rows = WIDE ? a.group * wide : count << heads_log2;
-        for (int i = tid; i < rows * PIECES; i += kThreads) {
+        for (int i = st; i < rows * PIECES; i += 32 * SW) {
             const int r = i / PIECES, p = i % PIECES;
             const int g = WIDE ? r / wide : r & ((1 << heads_log2) - 1), tk = WIDE ? r - g * wide : r >> heads_log2;
             uint4 x = make_uint4(0, 0, 0, 0);
             if (g < a.group && tk < count) x = reinterpret_cast<const uint4 *>(q + ((size_t)tk * a.num_heads + g) * D)[p];
             *reinterpret_cast<uint4 *>(q_rows + (size_t)r * ROW + p * 16) = x;
         }
-        __syncthreads();
+        choice_sync<SW>();
         if (TILE > 1 || sizeof(T) == 4) {
-            if (tid < D) {
+            T *env = reinterpret_cast<T *>(q_rows + (size_t)rows * ROW);
+            for (int d = st; d < D; d += 32 * SW) {
                 float u = 0.f;
                 for (int r = 0; r < rows; ++r) { // (a head with an infinity has no finite score)
-                    const float x = fabsf(to_float(reinterpret_cast<const T *>(q_rows + (size_t)r * ROW)[tid]));
+                    const float x = fabsf(to_float(reinterpret_cast<const T *>(q_rows + (size_t)r * ROW)[d]));
                     if (x < INFINITY) u = fmaxf(u, x);
                 }
-                T *env = reinterpret_cast<T *>(q_rows + (size_t)rows * ROW);
                 if constexpr (sizeof(T) == 2)
-                    env[tid] = __float2bfloat16_rn(u);
+                    env[d] = __float2bfloat16_rn(u);
                 else
-                    env[tid] = u;
+                    env[d] = u;
             }
-            __syncthreads();
+            choice_sync<SW>();
         }
         if (cluster) cluster_wait(); // the first CTA's shared memory is there
         float mag = 0.f;
         int bad = INT_MAX;
         if constexpr (WIDE)
-            score_tokens<D>(a, s, rank * kWarps + warp, ctas * kWarps, lane, mag, bad);
+            score_tokens<D>(a, s, rank * SW + warp % SW, ctas * SW, lane, mag, bad);
         else
-            score_blocks<D, TILE == 1>(a, s, rank * kWarps + warp, ctas * kWarps, lane, mag, bad, q);
+            score_blocks<D, TILE == 1>(a, s, rank * SW + warp % SW, ctas * SW, lane, mag, bad, q);
         const uint32_t most = __reduce_max_sync(kFull, __float_as_uint(mag));
         bad = __reduce_min_sync(kFull, bad);
         if (lane == 0) {
@@ -909,17 +914,17 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
             cluster_arrive();
             cluster_wait();
         } else {
-            __syncthreads();
+            choice_sync<SW>();
         }
     }
     if (rank != 0 || at.skip) return;
     const int bad_block = nothing ? INT_MAX : sh.bad;
-    if (tid == 0 && (at.err || bad_block != INT_MAX)) flag_error(a.dev_err, at.err ? at.err : PA_DEVERR_BAD_BLOCK);
+    if (st == 0 && (at.err || bad_block != INT_MAX)) flag_error(a.dev_err, at.err ? at.err : PA_DEVERR_BAD_BLOCK);
     // the tokens' outputs, by W warps each
-    for (int i = warp / W; i < count; i += kWarps / W) {
+    for (int i = TILE == 1 ? 0 : warp; i < count; i += kWarps) {
         const int seen = at.pos + i < 0 ? 0 : (at.pos + i) / a.block_size + 1;
         int32_t *out = a.selected + ((size_t)(t + i) * a.num_kv_heads + h) * a.top_k;
-        const int wt = W == 1 ? lane : tid;
+        const int wt = tid % (32 * W);
         if (seen <= a.top_k) {
             for (int k = wt; k < a.top_k; k += 32 * W) out[k] = k < seen ? k : -1;
             continue;
@@ -942,29 +947,31 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         r.need = need;
         // 2 E, and the rounding of S
         r.width = (sizeof(T) == 2 ? (D / 16 + 2) * 0x1.02p-21f : (D / 16 + 6) * 0x1.02p-23f) * __uint_as_float(sh.mag);
-        choose<T, D, W>(keys + (size_t)i * row_keys, r, out + a.first, a, 1 << heads_log2, choice[W == 1 ? warp : 0], wt);
+        choose<T, D, W>(keys + (size_t)i * row_keys, r, out + a.first, a, 1 << heads_log2, choice[warp / W], wt);
     }
 }
 
-template <typename T, int D, int TILE>
+template <typename T, int D, int TILE, int W>
 int launch(const SelectArgs &a, int ctas, int tile, int heads_log2, size_t smem, cudaStream_t s)
 {
     static int raised[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return PA_ERR_DEVICE;
     if (!__atomic_load_n(&raised[dev], __ATOMIC_ACQUIRE)) {
-        cudaError_t e = cudaFuncSetAttribute(select_kernel<T, D, TILE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(select_kernel<T, D, TILE, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kSelectMaxBlocks * 4 + 16 + (kGroup + 1) * ((int)sizeof(T) * D + kPad));
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(select_kernel<T, D, TILE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            e = cudaFuncSetAttribute(select_kernel<T, D, TILE, W>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return launch_status(e);
         __atomic_store_n(&raised[dev], 1, __ATOMIC_RELEASE);
     }
     // tiles do not pass the end of a request: one more for each
     const long long tiles = TILE == 1 ? a.total_q : a.total_q / tile + (long long)a.batch;
-    if (tiles * a.num_kv_heads * ctas >= 1ll << 31) return PA_ERR_UNSUPPORTED;
+    const int per_cta = TILE == 1 ? kWarps / W : 1;
+    const long long grid = (tiles * a.num_kv_heads + per_cta - 1) / per_cta * ctas;
+    if (grid * per_cta >= 1ll << 31) return PA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * a.num_kv_heads * ctas));
+    cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -977,7 +984,7 @@ int launch(const SelectArgs &a, int ctas, int tile, int heads_log2, size_t smem,
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ctas > 1 ? 2 : 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, select_kernel<T, D, TILE>, a, ctas, tile, heads_log2));
+    return launch_status(cudaLaunchKernelEx(&cfg, select_kernel<T, D, TILE, W>, a, ctas, tile, heads_log2));
 }
 
 template <typename T, int D>
@@ -1001,9 +1008,21 @@ int launch_tile(const SelectArgs &a, cudaStream_t s)
     const long long fit = std::min<long long>(fill / units_of(tile), (a.max_blocks_per_seq + 16 * kWarps - 1) / (16 * kWarps));
     const int ctas = fit <= 1 ? 1 : fit <= 8 ? (int)fit : fit >= 16 ? 16 : 8; // (9 to 15 are slower than 8)
     if constexpr (sizeof(T) == 2)
-        if (tile > 1 && tile < 8) return launch<T, D, 4>(a, ctas, tile, heads_log2, smem_of(tile), s);
-    if (tile > 1) return launch<T, D, kTile>(a, ctas, tile, heads_log2, smem_of(tile), s);
-    return launch<T, D, 1>(a, ctas, 1, heads_log2, smem_of(1), s);
+        if (tile > 1 && tile < 8) return launch<T, D, 4, 1>(a, ctas, tile, heads_log2, smem_of(tile), s);
+    if (tile > 1) return launch<T, D, kTile, 1>(a, ctas, tile, heads_log2, smem_of(tile), s);
+    // Many rows: fewer warps each, which wait less for one another, while there are enough to fill two thirds of the
+    // places and none has more than 14 tiles of 16 blocks (fp32: 8).  8 warps, 4, 2, 1, us, 8 kv heads of 128 in bf16: 1000
+    // requests of up to 94 blocks 169, 100, 64, 51; 200 of up to 563 65, 57, 60, 71; 96 of up to 2048 86, 93, 122, 197;
+    // 200 in fp32 120, 123, 142, 205.
+    int warps = kWarps;
+    while (ctas == 1 && warps > 1 && a.max_blocks_per_seq <= (sizeof(T) == 2 ? 14 : 8) * 16 * (warps / 2) && 3 * rows * (warps / 2) >= 2 * fill * kWarps &&
+           smem_of(1) * (kWarps / (warps / 2)) <= 100 * 1024)
+        warps /= 2;
+    const size_t smem = smem_of(1) * (kWarps / warps);
+    if (warps == 1) return launch<T, D, 1, 1>(a, 1, 1, heads_log2, smem, s);
+    if (warps == 2) return launch<T, D, 1, 2>(a, 1, 1, heads_log2, smem, s);
+    if (warps == 4) return launch<T, D, 1, 4>(a, 1, 1, heads_log2, smem, s);
+    return launch<T, D, 1, kWarps>(a, ctas, 1, heads_log2, smem, s);
 }
 
 }  // namespace

@@ -156,6 +156,43 @@ def test_select_for_tiles_of_many_requests(dtype, batch, most):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("batch,width", [(137, 90), (271, 200), (271, 120), (541, 90), (547, 40)])
+@pytest.mark.parametrize("d,group,packed", [(64, 3, False), (128, 8, False), (64, 1, True), (128, 4, True)])
+def test_select_of_many_rows(dtype, batch, width, d, group, packed):
+    """Rows enough for four, two and one warps each, in numbers that leave places empty:
+    short and long ones side by side, close scores, a row with a bad entry and one with a bad length, rows of
+    requests left out; as packed queries, some requests without any and rows behind the last."""
+    bs, hkv, top = 16, 3, 7
+    assert (batch * hkv) % 8 != 0
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, width * bs + 1, batch).astype(np.int32)
+    lens[5], lens[9], lens[12], lens[20] = pa.PA_LEFT_OUT, width * bs, width * bs, 1
+    nb = 300
+    table = rng.integers(0, nb, (batch, width)).astype(np.int32)
+    bounds = _bounds(5, nb, hkv, d, dtype)
+    bounds[: nb // 2] = bounds[nb // 2:]  # scores that are equal
+    cu = new = None
+    if packed:
+        new = np.ones(batch, dtype=np.int64)
+        new[[3, 30, batch - 1]] = 0
+        cu = torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32))
+    q = torch.randn(batch, hkv * group, d, generator=torch.Generator().manual_seed(8)).to(dtype)
+    tokens = batch if cu is None else int(cu[-1])
+    want = np.full((batch, hkv, top), -9, dtype=np.int32)
+    clean = np.where(lens < 0, 0, lens)
+    want[:tokens] = _want(q[:tokens], bounds, torch.from_numpy(table), torch.from_numpy(clean), top, bs, cu=cu)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = _select(q, bounds, torch.from_numpy(table), torch.from_numpy(lens), top, bs, cu=cu, dev_err=err)
+    assert err.item() == 0 and np.array_equal(got, want)
+    table[9, width // 2], lens[12] = nb, width * bs + 1
+    rows = np.arange(batch) if cu is None else np.cumsum(new) - 1
+    want[rows[9]], want[rows[12]] = -1, -1
+    got = _select(q, bounds, torch.from_numpy(table), torch.from_numpy(lens), top, bs, cu=cu, dev_err=err)
+    assert err.item() == pa.DEVERR_BAD_BLOCK | pa.DEVERR_OVERFLOW
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("batch,hkv,part", [(3, 2, 25), (2, 1, 70), (5, 3, 4), (2, 2, 9)])
 def test_select_for_tiles_on_clusters(dtype, batch, hkv, part):
     """Few tiles of tokens over long contexts: a cluster of CTAs for each, in which the first
