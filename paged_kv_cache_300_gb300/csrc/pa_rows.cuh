@@ -40,7 +40,6 @@ __device__ __forceinline__ void check_lengths(const Args &a)
 struct QueryRow {
     int req;
     int pos;   // < 0: sees nothing (the rows behind it may, but for the same error or left-out request)
-    int left;  // the request's queries from row t on
     bool skip; // behind the last request: its outputs are left as they are
     int err;   // PA_DEVERR_* bits
 };
@@ -49,7 +48,7 @@ struct QueryRow {
 template <typename Args>
 __device__ __forceinline__ QueryRow request_row(const Args &a, int req, int back)
 {
-    QueryRow q{req, -(1 << 30), back + 1, false, 0};
+    QueryRow q{req, -(1 << 30), false, 0};
     const int kl = a.seqlens_k[req];
     if (kl == PA_LEFT_OUT) return q;
     if (kl < 0 || (long long)kl > (long long)a.max_blocks_per_seq * a.block_size) {
@@ -64,7 +63,7 @@ template <typename Args>
 __device__ __forceinline__ QueryRow query_row(const Args &a, int t, int lane)
 {
     if (a.cu_q == nullptr) return request_row(a, t, 0);
-    QueryRow q{t, -(1 << 30), 1, false, 0};
+    QueryRow q{t, -(1 << 30), false, 0};
     q.req = find_last([&](int r) { return (long long)a.cu_q[r]; }, a.batch, t, lane);
     if (q.req == a.batch) {
         q.skip = true;

@@ -114,12 +114,14 @@ struct Choice {
     alignas(16) uint32_t hist[BINS];
 };
 
-// Of the calling thread's W neighbouring warps.
+// Of the calling thread's W neighbouring warps.  (A barrier whose number is no constant costs all rows some 2%.)
 template <int W>
 __device__ __forceinline__ void choice_sync()
 {
     if (W == 1)
         __syncwarp();
+    else if (W == kWarps)
+        __syncthreads();
     else
         asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.x / (32 * W)), "n"(32 * W) : "memory");
 }
@@ -783,7 +785,7 @@ struct TileRows {
 };
 __device__ __forceinline__ TileRows tile_rows(const SelectArgs &a, int unit, int tile, int lane)
 {
-    TileRows t{0, 0, {0, -(1 << 30), 0, false, 0}};
+    TileRows t{0, 0, {0, -(1 << 30), false, 0}};
     const int c_first = a.cu_q[0];
     const int r = find_last([&](int i) { return (long long)a.cu_q[i] / tile + i; }, a.batch, unit, lane);
     if (c_first != 0) { // no row has a request: all are refused
