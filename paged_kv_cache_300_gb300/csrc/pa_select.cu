@@ -114,7 +114,8 @@ struct Choice {
     alignas(16) uint32_t hist[BINS];
 };
 
-// Of the calling thread's W neighbouring warps.  (A barrier whose number is no constant costs all rows some 2%.)
+// Of the calling thread's W neighbouring warps.  (With a numbered barrier for the CTA too, 96 requests
+// take 85.6 us instead of 83.0.)
 template <int W>
 __device__ __forceinline__ void choice_sync()
 {
