@@ -14,9 +14,9 @@
 // bf16.  A warp has a ring of its own: 16 tokens of one head are one TMA box for K
 // and one for V (128-byte swizzled), requested by the warp's first lane as soon as the
 // slot has been read.  The heads are on N of mma.sync as in the decode kernel:
-// S^T = K q^T, then O^T += V^T P^T with P moved by movmatrix, each weight as two bf16
-// numbers (one alone is off by 2^-9, which shows beside the output's own rounding; the
-// second product costs no loads).  V rows behind the query
+// S^T = K q^T, then O^T += V^T P^T with P moved by movmatrix, each weight as three bf16
+// numbers, which hold all of its 24 bits (values whose sum cancels show what one or two leave out;
+// the further products cost no loads).  V rows behind the query
 // are zeroed in shared memory, so that what an unused slot holds (even NaN) meets a
 // weight of 0 as a zero.
 //
@@ -195,10 +195,13 @@ __device__ __forceinline__ int look_up(const SparseArgs &a, const int32_t *list,
     return count;
 }
 
-// What rounding lo, hi to the bf16 pair w has left, as a bf16 pair.
-__device__ __forceinline__ uint32_t left_of(float lo, float hi, uint32_t w)
+// lo, hi as a bf16 pair; what that leaves stays in them (exact).
+__device__ __forceinline__ uint32_t take_bf16(float &lo, float &hi)
 {
-    return pack_bf16(lo - __uint_as_float(w << 16), hi - __uint_as_float(w & 0xffff0000u));
+    const uint32_t w = pack_bf16(lo, hi);
+    lo -= __uint_as_float(w << 16);
+    hi -= __uint_as_float(w & 0xffff0000u);
+    return w;
 }
 
 template <int D>
@@ -372,17 +375,20 @@ __global__ void __launch_bounds__(kThreads, 3)
             s[3] = exp2_approx(s[3] - mu1);
             l0 += s[0] + s[2];
             l1 += s[1] + s[3];
-            // ---- O^T[channel, head] += V^T P^T, a weight as the sum of two bf16 numbers
-            const uint32_t w0 = pack_bf16(s[0], s[1]), w1 = pack_bf16(s[2], s[3]);
-            const uint32_t b0 = movmatrix_trans(w0), b1 = movmatrix_trans(w1);
-            const uint32_t c0 = movmatrix_trans(left_of(s[0], s[1], w0)), c1 = movmatrix_trans(left_of(s[2], s[3], w1));
+            // ---- O^T[channel, head] += V^T P^T, a weight as the sum of three bf16 numbers
+            uint32_t w[3][2];
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    w[i][j] = movmatrix_trans(take_bf16(s[2 * j], s[2 * j + 1]));
 #pragma unroll
             for (int dm = 0; dm < KS; ++dm) {
                 const int d = dm * 16 + v_doff;
                 uint32_t r0, r1, r2, r3;
                 ldsm_x4_trans(vbase + (d >> 6) * R::SLAB + sw128_offset(v_toff, d & 63), r0, r1, r2, r3);
-                mma_bf16_16816(acc[dm], r0, r1, r2, r3, b0, b1);
-                mma_bf16_16816(acc[dm], r0, r1, r2, r3, c0, c1);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) mma_bf16_16816(acc[dm], r0, r1, r2, r3, w[i][0], w[i][1]);
             }
             __syncwarp(); // every lane has read the slot
             if (lane == 0 && ahead < units) request(r0, stage);

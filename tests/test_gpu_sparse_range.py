@@ -1,0 +1,60 @@
+"""Block-sparse calls where the numbers are hardest: weights whose sums cancel."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_300_gb300 as pa
+from tests.sparse_util import BF16, F32, f64, half_step, make_cache
+from tests.test_gpu_sparse import _attend
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _needs_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pa.load()
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [9, 1300])
+def test_sparse_holds_weights_to_fp32(dtype, d, rows):
+    """Values whose weighted sum cancels to some 2^-24 of its terms show what the weights are held to.
+
+    A score is one exact product k of 8 bits, at most 1 in magnitude, and the scale is ln 2, so a weight is
+    2^k: scale and its product with log2 e are off by 2^-24 each, the power by 2^-22 (ex2's bound), a difference
+    from the reference by 2^-24, so a weight by 2^-22 + 4 ln 2 2^-24 < 2^-22 + 2^-22 of itself.  What 24 bits hold it to:
+    2^-24.  The products' sums, 16 terms in three steps of at most 2^-21 of their magnitudes (bf16) or 16 fmas
+    and one join of two sides (fp32): 3 2^-21.  Numerator and the sum of weights each: (2 2^-22 + 2^-24 + 3 2^-21)
+    of their magnitudes; one division and the output's rounding."""
+    bs, hkv, group = 16, 2, 4
+    rng = np.random.default_rng(d + rows)
+    lens = [bs] * rows
+    c = make_cache(3, lens, hkv, d, bs, dtype)
+    k = torch.zeros_like(c["k"])
+    k[..., 0] = -torch.from_numpy(rng.integers(0, 128, tuple(k.shape[:3]))).to(dtype) / 128
+    q = torch.zeros(rows, hkv * group, d, dtype=dtype)
+    q[..., 0] = 1
+    # the last three values of a channel take back what the sum of those before has left, 8 bits each
+    w = np.exp2(f64(k)[..., 0])[..., None]
+    v = f64(torch.randn(c["v"].shape, generator=torch.Generator().manual_seed(d)).to(dtype))
+    v[:, -3:] = 0
+    for t in (-3, -2, -1):
+        left = -(w * v).sum(1) / w[:, t]
+        v[:, t] = f64(torch.from_numpy(left).to(BF16))
+    c["k"], c["v"] = k, torch.from_numpy(v).to(dtype)
+    sel = np.zeros((rows, hkv, 1), dtype=np.int32)
+    got = f64(_attend(c, q, sel, float(np.log(2.0)))).reshape(rows, hkv, group, d)
+    block = c["table"].numpy()[:, 0]
+    w, v = w[block].astype(np.longdouble), v[block].astype(np.longdouble)  # [rows, 16, hkv, 1 or d]
+    total = w.sum(1)
+    want, size = ((w * v).sum(1) / total)[:, :, None], ((w * np.abs(v)).sum(1) / total)[:, :, None]
+    assert (np.abs(want) < 2.0 ** -20 * size).mean() > 0.9
+    off = 2 * 2.0 ** -22 + 2.0 ** -24 + 3 * 2.0 ** -21
+    bound = off * (size + np.abs(want)) + (half_step(dtype) + 2.0 ** -23) * np.abs(want)
+    err = np.abs(got - want)
+    assert (err <= bound).all(), float((err / bound).max())
