@@ -16,7 +16,7 @@
 // slot has been read.  The heads are on N of mma.sync as in the decode kernel:
 // S^T = K q^T, then O^T += V^T P^T with P moved by movmatrix, each weight as three bf16
 // numbers, which hold all of its 24 bits (values whose sum cancels show what one or two leave out;
-// the further products cost no loads).  V rows behind the query
+// the further products cost no loads).  Units are summed by fp32 additions.  V rows behind the query
 // are zeroed in shared memory, so that what an unused slot holds (even NaN) meets a
 // weight of 0 as a zero.
 //
@@ -375,7 +375,9 @@ __global__ void __launch_bounds__(kThreads, 3)
             s[3] = exp2_approx(s[3] - mu1);
             l0 += s[0] + s[2];
             l1 += s[1] + s[3];
-            // ---- O^T[channel, head] += V^T P^T, a weight as the sum of three bf16 numbers
+            // ---- O^T[channel, head] += V^T P^T, a weight as the sum of three bf16 numbers, the least
+            // first.  The unit's products are added to the row's by an fp32 addition: a matrix product
+            // cuts its sum off (a row of 2048 units summed in it was off by 2^-15.5 of its magnitudes).
             uint32_t w[3][2];
 #pragma unroll
             for (int i = 0; i < 3; ++i)
@@ -387,8 +389,11 @@ __global__ void __launch_bounds__(kThreads, 3)
                 const int d = dm * 16 + v_doff;
                 uint32_t r0, r1, r2, r3;
                 ldsm_x4_trans(vbase + (d >> 6) * R::SLAB + sw128_offset(v_toff, d & 63), r0, r1, r2, r3);
+                float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 3; ++i) mma_bf16_16816(acc[dm], r0, r1, r2, r3, w[i][0], w[i][1]);
+                for (int i = 2; i >= 0; --i) mma_bf16_16816(o, r0, r1, r2, r3, w[i][0], w[i][1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[dm][i] += o[i];
             }
             __syncwarp(); // every lane has read the slot
             if (lane == 0 && ahead < units) request(r0, stage);

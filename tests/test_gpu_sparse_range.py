@@ -1,11 +1,11 @@
-"""Block-sparse calls where the numbers are hardest: weights whose sums cancel."""
+"""Block-sparse calls where the numbers are hardest: weights whose sums cancel, long sums."""
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_cache_300_gb300 as pa
 from tests.sparse_util import BF16, F32, f64, half_step, make_cache
-from tests.test_gpu_sparse import _attend
+from tests.test_gpu_sparse import _attend, i32
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -58,3 +58,44 @@ def test_sparse_holds_weights_to_fp32(dtype, d, rows):
     bound = off * (size + np.abs(want)) + (half_step(dtype) + 2.0 ** -23) * np.abs(want)
     err = np.abs(got - want)
     assert (err <= bound).all(), float((err / bound).max())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_sparse_adds_units_with_rounding(d):
+    """Many keys of positive values, then a few that take their weighted sum back: each unit of 16
+    keys may cost its warp's sum half a step, and a sum that is cut off loses some two.
+
+    512 units a warp, whose sum grows evenly: 512 / 2 half steps of 2^-24 of its end.  Within a unit 3
+    products that cut off, each at most (17 / 4 + 1) 2^-23 of its magnitudes (addends at 2^-25 of the largest, the
+    sum at 2^-23).  A weight: 2 2^-22 as above and 2^-24.  Joins of warps: 3 2^-24 and 4 powers.  All of the
+    magnitudes' sum; the division and the output's rounding of what is left."""
+    bs, hkv, rows, top = 16, 1, 310, 2048
+    rng = np.random.default_rng(d)
+    c = make_cache(3, [4 * bs], hkv, d, bs, BF16, width=top)
+    turn = c["table"][0, :3].tolist()
+    table = np.array([turn[i % 3] for i in range(top - 1)] + [int(c["table"][0, 3])], dtype=np.int32)
+    c["table"] = torch.from_numpy(table).view(1, top).repeat(rows, 1)
+    c["lens"] = i32([top * bs] * rows)
+    c["k"] = torch.zeros_like(c["k"])
+    c["k"][..., 0] = -torch.from_numpy(rng.integers(0, 128, tuple(c["k"].shape[:3]))).to(BF16) / 128
+    w = np.exp2(f64(c["k"])[:, :, 0, 0])  # [blocks, bs]
+    v = f64((torch.rand(c["v"].shape, generator=torch.Generator().manual_seed(d)) + 1).to(BF16))[:, :, 0]
+    last, many = table[-1], [int((table[:-1] == p).sum()) for p in turn]
+    v[last] = 0
+    for t in range(4):
+        left = sum(n * (w[p][:, None] * v[p]).sum(0) for n, p in zip(many, turn)) + (w[last][:, None] * v[last]).sum(0)
+        v[last, t] = f64(torch.from_numpy(-left / w[last, t]).to(BF16))
+    c["v"][:, :, 0] = torch.from_numpy(v).to(BF16)
+    q = torch.zeros(rows, 2, d, dtype=BF16)
+    q[..., 0] = 1
+    sel = np.tile(np.arange(top, dtype=np.int32), (rows, 1, 1))
+    got = f64(_attend(c, q, sel, float(np.log(2.0))))
+    assert (got == got[:1, :1]).all()
+    w, v = w.astype(np.longdouble), v.astype(np.longdouble)
+    parts = [(n, w[p][:, None], v[p]) for n, p in zip(many + [1], turn + [last])]
+    total = sum(n * a.sum(0) for n, a, _ in parts)
+    want, size = sum(n * (a * b).sum(0) for n, a, b in parts) / total, sum(n * (a * abs(b)).sum(0) for n, a, b in parts) / total
+    assert (abs(want) < 2.0 ** -22 * size).all()
+    off = 256 * 2.0 ** -24 + 3 * 5.25 * 2.0 ** -23 + 2 * 2.0 ** -22 + 2.0 ** -24 + 3 * 2.0 ** -24 + 4 * 2.0 ** -22
+    bound = off * size + 2.0 ** -8 * abs(want)
+    assert (abs(got[0, 0] - want) <= bound).all(), float((abs(got[0, 0] - want) / bound).max())
