@@ -43,9 +43,9 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kGroup = 8; // most query heads of a kv head
 constexpr int kList = 64; // units that a warp looks up at a time
-// How far a score may pass the reference of its row's weights (log2): weights up to 2^8,
-// as exact as those up to 1.
-constexpr float kSlack = 8.f;
+// How far a score may pass the reference of its row's weights (log2).  Weights are 2^-kSlack (exact) of the
+// power: none passes 1, and sums reach no further than with the row's maximum as the reference.
+constexpr float kSlack = 8.f, kUnslack = 1.f / 256.f;
 // Tokens of a unit of the fp32 kernel: 4 KB of K.  (64 channels, 1200 rows of 64 blocks of 16: units of 16 tokens 103 us, of 8 137;
 // with blocks of 8, where a unit is half a load, 4000 rows 264 and 235.)
 constexpr int unit_f32(int d) { return 1024 / d; }
@@ -369,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, 3)
                 }
             }
             const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
-            s[0] = exp2_approx(s[0] - mu0);
-            s[1] = exp2_approx(s[1] - mu1);
-            s[2] = exp2_approx(s[2] - mu0);
-            s[3] = exp2_approx(s[3] - mu1);
+            s[0] = exp2_approx(s[0] - mu0) * kUnslack;
+            s[1] = exp2_approx(s[1] - mu1) * kUnslack;
+            s[2] = exp2_approx(s[2] - mu0) * kUnslack;
+            s[3] = exp2_approx(s[3] - mu1) * kUnslack;
             l0 += s[0] + s[2];
             l1 += s[1] + s[3];
             // ---- O^T[channel, head] += V^T P^T, a weight as the sum of three bf16 numbers, the least
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 4) sparse_f32_kernel(const SparseArg
                 const float mu = m == -INFINITY ? 0.f : m;
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
-                    s[b] = exp2f(s[b] - mu);
+                    s[b] = exp2f(s[b] - mu) * kUnslack;
                     l += s[b];
                 }
 #pragma unroll

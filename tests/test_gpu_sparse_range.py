@@ -1,11 +1,12 @@
-"""Block-sparse calls where the numbers are hardest: weights whose sums cancel, long sums."""
+"""Block-sparse calls where the numbers are hardest: weights whose sums cancel, long sums,
+values near the end of the numbers."""
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_cache_300_gb300 as pa
 from tests.sparse_util import BF16, F32, f64, half_step, make_cache
-from tests.test_gpu_sparse import _attend, i32
+from tests.test_gpu_sparse import _attend, _check, i32
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -99,3 +100,22 @@ def test_sparse_adds_units_with_rounding(d):
     off = 256 * 2.0 ** -24 + 3 * 5.25 * 2.0 ** -23 + 2 * 2.0 ** -22 + 2.0 ** -24 + 3 * 2.0 ** -24 + 4 * 2.0 ** -22
     bound = off * size + 2.0 ** -8 * abs(want)
     assert (abs(got[0, 0] - want) <= bound).all(), float((abs(got[0, 0] - want) / bound).max())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,rows", [(64, 1), (128, 1), (128, 40), (128, 930), (64, 6200)])
+def test_sparse_of_values_near_the_end_of_the_numbers(dtype, d, rows):
+    """Weights never pass 1, so that sums of as many values as have one stay finite: first keys of
+    score 0, then as many of score 7.5 (log2), as far as a maximum may grow before it is followed."""
+    bs, n = 16, 64
+    c = make_cache(2, [n * bs], 1, d, bs, dtype)
+    c["k"][:] = 0
+    c["k"][c["table"][0, n // 2:].long(), :, 0, 0] = 7.5
+    c["v"] = ((torch.rand(c["v"].shape, generator=torch.Generator().manual_seed(1)) + 1) * 2.0 ** 117).to(dtype)
+    q = torch.zeros(rows, 2, d, dtype=dtype)
+    q[..., 0] = 1
+    sel = np.arange(n, dtype=np.int32).reshape(1, 1, n)
+    big = dict(c, table=c["table"].repeat(rows, 1), lens=c["lens"].repeat(rows))
+    got = _attend(big, q, np.repeat(sel, rows, 0), float(np.log(2.0)))
+    assert torch.equal(got, got[:1].expand_as(got))
+    _check(got[:1], c, q[:1], sel, float(np.log(2.0)))
