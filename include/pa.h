@@ -497,7 +497,8 @@ int pa_cache_append_rotary(const void *q, const void *k, const void *v, const in
  * the others are those of largest
  *   score = max over the kv head's query heads g of sum_d max(q_gd, 0) hi_d + min(q_gd, 0) lo_d,
  * which no key between the block's bounds lo, hi exceeds in its product with q_g.  The
- * choice is that of the exact scores (ties: the lowest block), whatever the order of the
+ * choice is that of the exact scores (ties: the lowest block; scores that differ by less than
+ * 2^-56 of a sum of |q| |bound| may count as equal), whatever the order of the
  * sums (as long as the sums of |q| |bound| lie between 1e-30 and 3e38; a score that overflows
  * is an infinity).  A NaN ranks above all numbers.  Bounds of the last block are used only where last_blocks is
  * 0: a chunk's later tokens are in them.

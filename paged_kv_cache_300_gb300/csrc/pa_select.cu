@@ -109,7 +109,7 @@ struct Choice {
     static constexpr int BITS = W == 1 ? 8 : W == 2 ? 9 : W == 4 ? 10 : 11, BINS = 1 << BITS; // 8 bins a thread
     uint32_t bin, above, in, listed, result;
     uint32_t list[32];
-    float exact[32];
+    double exact[32];
     uint32_t warp[W][2];
     alignas(16) uint32_t hist[BINS];
 };
@@ -235,9 +235,10 @@ __device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint
 // magnitudes.  64-bit arithmetic would do, but this GPU has little: 2 us a block here.
 struct Sum3 {
     float a = 0.f, b = 0.f, c = 0.f;
-    static __device__ __forceinline__ float two_sum(float x, float y, float &left)
+    template <typename F>
+    static __device__ __forceinline__ F two_sum(F x, F y, F &left)
     {
-        const float s = x + y, t = s - x;
+        const F s = x + y, t = s - x;
         left = (x - (s - t)) + (y - t);
         return s;
     }
@@ -248,13 +249,13 @@ struct Sum3 {
         b = two_sum(b, e, f);
         c += f;
     }
-    __device__ __forceinline__ double value() const { return (double)a + ((double)b + (double)c); }
 };
 
-// The row's score of a block, exact to the last bits of a double.  Four lanes share a head, and neighbouring
-// `lanes` of them, a power of two, a block: `bounds` is theirs (null: none) and the score, in the first of them.
+// By how much the row's score of a block passes `cut`, which is near it: off by some 2^-60 of the magnitudes.  Four
+// lanes share a head, and neighbouring `lanes` of them, a power of two, a block: `bounds` is theirs (null: none) and the
+// result, in the first of them.
 template <typename T, int D>
-__device__ __forceinline__ double exact_score(const T *q, const T *bounds, int G, int lanes, int lane)
+__device__ __forceinline__ double score_above(float cut, const T *q, const T *bounds, int G, int lanes, int lane)
 {
     const int g = (lane & (lanes - 1)) >> 2;
     Sum3 sum;
@@ -280,9 +281,14 @@ __device__ __forceinline__ double exact_score(const T *q, const T *bounds, int G
                 if (sizeof(T) == 4) sum.add(fmaf(u, v, -p)); // (bf16 products are exact)
             }
     }
-    double s = sum.value();
-    s += __shfl_xor_sync(kFull, s, 1);
-    s += __shfl_xor_sync(kFull, s, 2);
+    double s = sum.a, rest = (double)sum.b + (double)sum.c;
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) {
+        double left;
+        s = Sum3::two_sum(s, __shfl_xor_sync(kFull, s, o), left);
+        rest += __shfl_xor_sync(kFull, rest, o) + left;
+    }
+    s = (s - (double)cut) + rest;
     // A head with an infinite q is -infinity where the row's fp32 score is finite; its sum above is NaN.
     if (!(s > -INFINITY)) s = -INFINITY;
     for (int k = 1; k < G; ++k) { // the largest
@@ -378,10 +384,11 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
             sure = mine_sure;
             open = mine_open;
         }
-        if (pass > 0 || !blurred || sure + open == need) break;
-        // more blocks than places within the error of the scores: again and exactly,
-        // as the difference from the cut (a float holds it to 2^-40 of the scores)
-        if (open <= 32) { // as good as always: a few
+        if (pass == 2 || !blurred || sure + open == need) break;
+        // more blocks than places within the error of the scores: again and exactly, as the difference
+        // from the cut.  A few are compared as doubles; of many first what a float holds of the differences,
+        // then, among those of the last float that is taken, what it has left (another 2^-24).
+        if (open <= 32) {
             if (tid == 0) sh.listed = 0;
             choice_sync<W>();
             for (int i = i0 + lane; i < i1; i += 32)
@@ -391,7 +398,7 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
             for (int c0 = warp * blocks; c0 < open; c0 += W * blocks) {
                 const int c = c0 + lane / lanes;
                 const T *bounds = c < open ? r.bounds + (size_t)r.table[sh.list[c]] * a.num_kv_heads * 2 * D : nullptr;
-                const float x = (float)(exact_score<T, D>(r.q, bounds, a.group, lanes, lane) - (double)cut);
+                const double x = score_above<T, D>(cut, r.q, bounds, a.group, lanes, lane);
                 if (c < open && lane % lanes == 0) sh.exact[c] = x;
             }
             choice_sync<W>();
@@ -413,8 +420,8 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
                 const int b = __ffs(todo) - 1;
                 todo &= todo - 1;
                 const T *bounds = r.bounds + (size_t)r.table[(i - lane) + b] * a.num_kv_heads * 2 * D;
-                const double score = __shfl_sync(kFull, exact_score<T, D>(r.q, bounds, a.group, 32, lane), 0);
-                if (lane == b) now = key_of((float)(score - (double)cut));
+                const double x = __shfl_sync(kFull, score_above<T, D>(cut, r.q, bounds, a.group, 32, lane), 0);
+                if (lane == b) now = key_of(pass == 0 || !(fabs(x) < INFINITY) ? (float)x : (float)(x - (double)(float)x));
             }
             if (i < i1) key[i] = now;
         }

@@ -1,12 +1,12 @@
 """Block-sparse calls where the numbers are hardest: weights whose sums cancel, long sums,
-values near the end of the numbers."""
+values near the end of the numbers, scores that differ by less than any float shows."""
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_cache_300_gb300 as pa
 from tests.sparse_util import BF16, F32, f64, half_step, make_cache
-from tests.test_gpu_sparse import _attend, _check, i32
+from tests.test_gpu_sparse import _attend, _bounds, _check, _select, i32
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -119,3 +119,50 @@ def test_sparse_of_values_near_the_end_of_the_numbers(dtype, d, rows):
     got = _attend(big, q, np.repeat(sel, rows, 0), float(np.log(2.0)))
     assert torch.equal(got, got[:1].expand_as(got))
     _check(got[:1], c, q[:1], sel, float(np.log(2.0)))
+
+
+# ------------------------------------------------------------------ selection
+def _whole(x, bits):
+    """float64 -> whole numbers of 2^-bits, Python's own."""
+    m, e = np.frexp(x)
+    return np.array([int(f * 2.0 ** 53) * 2 ** (int(k) - 53 + bits) if f else 0 for f, k in zip(m.ravel(), e.ravel())],
+                    dtype=object).reshape(x.shape)
+
+
+def _exact_choice(q, bounds, top, bits):
+    """The choice of a single row among blocks 0 .. n - 1, the first and the last forced: q [G, D] and bounds
+    [n, 2, D] in whole numbers."""
+    x, lo, hi = _whole(q, bits), _whole(bounds[:, 0], bits), _whole(bounds[:, 1], bits)
+    score = [max(sum(u * (h if u > 0 else l) for u, h, l in zip(row, b_hi, b_lo)) for row in x) for b_hi, b_lo in zip(hi, lo)]
+    n = len(score)
+    rank = sorted(range(1, n - 1), key=lambda j: (-score[j], j))
+    return np.array(sorted([0, n - 1] + rank[:top - 2]), dtype=np.int32)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,top", [(26, 9), (400, 60)])
+@pytest.mark.parametrize("step", [-20, -30, -35, -37, -44])
+@pytest.mark.parametrize("rows,chunk", [(1, False), (19, True), (700, False)])
+def test_select_of_scores_that_no_float_tells_apart(dtype, n, top, step, rows, chunk):
+    """One channel's share of the scores is 2^step of the others', the same in all blocks; its
+    steps decide, however few or many blocks are in doubt and whoever chooses.  Channels 24 and on
+    and 56 and on are added up apart from the others: there, it is the only one that is not 0."""
+    d, bs = 64, 16
+    for seed, at in ((4, 0), (5, 24)):
+        rng = np.random.default_rng(seed)
+        bounds = _bounds(seed, 1, 1, d, dtype).repeat(n, 1, 1, 1).clone()
+        bounds[:, 0, 1, at] = torch.from_numpy(rng.integers(1, 200, n)).to(dtype) * 2.0 ** -6
+        q = torch.randn(4, d, generator=torch.Generator().manual_seed(seed)).abs() + 1
+        if at:
+            q[:, 24:32] = q[:, 56:] = 0
+        q[:, at] = 2.0 ** step
+        q, bounds = q.to(BF16).to(dtype), bounds.to(BF16).to(dtype)
+        table = torch.from_numpy(rng.permutation(n).astype(np.int32)).view(1, n)
+        want = _exact_choice(f64(q), f64(bounds[table[0].long(), 0]), top, 140)
+        many = q.view(1, 4, d).repeat(rows, 1, 1)
+        if chunk:
+            got = _select(many, bounds, table, i32([n * bs]), top, bs, cu=i32([0, rows]))
+            got = got[rows - bs:]  # (the others see a block less)
+        else:
+            got = _select(many, bounds, table.repeat(rows, 1), i32([n * bs] * rows), top, bs)
+        assert (got == want).all()
