@@ -28,7 +28,7 @@
 //   (|accumulator| + |products|; a chain of 8 steps, which this allows 2^-18.7 of its magnitudes, was
 //   off by 2^-19.75 at most in 2.5 million sums of each of five kinds); D / 16 steps a chain: E < 2^-22 (D / 16 + 2) S with S >=
 //   sum |q||b| of every head and block.  S is the largest over the blocks of sum_d u_d max(|lo_d|, |hi_d|),
-//   u the |q| of a head or, for tiles of tokens, the largest |q| of all their heads (one column more).  (fp32: D / 16 + 5
+//   u the |q| of a head or, for tiles of tokens and in fp32, the largest |q| of all their heads (one column more).  (fp32: D / 16 + 5
 //   roundings of 2^-24.)  L1(q) max|b| costs no product but is some 8 times as much, and then many rows
 //   need exact scores (one request: 13.1 us instead of 6.4).
 //
@@ -38,6 +38,7 @@
 // columns), bound by the latency of two CTAs an SM (the products alone, 8 cycles each, are 8 us): some 24 us score, the rest
 // chooses, 4 of it by exact scores.  One token of 313 blocks 6.6 us.
 #include <algorithm>
+#include <float.h>
 #include <limits.h>
 #include <type_traits>
 
@@ -53,6 +54,8 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kGroup = 8;   // most query heads of a kv head
 constexpr int kTile = 16;   // most tokens of a CTA: a warp chooses for two
 constexpr int kPad = 64;    // bytes behind a staged q row: neighbouring rows on other banks
+// The largest |q| of all heads is kept divided by this: its sum with the bounds stays finite where each head's is.
+constexpr float kShrink = 256.f;
 
 // Order-preserving map of floats to integers; a NaN is above everything, 0 is no float's.
 __device__ __forceinline__ uint32_t key_of(float x)
@@ -349,7 +352,7 @@ __device__ __forceinline__ void choose(uint32_t *key, const Row<T> &r, int32_t *
     const bool blurred = fabsf(cut) < INFINITY && r.width > 0.f && r.width < INFINITY;
     if (blurred) {
         low = key_of(cut - r.width);
-        high = key_of(cut + r.width);
+        high = key_of(fminf(cut + r.width, FLT_MAX)); // (infinities stay above)
     }
     // each warp has a run of a multiple of 128 keys, so that places follow from counts
     const int per = ((n + 128 * W - 1) / (128 * W)) * 128, i0 = warp * per, i1 = min(n, i0 + per);
@@ -900,9 +903,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
                     if (x < INFINITY) u = fmaxf(u, x);
                 }
                 if constexpr (sizeof(T) == 2)
-                    env[d] = __float2bfloat16_rn(u);
+                    env[d] = __float2bfloat16_ru(u * (1.f / kShrink));
                 else
-                    env[d] = u;
+                    env[d] = __fmul_ru(u, 1.f / kShrink);
             }
             choice_sync<SW>();
         }
@@ -956,7 +959,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         r.first = a.first;
         r.need = need;
         // 2 E, and the rounding of S
-        r.width = (sizeof(T) == 2 ? (D / 16 + 2) * 0x1.02p-21f : (D / 16 + 6) * 0x1.02p-23f) * __uint_as_float(sh.mag);
+        r.width = (sizeof(T) == 2 ? (D / 16 + 2) * 0x1.02p-21f : (D / 16 + 6) * 0x1.02p-23f) * __uint_as_float(sh.mag) *
+                  (TILE > 1 || sizeof(T) == 4 ? kShrink : 1.f);
         choose<T, D, W>(keys + (size_t)i * row_keys, r, out + a.first, a, 1 << heads_log2, choice[warp / W], wt);
     }
 }

@@ -166,3 +166,25 @@ def test_select_of_scores_that_no_float_tells_apart(dtype, n, top, step, rows, c
         else:
             got = _select(many, bounds, table.repeat(rows, 1), i32([n * bs] * rows), top, bs)
         assert (got == want).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,top", [(26, 9), (400, 60)])
+@pytest.mark.parametrize("tokens", [1, 16])
+def test_select_of_heads_whose_largest_channels_differ(dtype, n, top, tokens):
+    """Each head's products add up to less than 2^128, those of the largest |q| of all heads do not: the
+    scores are in doubt all the same, and 24 bits of them are equal."""
+    d, bs = 64, 16
+    rng = np.random.default_rng(n)
+    bounds = torch.ones(n, 1, 2, d, dtype=dtype)
+    bounds[:, 0, 0] = -1
+    bounds[:, 0, 1, 5] = torch.from_numpy(rng.integers(1, 200, n)).to(dtype) * 2.0 ** -8
+    q = torch.zeros(tokens, 4, d, dtype=dtype)
+    for g in range(4):  # 2^127 and a half each
+        q[:, g, 16 * g] = 1.5 * 2.0 ** 126 if g else 2.0 ** 127
+        q[:, g, 5] = 2.0 ** 100
+    table = torch.from_numpy(rng.permutation(n).astype(np.int32)).view(1, n)
+    got = _select(q, bounds, table, i32([n * bs]), top, bs, cu=i32([0, tokens]))
+    step = f64(bounds[table[0].long(), 0, 1, 5])
+    rank = sorted(range(1, n - 1), key=lambda j: (-step[j], j))
+    assert (got == np.array(sorted([0, n - 1] + rank[:top - 2]), dtype=np.int32)).all()
