@@ -24,9 +24,10 @@
 // than the places left, their scores are made again to some 60 bits, as differences
 // from t, and chosen among by the same histograms.  A warp chooses for a token of a tile;
 // the warps that scored it for a token alone: all of the CTA's, or with many rows 4, 2 or one.
-//   E: an m16n8k16 step is taken to be off by at most 2^-22 of the magnitudes it adds
-//   (|accumulator| + |products|; a chain of 8 steps, which this allows 2^-18.7 of its magnitudes, was
-//   off by 2^-19.75 at most in 2.5 million sums of each of five kinds); D / 16 steps a chain: E < 2^-22 (D / 16 + 2) S with S >=
+//   E: an m16n8k16 step keeps of each of its 17 addends what is above 2^-25 of the largest and cuts its sum off to 24
+//   bits (as measured with a product of 1 and others from 2^-20 to 2^-30 of it), so it is off by at most 2.5 2^-22 of the
+//   magnitudes; a chain of 8 steps that begins with one large product is off by 2^-18 = 8 * 2 2^-22 of them.  D / 16 steps a
+//   chain and the sum of two chains: E < 2^-22 (2.5 D / 16 + 1 / 2) S with S >=
 //   sum |q||b| of every head and block.  S is the largest over the blocks of sum_d u_d max(|lo_d|, |hi_d|),
 //   u the |q| of a head or, for tiles of tokens and in fp32, the largest |q| of all their heads (one column more).  (fp32: D / 16 + 5
 //   roundings of 2^-24.)  L1(q) max|b| costs no product but is some 8 times as much, and then many rows
@@ -959,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 4 && TILE > 1 ? 3 : 2) 
         r.first = a.first;
         r.need = need;
         // 2 E, and the rounding of S
-        r.width = (sizeof(T) == 2 ? (D / 16 + 2) * 0x1.02p-21f : (D / 16 + 6) * 0x1.02p-23f) * __uint_as_float(sh.mag) *
+        r.width = (sizeof(T) == 2 ? (2.5f * (D / 16) + 0.5f) * 0x1.02p-21f : (D / 16 + 6) * 0x1.02p-23f) * __uint_as_float(sh.mag) *
                   (TILE > 1 || sizeof(T) == 4 ? kShrink : 1.f);
         choose<T, D, W>(keys + (size_t)i * row_keys, r, out + a.first, a, 1 << heads_log2, choice[warp / W], wt);
     }

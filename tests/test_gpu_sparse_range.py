@@ -188,3 +188,29 @@ def test_select_of_heads_whose_largest_channels_differ(dtype, n, top, tokens):
     step = f64(bounds[table[0].long(), 0, 1, 5])
     rank = sorted(range(1, n - 1), key=lambda j: (-step[j], j))
     assert (got == np.array(sorted([0, n - 1] + rank[:top - 2]), dtype=np.int32)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens", [1, 24])
+def test_select_of_one_large_product_beside_many_small_ones(dtype, d, tokens):
+    """A large product first and d - 1 small ones behind it that a matrix product drops whole: positive ones in
+    some blocks, negative ones in the others, which hold one more product that makes up for most of the difference."""
+    bs, n, top = 16, 120, 42
+    rng = np.random.default_rng(d)
+    q = torch.full((tokens, 2, d), 1.9921875 * 2.0 ** -13)
+    q[..., 0] = 1
+    small = (d - 1) * 1.9921875 * 2.0 ** -26  # what is dropped
+    more = 0.95 * 2 * small  # the others are less by 2 small - more
+    high = rng.permutation(n - 2)[:top - 2] + 1
+    bounds = torch.full((n, 1, 2, d), -2.0 ** -13)
+    bounds[high, 0, 1, 1:] = 2.0 ** -13
+    bounds[..., 0] = 1
+    other = np.setdiff1d(np.arange(n), high)
+    bounds[other, 0, 1, 1] = more / (1.9921875 * 2.0 ** -13)
+    q, bounds = q.to(dtype), bounds.to(dtype)
+    want = np.array(sorted([0, n - 1] + high.tolist()), dtype=np.int32)
+    table = torch.arange(n, dtype=torch.int32).view(1, n)
+    assert np.array_equal(_exact_choice(f64(q)[0], f64(bounds)[:, 0], top, 140), want)
+    got = _select(q, bounds, table, i32([n * bs]), top, bs, cu=i32([0, tokens]))
+    assert (got[-bs:] == want).all()
