@@ -5,8 +5,9 @@ import pytest
 import torch
 
 import paged_kv_cache_300_gb300 as pa
+from oracle import sparse as ref
 from tests.sparse_util import BF16, F32, f64, half_step, make_cache
-from tests.test_gpu_sparse import _attend, _bounds, _check, _select, i32
+from tests.test_gpu_sparse import _attend, _bounds, _check, _random_choice, _select, i32
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -214,3 +215,32 @@ def test_select_of_one_large_product_beside_many_small_ones(dtype, d, tokens):
     assert np.array_equal(_exact_choice(f64(q)[0], f64(bounds)[:, 0], top, 140), want)
     got = _select(q, bounds, table, i32([n * bs]), top, bs, cu=i32([0, tokens]))
     assert (got[-bs:] == want).all()
+
+
+# ------------------------------------------------------------------ the error of whole outputs
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 8, 2), (64, 6, 1), (64, 16, 2)])
+@pytest.mark.parametrize("chunk", [False, True])
+def test_sparse_error_of_whole_outputs(dtype, d, hq, hkv, chunk):
+    """The relative 2-norm of the error, which is that of fp32 arithmetic and not of less.
+
+    Roundings are half a step at most and of any sign, so sums of n of them grow as the root of n.  A score's
+    d products: root(d) 2^-24 of scale times the root of their squares' sum, less than 3 here; ex2: 2^-22.  Weighted
+    values: root(300) 2^-25 of their sum.  Together e < (3 root(128) + 4 + 9) 2^-24 = 47 2^-24 of the output: the bound in
+    fp32.  A bf16 output is the neighbour of the rounded exact value with a chance of e over a step, 2^-8 to
+    2^-7 of it, and then off by a step: in the 2-norm root(e 2^-7) of the outputs."""
+    bs, top, batch = 16, 20, 24
+    rng = np.random.default_rng(d)
+    lens = [int(n) for n in rng.integers(200, 1500, batch)]
+    cu = None
+    if chunk:
+        cu = np.concatenate([[0], np.cumsum(rng.integers(1, 6, batch))]).astype(np.int32)
+    c = make_cache(d, lens, hkv, d, bs, dtype)
+    q = torch.randn(batch if cu is None else int(cu[-1]), hq, d, generator=torch.Generator().manual_seed(d)).to(dtype)
+    sel = _random_choice(rng, lens, hkv, bs, top, cu)
+    got = f64(_attend(c, q, sel, cu=cu))
+    want, _ = ref.attend(f64(q), f64(c["k"]), f64(c["v"]), c["table"].numpy(), np.array(lens), sel, d ** -0.5, cu)
+    e = 47 * 2.0 ** -24
+    if dtype == BF16:
+        want, e = f64(torch.from_numpy(want).to(BF16)), (e * 2.0 ** -7) ** 0.5
+    assert np.linalg.norm(got - want) <= e * np.linalg.norm(want), np.linalg.norm(got - want) / np.linalg.norm(want)
