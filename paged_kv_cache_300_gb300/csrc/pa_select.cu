@@ -280,7 +280,7 @@ __device__ __forceinline__ double score_above(float cut, const T *q, const T *bo
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float u = to_float(x[i][j]), v = u > 0.f ? to_float(hi[i][j]) : to_float(lo[i][j]); // the other product is 0
-                const float p = u * v;
+                const float p = __fmul_rn(u, v); // (never taken into an addition: what it rounds off is added too)
                 sum.add(p);
                 if (sizeof(T) == 4) sum.add(fmaf(u, v, -p)); // (bf16 products are exact)
             }

@@ -244,3 +244,31 @@ def test_sparse_error_of_whole_outputs(dtype, d, hq, hkv, chunk):
     if dtype == BF16:
         want, e = f64(torch.from_numpy(want).to(BF16)), (e * 2.0 ** -7) ** 0.5
     assert np.linalg.norm(got - want) <= e * np.linalg.norm(want), np.linalg.norm(got - want) / np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("n,top", [(40, 14), (400, 60)])
+@pytest.mark.parametrize("rows,chunk", [(1, False), (19, True), (700, False)])
+def test_select_of_products_that_fp32_rounds(n, top, rows, chunk):
+    """fp32 operands of 24 bits whose products are rounded: blocks in which two channels' shares are
+    moved against each other, so that sums differ by the last bits of the bounds."""
+    d, bs = 64, 16
+    for seed in (1, 2, 3):
+        rng = np.random.default_rng(seed)
+        q = (rng.random((4, d)) + 1).astype(np.float32)
+        q[1:] *= np.float32(0.5)  # the first head decides
+        one = (rng.random((2, d)) + 1).astype(np.float32)
+        one[0] = -one[0]
+        bounds = np.repeat(one[None], n, 0)
+        for j in range(n):
+            a, b = rng.permutation(d)[:2]
+            more = rng.random() / 4
+            bounds[j, 1, a] += np.float32(more)
+            bounds[j, 1, b] -= np.float32(more * q[0, a] / q[0, b])
+        want = _exact_choice(q.astype(np.float64), bounds.astype(np.float64), top, 60)
+        table = torch.arange(n, dtype=torch.int32).view(1, n)
+        many, held = torch.from_numpy(q).view(1, 4, d).repeat(rows, 1, 1), torch.from_numpy(bounds).view(n, 1, 2, d)
+        if chunk:
+            got = _select(many, held, table, i32([n * bs]), top, bs, cu=i32([0, rows]))[rows - bs:]
+        else:
+            got = _select(many, held, table.repeat(rows, 1), i32([n * bs] * rows), top, bs)
+        assert (got == want).all()
