@@ -467,7 +467,7 @@ int pa_rotary(const void *q, const void *k, const int32_t *positions, const floa
  * block, as pa_select_blocks takes them.  A token at offset 0 starts its block's bounds
  * anew, others widen them; NaN wins.  (Tokens that are taken back and written again leave
  * bounds that may be wider than need be, until the block starts anew.)  The rows of one block have to follow one another,
- * in order of their offsets (as pa_block_tables packs them).  Blocks that get no token
+ * in order of their offsets, with no padding between (as pa_block_tables packs them).  Blocks that get no token
  * are left alone.
  */
 int pa_cache_append_rotary(const void *q, const void *k, const void *v, const int32_t *slot_map,
@@ -504,7 +504,8 @@ int pa_cache_append_rotary(const void *q, const void *k, const void *v, const in
  * 0: a chunk's later tokens are in them.
  * dtype is that of q and bounds.  first_blocks + last_blocks <= top_k;
  * max_blocks_per_seq <= 49152; top_k at most 2^20; num_heads / num_kv_heads <= 8; head_dim 64 or 128;
- * total_q * num_kv_heads < 2^27.
+ * total_q * num_kv_heads < 2^27.  How the work is shared out follows max_blocks_per_seq, not the
+ * lengths: a table much wider than the longest request takes up to three times as long.
  * A needed block_table entry that is no block sets PA_DEVERR_BAD_BLOCK, a length beyond
  * the table PA_DEVERR_OVERFLOW: the rows are -1.  cu_seq_lens_q that does not start at 0 or
  * decreases sets PA_DEVERR_BAD_CU; rows are then -1, left as they were or another request's.

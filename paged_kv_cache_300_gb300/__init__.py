@@ -861,7 +861,7 @@ def pa_select_blocks(q, bounds, block_table, seqlens_k, top_k: int, block_size: 
     seqlens_k [B] with the new tokens; cu_seq_lens_q [B + 1] locates the requests'
     queries (None: one of each).  Returns selected [Tq, Hkv, top_k] int32: logical blocks,
     ascending, the first first_blocks and last last_blocks visible ones always among
-    them, -1 behind the last."""
+    them, -1 behind the last.  A table no wider than the longest request is fastest."""
     tq, hq, d = q.shape
     index, dtype = q.get_device(), q.dtype
     if index < 0:

@@ -33,7 +33,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
-// Heads of a thread group: their loads are in flight together, 32 bytes each and lane.
+// Heads of a thread group: their loads are in flight together, 32 bytes each and lane (fp32: 64).
 template <typename T>
 constexpr int kHeadsOf = 8 / (int)sizeof(T);
 constexpr int kMaxAxes = 4;

@@ -33,11 +33,11 @@
 //   roundings of 2^-24.)  L1(q) max|b| costs no product but is some 8 times as much, and then many rows
 //   need exact scores (one request: 13.1 us instead of 6.4).
 //
-// Measured (one GB300): 96 requests of 4096 to 32768 tokens, 64 / 8 heads of 128, 128 of their blocks of 16: 83 us
-// for 451 MB; 7 TB/s while all CTAs score, less where some choose (4 us a row) and while the last rows end (20 us).
-// 565 tokens of 5 chunks, 32 / 8 heads, 64 of up to 750 blocks: 43 us (49 with the heads of a token on neighbouring
+// Measured (one GB300): 96 requests of 4096 to 32768 tokens, 64 / 8 heads of 128, 128 of their blocks of 16: 86 us
+// for 451 MB (83 with half the window of doubt and compared as floats); 7 TB/s while all CTAs score, less where some choose (4 us a row) and while the last rows end (20 us).
+// 565 tokens of 5 chunks, 32 / 8 heads, 64 of up to 750 blocks: 45 us (6 more with the heads of a token on neighbouring
 // columns), bound by the latency of two CTAs an SM (the products alone, 8 cycles each, are 8 us): some 24 us score, the rest
-// chooses, 4 of it by exact scores.  One token of 313 blocks 6.6 us.
+// chooses, 5 of it by exact scores.  One token of 313 blocks 6.5 us, 9.5 where a row is in doubt.
 #include <algorithm>
 #include <float.h>
 #include <limits.h>
@@ -143,15 +143,16 @@ __device__ __forceinline__ void each4(const uint32_t *key, int i, const F &f)
     f(k.w, i + 3);
 }
 
-// The need-th largest of the keys in [lo, hi] (need >= 1, at most as many as there are; lo >= 1).
-// `tid` counts the threads of the W warps.
-// `cleared`: the histogram and the list are empty already, for all threads to see.
+// Empties the histogram and the list.  `tid` counts the threads of the W warps, here and below.
 template <int W>
 __device__ __forceinline__ void clear(Choice<W> &sh, int tid)
 {
     for (int i = 4 * tid; i < Choice<W>::BINS; i += 128 * W) *reinterpret_cast<uint4 *>(&sh.hist[i]) = make_uint4(0, 0, 0, 0);
     if (tid == 0) sh.listed = 0;
 }
+
+// The need-th largest of the keys in [lo, hi] (need >= 1, at most as many as there are; lo >= 1).
+// `cleared`: the histogram and the list are empty already, for all threads to see.
 template <int W>
 __device__ __forceinline__ uint32_t kth_largest(const uint32_t *key, int n, uint32_t need, uint32_t lo, uint32_t hi,
                                                 Choice<W> &sh, int tid, bool cleared)

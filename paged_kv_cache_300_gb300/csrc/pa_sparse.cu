@@ -8,8 +8,8 @@
 // A row is a cluster of 1 to 16 CTAs of kWarps warps, all of which take list
 // entries in turn and keep a softmax (m, l, accumulator) of their own: no split of
 // a row needs memory or counters outside the cluster, so calls share nothing and
-// can be captured as they are.  At the end a CTA joins its warps in shared memory,
-// and the cluster's CTAs join a share of the channels each, read from one another.
+// can be captured as they are.  At the end a CTA joins its warps in shared memory
+// and sends each of the cluster's CTAs its share of the channels, which joins what it is sent.
 //
 // bf16.  A warp has a ring of its own: 16 tokens of one head are one TMA box for K
 // and one for V (128-byte swizzled), requested by the warp's first lane as soon as the
@@ -25,10 +25,10 @@
 // their own, whose smaller state leaves room for twice the tokens and takes fewer shuffles
 // (64 requests, 8 kv heads of 128, 64 blocks of 16, 537 MB: 4 heads each 86 us, 111 in the kernel for 8; 8 heads each 123).
 //
-// Measured (one GB300): 96 requests, 64 / 8 heads of 128, 128 blocks of 16 tokens each: 120 us for 805 MB, 6.7 TB/s (99% of a
-// copy).  565 tokens of 5 chunks, 32 / 8 heads, 64 blocks each: 125 us for 2.4 GB out of L2 (164 MB of it from DRAM), 19 TB/s;
-// tensor pipe 36%, issue slots 41%.  One token of 64 blocks: 5.2 us, of which the loop is 0.8 and the join of 8 CTAs 1.9.
-// fp32, 13 requests, 12 / 3 heads of 64, 17 blocks of 32: 6.3 us.
+// Measured (one GB300): 96 requests, 64 / 8 heads of 128, 128 blocks of 16 tokens each: 123 us for 805 MB, 6.5 TB/s (97% of a
+// copy).  565 tokens of 5 chunks, 32 / 8 heads, 64 blocks each: 138 us for 2.4 GB out of L2 (160 MB of it from DRAM), 17 TB/s;
+// tensor pipe 44%, issue slots 48% (129 us with two numbers a weight, summed in the products).  One token of 64 blocks: 5.4 us, of
+// which the join of 8 CTAs is 1.9.  fp32, 13 requests, 12 / 3 heads of 64, 17 blocks of 32: 7.0 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -593,8 +593,9 @@ __global__ void __launch_bounds__(kThreads, 4) sparse_f32_kernel(const SparseArg
 // How a row is split.  Few rows: a cluster of CTAs each, up to four CTAs an SM in all, while each warp
 // has two units.  Many (`pairs` an SM and more):
 // two warps a row instead of four, which spend less on beginning and joining rows.  64 blocks of
-// 16 tokens, four warps and two, us: head_dim 128, 896 rows 34.7 and 32.2, 1616 rows 58.8 and 51.8, 7000 rows
-// 213 and 194; head_dim 64, 3000 rows 79.4 and 82.6, 7000 rows 170 and 156.
+// 16 tokens, four warps and two, us, rows of one chunk: head_dim 128, 896 rows 32.4 and 29.4, 1600 rows 58.0 and 56.0,
+// 7000 rows 233 and 213; head_dim 64, 3000 rows 81.5 and 77.5, 7000 rows 181 and 160.  Rows with blocks of their own, out
+// of DRAM: 896 rows 74.9 and 75.0, 7000 rows 528 and 529; head_dim 64, 3000 rows 151 and 154, 7000 rows 339 and 341.
 struct Split {
     int ctas, warps;
 };
