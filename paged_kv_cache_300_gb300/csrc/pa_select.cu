@@ -119,7 +119,7 @@ struct Choice {
 };
 
 // Of the calling thread's W neighbouring warps.  (With a numbered barrier for the CTA too, 96 requests
-// take 85.6 us instead of 83.0.)
+// take 2.6 us more.)
 template <int W>
 __device__ __forceinline__ void choice_sync()
 {
@@ -534,7 +534,7 @@ __device__ __forceinline__ void score_blocks(const SelectArgs &a, const Scoring 
     }
     for (int tile = first; tile < tiles; tile += step) {
         // One token has one pass of products, behind each of which the next tile's bounds take its place (96 requests:
-        // 86.0 us without, 83.1); with several the registers do not suffice for that.
+        // 2.9 us less); with several the registers do not suffice for that.
         const bool more = ONE && tile + step < tiles;
         if (ONE) rows_of(tile + step);
         if (!ONE) {
@@ -1017,7 +1017,7 @@ int launch_tile(const SelectArgs &a, cudaStream_t s)
     auto units_of = [&](int t) { return t == 1 ? rows : (a.total_q / t + (long long)a.batch) * a.num_kv_heads; };
     const long long fill = 2ll * num_sms();
     // .. 16 only where there are several for every place: they read the bounds half as often, but take longer
-    // (8 kv heads, 565 tokens of 5 requests: 45.9 us, with 8 43.6; 4096 of 2: 283 and 323).
+    // (8 kv heads, 565 tokens of 5 requests: 48.7 us, with 8 45.2; 4096 of 2: 248 and 288).
     if (tile == kTile && units_of(tile) < 2 * fill) tile /= 2;
     // Few rows or tiles: a cluster of CTAs each, as many as are resident at a time (two an SM)
     // while each warp has a tile of 16 blocks.
@@ -1028,8 +1028,8 @@ int launch_tile(const SelectArgs &a, cudaStream_t s)
     if (tile > 1) return launch<T, D, kTile, 1>(a, ctas, tile, heads_log2, smem_of(tile), s);
     // Many rows: fewer warps each, which wait less for one another, while there are enough to fill two thirds of the
     // places and none has more than 14 tiles of 16 blocks (fp32: 8).  8 warps, 4, 2, 1, us, 8 kv heads of 128 in bf16: 1000
-    // requests of up to 94 blocks 169, 100, 64, 51; 200 of up to 563 65, 57, 60, 71; 96 of up to 2048 86, 93, 122, 197;
-    // 200 in fp32 120, 123, 142, 205.
+    // requests of up to 94 blocks 166, 100, 65, 52; 200 of up to 562 64, 57, 60, 72; 96 of up to 2034 86, 94, 122, 372;
+    // 200 in fp32 118, 123, 142, 206.
     int warps = kWarps;
     while (ctas == 1 && warps > 1 && a.max_blocks_per_seq <= (sizeof(T) == 2 ? 14 : 8) * 16 * (warps / 2) && 3 * rows * (warps / 2) >= 2 * fill * kWarps &&
            smem_of(1) * (kWarps / (warps / 2)) <= 100 * 1024)
